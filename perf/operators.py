@@ -195,8 +195,8 @@ def prepare(case, seed):
         s["v"] = qkv[:, (hq + hkv) * hd:].view(n, hkv, hd)
         s["positions"] = torch.randint(0, case["far"], (case["axes"], n), generator=gen, device=DEV)
         pairs = case["rot"] // 2
-        s["inv_freq"] = [10000.0 ** (-i / pairs) for i in range(pairs)]
-        s["pair_axis"] = _sections(pairs, case["axes"])
+        s["inv_freq"] = 10000.0 ** (-torch.arange(pairs, dtype=torch.float64, device=DEV) / pairs)
+        s["pair_axis"] = _ints(_sections(pairs, case["axes"]))
         blocks = -(-n // bs) + 1
         s["slots"] = torch.randperm(blocks * bs, generator=gen, device=DEV)[:n].contiguous()
         s["slots"][torch.rand(n, generator=gen, device=DEV) < 0.01] = -1  # padding tokens of the batch
@@ -347,9 +347,7 @@ def _turn(x, cos, sin, rot, interleaved):
 
 def _rope_plain(s):
     case = s["case"]
-    freq = torch.tensor(s["inv_freq"], dtype=torch.float64, device=DEV)
-    axis = torch.tensor(s["pair_axis"], device=DEV)
-    angle = s["positions"][axis].t().double() * freq  # far positions lose their angle in 32 bits
+    angle = s["positions"][s["pair_axis"]].t().double() * s["inv_freq"]  # far positions lose their angle in 32 bits
     cos, sin = torch.cos(angle).float()[:, None], torch.sin(angle).float()[:, None]
     s["q_out"].copy_(_turn(s["q"].float(), cos, sin, case["rot"], case["interleaved"]))
     k = _turn(s["k"].float(), cos, sin, case["rot"], case["interleaved"])
@@ -515,8 +513,8 @@ def _rope_exact(s):
     case = s["case"]
     rot = case["rot"]
     half = rot // 2
-    freq = torch.tensor(s["inv_freq"], dtype=torch.float64, device=DEV)
-    angle = torch.stack([s["positions"][a].double() * freq[i] for i, a in enumerate(s["pair_axis"])], 1)
+    angle = torch.stack([s["positions"][a].double() * s["inv_freq"][i]
+                         for i, a in enumerate(s["pair_axis"].tolist())], 1)
     turn = torch.polar(torch.ones_like(angle), angle)[:, None]
 
     def rotated(x):
