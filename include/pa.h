@@ -417,6 +417,203 @@ PA_API pa_status pa_decode_noalloc(void* out, const void* q, const void* k_cache
                                    int32_t block_size, int32_t max_context, float scale, int dtype,
                                    void* stream);
 
+/*
+ * ---- Rotary positions, attention weights and eviction ----------------------
+ * The operators a long-context server runs around the attention above: keys
+ * and queries are rotated by their positions as they enter the cache, the
+ * attention a cached token receives is summed up, and tokens that receive
+ * little are dropped.  Positions are an input of the rotation only; the
+ * cache index of a token (its place in the block table) and its position are
+ * different numbers once tokens have been dropped.  The pages describe the
+ * paged cache underneath ("分页 KV Cache", §块表与 slot mapping and
+ * §分页注意力) and have no counterpart for these.
+ */
+
+/*
+ * pa_rope_write_kv -- rotate q and k, write k and v to their slots.
+ * Token t, rotary pair i (0 <= i < rot_dim / 2):
+ *   angle = positions[pair_axis[i] * n + t] * inv_freq[i]
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)
+ * The pair is elements (i, i + rot_dim / 2) of each head, or (2i, 2i + 1)
+ * with interleaved != 0; elements from rot_dim on pass through.  Several axes
+ * (time, height, width) give each pair the position of its axis; one axis is
+ * ordinary rotary embedding.  Angles are exact in the position: whole turns
+ * are dropped in integer arithmetic, so far positions lose nothing.
+ * q_out gets every token's rotated query heads; k (rotated) and v go to row
+ * slot_mapping[t] of the pools as pa_write_kv puts them, and a negative slot
+ * skips that write (q_out is still written).  Slots must be distinct (check
+ * mode rejects duplicates).  Values are rotated in fp32 and rounded once.
+ *   q_out:        device [n, num_heads, head_dim]; may be q itself when
+ *                 q_stride == num_heads * head_dim, otherwise no overlap
+ *   q, k, v:      device, token t at q + t * q_stride (k_stride, v_stride)
+ *                 elements, its heads contiguous: slices of one fused
+ *                 projection need no copy.  Strides may not be smaller than
+ *                 a token's row
+ *   positions:    device int64 [num_axes, n], any sign
+ *   inv_freq:     device double [rot_dim / 2]
+ *   pair_axis:    device int32 [rot_dim / 2], each in [0, num_axes) (check
+ *                 mode rejects others), or NULL: axis 0
+ *   rot_dim:      even, 2 <= rot_dim <= head_dim <= 256
+ *   num_heads:    a multiple of num_kv_heads, or 0: keys and values only
+ *                 (q and q_out are then ignored)
+ * The pools 16-byte aligned.  Moves 16-byte vectors where head_dim, rot_dim,
+ * strides and addresses allow it, else single elements.
+ */
+PA_API pa_status pa_rope_write_kv(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, const int64_t* positions, int32_t num_axes,
+                                  const double* inv_freq, const int32_t* pair_axis, int32_t rot_dim, int interleaved,
+                                  const int64_t* slot_mapping, int64_t n, void* k_cache, void* v_cache,
+                                  int32_t num_blocks, int32_t block_size, int32_t num_heads, int32_t num_kv_heads,
+                                  int32_t head_dim, int dtype, void* stream);
+
+/*
+ * pa_rope_write_kv_fp8 -- the same into a quantized cache: the rotated k rows
+ * (the fp32 values, not rounded to dtype first) and the v rows are quantized
+ * as pa_write_kv_fp8 does it.
+ *   k_codes, v_codes:   device uint8 [num_blocks, block_size, num_kv_heads, head_dim]
+ *   k_scales, v_scales: device fp32 [num_blocks, num_kv_heads, block_size]
+ */
+PA_API pa_status pa_rope_write_kv_fp8(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, const int64_t* positions, int32_t num_axes,
+                                      const double* inv_freq, const int32_t* pair_axis, int32_t rot_dim,
+                                      int interleaved, const int64_t* slot_mapping, int64_t n, void* k_codes,
+                                      void* v_codes, float* k_scales, float* v_scales, int32_t num_blocks,
+                                      int32_t block_size, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int dtype, void* stream);
+
+/*
+ * pa_decode_weights -- pa_decode that also accounts for the attention each
+ * cached token received: with p_h the softmax weights of query head h,
+ *   w(j) = sum over the query heads h of KV head kv of p_h(j),   j < L,
+ *   weights[s, kv, j] += w(j) for j < L - 1, and = w(j) for j = L - 1
+ * (the newest token, whose query this is, has no history).  out is
+ * pa_decode's.  Entries from L on are left as they are, and a sequence with
+ * L = 0 gets a zero row of out and no weights.  Weights are fp32, summed in a
+ * fixed order: the same inputs give the same bits.
+ *   weights:   device fp32 [num_seqs, num_kv_heads, weights_stride], row s
+ *              belonging to sequence s as its block-table row does;
+ *              weights_stride >= max_context
+ *   workspace: pa_decode_weights_workspace_size(...) bytes, 16-byte aligned;
+ *              its content on entry does not matter
+ * The other arguments and the kernels' conditions are pa_decode's.  Weights
+ * are per sequence, so sequences may share blocks.
+ */
+PA_API size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size, int32_t max_context, int dtype);
+PA_API pa_status pa_decode_weights(void* out, float* weights, int64_t weights_stride, const void* q,
+                                   const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                   int32_t max_blocks, const int32_t* context_lens, int32_t num_seqs,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                   int32_t block_size, int32_t max_context, float scale, int dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * pa_decode_weights_fp8 -- the same over a quantized cache (see
+ * pa_decode_fp8).  The query enters the products unscaled, so on the
+ * tensor-core path |q| must lie inside the f16 range.
+ */
+PA_API size_t pa_decode_weights_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t block_size, int32_t max_context,
+                                                   int dtype);
+PA_API pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weights_stride, const void* q,
+                                       const void* k_codes, const void* v_codes, const float* k_scales,
+                                       const float* v_scales, const int32_t* block_tables, int32_t max_blocks,
+                                       const int32_t* context_lens, int32_t num_seqs, int32_t num_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                       int32_t block_size, int32_t max_context, float scale, int dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pa_prompt_weights -- the same account for a step of many new tokens (a
+ * prompt or a chunk of one), beside pa_varlen: the query rows counted are the
+ * last min(n_i, window) of request i's n_i new tokens, all of them when
+ * window is 0, each at its own position and (causal != 0) blind to later
+ * keys; with p the softmax of a row over the keys it sees,
+ *   w(j) = sum over counted rows and the query heads of KV head kv of p(j),
+ *   weights[i, kv, j] += w(j) for j < L_i - n_i (cached before this step),
+ *   weights[i, kv, j]  = w(j) for L_i - n_i <= j < L_i (new).
+ * A request without new tokens keeps its weights as they are; entries from
+ * L_i on are left as they are.  A fixed order of summation, fp32.
+ *   weights, weights_stride: as for pa_decode_weights
+ *   q, cu_seqlens_q, seq_lens, block_tables, total_q, max_q, causal: as for pa_varlen
+ *   window:    >= 0
+ *   workspace: pa_prompt_weights_workspace_size(...) bytes, 16-byte aligned
+ * bf16/f16 with head_dim 64 or 128 and block_size 8 or a multiple of 16 up to
+ * 256 run on the tcgen05 kernels (PA_OPT_VARLEN_KERNEL pins a kernel as it
+ * does for pa_varlen), the rest on the CUDA cores.
+ */
+PA_API size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                               int32_t max_context, int32_t window, int dtype);
+PA_API pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
+                                   const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                                   const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t total_q, int32_t max_q,
+                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                                   int32_t block_size, int32_t max_context, int32_t window, float scale, int causal,
+                                   int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* pa_prompt_weights_fp8 -- the same over a quantized cache's keys. */
+PA_API size_t pa_prompt_weights_fp8_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q,
+                                                   int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                   int32_t block_size, int32_t max_context, int32_t window,
+                                                   int dtype);
+PA_API pa_status pa_prompt_weights_fp8(float* weights, int64_t weights_stride, const void* q, const void* k_codes,
+                                       const float* k_scales, const int32_t* block_tables, int32_t max_blocks,
+                                       const int32_t* seq_lens, const int32_t* cu_seqlens_q, int32_t num_seqs,
+                                       int32_t total_q, int32_t max_q, int32_t num_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t num_blocks, int32_t block_size, int32_t max_context,
+                                       int32_t window, float scale, int causal, int dtype, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * pa_evict -- drop the tokens with the least accumulated weight, per sequence
+ * and KV head, down to `keep`, and bring the kept rows to the front.
+ * For (s, h) with L = context_lens[s] cached tokens, n = seen_lens[s] tokens
+ * seen in all (its positions are 0 .. n-1) and c = recorded_lens[s]:
+ *   position(j) = positions[s, h, j]  for j < c (recorded by an earlier call),
+ *                 n - L + j           for c <= j < L (appended since, in order);
+ *   L <= keep: every token is kept;
+ *   L > keep:  held are the tokens with position < num_sink or position >=
+ *              n - num_recent; then the others by weights[s, h, j], largest
+ *              first (NaN above every number, -0 equal to +0, equal weights by
+ *              lower index), until keep are.
+ * Destination index i < new_lens[s] = min(L, keep) receives token i if that is
+ * kept, else the next kept token with index >= keep, in index order.  Its K
+ * and V rows go to the slot of index i through new_block_tables, its weight
+ * and position to entry i of weights_out and positions_out.  In place
+ * (new_block_tables holding the same blocks) only rows that change are
+ * written; a destination block other than the source's receives every row.
+ * The order of a head's rows is not preserved and differs between heads:
+ * attention with rotated keys does not depend on it, and the next call finds
+ * the positions in positions_out.  Rows and entries from new_lens[s] on are
+ * left as they are.
+ *   weights, positions:         device fp32 / int32 [num_seqs, num_kv_heads, weights_stride]
+ *   weights_out, positions_out: the same shapes; each either its input
+ *                 itself or memory apart from it.  positions_out may be NULL
+ *   positions, recorded_lens: both NULL: nothing recorded yet
+ *   seen_lens:    NULL: context_lens (never evicted)
+ *   new_lens:     device int32 [num_seqs], apart from the other arrays
+ *   block_tables, new_block_tables: device int32 [num_seqs, max_blocks],
+ *                 [num_seqs, new_max_blocks].  A block that is written may
+ *                 not be read by, or written for, another (sequence, logical
+ *                 block) of the same call (check mode rejects it): sequences
+ *                 that share a block are given other destination blocks
+ *   k_scales, v_scales: the scale pools of a quantized cache (dtype
+ *                 PA_FP8_E4M3), which move with the codes; NULL otherwise
+ *   keep >= 1; num_sink, num_recent >= 0; num_sink + num_recent <= keep
+ *   workspace:    pa_evict_workspace_size(...) bytes, 16-byte aligned
+ * Rows are moved bit for bit.
+ */
+PA_API size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep);
+PA_API pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* new_lens, const float* weights,
+                          const int32_t* positions, const int32_t* recorded_lens, const int32_t* seen_lens,
+                          int64_t weights_stride, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                          const int32_t* block_tables, int32_t max_blocks, const int32_t* new_block_tables,
+                          int32_t new_max_blocks, const int32_t* context_lens, int32_t num_seqs,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+                          int32_t max_context, int32_t keep, int32_t num_sink, int32_t num_recent, int dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

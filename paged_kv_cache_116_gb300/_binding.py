@@ -23,7 +23,11 @@ EXPORTS = ("pa_status_string", "pa_last_error", "pa_set_option", "pa_get_option"
            "pa_device_status", "pa_slot_mapping", "pa_write_kv", "pa_copy_blocks", "pa_decode_workspace_size",
            "pa_decode", "pa_decode_append", "pa_varlen_workspace_size", "pa_varlen", "pa_decode_noalloc",
            "pa_swap_blocks", "pa_write_kv_fp8", "pa_decode_fp8_workspace_size", "pa_decode_fp8",
-           "pa_decode_append_fp8", "pa_selftest_wait_timeout", "pa_varlen_fp8_workspace_size", "pa_varlen_fp8")
+           "pa_decode_append_fp8", "pa_selftest_wait_timeout", "pa_varlen_fp8_workspace_size", "pa_varlen_fp8",
+           "pa_rope_write_kv", "pa_rope_write_kv_fp8", "pa_decode_weights_workspace_size", "pa_decode_weights",
+           "pa_decode_weights_fp8_workspace_size", "pa_decode_weights_fp8", "pa_prompt_weights_workspace_size",
+           "pa_prompt_weights", "pa_prompt_weights_fp8_workspace_size", "pa_prompt_weights_fp8",
+           "pa_evict_workspace_size", "pa_evict")
 
 
 class PAError(RuntimeError):
@@ -74,6 +78,25 @@ def lib():
         "pa_varlen_fp8_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, i32, ci], sz),
         "pa_varlen_fp8": ([vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, cf,
                            ci, ci, vp, sz, vp], ci),
+        "pa_rope_write_kv": ([vp, vp, vp, vp, i64, i64, i64, vp, i32, vp, vp, i32, ci, vp, i64, vp, vp, i32, i32, i32,
+                              i32, i32, ci, vp], ci),
+        "pa_rope_write_kv_fp8": ([vp, vp, vp, vp, i64, i64, i64, vp, i32, vp, vp, i32, ci, vp, i64, vp, vp, vp, vp,
+                                  i32, i32, i32, i32, i32, ci, vp], ci),
+        "pa_decode_weights_workspace_size": ([i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_decode_weights": ([vp, vp, i64, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, cf, ci, vp,
+                               sz, vp], ci),
+        "pa_decode_weights_fp8_workspace_size": ([i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_decode_weights_fp8": ([vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32,
+                                   cf, ci, vp, sz, vp], ci),
+        "pa_prompt_weights_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_prompt_weights": ([vp, i64, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, cf,
+                               ci, ci, vp, sz, vp], ci),
+        "pa_prompt_weights_fp8_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_prompt_weights_fp8": ([vp, i64, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                   i32, cf, ci, ci, vp, sz, vp], ci),
+        "pa_evict_workspace_size": ([i32, i32, i32, i32], sz),
+        "pa_evict": ([vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
+                      i32, i32, i32, i32, ci, vp, sz, vp], ci),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -345,3 +368,214 @@ def pa_varlen_fp8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, se
                              _ptr(workspace), ws_bytes, _stream(stream))
     _check(st, "pa_varlen_fp8")
     return out
+
+
+def _rope_rows(name, t, heads, hd):
+    """Token stride (elements) of q, k or v [n, heads, hd]: heads contiguous, tokens at any stride."""
+    if not t.is_cuda or tuple(t.shape[1:]) != (heads, hd) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd):
+        raise ValueError("%s must be a CUDA tensor [n, %d, %d] whose heads are contiguous" % (name, heads, hd))
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * hd)
+
+
+def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd):
+    _dev(q_out, positions, inv_freq, slot_mapping, pair_axis)
+    if positions.dim() == 1:
+        positions = positions[None]
+    n = positions.shape[1]
+    if positions.dtype != torch.int64 or inv_freq.dtype != torch.float64 or slot_mapping.dtype != torch.int64:
+        raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
+    if pair_axis is not None and (pair_axis.dtype != torch.int32 or pair_axis.numel() != inv_freq.numel()):
+        raise ValueError("pair_axis must be int32 with one entry per frequency")
+    if k.shape[0] != n or v.shape[0] != n or slot_mapping.shape[0] != n or k.dtype != v.dtype:
+        raise ValueError("q, k, v, positions and slot_mapping must hold the same number of tokens, k and v one dtype")
+    hq, qs = 0, 0
+    if q is not None:
+        hq = q.shape[1]
+        if tuple(q_out.shape) != (n, hq, hd) or q.dtype != k.dtype or q_out.dtype != k.dtype:
+            raise ValueError("q_out must be [n, heads, head_dim], and q, q_out, k and v of one dtype")
+        qs = _rope_rows("q", q, hq, hd)
+    ks, vs = _rope_rows("k", k, hkv, hd), _rope_rows("v", v, hkv, hd)
+    return (_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(positions), positions.shape[0], _ptr(inv_freq),
+            _ptr(pair_axis), 2 * inv_freq.numel()), n, hq
+
+
+def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, pair_axis=None,
+                     interleaved=False, stream=None):
+    """Rotate q [n, Hq, hd] into q_out and k [n, Hkv, hd] into the cache, v with it, at slot_mapping [n].
+
+    positions [num_axes, n] (or [n]) int64, inv_freq [rot_dim / 2] float64, pair_axis [rot_dim / 2] int32 (None: one
+    axis), all on the device.  Tokens of q, k and v may lie at any stride; q None: keys and values only."""
+    _dev(k_cache, v_cache)
+    nb, bs, hkv, hd = k_cache.shape
+    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
+    if k.dtype != k_cache.dtype:
+        raise ValueError("k and the cache must be of one dtype")
+    st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
+                                nb, bs, hq, hkv, hd, _dtype(k), _stream(stream))
+    _check(st, "pa_rope_write_kv")
+    return q_out
+
+
+def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_codes, v_codes, k_scales, v_scales,
+                         pair_axis=None, interleaved=False, stream=None):
+    """pa_rope_write_kv into a quantized cache: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
+    _dev(k_codes, v_codes, k_scales, v_scales)
+    nb, bs, hkv, hd = k_codes.shape
+    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
+    _scale_pools(nb, hkv, bs, k_scales, v_scales)
+    st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _ptr(slot_mapping), n, _ptr(k_codes),
+                                    _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
+                                    _stream(stream))
+    _check(st, "pa_rope_write_kv_fp8")
+    return q_out
+
+
+def _scale_pools(nb, hkv, bs, *scales):
+    for s in scales:
+        if tuple(s.shape) != (nb, hkv, bs) or s.dtype != torch.float32:
+            raise ValueError("scales must be float32 [num_blocks, num_kv_heads, block_size]")
+
+
+def _weight_rows(name, t, S, hkv, dtype=torch.float32):
+    if t.dim() != 3 or tuple(t.shape[:2]) != (S, hkv) or t.dtype != dtype:
+        raise ValueError("%s must be %s [num_seqs, num_kv_heads, weights_stride]" % (name, dtype))
+    return t.shape[2]
+
+
+def _i32(*ts):
+    for t in ts:
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("block tables, lengths and cu_seqlens_q must be int32")
+
+
+def _ws(workspace):
+    return _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def pa_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                                                  code)
+
+
+def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens, max_context, scale, workspace,
+                      stream=None):
+    """pa_decode that adds each cached token's attention weight (summed over the query heads of a KV head) to
+    weights [S, Hkv, stride] fp32; the newest token's entry is set."""
+    _dev(out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    _i32(block_tables, context_lens)
+    nb, bs, hkv, hd = k_cache.shape
+    S, hq, _ = q.shape
+    stride = _weight_rows("weights", weights, S, hkv)
+    st = lib().pa_decode_weights(_ptr(out), _ptr(weights), stride, _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, hq, hkv, hd, nb,
+                                 bs, max_context, float(scale), _dtype(q), *_ws(workspace), _stream(stream))
+    _check(st, "pa_decode_weights")
+    return out
+
+
+def pa_decode_weights_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_decode_weights_fp8_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                      max_context, code)
+
+
+def pa_decode_weights_fp8(out, weights, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens,
+                          max_context, scale, workspace, stream=None):
+    """pa_decode_weights over a quantized cache: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
+    _dev(out, weights, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, workspace)
+    _i32(block_tables, context_lens)
+    nb, bs, hkv, hd = k_codes.shape
+    S, hq, _ = q.shape
+    _scale_pools(nb, hkv, bs, k_scales, v_scales)
+    stride = _weight_rows("weights", weights, S, hkv)
+    st = lib().pa_decode_weights_fp8(_ptr(out), _ptr(weights), stride, _ptr(q), _ptr(k_codes), _ptr(v_codes),
+                                     _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
+                                     _ptr(context_lens), S, hq, hkv, hd, nb, bs, max_context, float(scale), _dtype(q),
+                                     *_ws(workspace), _stream(stream))
+    _check(st, "pa_decode_weights_fp8")
+    return out
+
+
+def pa_prompt_weights_workspace_size(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size,
+                                     max_context, window, dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_prompt_weights_workspace_size(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim,
+                                                  block_size, max_context, window, code)
+
+
+def pa_prompt_weights(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q, max_q, max_context, window, scale,
+                      causal=True, workspace=None, stream=None):
+    """Attention weights that the last `window` (0: all) new tokens of each request give its cached tokens: added to
+    weights [S, Hkv, stride] fp32 for tokens cached before the step, set for new ones.  q [T, Hq, hd]."""
+    _dev(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q, workspace)
+    _i32(block_tables, seq_lens, cu_seqlens_q)
+    nb, bs, hkv, hd = k_cache.shape
+    T, hq, _ = q.shape
+    S = seq_lens.shape[0]
+    stride = _weight_rows("weights", weights, S, hkv)
+    st = lib().pa_prompt_weights(_ptr(weights), stride, _ptr(q), _ptr(k_cache), _ptr(block_tables),
+                                 block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), S, T, max_q, hq, hkv, hd,
+                                 nb, bs, max_context, window, float(scale), 1 if causal else 0, _dtype(q),
+                                 *_ws(workspace), _stream(stream))
+    _check(st, "pa_prompt_weights")
+    return weights
+
+
+def pa_prompt_weights_fp8_workspace_size(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size,
+                                         max_context, window, dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_prompt_weights_fp8_workspace_size(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim,
+                                                      block_size, max_context, window, code)
+
+
+def pa_prompt_weights_fp8(weights, q, k_codes, k_scales, block_tables, seq_lens, cu_seqlens_q, max_q, max_context,
+                          window, scale, causal=True, workspace=None, stream=None):
+    """pa_prompt_weights over a quantized cache's keys: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
+    _dev(weights, q, k_codes, k_scales, block_tables, seq_lens, cu_seqlens_q, workspace)
+    _i32(block_tables, seq_lens, cu_seqlens_q)
+    nb, bs, hkv, hd = k_codes.shape
+    T, hq, _ = q.shape
+    S = seq_lens.shape[0]
+    _scale_pools(nb, hkv, bs, k_scales)
+    stride = _weight_rows("weights", weights, S, hkv)
+    st = lib().pa_prompt_weights_fp8(_ptr(weights), stride, _ptr(q), _ptr(k_codes), _ptr(k_scales),
+                                     _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), S,
+                                     T, max_q, hq, hkv, hd, nb, bs, max_context, window, float(scale),
+                                     1 if causal else 0, _dtype(q), *_ws(workspace), _stream(stream))
+    _check(st, "pa_prompt_weights_fp8")
+    return weights
+
+
+def pa_evict_workspace_size(num_seqs, num_kv_heads, max_context, keep):
+    return lib().pa_evict_workspace_size(num_seqs, num_kv_heads, max_context, keep)
+
+
+def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, block_tables, new_block_tables,
+             context_lens, max_context, keep, num_sink, num_recent, positions=None, recorded_lens=None,
+             seen_lens=None, k_scales=None, v_scales=None, workspace=None, stream=None):
+    """Drop the cached tokens with the least weight, per sequence and KV head, down to `keep` (besides the first
+    num_sink and the newest num_recent positions); kept rows move to the front, through new_block_tables.
+
+    weights, weights_out [S, Hkv, stride] fp32; positions, positions_out the same in int32 (positions_out may be
+    None); new_lens, recorded_lens, seen_lens [S] int32.  Quantized pools (uint8) come with their scale pools."""
+    _dev(new_lens, weights_out, positions_out, weights, k_cache, v_cache, block_tables, new_block_tables, context_lens,
+         positions, recorded_lens, seen_lens, k_scales, v_scales, workspace)
+    _i32(new_lens, block_tables, new_block_tables, context_lens, recorded_lens, seen_lens)
+    nb, bs, hkv, hd = k_cache.shape
+    S = context_lens.shape[0]
+    stride = _weight_rows("weights", weights, S, hkv)
+    rows = [("weights_out", weights_out, torch.float32), ("positions_out", positions_out, torch.int32),
+            ("positions", positions, torch.int32)]
+    for name, t, dt in rows:
+        if t is not None and _weight_rows(name, t, S, hkv, dt) != stride:
+            raise ValueError("%s must have the row stride of weights" % name)
+    if k_scales is not None:
+        _scale_pools(nb, hkv, bs, k_scales, v_scales)
+    st = lib().pa_evict(_ptr(weights_out), _ptr(positions_out), _ptr(new_lens), _ptr(weights), _ptr(positions),
+                        _ptr(recorded_lens), _ptr(seen_lens), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                        _ptr(v_scales), _ptr(block_tables), block_tables.shape[1], _ptr(new_block_tables),
+                        new_block_tables.shape[1], _ptr(context_lens), S, hkv, hd, nb, bs, max_context, keep,
+                        num_sink, num_recent, _pool_dtype(k_cache), *_ws(workspace), _stream(stream))
+    _check(st, "pa_evict")
+    return new_lens

@@ -106,6 +106,75 @@ pa_status check_slots(const int64_t* slot_mapping, int64_t n, int32_t num_blocks
     return PA_OK;
 }
 
+// Check-mode validation of a varlen batch: cu_seqlens_q, lengths and tables.
+pa_status check_varlen(const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                       const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t total_q, int32_t max_q,
+                       int32_t num_blocks, int32_t block_size, int32_t max_context, cudaStream_t st) {
+    pa_status err = PA_OK;
+    std::vector<int32_t> lens, cu;
+    if (!to_host(lens, seq_lens, num_seqs, st, &err) || !to_host(cu, cu_seqlens_q, num_seqs + 1, st, &err))
+        return err;
+    if (cu[0] != 0 || cu[num_seqs] != total_q)
+        return fail(PA_ERR_INDEX, "cu_seqlens_q must start at 0 and end at total_q");
+    for (int32_t i = 0; i < num_seqs; ++i) {
+        const int32_t nn = cu[i + 1] - cu[i];
+        if (nn < 0) return fail(PA_ERR_INDEX, "cu_seqlens_q must be non-decreasing");
+        if (nn > max_q) return fail(PA_ERR_INDEX, "request " + std::to_string(i) + " has more than max_q queries");
+        if (nn > lens[i])
+            return fail(PA_ERR_INDEX, "request " + std::to_string(i) + " has more new tokens than context");
+    }
+    return check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
+}
+
+// Check-mode validation of an eviction: lengths, both tables, and that a
+// block that may be written is read or written for one (sequence, logical
+// block) only.
+pa_status check_evict(const int32_t* recorded_lens, const int32_t* seen_lens, const int32_t* block_tables, int32_t max_blocks,
+                      const int32_t* new_block_tables, int32_t new_max_blocks, const int32_t* context_lens,
+                      int32_t num_seqs, int32_t num_blocks, int32_t block_size, int32_t max_context, int32_t keep,
+                      cudaStream_t st) {
+    pa_status err = PA_OK;
+    std::vector<int32_t> lens, kept, rec, seen, from, to;
+    if (!to_host(lens, context_lens, num_seqs, st, &err)) return err;
+    err = check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
+    if (err != PA_OK) return err;
+    for (int32_t L : lens) kept.push_back(std::min(L, keep));
+    err = check_tables(new_block_tables, num_seqs, new_max_blocks, kept, num_blocks, block_size, max_context, st);
+    if (err != PA_OK) return err;
+    if (recorded_lens && !to_host(rec, recorded_lens, num_seqs, st, &err)) return err;
+    if (seen_lens && !to_host(seen, seen_lens, num_seqs, st, &err)) return err;
+    for (int32_t s = 0; s < num_seqs; ++s) {
+        if (recorded_lens && (rec[s] < 0 || rec[s] > lens[s]))
+            return fail(PA_ERR_INDEX, "sequence " + std::to_string(s) + ": recorded_lens outside [0, context length]");
+        if (seen_lens && seen[s] < lens[s])
+            return fail(PA_ERR_INDEX, "sequence " + std::to_string(s) + ": seen_lens below the context length");
+    }
+    if (!to_host(from, block_tables, (int64_t)num_seqs * max_blocks, st, &err) ||
+        !to_host(to, new_block_tables, (int64_t)num_seqs * new_max_blocks, st, &err))
+        return err;
+    // who reads a block: its (sequence, logical block), or several
+    constexpr int64_t kNobody = -1, kSeveral = -2;
+    std::vector<int64_t> reader((size_t)num_blocks, kNobody), writer((size_t)num_blocks, kNobody);
+    for (int32_t s = 0; s < num_seqs; ++s)
+        for (int64_t b = 0; b * block_size < lens[s]; ++b) {
+            int64_t& r = reader[from[(size_t)s * max_blocks + b]];
+            r = r == kNobody ? ((int64_t)s << 32 | b) : kSeveral;
+        }
+    for (int32_t s = 0; s < num_seqs; ++s)
+        for (int64_t b = 0; b * block_size < kept[s]; ++b) {
+            const int32_t id = to[(size_t)s * new_max_blocks + b];
+            const int64_t me = (int64_t)s << 32 | b;
+            if (id == from[(size_t)s * max_blocks + b] && lens[s] <= keep) continue;  // in place, nothing dropped
+            if (writer[id] != kNobody)
+                return fail(PA_ERR_INDEX, "block " + std::to_string(id) + " is the destination of two blocks");
+            writer[id] = me;
+            if (reader[id] != kNobody && reader[id] != me)
+                return fail(PA_ERR_INDEX, "block " + std::to_string(id) +
+                                              " is written for one sequence and read for another logical block");
+        }
+    return PA_OK;
+}
+
 }  // namespace
 
 namespace pa {
@@ -114,6 +183,13 @@ namespace pa {
 void record_error(const std::string& msg) { g_last_error = msg; }
 
 bool check_mode_on() { return check_mode(); }
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
 
 int check_decode_indices(const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
                          int32_t num_seqs, int32_t num_blocks, int32_t block_size, int32_t max_context,
@@ -611,20 +687,8 @@ static pa_status varlen_impl(void* out, const void* q, const void* k_cache, cons
     const bool use_um = um_ok && (want == 2 || want == 0);
     cudaStream_t st = as_stream(stream);
     if (check_mode()) {
-        pa_status err = PA_OK;
-        std::vector<int32_t> lens, cu;
-        if (!to_host(lens, seq_lens, num_seqs, st, &err) || !to_host(cu, cu_seqlens_q, num_seqs + 1, st, &err))
-            return err;
-        if (cu[0] != 0 || cu[num_seqs] != total_q)
-            return fail(PA_ERR_INDEX, "cu_seqlens_q must start at 0 and end at total_q");
-        for (int32_t i = 0; i < num_seqs; ++i) {
-            const int32_t nn = cu[i + 1] - cu[i];
-            if (nn < 0) return fail(PA_ERR_INDEX, "cu_seqlens_q must be non-decreasing");
-            if (nn > max_q) return fail(PA_ERR_INDEX, "request " + std::to_string(i) + " has more than max_q queries");
-            if (nn > lens[i])
-                return fail(PA_ERR_INDEX, "request " + std::to_string(i) + " has more new tokens than context");
-        }
-        err = check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
+        pa_status err = check_varlen(block_tables, max_blocks, seq_lens, cu_seqlens_q, num_seqs, total_q, max_q,
+                                     num_blocks, block_size, max_context, st);
         if (err != PA_OK) return err;
     }
     pa::AttnArgs a{};
@@ -704,6 +768,401 @@ pa_status pa_varlen_fp8(void* out, const void* q, const void* k_codes, const voi
     return varlen_impl(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, max_blocks, seq_lens,
                        cu_seqlens_q, num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, num_blocks,
                        block_size, max_context, scale, causal, dtype, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ rotary write
+
+static pa_status rope_impl(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int64_t* positions, int32_t num_axes,
+                           const double* inv_freq, const int32_t* pair_axis, int32_t rot_dim, int interleaved,
+                           const int64_t* slot_mapping, int64_t n, void* k_cache, void* v_cache, float* k_scales,
+                           float* v_scales, bool fp8, int32_t num_blocks, int32_t block_size, int32_t num_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int dtype, void* stream) {
+    if (num_heads < 0) return fail(PA_ERR_INVALID_ARG, "num_heads must be non-negative");
+    pa_status g = check_geometry(num_heads ? num_heads : num_kv_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                                 dtype);
+    if (g != PA_OK) return g;
+    if (head_dim > 256) return fail(PA_ERR_UNSUPPORTED, "head_dim must be at most 256");
+    if (n < 0) return fail(PA_ERR_INVALID_ARG, "n must be non-negative");
+    if (n > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "n must fit in int32");
+    if (num_axes < 1) return fail(PA_ERR_INVALID_ARG, "num_axes must be positive");
+    if (rot_dim < 2 || rot_dim % 2 || rot_dim > head_dim)
+        return fail(PA_ERR_INVALID_ARG, "rot_dim must be even and in [2, head_dim]");
+    if (n == 0) return PA_OK;
+    if ((num_heads && (!q_out || !q)) || !k || !v || !positions || !inv_freq || !slot_mapping || !k_cache || !v_cache ||
+        (fp8 && (!k_scales || !v_scales)))
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    const int64_t krow = (int64_t)num_kv_heads * head_dim;
+    if ((num_heads && q_stride < (int64_t)num_heads * head_dim) || k_stride < krow || v_stride < krow)
+        return fail(PA_ERR_INVALID_ARG, "strides may not be smaller than a token's row");
+    if (num_heads && q_out == q && q_stride != (int64_t)num_heads * head_dim)
+        return fail(PA_ERR_INVALID_ARG, "q_out may be q only when q is contiguous");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
+    cudaStream_t st = as_stream(stream);
+    if (check_mode()) {
+        pa_status err = check_slots(slot_mapping, n, num_blocks, block_size, st);
+        if (err != PA_OK) return err;
+        std::vector<int32_t> ax;
+        if (pair_axis) {
+            if (!to_host(ax, pair_axis, rot_dim / 2, st, &err)) return err;
+            for (int i = 0; i < rot_dim / 2; ++i)
+                if (ax[i] < 0 || ax[i] >= num_axes)
+                    return fail(PA_ERR_INDEX, "pair " + std::to_string(i) + ": axis outside [0, num_axes)");
+        }
+    }
+    pa::RopeArgs a{};
+    a.q_out = num_heads ? q_out : nullptr;
+    a.q = num_heads ? q : nullptr;
+    a.k = k;
+    a.v = v;
+    a.q_stride = num_heads ? q_stride : 0;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.num_axes = num_axes;
+    a.inv_freq = inv_freq;
+    a.pair_axis = pair_axis;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.slots = slot_mapping;
+    a.n = n;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    cudaError_t e = pa::launch_rope_write(a, dtype, fp8, st);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_rope_write_kv launch");
+}
+
+// ------------------------------------------------------------------ attention weights
+
+// Sizes and pointers the weight entry points share; `a` gets everything but
+// the stats buffer.
+static pa_status weights_args(pa::WeightArgs& a, float* weights, int64_t weights_stride, const void* q,
+                              const void* k_cache, const float* k_scales, const int32_t* block_tables,
+                              int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu, int32_t num_seqs,
+                              int32_t total_q, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int32_t max_context, int32_t window, float scale, int causal,
+                              int dtype) {
+    if (weights_stride < max_context)
+        return fail(PA_ERR_INVALID_ARG, "weights_stride may not be smaller than max_context");
+    a.weights = weights;
+    a.weights_stride = weights_stride;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.k_scales = k_scales;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.cu = cu;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.block_size = block_size;
+    a.max_context = max_context;
+    a.window = window;
+    a.causal = causal ? 1 : 0;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.dtype = dtype;
+    a.kv_fp8 = k_scales != nullptr;
+    return PA_OK;
+}
+
+// Requests s0 .. s0 + count - 1 of a.
+static pa::WeightArgs weights_part(const pa::WeightArgs& a, int32_t s0, int32_t count) {
+    pa::WeightArgs c = a;
+    c.num_seqs = count;
+    c.weights = a.weights + (int64_t)s0 * a.num_kv_heads * a.weights_stride;
+    c.block_tables = a.block_tables + (int64_t)s0 * a.max_blocks;
+    c.seq_lens = a.seq_lens + s0;
+    if (a.cu) {
+        c.cu = a.cu + s0;
+    } else {  // one query per request
+        c.q = static_cast<const uint8_t*>(a.q) + (int64_t)s0 * a.num_heads * a.head_dim * pa::elt_size(a.dtype);
+        c.stats = a.stats + (int64_t)s0 * a.num_heads;
+        c.total_q = count;
+    }
+    return c;
+}
+
+static size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+static size_t decode_weights_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t max_context, int dtype, bool fp8) {
+    if (num_seqs <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads || max_context < 0)
+        return 0;
+    return align256(decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, fp8)) +
+           (size_t)num_seqs * num_heads * sizeof(float2);
+}
+
+static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_stride, const void* q,
+                                     const void* k_cache, const void* v_cache, const float* k_scales,
+                                     const float* v_scales, const int32_t* block_tables, int32_t max_blocks,
+                                     const int32_t* context_lens, int32_t num_seqs, int32_t num_heads,
+                                     int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+                                     int32_t max_context, float scale, int dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    pa_status g = check_geometry(num_heads, num_kv_heads, head_dim, num_blocks, block_size, dtype);
+    if (g != PA_OK) return g;
+    if (num_seqs < 0 || max_context < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs, max_blocks and max_context must be non-negative");
+    if (num_seqs == 0) return PA_OK;
+    if (!weights) return fail(PA_ERR_INVALID_ARG, "null pointer");
+    pa::WeightArgs a{};
+    g = weights_args(a, weights, weights_stride, q, k_cache, k_scales, block_tables, max_blocks, context_lens, nullptr,
+                     num_seqs, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, 0, scale, 1,
+                     dtype);
+    if (g != PA_OK) return g;
+    const size_t need = decode_weights_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                                                 dtype, k_scales != nullptr);
+    if (!workspace || workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
+                                          std::to_string(need) + " needed");
+    const size_t dec = align256(decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                                                 dtype, k_scales != nullptr));
+    g = decode_impl(out, q, nullptr, nullptr, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks,
+                    context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_context,
+                    scale, dtype, workspace, dec, stream);
+    if (g != PA_OK) return g;
+    a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + dec);
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
+        cudaError_t e = pa::launch_weights_simt(
+            weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch)), as_stream(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "pa_decode_weights launch");
+    }
+    return PA_OK;
+}
+
+static size_t prompt_weights_workspace(int32_t num_seqs, int32_t total_q, int32_t num_heads, int32_t num_kv_heads) {
+    if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return 0;
+    return (size_t)total_q * num_heads * sizeof(float2);
+}
+
+static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
+                                     const float* k_scales, const int32_t* block_tables, int32_t max_blocks,
+                                     const int32_t* seq_lens, const int32_t* cu_seqlens_q, int32_t num_seqs,
+                                     int32_t total_q, int32_t max_q, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t num_blocks, int32_t block_size, int32_t max_context,
+                                     int32_t window, float scale, int causal, int dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    pa_status g = check_geometry(num_heads, num_kv_heads, head_dim, num_blocks, block_size, dtype);
+    if (g != PA_OK) return g;
+    if (num_seqs < 0 || total_q < 0 || max_q < 0 || max_blocks < 0 || max_context < 0 || window < 0)
+        return fail(PA_ERR_INVALID_ARG, "sizes must be non-negative");
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (!weights || !q || !k_cache || !block_tables || !seq_lens || !cu_seqlens_q)
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q) || !aligned16(k_cache)) return fail(PA_ERR_INVALID_ARG, "q and the cache must be 16-byte aligned");
+    if (k_scales && !aligned16(k_scales)) return fail(PA_ERR_INVALID_ARG, "k_scales must be 16-byte aligned");
+    if (!pa::attn_simt_supported(dtype, head_dim)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be in [1, 256]");
+    pa::WeightArgs a{};
+    g = weights_args(a, weights, weights_stride, q, k_cache, k_scales, block_tables, max_blocks, seq_lens,
+                     cu_seqlens_q, num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                     window, scale, causal, dtype);
+    if (g != PA_OK) return g;
+    const size_t need = prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
+    if (!workspace || workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
+                                          std::to_string(need) + " needed");
+    if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    cudaStream_t st = as_stream(stream);
+    if (check_mode()) {
+        pa_status err = check_varlen(block_tables, max_blocks, seq_lens, cu_seqlens_q, num_seqs, total_q, max_q,
+                                     num_blocks, block_size, max_context, st);
+        if (err != PA_OK) return err;
+    }
+    a.stats = static_cast<float2*>(workspace);
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
+        cudaError_t e = pa::launch_weights_simt(
+            weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch)), st);
+        if (e != cudaSuccess) return cuda_fail(e, "pa_prompt_weights launch");
+    }
+    return PA_OK;
+}
+
+extern "C" {
+
+pa_status pa_rope_write_kv(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, const int64_t* positions, int32_t num_axes,
+                           const double* inv_freq, const int32_t* pair_axis, int32_t rot_dim, int interleaved,
+                           const int64_t* slot_mapping, int64_t n, void* k_cache, void* v_cache, int32_t num_blocks,
+                           int32_t block_size, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int dtype,
+                           void* stream) {
+    return rope_impl(q_out, q, k, v, q_stride, k_stride, v_stride, positions, num_axes, inv_freq, pair_axis, rot_dim,
+                     interleaved, slot_mapping, n, k_cache, v_cache, nullptr, nullptr, false, num_blocks, block_size,
+                     num_heads, num_kv_heads, head_dim, dtype, stream);
+}
+
+pa_status pa_rope_write_kv_fp8(void* q_out, const void* q, const void* k, const void* v, int64_t q_stride,
+                               int64_t k_stride, int64_t v_stride, const int64_t* positions, int32_t num_axes,
+                               const double* inv_freq, const int32_t* pair_axis, int32_t rot_dim, int interleaved,
+                               const int64_t* slot_mapping, int64_t n, void* k_codes, void* v_codes, float* k_scales,
+                               float* v_scales, int32_t num_blocks, int32_t block_size, int32_t num_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int dtype, void* stream) {
+    return rope_impl(q_out, q, k, v, q_stride, k_stride, v_stride, positions, num_axes, inv_freq, pair_axis, rot_dim,
+                     interleaved, slot_mapping, n, k_codes, v_codes, k_scales, v_scales, true, num_blocks, block_size,
+                     num_heads, num_kv_heads, head_dim, dtype, stream);
+}
+
+size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t max_context, int dtype) {
+    return decode_weights_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, false);
+}
+
+pa_status pa_decode_weights(void* out, float* weights, int64_t weights_stride, const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* block_tables, int32_t max_blocks,
+                            const int32_t* context_lens, int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t num_blocks, int32_t block_size, int32_t max_context,
+                            float scale, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return decode_weights_impl(out, weights, weights_stride, q, k_cache, v_cache, nullptr, nullptr, block_tables,
+                               max_blocks, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_context, scale, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t pa_decode_weights_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int32_t block_size, int32_t max_context, int dtype) {
+    return decode_weights_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, true);
+}
+
+pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weights_stride, const void* q, const void* k_codes,
+                                const void* v_codes, const float* k_scales, const float* v_scales,
+                                const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+                                int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_seqs > 0 && (!k_scales || !v_scales)) return fail(PA_ERR_INVALID_ARG, "null pointer");
+    return decode_weights_impl(out, weights, weights_stride, q, k_codes, v_codes, k_scales, v_scales, block_tables,
+                               max_blocks, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_context, scale, dtype, workspace, workspace_bytes, stream);
+}
+
+size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                        int32_t max_context, int32_t window, int dtype) {
+    (void)max_q, (void)head_dim, (void)block_size, (void)max_context, (void)window, (void)dtype;
+    return prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
+}
+
+pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
+                            const int32_t* block_tables, int32_t max_blocks, const int32_t* seq_lens,
+                            const int32_t* cu_seqlens_q, int32_t num_seqs, int32_t total_q, int32_t max_q,
+                            int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks,
+                            int32_t block_size, int32_t max_context, int32_t window, float scale, int causal,
+                            int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return prompt_weights_impl(weights, weights_stride, q, k_cache, nullptr, block_tables, max_blocks, seq_lens,
+                               cu_seqlens_q, num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_context, window, scale, causal, dtype, workspace, workspace_bytes,
+                               stream);
+}
+
+size_t pa_prompt_weights_fp8_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                            int32_t max_context, int32_t window, int dtype) {
+    (void)max_q, (void)head_dim, (void)block_size, (void)max_context, (void)window, (void)dtype;
+    return prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
+}
+
+pa_status pa_prompt_weights_fp8(float* weights, int64_t weights_stride, const void* q, const void* k_codes,
+                                const float* k_scales, const int32_t* block_tables, int32_t max_blocks,
+                                const int32_t* seq_lens, const int32_t* cu_seqlens_q, int32_t num_seqs,
+                                int32_t total_q, int32_t max_q, int32_t num_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t num_blocks, int32_t block_size, int32_t max_context,
+                                int32_t window, float scale, int causal, int dtype, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    if (num_seqs > 0 && total_q > 0 && !k_scales) return fail(PA_ERR_INVALID_ARG, "null pointer");
+    return prompt_weights_impl(weights, weights_stride, q, k_codes, k_scales, block_tables, max_blocks, seq_lens,
+                               cu_seqlens_q, num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, num_blocks,
+                               block_size, max_context, window, scale, causal, dtype, workspace, workspace_bytes,
+                               stream);
+}
+
+// ------------------------------------------------------------------ eviction
+
+size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep) {
+    if (num_seqs <= 0 || num_kv_heads <= 0 || max_context < 0 || keep <= 0) return 0;
+    return pa::evict_workspace(num_seqs, num_kv_heads, max_context, keep);
+}
+
+pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* new_lens, const float* weights,
+                   const int32_t* positions, const int32_t* recorded_lens, const int32_t* seen_lens,
+                   int64_t weights_stride, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                   const int32_t* block_tables, int32_t max_blocks, const int32_t* new_block_tables,
+                   int32_t new_max_blocks, const int32_t* context_lens, int32_t num_seqs, int32_t num_kv_heads,
+                   int32_t head_dim, int32_t num_blocks, int32_t block_size, int32_t max_context, int32_t keep,
+                   int32_t num_sink, int32_t num_recent, int dtype, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+    pa_status g = check_geometry(num_kv_heads, num_kv_heads, head_dim, num_blocks, block_size, dtype, true);
+    if (g != PA_OK) return g;
+    if (num_seqs < 0 || max_blocks < 0 || new_max_blocks < 0 || max_context < 0)
+        return fail(PA_ERR_INVALID_ARG, "sizes must be non-negative");
+    if (keep < 1 || num_sink < 0 || num_recent < 0 || (int64_t)num_sink + num_recent > keep)
+        return fail(PA_ERR_INVALID_ARG, "keep must be positive and hold num_sink + num_recent tokens");
+    if (weights_stride < max_context)
+        return fail(PA_ERR_INVALID_ARG, "weights_stride may not be smaller than max_context");
+    if (num_seqs == 0) return PA_OK;
+    if (!weights_out || !new_lens || !weights || !k_cache || !v_cache || !block_tables || !new_block_tables ||
+        !context_lens)
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if ((recorded_lens != nullptr) != (positions != nullptr))
+        return fail(PA_ERR_INVALID_ARG, "positions and recorded_lens go together");
+    const bool fp8 = dtype == PA_FP8_E4M3;
+    if (fp8 != (k_scales != nullptr) || fp8 != (v_scales != nullptr))
+        return fail(PA_ERR_INVALID_ARG, "k_scales and v_scales go with PA_FP8_E4M3 pools, and only with them");
+    if (new_lens == context_lens || new_lens == recorded_lens || new_lens == seen_lens)
+        return fail(PA_ERR_INVALID_ARG, "new_lens must be memory apart from the other arrays");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
+    if ((int64_t)num_seqs * num_kv_heads > (1 << 24))
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads must be at most 2^24");
+    const size_t need = pa::evict_workspace(num_seqs, num_kv_heads, max_context, keep);
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
+                                          std::to_string(need) + " needed");
+    if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    cudaStream_t st = as_stream(stream);
+    if (check_mode()) {
+        pa_status err = check_evict(recorded_lens, seen_lens, block_tables, max_blocks, new_block_tables, new_max_blocks,
+                                    context_lens, num_seqs, num_blocks, block_size, max_context, keep, st);
+        if (err != PA_OK) return err;
+    }
+    pa::EvictArgs a{};
+    a.weights_out = weights_out;
+    a.positions_out = positions_out;
+    a.new_lens = new_lens;
+    a.weights = weights;
+    a.positions = positions;
+    a.recorded_lens = recorded_lens;
+    a.seen_lens = seen_lens;
+    a.stride = weights_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.new_block_tables = new_block_tables;
+    a.new_max_blocks = new_max_blocks;
+    a.context_lens = context_lens;
+    a.num_seqs = num_seqs;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.max_context = max_context;
+    a.keep = keep;
+    a.num_sink = num_sink;
+    a.num_recent = num_recent;
+    a.row_bytes = (int64_t)head_dim * pa::elt_size(dtype);
+    a.map = static_cast<int32_t*>(workspace);
+    cudaError_t e = pa::launch_evict(a, st);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_evict launch");
 }
 
 }  // extern "C"

@@ -134,4 +134,96 @@ cudaError_t launch_varlen_umma(const AttnArgs& a, int32_t num_blocks, void* work
                                cudaStream_t stream);
 uint32_t varlen_umma_status(bool clear);
 
+// ---- rotary positions with the K/V write (pa_rope.cu)
+struct RopeArgs {
+    void* q_out;
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int64_t* positions;              // [num_axes, n]
+    int32_t num_axes;
+    const double* inv_freq;    // [rot_dim / 2]
+    const int32_t* pair_axis;  // [rot_dim / 2], or nullptr: axis 0
+    int32_t rot_dim;
+    int interleaved;
+    const int64_t* slots;
+    int64_t n;
+    void* k_cache;
+    void* v_cache;
+    float* k_scales;
+    float* v_scales;
+    int32_t num_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t block_size;
+    int32_t tpb = 1;  // tokens per CTA (set by the launcher)
+};
+cudaError_t launch_rope_write(const RopeArgs& a, int dtype, bool fp8, cudaStream_t stream);
+
+// ---- attention weights of cached tokens (pa_weights_simt.cu)
+struct WeightArgs {
+    float* weights;  // [num_seqs, num_kv_heads, weights_stride]
+    int64_t weights_stride;
+    const void* q;
+    const void* k_cache;
+    const float* k_scales;
+    const int32_t* block_tables;
+    int32_t max_blocks;
+    const int32_t* seq_lens;
+    const int32_t* cu;  // nullptr: one query per request (row s = request s)
+    int32_t num_seqs;
+    int32_t total_q;
+    int32_t num_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t block_size;
+    int32_t max_context;
+    int32_t window;  // 0: every new token
+    int causal;
+    float scale_log2;
+    int dtype;
+    int kv_fp8;
+    float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
+};
+// Requests one launch handles (their tile counts' prefix lives in shared memory).
+constexpr int kWeightMaxSeqsPerLaunch = 4096;
+cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
+
+// ---- eviction by accumulated weight (pa_evict.cu)
+struct EvictArgs {
+    float* weights_out;
+    int32_t* positions_out;  // may be nullptr
+    int32_t* new_lens;
+    const float* weights;
+    const int32_t* positions;      // read below recorded_lens only
+    const int32_t* recorded_lens;  // nullptr: none recorded
+    const int32_t* seen_lens;      // nullptr: context_lens
+    int64_t stride;
+    void* k_cache;
+    void* v_cache;
+    float* k_scales;  // code pools only
+    float* v_scales;
+    const int32_t* block_tables;
+    int32_t max_blocks;
+    const int32_t* new_block_tables;
+    int32_t new_max_blocks;
+    const int32_t* context_lens;
+    int32_t num_seqs;
+    int32_t num_kv_heads;
+    int32_t block_size;
+    int32_t max_context;
+    int32_t keep;
+    int32_t num_sink;
+    int32_t num_recent;
+    int64_t row_bytes;  // of one head's K (or V) row
+    int32_t* map;       // workspace
+    int64_t map_stride = 0;
+};
+size_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
+// SMs of the current device.
+int sm_count();
+
 }  // namespace pa

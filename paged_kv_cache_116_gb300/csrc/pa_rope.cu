@@ -1,0 +1,284 @@
+// pa_rope.cu -- rotary positions on one or more axes, applied to q and k in
+// the kernel that writes K and V to their slots.
+//
+// For token t and rotary pair i (rot_dim / 2 of them per head),
+//   angle = positions[axis(i), t] * inv_freq[i],
+//   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
+// where the pair is elements (i, i + rot_dim / 2) of the head, or (2i, 2i+1)
+// when interleaved; elements from rot_dim on are passed through.  The rotated
+// q goes to q_out, the rotated k and the unchanged v to row slot_mapping[t]
+// of the pool, exactly where the plain write puts a row ("分页 KV Cache",
+// PagedKVCache.write) -- or, into a quantized cache, as E4M3 codes with one
+// scale per (token, KV head) row, quantized as the quantizing write does it
+// from the fp32 rotated values (one rounding, not two).
+//
+// Angles.  A product of a far position and a frequency has no correct
+// fraction of a turn in fp32 (at position 2^20 the spacing of fp32 is 1/8
+// radian).  Here inv_freq[i] / (2 pi) becomes a 64-bit fraction of a turn F
+// by one integer product of its significand with 2^64 / (2 pi); the
+// position's turn is the low 64 bits of position * F (whole turns drop out of
+// the wrap-around, negative positions included), exact to 2^-64 turns per
+// position step, and sincospif takes its upper 32 bits.  No fp64 instruction
+// is spent on it.
+//
+// Bound: HBM.  q, k and v are read once and q_out and the rows written once.
+// A block takes `tpb` tokens: their sines and cosines go to shared memory
+// once and serve all heads; then every thread works 16-byte vectors, a
+// rotated item being the two vectors that hold both halves of 8 (16-bit) or
+// 4 (fp32) pairs, several items in flight per thread, the first ones fetched
+// while the angles are computed.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_launch.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+// inv_freq / (2 pi) as a fraction of a turn in 64 bits (two's complement).
+// freq = m 2^e with a 53-bit integer m: F = m * (2^64 / (2 pi)) * 2^e, whole
+// turns dropped; the truncations are below one unit of 2^-64 turns times
+// max(1, freq).
+__device__ __forceinline__ uint64_t turn_fraction(double freq) {
+    const uint64_t b = (uint64_t)__double_as_longlong(freq);
+    const int ex = (int)((b >> 52) & 0x7ff);
+    uint64_t m = b & 0xfffffffffffffull;
+    if (ex) m |= 1ull << 52;
+    const uint64_t c = 0x28be60db9391054aull;  // floor(2^64 / (2 pi))
+    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    const int sh = 1075 - (ex ? ex : 1);  // -e
+    uint64_t f = 0;
+    if (sh <= 0) f = -sh < 64 ? lo << -sh : 0;
+    else if (sh < 64) f = (hi << (64 - sh)) | (lo >> sh);
+    else if (sh < 128) f = hi >> (sh - 64);
+    return (b >> 63) ? 0 - f : f;
+}
+
+template <typename T, int VEC> struct alignas(VEC == 1 ? sizeof(T) : 16) RVec { T e[VEC]; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ RVec<T, VEC> load_vec(const T* p) {
+    RVec<T, VEC> v;
+    if constexpr (VEC == 1) {
+        v.e[0] = *p;
+    } else {
+        uint4 r;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        memcpy(&v, &r, 16);
+    }
+    return v;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const RVec<T, VEC>& v) {
+    *reinterpret_cast<RVec<T, VEC>*>(p) = v;
+}
+
+// VEC: elements per vector (16 bytes, or 1 where sizes or alignment do not
+// allow it).  FP8: k and v rows are quantized into code pools.
+template <typename T, int VEC, bool FP8>
+__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs p) {
+    constexpr int U = 4;  // items in flight per thread
+    extern __shared__ float2 tab[];  // [tpb][rot / 2] cosine, sine
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int64_t t0 = (int64_t)blockIdx.x * p.tpb;
+    const int nt = (int)min((int64_t)p.tpb, p.n - t0);
+    const int half = p.rot_dim / 2, hd = p.head_dim, Hq = p.num_heads, Hkv = p.num_kv_heads;
+    const int R = half / VEC;                    // rotated items per head
+    const int per = R + (hd - p.rot_dim) / VEC;  // and the vectors passed through
+    const int n_rot = (Hq + (FP8 ? 0 : Hkv)) * per;
+    const int items = n_rot + (FP8 ? 0 : Hkv * (hd / VEC));
+    const int total = nt * items;
+    const T* q = static_cast<const T*>(p.q);
+    const T* k = static_cast<const T*>(p.k);
+    const T* v = static_cast<const T*>(p.v);
+
+    bool ready = false;
+    auto angles = [&]() {
+        for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+            const int t = i / half, pr = i - t * half;
+            const int ax = p.pair_axis ? min(max(p.pair_axis[pr], 0), p.num_axes - 1) : 0;
+            const double fr = p.inv_freq[pr];
+            const uint64_t turns = (uint64_t)p.positions[(int64_t)ax * p.n + t0 + t] * turn_fraction(fr);
+            // the nearest 32-bit fraction, as half turns in [-1, 1)
+            const float x = (float)(int32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
+            float s, c;
+            sincospif(x, &s, &c);
+            if (!isfinite(fr)) s = c = __int_as_float(0x7fc00000);
+            tab[i] = make_float2(c, s);
+        }
+        __syncthreads();
+        ready = true;
+    };
+
+    for (int base = 0; base < total; base += kRopeThreads * U) {
+        RVec<T, VEC> a[U], b[U];
+        T* dst[U];
+        int o0[U], o1[U], pr0[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int it = base + u * kRopeThreads + threadIdx.x;
+            dst[u] = nullptr;
+            if (it >= total) continue;
+            const int t = it / items;
+            int r = it - t * items;
+            const int64_t tok = t0 + t;
+            const T* src;
+            int e = -1;  // rotated item within the head, or -1
+            if (r < n_rot) {
+                const int head = r / per;
+                r -= head * per;
+                if (head < Hq) {
+                    src = q + tok * p.q_stride + (int64_t)head * hd;
+                    dst[u] = static_cast<T*>(p.q_out) + (tok * Hq + head) * hd;
+                } else {
+                    const int64_t slot = p.slots[tok];
+                    if (slot < 0) continue;
+                    src = k + tok * p.k_stride + (int64_t)(head - Hq) * hd;
+                    dst[u] = static_cast<T*>(p.k_cache) + (slot * Hkv + head - Hq) * hd;
+                }
+                if (r < R) e = r;
+                o0[u] = p.rot_dim + (r - R) * VEC;
+            } else {
+                const int64_t slot = p.slots[tok];
+                if (slot < 0) continue;
+                r = (r - n_rot) * VEC;  // element of the token's v row
+                src = v + tok * p.v_stride;
+                dst[u] = static_cast<T*>(p.v_cache) + slot * Hkv * hd;
+                o0[u] = r;
+            }
+            o1[u] = -1;
+            if (e >= 0) {
+                o0[u] = p.interleaved ? 2 * e * VEC : e * VEC;
+                o1[u] = p.interleaved ? o0[u] + VEC : o0[u] + half;
+                pr0[u] = t * half + e * VEC;
+                b[u] = load_vec<T, VEC>(src + o1[u]);
+            }
+            a[u] = load_vec<T, VEC>(src + o0[u]);
+        }
+        if (!ready) angles();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (dst[u] == nullptr) continue;
+            if (o1[u] >= 0) {
+                const float2* cs = tab + pr0[u];
+                if (VEC > 1 && p.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < VEC / 2; ++e) {
+                        const float2 c0 = cs[e], c1 = cs[VEC / 2 + e];
+                        const float x0 = Elt<T>::to_f(a[u].e[2 * e]), y0 = Elt<T>::to_f(a[u].e[2 * e + 1]);
+                        const float x1 = Elt<T>::to_f(b[u].e[2 * e]), y1 = Elt<T>::to_f(b[u].e[2 * e + 1]);
+                        a[u].e[2 * e] = Elt<T>::from_f(x0 * c0.x - y0 * c0.y);
+                        a[u].e[2 * e + 1] = Elt<T>::from_f(y0 * c0.x + x0 * c0.y);
+                        b[u].e[2 * e] = Elt<T>::from_f(x1 * c1.x - y1 * c1.y);
+                        b[u].e[2 * e + 1] = Elt<T>::from_f(y1 * c1.x + x1 * c1.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float2 c = cs[e];
+                        const float x = Elt<T>::to_f(a[u].e[e]), y = Elt<T>::to_f(b[u].e[e]);
+                        a[u].e[e] = Elt<T>::from_f(x * c.x - y * c.y);
+                        b[u].e[e] = Elt<T>::from_f(y * c.x + x * c.y);
+                    }
+                }
+                store_vec<T, VEC>(dst[u] + o1[u], b[u]);
+            }
+            store_vec<T, VEC>(dst[u] + o0[u], a[u]);
+        }
+    }
+
+    if constexpr (FP8) {
+        if (!ready) angles();
+        // one warp per (token, KV head, K|V) row: lane l holds pairs l, l+32,
+        // ... of the rotated part and elements rot + l, ... of the rest
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int row = warp; row < nt * Hkv * 2; row += kRopeThreads / 32) {
+            const int is_v = row & 1, h = (row >> 1) % Hkv, t = (row >> 1) / Hkv;
+            const int64_t tok = t0 + t, slot = p.slots[tok];
+            if (slot < 0) continue;
+            const T* src = is_v ? v + tok * p.v_stride + (int64_t)h * hd : k + tok * p.k_stride + (int64_t)h * hd;
+            const int rot = is_v ? 0 : p.rot_dim, hf = rot / 2;
+            float x[4], y[4], z[8], amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pr = lane + 32 * i;
+                if (pr >= hf) break;
+                const float2 c = tab[t * half + pr];
+                const float x0 = Elt<T>::to_f(src[p.interleaved ? 2 * pr : pr]);
+                const float y0 = Elt<T>::to_f(src[p.interleaved ? 2 * pr + 1 : pr + hf]);
+                x[i] = x0 * c.x - y0 * c.y;
+                y[i] = y0 * c.x + x0 * c.y;
+                amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = rot + lane + 32 * i;
+                if (e >= hd) break;
+                z[i] = Elt<T>::to_f(src[e]);
+                amax = fmaxf(amax, fabsf(z[i]));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+            uint8_t* d = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + (slot * Hkv + h) * hd;
+            auto code = [&](float f) {
+                return (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(f, sc), __NV_SATFINITE, __NV_E4M3);
+            };
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pr = lane + 32 * i;
+                if (pr >= hf) break;
+                d[p.interleaved ? 2 * pr : pr] = code(x[i]);
+                d[p.interleaved ? 2 * pr + 1 : pr + hf] = code(y[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = rot + lane + 32 * i;
+                if (e >= hd) break;
+                d[e] = code(z[i]);
+            }
+            if (lane == 0) {
+                const int64_t blk = slot / p.block_size, off = slot - blk * p.block_size;
+                (is_v ? p.v_scales : p.k_scales)[(blk * Hkv + h) * p.block_size + off] = sc;
+            }
+        }
+    }
+}
+
+template <typename T, bool FP8>
+cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool al = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
+                      reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.q_out)) & 15) == 0;
+    const bool vec = al && a.head_dim % V == 0 && a.rot_dim % (2 * V) == 0 && a.q_stride % V == 0 &&
+                     a.k_stride % V == 0 && a.v_stride % V == 0;
+    RopeArgs p = a;
+    p.tpb = a.n >= 4 * 1216 ? 4 : (a.n >= 2 * 1216 ? 2 : 1);
+    const dim3 grid((unsigned)((a.n + p.tpb - 1) / p.tpb));
+    const size_t smem = (size_t)p.tpb * (a.rot_dim / 2) * sizeof(float2);
+    return vec ? launch_pdl_smem(rope_write_kernel<T, V, FP8>, grid, dim3(kRopeThreads), smem, stream, p)
+               : launch_pdl_smem(rope_write_kernel<T, 1, FP8>, grid, dim3(kRopeThreads), smem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_write(const RopeArgs& a, int dtype, bool fp8, cudaStream_t stream) {
+    switch (dtype) {
+        case 0: return fp8 ? launch_rope_typed<float, true>(a, stream) : launch_rope_typed<float, false>(a, stream);
+        case 1: return fp8 ? launch_rope_typed<__nv_bfloat16, true>(a, stream)
+                           : launch_rope_typed<__nv_bfloat16, false>(a, stream);
+        default: return fp8 ? launch_rope_typed<__half, true>(a, stream)
+                            : launch_rope_typed<__half, false>(a, stream);
+    }
+}
+
+}  // namespace pa

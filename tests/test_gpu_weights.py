@@ -1,0 +1,260 @@
+"""pa_decode_weights and pa_prompt_weights (16-bit, fp32 and quantized caches)
+against 64-bit softmax weights; tolerances from cache_ops.weight_rtol."""
+import numpy as np
+import pytest
+import torch
+
+from cache_ops import Batch, DTYPES, decode_exact, prompt_exact
+from helpers import within_tol
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def pa():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import paged_kv_cache_116_gb300 as pa
+
+    return pa
+
+
+def _start_weights(S, hkv, stride, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.rand((S, hkv, stride), generator=g) * 0.1
+
+
+def _check_weights(got, want, before, b, rtol):
+    """Entries inside each sequence within rtol (of the added part and the stored sum), the others untouched."""
+    for s, L in enumerate(b.lens):
+        assert torch.equal(got[s, :, L:], before[s, :, L:]), s
+        x, y = got[s, :, :L].double(), want[s, :, :L]
+        bad = (x - y).abs() > (rtol + 2.0 ** -23) * y.abs()
+        assert not bool(bad.any()), (s, float(((x - y).abs() / y.abs()).max()), rtol)
+
+
+def _decode(pa, b, dq, w, scale, ws=None, max_context=None):
+    S, hq, hd = dq.shape
+    mc = b.max_context if max_context is None else max_context
+    size = pa.pa_decode_weights_fp8_workspace_size if b.fp8 else pa.pa_decode_weights_workspace_size
+    if ws is None:
+        ws = torch.full((max(16, size(S, hq, b.hkv, hd, b.bs, mc, dq.dtype)),), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full_like(dq, float("nan"))
+    if b.fp8:
+        pa.pa_decode_weights_fp8(out, w, dq, b.dk, b.dv, *b.dscales, b.dtables, b.dlens, mc, scale, workspace=ws)
+    else:
+        pa.pa_decode_weights(out, w, dq, b.dk, b.dv, b.dtables, b.dlens, mc, scale, workspace=ws)
+    return out
+
+
+DECODE = [
+    # lens, hq, hkv, hd, bs, dtype, fp8
+    ([6, 13, 1, 20], 4, 2, 32, 4, "f32", False),
+    ([1, 17, 300, 0, 64, 1000], 32, 8, 128, 16, "bf16", False),
+    ([5, 1, 2, 16, 33], 12, 2, 128, 16, "f16", False),
+    ([700, 31], 40, 40, 64, 16, "f16", False),
+    ([129, 64, 2000], 16, 1, 128, 8, "bf16", False),
+    ([257, 90], 6, 2, 256, 64, "bf16", False),
+    ([77, 200], 8, 2, 128, 12, "bf16", False),      # a block size that is gathered row by row
+    ([40, 0, 3], 34, 2, 128, 16, "bf16", False),    # more query heads than the tensor-core kernel takes
+    ([50, 120], 4, 4, 100, 16, "f16", False),       # a head_dim it does not take
+    ([5000], 32, 8, 128, 16, "bf16", False),        # one long sequence, split
+    ([3500, 12, 1, 800], 32, 8, 128, 16, "bf16", True),
+    ([100, 37], 12, 2, 256, 16, "f16", True),
+    ([60, 19], 8, 8, 128, 8, "f16", True),
+    ([21, 48], 4, 2, 64, 16, "f32", True),
+]
+
+
+@pytest.mark.parametrize("case", DECODE)
+def test_decode_weights(pa, case):
+    lens, hq, hkv, hd, bs, dtype, fp8 = case
+    b = Batch(lens, hkv, hd, bs, dtype, 7, fp8).to(DEV)
+    q = torch.randn((len(lens), hq, hd), generator=torch.Generator().manual_seed(2)).to(DTYPES[dtype])
+    stride = b.max_context + 5
+    before = _start_weights(len(lens), hkv, stride, 4)
+    w = before.to(DEV)
+    scale = hd ** -0.5
+    out = _decode(pa, b, q.to(DEV), w, scale)
+    eo, ew, rtol = decode_exact(b, q, scale, before)
+    ok, err = within_tol(out.double().cpu().numpy(), eo.numpy(), dtype)
+    assert ok, err
+    _check_weights(w.cpu(), ew, before, b, rtol)
+
+
+def test_decode_weights_accumulate_and_repeat(pa):
+    """Three steps add up; two runs from the same start give the same bits; a larger max_context changes nothing
+    beyond the tolerance."""
+    b = Batch([900, 33, 256], 8, 128, 16, "bf16", 5).to(DEV)
+    q = torch.randn((3, 3, 32, 128), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    before = _start_weights(3, 8, 1000, 4)
+    runs = []
+    for mc in (None, None, 1000):
+        w = before.to(DEV)
+        for i in range(3):
+            _decode(pa, b, q[i].to(DEV), w, 0.088, max_context=mc)
+        runs.append(w.cpu())
+    want, rtol = before, 0.0
+    for i in range(3):
+        _, want, r = decode_exact(b, q[i], 0.088, want)
+        rtol = max(rtol, r)
+    for got in runs:
+        _check_weights(got, want, before, b, rtol + 3 * 2.0 ** -24)
+    assert torch.equal(runs[0], runs[1])
+
+
+def test_decode_weights_shared_blocks(pa):
+    """Two sequences over the same blocks keep separate weights."""
+    b = Batch([200, 200], 2, 128, 16, "bf16", 6)
+    b.tables[1] = b.tables[0]
+    b.to(DEV)
+    q = torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    before = _start_weights(2, 2, 200, 4)
+    w = before.to(DEV)
+    _decode(pa, b, q.to(DEV), w, 0.1)
+    _, want, rtol = decode_exact(b, q, 0.1, before)
+    _check_weights(w.cpu(), want, before, b, rtol)
+
+
+def test_decode_weights_large_scores(pa):
+    """Scores of several hundred: the weights stay within the tolerance their magnitude gives."""
+    b = Batch([300, 64], 2, 128, 16, "bf16", 6, spread=6.0).to(DEV)
+    q = (torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(2)) * 6).to(torch.bfloat16)
+    before = torch.zeros((2, 2, 300))
+    w = before.to(DEV)
+    _decode(pa, b, q.to(DEV), w, 0.2)
+    _, want, rtol = decode_exact(b, q, 0.2, before)
+    got = w.cpu()
+    for s, L in enumerate(b.lens):
+        err = (got[s, :, :L].double() - want[s, :, :L]).abs()
+        assert bool((err <= rtol * want[s, :, :L] + 1e-30).all())
+
+
+def test_decode_weights_nan_stays_in_its_sequence(pa):
+    b = Batch([100, 80], 2, 128, 16, "bf16", 6)
+    b.k[b.tables[0, 1].long(), 3, 0] = float("nan")  # a key of sequence 0, head 0
+    b.to(DEV)
+    q = torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    w = torch.zeros((2, 2, 100), device=DEV)
+    out = _decode(pa, b, q.to(DEV), w, 0.1).cpu()
+    got = w.cpu()
+    assert bool(got[0, 0].isnan().all()) and bool(out[0, :4].isnan().all())
+    assert bool(got[0, 1].isfinite().all()) and bool(got[1].isfinite().all()) and bool(out[1].isfinite().all())
+
+
+def test_decode_weights_graph_and_stream(pa):
+    b = Batch([1500, 1, 333, 64], 8, 128, 16, "bf16", 8).to(DEV)
+    gen = torch.Generator().manual_seed(1)
+    dq = torch.randn((4, 32, 128), generator=gen).to(torch.bfloat16).to(DEV)
+    n = pa.pa_decode_weights_workspace_size(4, 32, 8, 128, 16, 1500, torch.bfloat16)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    w = torch.zeros((4, 8, 1500), device=DEV)
+    out = torch.empty_like(dq)
+
+    def step(out, w, ws):
+        pa.pa_decode_weights(out, w, dq, b.dk, b.dv, b.dtables, b.dlens, 1500, 0.088, workspace=ws)
+
+    step(out, w, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="thread_local"):
+        step(out, w, ws)
+    ref_w, ref = torch.zeros_like(w), torch.empty_like(out)
+    w.zero_()
+    st = torch.cuda.Stream()
+    ws2 = torch.empty_like(ws)
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        dq.copy_(torch.randn(dq.shape, generator=gen).to(torch.bfloat16))
+        g.replay()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            step(ref, ref_w, ws2)
+        torch.cuda.current_stream().wait_stream(st)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(w, ref_w)
+
+
+def _prompt(pa, b, dq, cu, window, scale, w, causal=True):
+    T, hq, hd = dq.shape
+    S = len(b.lens)
+    mq = max(cu[i + 1] - cu[i] for i in range(S))
+    size = pa.pa_prompt_weights_fp8_workspace_size if b.fp8 else pa.pa_prompt_weights_workspace_size
+    n = size(S, T, mq, hq, b.hkv, hd, b.bs, b.max_context, window, dq.dtype)
+    ws = torch.full((max(16, n),), 0xFF, dtype=torch.uint8, device=DEV)
+    dcu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    if b.fp8:
+        pa.pa_prompt_weights_fp8(w, dq, b.dk, b.dscales[0], b.dtables, b.dlens, dcu, mq, b.max_context, window, scale,
+                                 causal=causal, workspace=ws)
+    else:
+        pa.pa_prompt_weights(w, dq, b.dk, b.dtables, b.dlens, dcu, mq, b.max_context, window, scale, causal=causal,
+                             workspace=ws)
+
+
+PROMPT = [
+    # new, lens, hq, hkv, hd, bs, dtype, window, causal, fp8
+    ([5, 3, 1], [6, 13, 1], 4, 2, 32, 4, "f32", 0, True, False),
+    ([300, 64, 1, 0, 17], [300, 200, 40, 25, 17], 12, 2, 128, 16, "bf16", 0, True, False),
+    ([300, 64, 1, 0, 17], [300, 200, 40, 25, 17], 12, 2, 128, 16, "bf16", 32, True, False),
+    ([129, 700], [129, 1500], 8, 2, 64, 16, "f16", 0, True, False),
+    ([40, 33], [2000, 129], 32, 8, 128, 32, "bf16", 16, True, False),
+    ([200, 90], [260, 128], 4, 4, 128, 8, "f16", 0, False, False),
+    ([64, 10], [200, 500], 40, 2, 128, 16, "bf16", 8, True, False),
+    ([3], [5000], 16, 1, 128, 16, "bf16", 0, True, False),
+    ([90, 31], [150, 260], 6, 2, 256, 16, "bf16", 0, True, False),
+    ([50, 60], [77, 80], 4, 2, 128, 12, "f16", 0, True, False),
+    ([130, 20], [300, 600], 8, 2, 128, 16, "bf16", 0, True, True),
+    ([64, 20], [64, 900], 12, 2, 128, 16, "f16", 24, True, True),
+    ([20, 9], [50, 9], 4, 2, 64, 16, "f32", 0, True, True),
+]
+
+
+@pytest.mark.parametrize("case", PROMPT)
+def test_prompt_weights(pa, case):
+    new, lens, hq, hkv, hd, bs, dtype, window, causal, fp8 = case
+    b = Batch(lens, hkv, hd, bs, dtype, 17, fp8).to(DEV)
+    cu = [0] + list(np.cumsum(new))
+    q = torch.randn((cu[-1], hq, hd), generator=torch.Generator().manual_seed(12)).to(DTYPES[dtype])
+    before = _start_weights(len(lens), hkv, b.max_context + 3, 4)
+    w = before.to(DEV)
+    scale = hd ** -0.5
+    _prompt(pa, b, q.to(DEV), cu, window, scale, w, causal)
+    want, rtol = prompt_exact(b, q, cu, window, scale, causal, before)
+    got = w.cpu()
+    _check_weights(got, want, before, b, rtol)
+    again = before.to(DEV)
+    _prompt(pa, b, q.to(DEV), cu, window, scale, again, causal)
+    assert torch.equal(again.cpu(), got)
+
+
+def test_prompt_weights_of_single_tokens_match_decode(pa):
+    """One new token per request: the prompt form and the decode form add the same weights."""
+    b = Batch([300, 5, 64, 1], 2, 128, 16, "bf16", 21).to(DEV)
+    q = torch.randn((4, 8, 128), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    before = _start_weights(4, 2, 300, 9)
+    w1, w2 = before.to(DEV), before.to(DEV)
+    _decode(pa, b, q.to(DEV), w1, 0.09)
+    _prompt(pa, b, q.to(DEV), [0, 1, 2, 3, 4], 0, 0.09, w2)
+    _, want, rtol = decode_exact(b, q, 0.09, before)
+    _check_weights(w1.cpu(), want, before, b, rtol)
+    _check_weights(w2.cpu(), want, before, b, rtol)
+
+
+def test_prompt_weights_many_requests(pa):
+    """More requests than one launch lists (their prefix lives in shared memory)."""
+    S = 4100
+    b = Batch([2] * S, 1, 64, 16, "bf16", 3).to(DEV)
+    q = torch.randn((S, 2, 64), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    before = torch.zeros((S, 1, 2))
+    for form in ("prompt", "decode"):
+        w = before.to(DEV)
+        if form == "prompt":
+            _prompt(pa, b, q.to(DEV), list(range(S + 1)), 0, 0.125, w)
+        else:
+            _decode(pa, b, q.to(DEV), w, 0.125)
+        k = torch.stack([b.k[b.tables[s, 0].long(), :2, 0] for s in range(S)]).double()
+        want = torch.softmax(torch.einsum("sgd,std->sgt", q.double(), k) * 0.125, -1).sum(1)
+        assert bool(((w.cpu()[:, 0].double() - want).abs() <= 1e-4 * want).all()), form
