@@ -239,7 +239,8 @@ pa_status pa_device_status(int clear) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "pa_device_status");
     const uint32_t bits =
-        pa::decode_tc_status(clear != 0) | pa::varlen_umma_status(clear != 0) | pa::selftest_status(clear != 0);
+        pa::decode_tc_status(clear != 0) | pa::decode_weights_status(clear != 0) |
+                          pa::varlen_umma_status(clear != 0) | pa::selftest_status(clear != 0);
     if (bits & 1u) return fail(PA_ERR_TIMEOUT, "a kernel's bounded barrier wait ran out");
     return PA_OK;
 }
@@ -466,13 +467,14 @@ size_t pa_decode_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t
 
 }  // extern "C"
 
-// k_scales != nullptr: the caches hold E4M3 codes with these scales.
-static pa_status decode_impl(void* out, const void* q, const void* k_new, const void* v_new, const void* k_cache,
-                             const void* v_cache, const float* k_scales, const float* v_scales,
+// The decode's argument checks and kernel arguments.  k_scales != nullptr: the
+// caches hold E4M3 codes with these scales.
+static pa_status decode_args(pa::AttnArgs& a, void* out, const void* q, const void* k_new, const void* v_new,
+                             const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
                              const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
                              int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
                              int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int dtype,
-                             void* workspace, size_t workspace_bytes, void* stream) {
+                             cudaStream_t st) {
     const bool fp8 = k_scales != nullptr;
     pa_status g = check_geometry(num_heads, num_kv_heads, head_dim, num_blocks, block_size, dtype);
     if (g != PA_OK) return g;
@@ -492,7 +494,6 @@ static pa_status decode_impl(void* out, const void* q, const void* k_new, const 
     if (!pa::attn_simt_supported(dtype, head_dim)) return fail(PA_ERR_UNSUPPORTED, "head_dim must be in [1, 256]");
     if (fp8 && (!v_scales || !aligned16(k_scales) || !aligned16(v_scales)))
         return fail(PA_ERR_INVALID_ARG, "k_scales and v_scales must be non-null and 16-byte aligned");
-    cudaStream_t st = as_stream(stream);
     if (check_mode()) {
         pa_status err = PA_OK;
         std::vector<int32_t> lens;
@@ -500,7 +501,6 @@ static pa_status decode_impl(void* out, const void* q, const void* k_new, const 
         err = check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
         if (err != PA_OK) return err;
     }
-    pa::AttnArgs a{};
     a.out = out;
     a.q = q;
     a.k_cache = k_cache;
@@ -518,10 +518,40 @@ static pa_status decode_impl(void* out, const void* q, const void* k_new, const 
     a.scale = scale;
     a.causal = 1;
     a.dtype = dtype;
+    a.max_context = max_context;
     a.kv_fp8 = fp8 ? 1 : 0;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
+    return PA_OK;
+}
 
+// Sequences s0 .. s0 + count - 1 of a.
+static pa::AttnArgs decode_part(const pa::AttnArgs& a, int32_t s0, int32_t count) {
+    const int64_t row = (int64_t)a.num_heads * a.head_dim * pa::elt_size(a.dtype);
+    pa::AttnArgs c = a;
+    c.num_seqs = count;
+    c.total_q = count;
+    c.out = static_cast<uint8_t*>(a.out) + s0 * row;
+    c.q = static_cast<const uint8_t*>(a.q) + s0 * row;
+    c.block_tables = a.block_tables + (int64_t)s0 * a.max_blocks;
+    c.seq_lens = a.seq_lens + s0;
+    return c;
+}
+
+static pa_status decode_impl(void* out, const void* q, const void* k_new, const void* v_new, const void* k_cache,
+                             const void* v_cache, const float* k_scales, const float* v_scales,
+                             const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+                             int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int dtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    const bool fp8 = k_scales != nullptr;
+    const bool append = k_new != nullptr || v_new != nullptr;
+    cudaStream_t st = as_stream(stream);
+    pa::AttnArgs a{};
+    pa_status g = decode_args(a, out, q, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks,
+                              context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, block_size,
+                              max_context, scale, dtype, st);
+    if (g != PA_OK || num_seqs == 0) return g;
     const int G = num_heads / num_kv_heads;
     const int64_t row_bytes = (int64_t)num_kv_heads * head_dim * pa::elt_size(dtype);
     pa_status sel;
@@ -573,16 +603,8 @@ static pa_status decode_impl(void* out, const void* q, const void* k_new, const 
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                           std::to_string(need) + " needed");
     if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-    const int64_t elt = pa::elt_size(dtype);
     for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kDecodeMaxSeqsPerLaunch) {
-        pa::AttnArgs c = a;
-        const int32_t cnt = std::min(num_seqs - s0, pa::kDecodeMaxSeqsPerLaunch);
-        c.num_seqs = cnt;
-        c.total_q = cnt;
-        c.out = static_cast<uint8_t*>(out) + (int64_t)s0 * num_heads * head_dim * elt;
-        c.q = static_cast<const uint8_t*>(q) + (int64_t)s0 * num_heads * head_dim * elt;
-        c.block_tables = block_tables + (int64_t)s0 * max_blocks;
-        c.seq_lens = context_lens + s0;
+        pa::AttnArgs c = decode_part(a, s0, std::min(num_seqs - s0, pa::kDecodeMaxSeqsPerLaunch));
         if (fused_append) {
             c.k_new = static_cast<const uint8_t*>(k_new) + (int64_t)s0 * row_bytes;
             c.v_new = static_cast<const uint8_t*>(v_new) + (int64_t)s0 * row_bytes;
@@ -896,12 +918,38 @@ static pa::WeightArgs weights_part(const pa::WeightArgs& a, int32_t s0, int32_t 
 
 static size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Workspace of the weighted decode.  Tensor-core path: the split records,
+// the row statistics of units worked whole, the scores; CUDA-core path: the
+// row statistics.
+struct DecodeWeightsSpace {
+    bool tc = false;
+    int grid = 0;
+    size_t records = 0, stats = 0, scores = 0;
+    size_t total() const { return records + stats + scores; }
+};
+static DecodeWeightsSpace decode_weights_space(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size, int32_t max_context, int dtype,
+                                               bool fp8, pa_status* sel) {
+    DecodeWeightsSpace w;
+    const int G = num_heads / num_kv_heads;
+    w.tc = use_decode_tc(dtype, head_dim, block_size, G, fp8, sel);
+    w.stats = align256((size_t)num_seqs * num_heads * sizeof(float2));
+    if (w.tc) {
+        w.grid = pa::decode_weights_grid(num_seqs, num_kv_heads, head_dim, block_size, max_context, dtype, G,
+                                         g_options[PA_OPT_DECODE_CTAS], fp8);
+        w.records = align256(pa::decode_tc_workspace(num_seqs, num_kv_heads, G, head_dim, w.grid, fp8));
+        w.scores = pa::decode_weights_scores(num_seqs, num_heads, max_context);
+    }
+    return w;
+}
+
 static size_t decode_weights_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t block_size, int32_t max_context, int dtype, bool fp8) {
     if (num_seqs <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads || max_context < 0)
         return 0;
-    return align256(decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, fp8)) +
-           (size_t)num_seqs * num_heads * sizeof(float2);
+    pa_status sel;
+    return decode_weights_space(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, fp8, &sel)
+        .total();
 }
 
 static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_stride, const void* q,
@@ -911,33 +959,49 @@ static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_
                                      int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
                                      int32_t max_context, float scale, int dtype, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-    pa_status g = check_geometry(num_heads, num_kv_heads, head_dim, num_blocks, block_size, dtype);
-    if (g != PA_OK) return g;
-    if (num_seqs < 0 || max_context < 0)
-        return fail(PA_ERR_INVALID_ARG, "num_seqs, max_blocks and max_context must be non-negative");
-    if (num_seqs == 0) return PA_OK;
+    const bool fp8 = k_scales != nullptr;
+    pa::AttnArgs a{};
+    pa_status g = decode_args(a, out, q, nullptr, nullptr, k_cache, v_cache, k_scales, v_scales, block_tables,
+                              max_blocks, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                              block_size, max_context, scale, dtype, as_stream(stream));
+    if (g != PA_OK || num_seqs == 0) return g;
     if (!weights) return fail(PA_ERR_INVALID_ARG, "null pointer");
-    pa::WeightArgs a{};
-    g = weights_args(a, weights, weights_stride, q, k_cache, k_scales, block_tables, max_blocks, context_lens, nullptr,
-                     num_seqs, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, 0, scale, 1,
-                     dtype);
+    pa::WeightArgs wa{};
+    g = weights_args(wa, weights, weights_stride, q, k_cache, k_scales, block_tables, max_blocks, context_lens,
+                     nullptr, num_seqs, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, 0, scale,
+                     1, dtype);
     if (g != PA_OK) return g;
-    const size_t need = decode_weights_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context,
-                                                 dtype, k_scales != nullptr);
-    if (!workspace || workspace_bytes < need)
+    const DecodeWeightsSpace sp =
+        decode_weights_space(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, fp8, &g);
+    if (g != PA_OK) return g;
+    if (!workspace || workspace_bytes < sp.total())
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
-                                          std::to_string(need) + " needed");
-    const size_t dec = align256(decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context,
-                                                 dtype, k_scales != nullptr));
-    g = decode_impl(out, q, nullptr, nullptr, k_cache, v_cache, k_scales, v_scales, block_tables, max_blocks,
-                    context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_context,
-                    scale, dtype, workspace, dec, stream);
-    if (g != PA_OK) return g;
-    a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + dec);
-    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
-        cudaError_t e = pa::launch_weights_simt(
-            weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch)), as_stream(stream));
+                                          std::to_string(sp.total()) + " needed");
+    if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t st = as_stream(stream);
+    if (!sp.tc) {
+        cudaError_t e = pa::launch_attn_simt(a, st);
         if (e != cudaSuccess) return cuda_fail(e, "pa_decode_weights launch");
+        wa.stats = reinterpret_cast<float2*>(ws);
+        for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
+            e = pa::launch_weights_simt(weights_part(wa, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch)), st);
+            if (e != cudaSuccess) return cuda_fail(e, "pa_decode_weights launch");
+        }
+        return PA_OK;
+    }
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kDecodeMaxSeqsPerLaunch) {
+        const int32_t cnt = std::min(num_seqs - s0, pa::kDecodeMaxSeqsPerLaunch);
+        pa::AttnArgs c = decode_part(a, s0, cnt);
+        pa::DecodeWeights w;
+        w.weights = weights + (int64_t)s0 * num_kv_heads * weights_stride;
+        w.stride = weights_stride;
+        w.row_stats = reinterpret_cast<float2*>(ws + sp.records);
+        w.scores = reinterpret_cast<float*>(ws + sp.records + sp.stats);
+        std::string err;
+        cudaError_t e = pa::launch_decode_weights(c, num_blocks, sp.grid, ws, w, &err, st);
+        if (e != cudaSuccess)
+            return err.empty() ? cuda_fail(e, "pa_decode_weights launch") : fail(PA_ERR_CUDA, "pa_decode_weights: " + err);
     }
     return PA_OK;
 }

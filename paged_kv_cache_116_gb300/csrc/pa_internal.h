@@ -119,6 +119,20 @@ size_t decode_tc_workspace(int32_t num_seqs, int32_t num_kv_heads, int32_t group
 cudaError_t launch_decode_tc(const AttnArgs& a, int32_t num_blocks, int grid_ctas, void* workspace,
                              std::string* err, cudaStream_t stream);
 uint32_t decode_tc_status(bool clear);
+
+// ---- the same with the attention weights (pa_decode_weights.cu)
+struct DecodeWeights {
+    float* weights;  // [num_seqs, num_kv_heads, stride]
+    int64_t stride;
+    float* scores;      // decode_weights_scores(...) bytes
+    float2* row_stats;  // [num_seqs, num_heads]
+};
+int decode_weights_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t max_context, int dtype, int32_t group, int64_t ctas_override, bool kv_fp8);
+size_t decode_weights_scores(int32_t num_seqs, int32_t num_heads, int32_t max_context);
+cudaError_t launch_decode_weights(const AttnArgs& a, int32_t num_blocks, int grid_ctas, void* workspace,
+                                  const DecodeWeights& w, std::string* err, cudaStream_t stream);
+uint32_t decode_weights_status(bool clear);
 // ---- self-test of the failure path (pa_selftest.cu): one CTA waits on a
 // barrier nothing completes for `polls` polls and sets its status word's
 // timeout bit (pa_selftest_wait_timeout).
