@@ -240,7 +240,8 @@ pa_status pa_device_status(int clear) {
     if (e != cudaSuccess) return cuda_fail(e, "pa_device_status");
     const uint32_t bits =
         pa::decode_tc_status(clear != 0) | pa::decode_weights_status(clear != 0) |
-                          pa::varlen_umma_status(clear != 0) | pa::selftest_status(clear != 0);
+                          pa::varlen_umma_status(clear != 0) | pa::weights_umma_status(clear != 0) |
+                          pa::selftest_status(clear != 0);
     if (bits & 1u) return fail(PA_ERR_TIMEOUT, "a kernel's bounded barrier wait ran out");
     return PA_OK;
 }
@@ -1006,9 +1007,23 @@ static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_
     return PA_OK;
 }
 
-static size_t prompt_weights_workspace(int32_t num_seqs, int32_t total_q, int32_t num_heads, int32_t num_kv_heads) {
-    if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return 0;
-    return (size_t)total_q * num_heads * sizeof(float2);
+// The prompt form's path (PA_OPT_VARLEN_KERNEL pins it), its splits and its
+// workspace: the row statistics, one piece per split.
+struct PromptWeightsPlan {
+    bool tc = false;
+    int splits = 1;
+    size_t bytes = 0;
+};
+static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                             int32_t max_context, int32_t window, int dtype, bool fp8) {
+    PromptWeightsPlan p;
+    if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return p;
+    const int G = num_heads / num_kv_heads;
+    p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, block_size, G, fp8);
+    if (p.tc) p.splits = pa::weights_umma_splits(num_seqs, total_q, num_kv_heads, G, max_context, window);
+    p.bytes = (size_t)p.splits * total_q * num_heads * sizeof(float2);
+    return p;
 }
 
 static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
@@ -1033,10 +1048,14 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
                      cu_seqlens_q, num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context,
                      window, scale, causal, dtype);
     if (g != PA_OK) return g;
-    const size_t need = prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
-    if (!workspace || workspace_bytes < need)
+    const PromptWeightsPlan plan = prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size,
+                                                       max_context, window, dtype, k_scales != nullptr);
+    if (g_options[PA_OPT_VARLEN_KERNEL] == 2 && !plan.tc)
+        return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 caches, head_dim 64/128/256, block_size "
+                                        "8 or a multiple of 16 up to 256 and at most 128 query heads per KV head");
+    if (!workspace || workspace_bytes < plan.bytes)
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
-                                          std::to_string(need) + " needed");
+                                          std::to_string(plan.bytes) + " needed");
     if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     cudaStream_t st = as_stream(stream);
     if (check_mode()) {
@@ -1046,9 +1065,12 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     }
     a.stats = static_cast<float2*>(workspace);
     for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
-        cudaError_t e = pa::launch_weights_simt(
-            weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch)), st);
-        if (e != cudaSuccess) return cuda_fail(e, "pa_prompt_weights launch");
+        const pa::WeightArgs c = weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch));
+        std::string err;
+        cudaError_t e = plan.tc ? pa::launch_weights_umma(c, num_blocks, plan.splits, &err, st)
+                                : pa::launch_weights_simt(c, st);
+        if (e != cudaSuccess)
+            return err.empty() ? cuda_fail(e, "pa_prompt_weights launch") : fail(PA_ERR_CUDA, "pa_prompt_weights: " + err);
     }
     return PA_OK;
 }
@@ -1112,8 +1134,10 @@ pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weights_strid
 size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                         int32_t max_context, int32_t window, int dtype) {
-    (void)max_q, (void)head_dim, (void)block_size, (void)max_context, (void)window, (void)dtype;
-    return prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
+    (void)max_q;
+    return prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context, window,
+                               dtype, false)
+        .bytes;
 }
 
 pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
@@ -1131,8 +1155,10 @@ pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* 
 size_t pa_prompt_weights_fp8_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                             int32_t max_context, int32_t window, int dtype) {
-    (void)max_q, (void)head_dim, (void)block_size, (void)max_context, (void)window, (void)dtype;
-    return prompt_weights_workspace(num_seqs, total_q, num_heads, num_kv_heads);
+    (void)max_q;
+    return prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context, window,
+                               dtype, true)
+        .bytes;
 }
 
 pa_status pa_prompt_weights_fp8(float* weights, int64_t weights_stride, const void* q, const void* k_codes,

@@ -203,6 +203,14 @@ struct WeightArgs {
 // Requests one launch handles (their tile counts' prefix lives in shared memory).
 constexpr int kWeightMaxSeqsPerLaunch = 4096;
 cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
+// The same on the tensor cores (pa_weights_umma.cu).  stats then holds
+// `splits` pieces of [total_q, num_heads] (maximum, sum).
+bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, bool kv_fp8);
+int weights_umma_splits(int32_t num_seqs, int32_t total_q, int32_t num_kv_heads, int32_t group, int32_t max_context,
+                        int32_t window);
+cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, int splits, std::string* err,
+                                cudaStream_t stream);
+uint32_t weights_umma_status(bool clear);
 
 // ---- eviction by accumulated weight (pa_evict.cu)
 struct EvictArgs {

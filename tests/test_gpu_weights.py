@@ -209,6 +209,11 @@ PROMPT = [
     ([130, 20], [300, 600], 8, 2, 128, 16, "bf16", 0, True, True),
     ([64, 20], [64, 900], 12, 2, 128, 16, "f16", 24, True, True),
     ([20, 9], [50, 9], 4, 2, 64, 16, "f32", 0, True, True),
+    ([1200, 300], [1300, 4000], 8, 2, 128, 16, "f16", 0, True, False),
+    ([600, 2], [900, 3], 14, 2, 64, 64, "bf16", 0, True, False),
+    ([70, 5], [90, 700], 128, 1, 64, 16, "bf16", 0, True, False),
+    ([40, 129], [40, 260], 4, 2, 256, 8, "f16", 0, True, False),
+    ([33, 1], [9000, 2500], 32, 8, 128, 256, "bf16", 32, True, False),
 ]
 
 
