@@ -1007,22 +1007,24 @@ static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_
     return PA_OK;
 }
 
-// The prompt form's path (PA_OPT_VARLEN_KERNEL pins it), its splits and its
-// workspace: the row statistics, one piece per split.
+// The prompt form's path (PA_OPT_VARLEN_KERNEL pins it), how its work is cut,
+// and its workspace.
 struct PromptWeightsPlan {
     bool tc = false;
-    int splits = 1;
-    size_t bytes = 0;
+    pa::WeightPlan cut;
+    size_t bytes() const { return cut.stats_bytes + cut.partial_bytes; }
 };
-static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, int32_t num_heads,
+static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                              int32_t max_context, int32_t window, int dtype, bool fp8) {
     PromptWeightsPlan p;
     if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return p;
     const int G = num_heads / num_kv_heads;
     p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, block_size, G, fp8);
-    if (p.tc) p.splits = pa::weights_umma_splits(num_seqs, total_q, num_kv_heads, G, max_context, window);
-    p.bytes = (size_t)p.splits * total_q * num_heads * sizeof(float2);
+    if (p.tc)
+        p.cut = pa::weights_umma_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, max_context, window);
+    else
+        p.cut.stats_bytes = (size_t)total_q * num_heads * sizeof(float2);
     return p;
 }
 
@@ -1048,14 +1050,14 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
                      cu_seqlens_q, num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context,
                      window, scale, causal, dtype);
     if (g != PA_OK) return g;
-    const PromptWeightsPlan plan = prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size,
-                                                       max_context, window, dtype, k_scales != nullptr);
+    const PromptWeightsPlan plan = prompt_weights_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim,
+                                                       block_size, max_context, window, dtype, k_scales != nullptr);
     if (g_options[PA_OPT_VARLEN_KERNEL] == 2 && !plan.tc)
         return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 caches, head_dim 64/128/256, block_size "
                                         "8 or a multiple of 16 up to 256 and at most 128 query heads per KV head");
-    if (!workspace || workspace_bytes < plan.bytes)
+    if (!workspace || workspace_bytes < plan.bytes())
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
-                                          std::to_string(plan.bytes) + " needed");
+                                          std::to_string(plan.bytes()) + " needed");
     if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     cudaStream_t st = as_stream(stream);
     if (check_mode()) {
@@ -1064,10 +1066,14 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
         if (err != PA_OK) return err;
     }
     a.stats = static_cast<float2*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut.stats_bytes);
+    a.key_splits = plan.cut.key_splits;
+    a.row_splits = plan.cut.row_splits;
+    a.few_rows = plan.cut.few_rows ? 1 : 0;
     for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
         const pa::WeightArgs c = weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch));
         std::string err;
-        cudaError_t e = plan.tc ? pa::launch_weights_umma(c, num_blocks, plan.splits, &err, st)
+        cudaError_t e = plan.tc ? pa::launch_weights_umma(c, num_blocks, &err, st)
                                 : pa::launch_weights_simt(c, st);
         if (e != cudaSuccess)
             return err.empty() ? cuda_fail(e, "pa_prompt_weights launch") : fail(PA_ERR_CUDA, "pa_prompt_weights: " + err);
@@ -1134,10 +1140,9 @@ pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weights_strid
 size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                         int32_t max_context, int32_t window, int dtype) {
-    (void)max_q;
-    return prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context, window,
-                               dtype, false)
-        .bytes;
+    return prompt_weights_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                               window, dtype, false)
+        .bytes();
 }
 
 pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* q, const void* k_cache,
@@ -1155,10 +1160,9 @@ pa_status pa_prompt_weights(float* weights, int64_t weights_stride, const void* 
 size_t pa_prompt_weights_fp8_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                             int32_t max_context, int32_t window, int dtype) {
-    (void)max_q;
-    return prompt_weights_plan(num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, max_context, window,
-                               dtype, true)
-        .bytes;
+    return prompt_weights_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                               window, dtype, true)
+        .bytes();
 }
 
 pa_status pa_prompt_weights_fp8(float* weights, int64_t weights_stride, const void* q, const void* k_codes,

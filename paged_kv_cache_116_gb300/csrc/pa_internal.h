@@ -199,17 +199,28 @@ struct WeightArgs {
     int dtype;
     int kv_fp8;
     float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
+    float* partial = nullptr;
+    int key_splits = 1;
+    int row_splits = 1;
+    int few_rows = 0;
 };
 // Requests one launch handles (their tile counts' prefix lives in shared memory).
 constexpr int kWeightMaxSeqsPerLaunch = 4096;
 cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
-// The same on the tensor cores (pa_weights_umma.cu).  stats then holds
-// `splits` pieces of [total_q, num_heads] (maximum, sum).
+// The same on the tensor cores (pa_weights_umma.cu), which cut the work as
+// their plan says.  stats then holds key_splits pieces of [total_q, num_heads]
+// (maximum, sum), partial row_splits pieces of [num_seqs, num_kv_heads,
+// max_context].
+struct WeightPlan {
+    int key_splits = 1;
+    int row_splits = 1;
+    bool few_rows = false;  // row_splits then cuts the keys, without partial weights
+    size_t stats_bytes = 0, partial_bytes = 0;
+};
 bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, bool kv_fp8);
-int weights_umma_splits(int32_t num_seqs, int32_t total_q, int32_t num_kv_heads, int32_t group, int32_t max_context,
-                        int32_t window);
-cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, int splits, std::string* err,
-                                cudaStream_t stream);
+WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t max_context, int32_t window);
+cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream);
 uint32_t weights_umma_status(bool clear);
 
 // ---- eviction by accumulated weight (pa_evict.cu)
