@@ -199,6 +199,8 @@ struct WeightArgs {
     int dtype;
     int kv_fp8;
     float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
+    float* tile_stats = nullptr;
+    int stat_tiles = 0;
     float* partial = nullptr;
     int key_splits = 1;
     int row_splits = 1;
@@ -215,7 +217,8 @@ struct WeightPlan {
     int key_splits = 1;
     int row_splits = 1;
     bool few_rows = false;  // row_splits then cuts the keys, without partial weights
-    size_t stats_bytes = 0, partial_bytes = 0;
+    int stat_tiles = 0;     // tile_stats: [num_kv_heads, stat_tiles, 2, 128]
+    size_t stats_bytes = 0, tile_stats_bytes = 0, partial_bytes = 0;
 };
 bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, bool kv_fp8);
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,

@@ -30,14 +30,17 @@
 // gridDim.y: in pass 1 pass 2 joins the pieces' (maximum, sum) as it reads
 // them, in pass 2 the pieces' partial weights are added by a third kernel.
 //
-// Roles: per (stationary tile x, parity of the streamed tile) a group of four
-// warps that works the accumulator tile, one row or key per thread; then one
-// warp that loads tiles by TMA (128-byte swizzle; keys through the block
-// table, one 16-token group per box) and one whose first lane issues the MMAs.
-// Every group has its own 128-column accumulator, so MMAs run under the other
-// groups' exponentials.  Every wait is bounded; on expiry the CTA sets a status
-// bit, abandons its work, waits (bounded) for its loads in flight and frees
-// its tensor memory.
+// Roles (19 warps up to head_dim 128): four groups of four warps work the
+// accumulator tiles, one row or key per thread; one warp loads tiles by TMA
+// (128-byte swizzle; keys through the block table, one 16-token group per
+// box); one warp per stationary tile issues its MMAs (one warp for both left
+// the tensor pipe idle while it waited: 590 of 1,090 cycles per accumulator).
+// Accumulators are (stationary tile x, parity of the streamed tile), 128
+// columns each.  In pass 1 a group owns one of them; in pass 2 it owns half of
+// the columns of both tiles' accumulators of a parity, so that every column
+// statistic it reads from shared memory serves two keys.  Every wait is
+// bounded; on expiry the CTA sets a status bit, abandons its work, waits
+// (bounded) for its loads in flight and frees its tensor memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -57,6 +60,24 @@
 namespace pa {
 namespace {
 
+
+// One lane of a converged warp.  MMAs issued under it, with operands that the
+// compiler knows to be the same in every lane (shuffled from lane 0), go out
+// one per 64 cycles; the same loop under `if (lane == 0)` takes 115-138 cycles
+// per MMA (128 x 128 x 16), because every descriptor then has to be moved to
+// uniform registers one by one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint32_t lane0(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+// Shared-memory matrix descriptor of a 128-byte-swizzled tile from its low
+// word (address >> 4 | leading byte offset): stride 1024 bytes, version 1.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t lo) {
+    return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
+}
+
 __device__ unsigned int g_weights_status;
 
 constexpr int TM = 128;                       // rows of A and columns of B
@@ -70,20 +91,22 @@ struct WGeo {
     static constexpr int NA = HD <= 128 ? 2 : 1;    // stationary tiles
     static constexpr int RING = HD == 64 ? 6 : HD == 128 ? 4 : 2;  // streamed tiles in flight
     static constexpr int NWG = 2 * NA;              // accumulators and their warp groups
-    static constexpr int W_PROD = 4 * NWG, W_MMA = W_PROD + 1, NTHREADS = 32 * (W_MMA + 1);
+    static constexpr int NPROD = 2;                 // loading warps
+    static constexpr int W_PROD = 4 * NWG, W_MMA = W_PROD + NPROD, NTHREADS = 32 * (W_MMA + NA);
     static constexpr uint32_t TMEM_COLS = NWG * TM;
     static constexpr int CH = HD / 64;        // 128-byte chunks of a row
     static constexpr int CHB = TM * 128;      // bytes of one chunk of a tile
     static constexpr int TILE = CH * CHB;
     static constexpr int RING_OFF = NA * TILE;
-    // per group two buffers of -M[128] and 1 / l[128]
+    // pass 2: the streamed query tiles' statistics, SRING x {-M, 1 / l}[128];
+    // few rows: the stationary ones', [NA]{-M, 1 / l}[128]
+    static constexpr int SRING = 8;
     static constexpr int STAT_OFF = RING_OFF + RING * TILE;
-    static constexpr int JOIN_OFF = STAT_OFF + NWG * 4 * TM * 4;  // results handed over, float2[2][128]
-    static constexpr int BAR_OFF = JOIN_OFF + 2 * TM * 8;
+    static constexpr int JOIN_OFF = STAT_OFF + SRING * 2 * TM * 4;  // results handed over, float2[3][128]
+    static constexpr int BAR_OFF = JOIN_OFF + 3 * TM * 8;
     // a_full, a_empty, b_full[RING], b_empty[RING], d_full[NWG],
-    // d_empty[NWG], s_full[NWG] (statistics are in shared memory), j_full[2],
-    // j_empty[2] (results handed over)
-    static constexpr int NBAR = 2 + 2 * RING + 3 * NWG + 4;
+    // s_full[SRING], d_empty[NWG], s_empty[SRING], g_bar, j_full[3], j_empty[3]
+    static constexpr int NBAR = 2 + 2 * RING + 2 * NWG + 2 * SRING + 7;
     static constexpr int ADDR_OFF = BAR_OFF + NBAR * 8;
     static constexpr int PREF_OFF = ADDR_OFF + 16;
 };
@@ -100,6 +123,24 @@ struct Item {
     int a0, na;  // first stationary tile (query tile, or key tile in pass 2) and how many
     int b0, b1;  // streamed tiles
 };
+
+// The statistics of one row (an index into a piece of p.stats), joined over
+// pass 1's key splits: (-M, 1 / l).
+__device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) {
+    const int64_t part = (int64_t)p.total_q * p.num_heads;
+    float2 s = __ldcg(p.stats + row);
+    for (int z = 1; z < p.key_splits; ++z) {
+        const float2 o = __ldcg(p.stats + z * part + row);
+        const float mn = fmaxf(s.x, o.x);
+        if (mn == -INFINITY) {  // no key, or none with a number for a score
+            s.y += o.y;
+            continue;
+        }
+        s.y = s.y * exp2f(s.x - mn) + o.y * exp2f(o.x - mn);
+        s.x = mn;
+    }
+    return make_float2(s.x == -INFINITY ? 0.f : -s.x, 1.f / s.y);
+}
 
 enum Pass { kRowStats = 1, kKeyWeights = 2, kFewRows = 3 };
 
@@ -120,14 +161,15 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     uint64_t* b_full = bars + 2;
     uint64_t* b_empty = b_full + RING;
     uint64_t* d_full = b_empty + RING;
-    uint64_t* d_empty = d_full + Gm::NWG;
-    uint64_t* s_full = d_empty + Gm::NWG;
-    uint64_t* j_full = s_full + Gm::NWG;
-    uint64_t* j_empty = j_full + 2;
-    float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);  // [NWG][2][2][TM]
+    uint64_t* s_full = d_full + Gm::NWG;
+    uint64_t* d_empty = s_full + Gm::SRING;
+    uint64_t* s_empty = d_empty + Gm::NWG;
+    uint64_t* g_bar = s_empty + Gm::SRING;
+    uint64_t* j_full = g_bar + 1;
+    uint64_t* j_empty = j_full + 3;
+    float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);
     float2* join_s = reinterpret_cast<float2*>(base + Gm::JOIN_OFF);
     volatile uint32_t* taddr_slot = reinterpret_cast<volatile uint32_t*>(base + Gm::ADDR_OFF);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(base + Gm::ADDR_OFF + 4);
     int32_t* prefix = reinterpret_cast<int32_t*>(base + Gm::PREF_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -140,10 +182,14 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < Gm::NBAR; ++i) {
             const uint64_t* b = bars + i;
-            // d_empty: one arrival per warp of a group; s_full and j_*: one per thread of it
-            mbar_init(bars + i, b >= s_full ? 128u : b >= d_empty ? 4u : 1u);
+            // a_empty, b_empty: one commit per issuing warp; from d_empty on
+            // one arrival per warp: of the groups that work the accumulator
+            // or tile, of all groups (g_bar), of one group (j_*)
+            const uint32_t groups =
+                b >= j_full ? 1 : b >= g_bar ? Gm::NWG : b < s_empty && PASS == kRowStats ? 1 : NA;
+            const bool per_mma = b == a_empty || (b >= b_empty && b < d_full);
+            mbar_init(bars + i, b >= d_empty ? 4 * groups : per_mma ? NA : 1u);
         }
-        *abort_flag = 0;
         mbar_fence_init();
     }
     // tensor memory is taken after the previous grid is done: its CTAs may
@@ -203,13 +249,17 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         w.b0 += (int)((int64_t)n * blockIdx.y / gridDim.y);
         return w;
     };
-    auto fail = [&]() {
-        *abort_flag = 1;
-        atomicOr(&g_weights_status, kStatusTimeout);
+    // where query tile t of a request keeps its statistics: distinct for every
+    // (request, tile), since a request's ceil(rows / T) tiles fit between its
+    // floor(row0 / T) + s and the next request's
+    auto stat_tile = [&](const WeightSeq& sq, int h, int t) -> int64_t {
+        return (int64_t)h * p.stat_tiles + sq.row0 / TT + sq.s + t;
     };
+    auto fail = [&]() { atomicOr(&g_weights_status, kStatusTimeout); };
 
-    if (warp == Gm::W_PROD) {
-        // ---------------- producer
+    if (warp >= Gm::W_PROD && warp < Gm::W_MMA) {
+        // ---------------- producer `me` of every NPROD-th streamed tile; the first also loads the stationary ones
+        const int me = warp - Gm::W_PROD;
         const uint64_t pol = l2_policy_evict_last();  // keys are read twice, query tiles by every key tile
         const int bsz = p.block_size, halves = bsz == 8 ? 2 : 1;
         const int nbox = NGRP * halves;  // boxes along the keys of a tile
@@ -250,7 +300,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             int ok = 0;
             if (lane == 0) {
-                ok = mbar_wait_ns(bar, parity, WAIT_NS) && !*abort_flag;
+                ok = mbar_wait_ns(bar, parity, WAIT_NS);
                 if (!ok) fail();
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
@@ -258,9 +308,12 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
             const Item w = item_at(it);
             if (w.b0 >= w.b1) continue;
-            int32_t row = kKeysStream ? key_row(w, w.b0) : 0;
-            if (!(run = wait(a_empty, (uint32_t)(na & 1) ^ 1u))) break;
-            if (kKeysStream) {
+            const int mine = w.b0 + (nb + me) % Gm::NPROD;  // this warp's first tile of the item
+            int32_t row = kKeysStream && mine < w.b1 ? key_row(w, mine) : 0;
+            if (me == 0 && !(run = wait(a_empty, (uint32_t)(na & 1) ^ 1u))) break;
+            if (me != 0) {
+                // (the first producer's)
+            } else if (kKeysStream) {
                 expect(a_full, w.na * query_bytes);
                 for (int x = 0; x < w.na; ++x) load_queries(w, w.a0 + x, base + x * Gm::TILE, a_full);
             } else {
@@ -272,172 +325,164 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             }
             ++na;
             for (int t = w.b0; t < w.b1; ++t, ++nb) {
+                if ((nb + me) % Gm::NPROD) continue;
                 const int slot = nb % RING;
                 uint8_t* dst = base + Gm::RING_OFF + slot * Gm::TILE;
                 if (!(run = wait(&b_empty[slot], (uint32_t)(nb / RING & 1) ^ 1u))) break;
                 if (kKeysStream) {
                     expect(&b_full[slot], key_groups(w, t) * group_bytes);
                     load_keys(w, t, row, dst, &b_full[slot]);
-                    if (t + 1 < w.b1) row = key_row(w, t + 1);
+                    if (t + Gm::NPROD < w.b1) row = key_row(w, t + Gm::NPROD);
                 } else {
                     expect(&b_full[slot], query_bytes);
                     load_queries(w, t, dst, &b_full[slot]);
+                    const int sl = nb % Gm::SRING;
+                    if (!(run = wait(&s_empty[sl], (uint32_t)(nb / Gm::SRING & 1) ^ 1u))) break;
+                    expect(&s_full[sl], 2 * TM * 4);
+                    if (lane == 0)
+                        bulk_g2s(stat_s + sl * 2 * TM, p.tile_stats + stat_tile(w.sq, w.h, t) * 2 * TM, 2 * TM * 4,
+                                 &s_full[sl]);
                 }
             }
         }
         if (!run) {  // copies in flight land before the CTA's shared memory is given up
-            if (na) mbar_wait_ns(a_full, (uint32_t)(na - 1) & 1u, WAIT_NS);
-            for (int j = max(0, nb - RING); j < nb; ++j)
-                mbar_wait_ns(&b_full[j % RING], (uint32_t)(j / RING) & 1u, WAIT_NS);
+            if (me == 0 && na) mbar_wait_ns(a_full, (uint32_t)(na - 1) & 1u, WAIT_NS);
+            for (int j = max(0, nb - RING); j <= nb; ++j)
+                if ((j + me) % Gm::NPROD == 0 && j < nb + (PASS == kKeyWeights))
+                    mbar_wait_ns(&b_full[j % RING], (uint32_t)(j / RING) & 1u, WAIT_NS);
+            if (PASS == kKeyWeights)
+                for (int j = max(0, nb - Gm::SRING); j < nb; ++j)
+                    if ((j + me) % Gm::NPROD == 0)
+                        mbar_wait_ns(&s_full[j % Gm::SRING], (uint32_t)(j / Gm::SRING) & 1u, WAIT_NS);
         }
-    } else if (warp == Gm::W_MMA) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_f16(TM, TM, kBF16, false);
-            const uint32_t s_base = smem_u32(base);
-            int na = 0, nb = 0, nx[2] = {0, 0}, last = -1;
-            bool run = true;
-            for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
-                const Item w = item_at(it);
-                if (w.b0 >= w.b1) continue;
-                if (!(run = mbar_wait_ns(a_full, (uint32_t)na & 1u, WAIT_NS) && !*abort_flag)) break;
-                ++na;
-                for (int t = w.b0; t < w.b1 && run; ++t, ++nb) {
-                    const int slot = nb % RING;
-                    run = mbar_wait_ns(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS);
-                    const uint32_t b_s = s_base + Gm::RING_OFF + slot * Gm::TILE;
-#pragma unroll
-                    for (int x = 0; x < NA; ++x) {
-                        if (x >= w.na || !run) break;
-                        const int d = 2 * x + (nx[x] & 1);
-                        run = mbar_wait_ns(&d_empty[d], ((uint32_t)(nx[x] >> 1) & 1u) ^ 1u, WAIT_NS) && !*abort_flag;
-                        if (!run) break;
-                        ++nx[x];
-                        tc_fence_after();
-                        const uint32_t a_s = s_base + x * Gm::TILE;
-                        // the accumulator's lanes are query rows, or keys
-                        const uint32_t l_s = PASS == kFewRows ? b_s : a_s, c_s = PASS == kFewRows ? a_s : b_s;
+    } else if (warp >= Gm::W_MMA) {
+        // ---------------- MMA issuer of stationary tile x
+        const uint32_t x = lane0(warp - Gm::W_MMA);
+        const uint32_t idesc = umma_idesc_f16(TM, TM, kBF16, false);
+        const uint32_t s_lo = lane0(smem_u32(base) >> 4 | 1u << 16), a_lo = s_lo + x * (Gm::TILE / 16);
+        const uint32_t d_x = lane0(tmem) + x * 2 * TM;
+        int na = 0, nb = 0, nd[2] = {0, 0}, last = -1;  // items, streamed tiles, accumulators of each parity
+        bool run = true;
+        for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
+            const Item w = item_at(it);
+            if (w.b0 >= w.b1) continue;
+            if (!(run = mbar_wait_ns(a_full, (uint32_t)na & 1u, WAIT_NS))) break;
+            ++na;
+            const bool mine = (int)x < w.na;
+            for (int t = w.b0; t < w.b1; ++t, ++nb) {
+                const int slot = nb % RING, par = nb & 1, turn = par ? nd[1] : nd[0];
+                run = mbar_wait_ns(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
+                      (!mine || mbar_wait_ns(&d_empty[2 * x + par], ((uint32_t)turn & 1u) ^ 1u, WAIT_NS));
+                if (!__all_sync(0xffffffffu, run)) {
+                    run = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t b_lo = lane0(s_lo + (Gm::RING_OFF + slot * Gm::TILE) / 16);
+                // the accumulator's lanes are query rows, or keys
+                const uint32_t l_lo = PASS == kFewRows ? b_lo : a_lo, c_lo = PASS == kFewRows ? a_lo : b_lo;
+                const uint32_t d = lane0(d_x + par * TM);
+                if (elect_one()) {
+                    if (mine) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 16; ++kk) {
-                            const int c = kk >> 2, ko = (kk & 3) * 32;
-                            umma_f16(tmem + d * TM, umma_sdesc_sw128(l_s + c * Gm::CHB + ko, 16, 1024),
-                                     umma_sdesc_sw128(c_s + c * Gm::CHB + ko, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+                            const uint32_t off = ((kk >> 2) * Gm::CHB + (kk & 3) * 32) / 16;
+                            umma_f16(d, sw128_desc(l_lo + off), sw128_desc(c_lo + off), idesc, kk > 0 ? 1u : 0u);
                         }
-                        if (x == w.na - 1) {
-                            umma_commit(&b_empty[slot]);
-                            if (t == w.b1 - 1) umma_commit(a_empty);
-                        }
-                        umma_commit(&d_full[d]);
-                        last = d;
+                        umma_commit(&d_full[2 * x + par]);
                     }
+                    umma_commit(&b_empty[slot]);
+                    if (t == w.b1 - 1) umma_commit(a_empty);
+                }
+                __syncwarp();
+                if (mine) {
+                    ++(par ? nd[1] : nd[0]);
+                    last = par;
                 }
             }
-            if (!run) {
-                fail();
-                if (last >= 0)  // MMAs in flight
-                    mbar_wait_ns(&d_full[last], (uint32_t)((nx[last >> 1] - 1) >> 1) & 1u, WAIT_NS);
-            }
+        }
+        if (!run) {
+            if (lane == 0) fail();
+            if (last >= 0)  // MMAs in flight
+                mbar_wait_ns(&d_full[2 * x + last], (uint32_t)((last ? nd[1] : nd[0]) - 1) & 1u, WAIT_NS);
         }
     } else {
-        // ---------------- accumulator tiles: one row or key per thread
-        const int wg = warp >> 2, x = wg >> 1, par = wg & 1, m = threadIdx.x & 127;
-        const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16) + wg * TM;
+        // ---------------- accumulator tiles: one row or key per thread.  Group
+        // (hi, par): the streamed tiles of parity par; in pass 1 stationary
+        // tile hi, in pass 2 columns 64 hi .. 64 hi + 63 of every tile.
+        const int wg = warp >> 2, hi = wg >> 1, par = wg & 1, m = threadIdx.x & 127;
+        constexpr int HC = TM / NA;  // columns of a group in pass 2
+        const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + par * TM;  // + 2 TM x
         const float sl = p.scale_log2;
         const int64_t part = (int64_t)p.total_q * p.num_heads;  // rows of one split's statistics
-        int nx = 0, n_stat = 0, n_join = 0;  // streamed tiles of x; this group's statistics and handovers
+        int nx = 0, n_meet = 0, n_join = 0;  // streamed tiles; barriers gone through
+        int n_d[2] = {0, 0};                 // accumulators of x worked by this group
         bool run = true;
-        auto release = [&]() {
+        auto release = [&](int x) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[wg]);
+            if (lane == 0) mbar_arrive(&d_empty[2 * x + par]);
         };
-        auto acquire = [&]() -> bool {
-            const bool ok = !*abort_flag && mbar_wait_ns(&d_full[wg], (uint32_t)(nx >> 1) & 1u, WAIT_NS);
+        auto acquire = [&](int x) -> bool {
+            const bool ok = mbar_wait_ns(&d_full[2 * x + par], (uint32_t)n_d[x]++ & 1u, WAIT_NS);
             tc_fence_after();
             return ok;
         };
         // a giving group hands its values to the receiving one through buffer j
-        auto hand_over = [&](int j, bool give, float2& v) -> bool {
-            const uint32_t ph = (uint32_t)n_join++ & 1u;
-            if (give) {
-                if (*abort_flag || !mbar_wait_ns(&j_empty[j], ph ^ 1u, WAIT_NS)) return false;
-                join_s[j * TM + m] = v;
-                mbar_arrive(&j_full[j]);
-            } else {
-                if (*abort_flag || !mbar_wait_ns(&j_full[j], ph, WAIT_NS)) return false;
-                v = join_s[j * TM + m];
-                mbar_arrive(&j_empty[j]);
-            }
+        auto give = [&](int j, float2 v) -> bool {
+            if (!mbar_wait_ns(&j_empty[j], ((uint32_t)n_join++ & 1u) ^ 1u, WAIT_NS)) return false;
+            join_s[j * TM + m] = v;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&j_full[j]);
             return true;
         };
-        // statistics of query tile t's row m, joined over pass 1's splits: (-M, 1 / l)
-        auto row_stat = [&](const Item& w, int t) -> float2 {
-            const int tok = t * TT + m / G;
-            if (m >= TT * G || tok >= w.sq.rows) return make_float2(0.f, 0.f);
-            const float2* st = p.stats + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + m % G;
-            float2 s = __ldcg(st);
-            for (int z = 1; z < p.key_splits; ++z) {
-                const float2 o = __ldcg(st + z * part);
-                const float mn = fmaxf(s.x, o.x);
-                if (mn == -INFINITY) {  // no key, or none with a number for a score
-                    s.y += o.y;
-                    continue;
-                }
-                s.y = s.y * exp2f(s.x - mn) + o.y * exp2f(o.x - mn);
-                s.x = mn;
-            }
-            return make_float2(s.x == -INFINITY ? 0.f : -s.x, 1.f / s.y);
-        };
-        // this thread's statistics into the group's next buffer; false if the wait ran out
-        auto share_stat = [&](float2 st, float*& nm) -> bool {
-            const uint32_t ph = (uint32_t)n_stat++ & 1u;
-            nm = stat_s + (2 * wg + ph) * 2 * TM;
-            nm[m] = st.x;
-            nm[TM + m] = st.y;
-            // (a buffer written two turns ago is free: every thread has been
-            // through the barrier of the turn between)
-            mbar_arrive(&s_full[wg]);
+        auto take = [&](int j, uint32_t turn, float2& v) -> bool {
+            if (!mbar_wait_ns(&j_full[j], turn & 1u, WAIT_NS)) return false;
+            v = join_s[j * TM + m];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&j_empty[j]);
             return true;
         };
-        auto stat_ready = [&]() -> bool {
-            return !*abort_flag && mbar_wait_ns(&s_full[wg], (uint32_t)(n_stat - 1) & 1u, WAIT_NS);
+        // a bounded barrier of all groups
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(g_bar);
+            return mbar_wait_ns(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
         };
-        // sum over the columns [c0, c1) of exp2(x - M) / l for this thread's key
-        auto key_sum = [&](const float* nm, int c0, int c1) -> float {
-            const float* il = nm + TM;
-            const bool full = __all_sync(0xffffffffu, c0 <= 0 && c1 == TT * G);
-            // summed tile by tile: a running sum over thousands of rows would
-            // round at its own size in every addition
-            unsigned long long acc2 = f32x2_pack(0.f, 0.f);
-            float acc = 0.f;
-            const unsigned long long sv = f32x2_pack(sl, sl);
+        // statistics of query tile t's row r, joined over pass 1's splits: (-M, 1 / l)
+        auto row_stat = [&](const Item& w, int t, int r) -> float2 {
+            const int tok = t * TT + r / G;
+            if (r >= TT * G || tok >= w.sq.rows) return make_float2(0.f, 0.f);
+            return joined_stat(p, (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + r % G);
+        };
+        // exp2(x - M) / l of `n` accumulators' columns [q, q + 16) for this
+        // thread's keys, added to v[]: column c counts where lo[] <= c < end
+        auto add_columns = [&](auto count, const float (&a)[2][16], const float* nm, const float* il, int c0, bool full,
+                               const int (&lo)[2], int end, float (&v)[2], unsigned long long (&v2)[2]) {
+            constexpr int N = decltype(count)::value;
+            if (full) {
+                const unsigned long long sv = f32x2_pack(sl, sl);
 #pragma unroll
-            for (int q = 0; q < TM / 32; ++q) {
-                float a[32];
-                tmem_ld32(d + 32 * q, a);
-                tmem_wait_ld();
-                if (full) {
+                for (int j = 0; j < 4; ++j) {
+                    const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);
+                    const float4 i4 = *reinterpret_cast<const float4*>(il + 4 * j);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 n4 = *reinterpret_cast<const float4*>(nm + 32 * q + 4 * j);
-                        const float4 i4 = *reinterpret_cast<const float4*>(il + 32 * q + 4 * j);
+                    for (int k = 0; k < N; ++k) {
                         float x0, x1, x2, x3;
-                        f32x2_unpack(fma_f32x2(f32x2_pack(a[4 * j], a[4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
-                        f32x2_unpack(fma_f32x2(f32x2_pack(a[4 * j + 2], a[4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
-                        acc2 = fma_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), f32x2_pack(i4.x, i4.y), acc2);
-                        acc2 = fma_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), f32x2_pack(i4.z, i4.w), acc2);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int c = 32 * q + j;
-                        if (c >= c0 && c < c1) acc = fmaf(fast_exp2(fmaf(a[j], sl, nm[c])), il[c], acc);
+                        f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j], a[k][4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
+                        f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j + 2], a[k][4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
+                        v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), f32x2_pack(i4.x, i4.y), v2[k]);
+                        v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), f32x2_pack(i4.z, i4.w), v2[k]);
                     }
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        if (c0 + j >= lo[k] && c0 + j < end)
+                            v[k] = fmaf(fast_exp2(fmaf(a[k][j], sl, nm[j])), il[j], v[k]);
             }
-            float s0, s1;
-            f32x2_unpack(acc2, s0, s1);
-            return acc + (s0 + s1);
         };
         auto store_weight = [&](const Item& w, int key, float v) {
             if (key >= w.sq.L) return;
@@ -451,15 +496,19 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         };
         for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
             const Item w = item_at(it);
-            if (x >= w.na) continue;
             if constexpr (PASS == kRowStats) {
+                if (hi >= w.na) {
+                    nx += w.b1 - w.b0;
+                    continue;
+                }
+                const int x = hi;
                 const int tok = (w.a0 + x) * TT + m / G, g = m % G;
                 const bool valid = m < TT * G && tok < w.sq.rows;
                 const int last = p.causal ? w.sq.L - w.sq.rows + tok : w.sq.L - 1;  // last key the row sees
                 float m_used = -INFINITY, l = 0.f;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if ((nx & 1) != par) continue;
-                    if (!(run = acquire())) break;
+                    if (!(run = acquire(x))) break;
                     // rows that hold no query are never stored; they take the
                     // unmasked path with their warp
                     const int vis = valid ? min(last - t * TM, TM - 1) : TM - 1;
@@ -477,7 +526,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                         for (int q = 0; q < TM / 32; ++q) {
                             float a[32];
-                            tmem_ld32(d + 32 * q, a);
+                            tmem_ld32(acc + 2 * TM * x + 32 * q, a);
                             tmem_wait_ld();
                             if (full) {
 #pragma unroll
@@ -501,7 +550,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                         for (int q = 0; q < TM / 32; ++q) {
                             float a[32];
-                            tmem_ld32(d + 32 * q, a);
+                            tmem_ld32(acc + 2 * TM * x + 32 * q, a);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -528,11 +577,14 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         settle(max_pass());
                     }
                     l = fmaf(l, alpha, sum);
-                    release();
+                    release(x);
                 }
-                float2 o = make_float2(m_used, l);
-                if (run) run = hand_over(x, par == 1, o);
-                if (run && par == 0) {
+                if (!run) break;
+                if (par == 1) {
+                    run = give(x, make_float2(m_used, l));
+                } else {
+                    float2 o;
+                    if (!(run = take(x, (uint32_t)n_join++, o))) break;
                     const float mn = fmaxf(m_used, o.x);
                     if (mn == -INFINITY) {
                         l += o.y;
@@ -540,51 +592,123 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         l = l * exp2f(m_used - mn) + o.y * exp2f(o.x - mn);
                         m_used = mn;
                     }
-                    if (valid)
+                    if (gridDim.y == 1 && !p.few_rows) {  // final: -M and 1 / l by column
+                        float* st = p.tile_stats + stat_tile(w.sq, w.h, w.a0 + x) * 2 * TM;
+                        st[m] = valid && m_used != -INFINITY ? -m_used : 0.f;
+                        st[TM + m] = valid ? 1.f / l : 0.f;
+                    } else if (valid) {
                         p.stats[(int64_t)blockIdx.y * part + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + g] =
                             make_float2(m_used, l);
+                    }
                 }
             } else if constexpr (PASS == kKeyWeights) {
-                const int key = (w.a0 + x) * TM + m;
-                const int mine = w.b0 + ((nx ^ par) & 1);  // this group's first tile
-                float2 st = mine < w.b1 ? row_stat(w, mine) : make_float2(0.f, 0.f);
-                float total = 0.f;
+                float total[2] = {0.f, 0.f};
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if ((nx & 1) != par) continue;
-                    float* nm;
-                    share_stat(st, nm);
-                    if (t + 2 < w.b1) st = row_stat(w, t + 2);
-                    if (!(run = stat_ready() && acquire())) break;
-                    // columns [c0, c1) are rows of this request that see the key
-                    const int c1 = min(TT, w.sq.rows - t * TT) * G;
-                    const int c0 = p.causal ? (key - (w.sq.L - w.sq.rows) - t * TT) * G : 0;
-                    total += key_sum(nm, c0, c1);
-                    release();
+                    const int sl = nx % Gm::SRING;
+                    const float* nm = stat_s + sl * 2 * TM + hi * HC;
+                    const float* il = nm + TM;
+                    if (!(run = mbar_wait_ns(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS) && acquire(0) &&
+                                (w.na < 2 || acquire(NA - 1))))
+                        break;
+                    // column c (query row) counts for key k where lo[k] <= c < end
+                    const int end = min(TT, w.sq.rows - t * TT) * G;
+                    int lo[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        lo[x] = p.causal ? ((w.a0 + x) * TM + m - (w.sq.L - w.sq.rows) - t * TT) * G : 0;
+                    const bool full = __all_sync(0xffffffffu, max(lo[0], lo[NA - 1]) <= 0 && end == TT * G);
+                    // summed tile by tile: a running sum over thousands of rows
+                    // would round at its own size in every addition
+                    float v[2] = {0.f, 0.f};
+                    unsigned long long v2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
+                    using Both = std::integral_constant<int, NA>;
+                    using One = std::integral_constant<int, 1>;
+#pragma unroll
+                    for (int q = 0; q < HC / 16; ++q) {
+                        float a[2][16];
+                        tmem_ld16(acc + hi * HC + 16 * q, a[0]);
+                        if (NA == 2 && w.na == 2) tmem_ld16(acc + 2 * TM + hi * HC + 16 * q, a[1]);
+                        tmem_wait_ld();
+                        if (q == HC / 16 - 1) {
+                            release(0);
+                            if (w.na == 2) release(NA - 1);
+                        }
+                        if (w.na == 2) add_columns(Both(), a, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                        else add_columns(One(), a, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                    }
+#pragma unroll
+                    for (int x = 0; x < NA; ++x) {
+                        float s0, s1;
+                        f32x2_unpack(v2[x], s0, s1);
+                        total[x] += v[x] + (s0 + s1);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sl]);
                 }
-                float2 o = make_float2(total, 0.f);
-                if (run) run = hand_over(x, par == 1, o);
-                if (run && par == 0) store_weight(w, key, total + o.x);
+                if (!run) break;
+                if (wg > 0) {
+                    run = give(wg - 1, make_float2(total[0], total[1]));
+                } else {
+                    for (int g = 0; g < Gm::NWG - 1 && run; ++g) {
+                        float2 o;
+                        if (!(run = take(g, (uint32_t)n_join, o))) break;
+                        total[0] += o.x;
+                        total[1] += o.y;
+                    }
+                    ++n_join;
+                    if (!run) break;
+                    store_weight(w, w.a0 * TM + m, total[0]);
+                    if (w.na == 2) store_weight(w, (w.a0 + 1) * TM + m, total[1]);
+                }
             } else {
-                // few rows: the item's query tile x stays, its statistics with it
-                float* nm;
-                if (w.b0 < w.b1) {
-                    share_stat(row_stat(w, x), nm);
-                    run = stat_ready();
+                if (w.b0 >= w.b1) continue;
+                // few rows: the item's query tiles stay, their statistics with them
+                if (!(run = meet())) break;  // the previous item's are used up
+                if (wg < NA) {
+                    const float2 st = row_stat(w, wg, m);
+                    stat_s[wg * 2 * TM + m] = st.x;
+                    stat_s[wg * 2 * TM + TM + m] = st.y;
                 }
-                const int c1 = min(TT, w.sq.rows - x * TT) * G;
-                for (int t = w.b0; t < w.b1 && run; ++t, ++nx) {
+                if (!(run = meet())) break;
+                for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if ((nx & 1) != par) continue;
-                    if (!(run = acquire())) break;
                     const int key = t * TM + m;
-                    const int c0 = p.causal ? (key - (w.sq.L - w.sq.rows) - x * TT) * G : 0;
-                    float v = key_sum(nm, c0, c1);
-                    release();
-                    if (w.na == 2) {  // tile 1's part of the same keys
-                        float2 o = make_float2(v, 0.f);
-                        if (!(run = hand_over(par, x == 1, o))) break;
+                    float v = 0.f;
+#pragma unroll
+                    for (int x = 0; x < NA; ++x) {
+                        if (x >= w.na) break;
+                        if (!(run = acquire(x))) break;
+                        const int end = min(TT, w.sq.rows - x * TT) * G;
+                        const int lo[2] = {p.causal ? (key - (w.sq.L - w.sq.rows) - x * TT) * G : 0, 0};
+                        const bool full = __all_sync(0xffffffffu, lo[0] <= 0 && end == TT * G);
+                        float vx[2] = {0.f, 0.f};
+                        unsigned long long v2[2] = {f32x2_pack(0.f, 0.f), 0};
+#pragma unroll
+                        for (int q = 0; q < HC / 16; ++q) {
+                            float a[2][16];
+                            tmem_ld16(acc + 2 * TM * x + hi * HC + 16 * q, a[0]);
+                            tmem_wait_ld();
+                            if (q == HC / 16 - 1) release(x);
+                            const float* nm = stat_s + x * 2 * TM + hi * HC + 16 * q;
+                            add_columns(std::integral_constant<int, 1>(), a, nm, nm + TM, hi * HC + 16 * q, full, lo, end,
+                                        vx, v2);
+                        }
+                        float s0, s1;
+                        f32x2_unpack(v2[0], s0, s1);
+                        v += vx[0] + (s0 + s1);
+                    }
+                    if (!run) break;
+                    if (NA == 2) {  // the other half of the columns
+                        if (hi == 1) {
+                            if (!(run = give(par, make_float2(v, 0.f)))) break;
+                            continue;
+                        }
+                        float2 o;
+                        if (!(run = take(par, (uint32_t)n_join++, o))) break;
                         v += o.x;
                     }
-                    if (x == 0) store_weight(w, key, v);
+                    store_weight(w, key, v);
                 }
             }
         }
@@ -594,6 +718,28 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == Gm::W_MMA) tmem_dealloc(tmem, Gm::TMEM_COLS);
+}
+
+// Joins pass 1's key splits into the statistics that pass 2 streams: a thread
+// per row of a (request, KV head, query tile).
+__global__ void __launch_bounds__(TM) stats_join_kernel(const WeightArgs p) {
+    extern __shared__ int32_t prefix[];
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int G = p.num_heads / p.num_kv_heads, TT = TM / G, m = threadIdx.x;
+    work_prefix(p, prefix, [&](const WeightSeq& sq) { return (sq.rows + TT - 1) / TT; });
+    const int64_t items = (int64_t)prefix[p.num_seqs] * p.num_kv_heads;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        int s, h, tile;
+        locate_work(prefix, p.num_seqs, p.num_kv_heads, it, s, h, tile);
+        const WeightSeq sq = weight_seq(p, s);
+        const int tok = tile * TT + m / G;
+        float2 v = make_float2(0.f, 0.f);
+        if (m < TT * G && tok < sq.rows) v = joined_stat(p, (int64_t)(sq.row0 + tok) * p.num_heads + h * G + m % G);
+        float* st = p.tile_stats + ((int64_t)h * p.stat_tiles + sq.row0 / TT + s + tile) * 2 * TM;
+        st[m] = v.x;
+        st[TM + m] = v.y;
+    }
 }
 
 // The row splits' partial weights, added in order into the weights.
@@ -677,6 +823,12 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
     auto ctas = [](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(n, kMaxCtas)); };
     e = launch_pdl_smem(k1, dim3(ctas(q_items), (unsigned)a.key_splits), block, smem, stream, tmQ, tmK, a);
     if (e != cudaSuccess) return e;
+    if (!a.few_rows && a.key_splits > 1) {
+        const int64_t tiles = (rows / TT + a.num_seqs) * a.num_kv_heads;
+        e = launch_pdl_smem(stats_join_kernel, dim3(ctas(tiles)), dim3(TM), (size_t)(a.num_seqs + 1) * sizeof(int32_t),
+                            stream, a);
+        if (e != cudaSuccess) return e;
+    }
     e = launch_pdl_smem(k2, dim3(ctas(k_items), (unsigned)a.row_splits), block, smem, stream, tmQ, tmK, a);
     if (e != cudaSuccess || a.few_rows || a.row_splits == 1) return e;
     const int64_t wrows = (int64_t)a.num_seqs * a.num_kv_heads;
@@ -713,7 +865,14 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     } else {
         w.row_splits = pieces((int64_t)num_seqs * num_kv_heads * up(k_tiles, NA), q_tiles, 8);
     }
-    w.stats_bytes = ((size_t)w.key_splits * total_q * num_heads * sizeof(float2) + 255) / 256 * 256;
+    // partial statistics (several key splits, or few rows: pass 2 joins them
+    // itself), and the statistics by query tile that pass 2 streams
+    auto round = [](size_t b) { return (b + 255) / 256 * 256; };
+    if (w.few_rows || w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
+    if (!w.few_rows) {
+        w.stat_tiles = total_q / TT + num_seqs + 1;
+        w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
+    }
     w.partial_bytes = !w.few_rows && w.row_splits > 1
                           ? (size_t)w.row_splits * std::min(num_seqs, kWeightMaxSeqsPerLaunch) * num_kv_heads *
                                 max_context * sizeof(float)
