@@ -601,7 +601,8 @@ PA_API pa_status pa_prompt_weights_fp8(float* weights, int64_t weights_stride, c
  *                 that share a block are given other destination blocks
  *   k_scales, v_scales: the scale pools of a quantized cache (dtype
  *                 PA_FP8_E4M3), which move with the codes; NULL otherwise
- *   keep >= 1; num_sink, num_recent >= 0; num_sink + num_recent <= keep
+ *   keep >= 1; num_sink, num_recent >= 0; num_sink + num_recent <= keep;
+ *   max_context <= 2^19
  *   workspace:    pa_evict_workspace_size(...) bytes, 16-byte aligned
  * Rows are moved bit for bit.
  */

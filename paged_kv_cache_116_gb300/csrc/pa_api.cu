@@ -1220,6 +1220,7 @@ pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* new_lens
         return fail(PA_ERR_INVALID_ARG, "the pools must be 16-byte aligned");
     if ((int64_t)num_seqs * num_kv_heads > (1 << 24))
         return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_kv_heads must be at most 2^24");
+    if (max_context > pa::kEvictMaxContext) return fail(PA_ERR_UNSUPPORTED, "max_context must be at most 2^19");
     const size_t need = pa::evict_workspace(num_seqs, num_kv_heads, max_context, keep);
     if (workspace_bytes < need || (need && !workspace))
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
@@ -1257,8 +1258,7 @@ pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* new_lens
     a.num_sink = num_sink;
     a.num_recent = num_recent;
     a.row_bytes = (int64_t)head_dim * pa::elt_size(dtype);
-    a.map = static_cast<int32_t*>(workspace);
-    cudaError_t e = pa::launch_evict(a, st);
+    cudaError_t e = pa::launch_evict(a, workspace, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_evict launch");
 }
 

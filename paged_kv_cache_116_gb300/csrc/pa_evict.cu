@@ -19,11 +19,19 @@
 // where its blocks are shared with someone else (every kept row is copied
 // there, into the same places).
 //
-// Two kernels.  evict_select_kernel, one CTA per (sequence, KV head), finds
-// the keep-th largest key by a radix selection of four 8-bit digits over
-// order-preserving integers of the weights, then writes the source index of
-// every destination index.  evict_move_kernel copies the rows, one warp per
-// destination row at a time.
+// Two kernels.
+//   evict_select_kernel, one CTA per (sequence, KV head): the tokens' keys
+//   (order-preserving integers of the weights, the held ones above all) are
+//   read once into shared memory; the keep-th largest is found by a radix
+//   selection of 11, 11 and 10 bits, which ends as soon as a digit's bucket is
+//   taken whole; one walk marks the kept tokens in a bit mask and counts holes
+//   and movers per warp, a second lists the movers by rank, and the threads
+//   then write each destination index's weight and position and list the
+//   rows to copy.
+//   evict_move_kernel copies the listed rows, all of the GPU's warps over all
+//   units' lists.
+// Bound: the select kernel by the latency of its few passes over shared
+// memory, the move kernel by HBM (each listed row is read and written once).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,7 +44,8 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kStageMax = 48 * 1024;  // keys held in shared memory; longer contexts re-read the weights
+constexpr int kBins = 2048;
 
 // Position of cached token j: recorded by an earlier eviction, or (appended
 // since) counted back from the newest.
@@ -66,110 +75,188 @@ __device__ __forceinline__ EvictUnit evict_unit(const EvictArgs& a, int u) {
     return e;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t sh_prefix;
-    __shared__ int sh_need, sh_cnt[32], sh_cnt2[32];
+// Dynamic shared memory: kept-token mask and holes before each of its words,
+// then (staged) the keys, whose place the movers take.
+size_t select_smem(int32_t max_context) {
+    const size_t words = ((size_t)max_context + 31) / 32;
+    return words * 8 + (max_context <= kStageMax ? (size_t)max_context * 4 : 0);
+}
+
+// NT threads; STAGED: the context fits in shared memory.
+template <int NT, bool STAGED>
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
+    constexpr int NW = NT / 32, PER = kBins / NT;  // warps; buckets per thread
+    extern __shared__ uint32_t dyn[];
+    __shared__ uint32_t hist[kBins];
+    __shared__ int sh_warp[2][NW];
+    __shared__ int sh_digit, sh_left, sh_count, sh_rows;
+    const int words_max = (a.max_context + 31) / 32;
+    uint32_t* mask = dyn;
+    int* holes_before = reinterpret_cast<int*>(dyn + words_max);
+    uint32_t* keys = dyn + 2 * words_max;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const EvictUnit e = evict_unit(a, blockIdx.x);
-    const int L = e.L, keep = a.keep;
-    if (tid == 0 && e.h == 0) a.new_lens[e.s] = min(L, keep);
-    if (L <= keep) return;  // everything stays; the move kernel copies by index
+    const int L = e.L, keep = a.keep, count = min(L, keep);
+    if (tid == 0) {
+        if (e.h == 0) a.new_lens[e.s] = count;
+        sh_rows = 0;
+    }
     const float* w = a.weights + e.row;
     const int32_t* pos = a.positions + e.row;  // read below recorded_lens only
-    int32_t* map = a.map + (int64_t)blockIdx.x * a.map_stride;
+    float* wo = a.weights_out + e.row;
+    int32_t* po = a.positions_out ? a.positions_out + e.row : nullptr;
+    if (L <= keep) {  // everything stays where it is; the move kernel copies by index
+        if (tid == 0 && a.counts) a.counts[blockIdx.x] = -1;
+        for (int i = tid; i < L; i += NT) {
+            if (wo != w) wo[i] = w[i];
+            if (po) po[i] = token_position(a, pos, i, L, e.c, e.seen);
+        }
+        return;
+    }
+    int* movers = STAGED ? reinterpret_cast<int*>(keys) : a.movers + (int64_t)blockIdx.x * a.list_stride;
     auto key = [&](int j) -> uint32_t {
         const int p = token_position(a, pos, j, L, e.c, e.seen);
         if (p < a.num_sink || p >= e.seen - a.num_recent) return 0xffffffffu;
         return weight_key(w[j]);
     };
-    // the keep-th largest key: digit by digit from the top
-    uint32_t prefix = 0, mask = 0;
+    auto key_at = [&](int j) -> uint32_t { return STAGED ? keys[j] : key(j); };
+    for (int b = tid; b < kBins; b += NT) hist[b] = 0;
+    __syncthreads();
+
+    // the keep-th largest key, digit by digit from the top: `prefix` under
+    // `bits`, of whose tokens `need` are taken
+    uint32_t prefix = 0, bits = 0;
     int need = keep;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < L; j += kSelThreads) {
-            const uint32_t k = key(j);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    bool tied = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 1024 : 2048;
+        for (int j = tid; j < L; j += NT) {
+            uint32_t k;
+            if (pass == 0) {
+                k = key(j);
+                if (STAGED) keys[j] = k;
+            } else {
+                k = key_at(j);
+            }
+            if ((k & bits) == prefix) atomicAdd(&hist[(k >> shift) & (width - 1)], 1u);
         }
         __syncthreads();
-        if (tid == 0) {
-            int left = need;
-            int d = 255;
-            while (d > 0 && (int)hist[d] < left) left -= (int)hist[d--];
-            sh_prefix = prefix | ((uint32_t)d << shift);
-            sh_need = left;
+        // buckets from the top: thread t holds PER of them
+        int mine[PER], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            mine[i] = (int)hist[kBins - 1 - (tid * PER + i)];
+            sum += mine[i];
         }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh_warp[0][warp] = incl;
         __syncthreads();
-        prefix = sh_prefix;
-        need = sh_need;
-        mask |= 255u << shift;
+        int before = incl - sum;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) before += i < warp ? sh_warp[0][i] : 0;
+        if (before < need && need <= before + sum) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (before < need && need <= before + mine[i]) {
+                    sh_digit = kBins - 1 - (tid * PER + i);
+                    sh_left = need - before;
+                    sh_count = mine[i];
+                }
+                before += mine[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) hist[kBins - 1 - (tid * PER + i)] = 0;
+        __syncthreads();
+        prefix |= (uint32_t)sh_digit << shift;
+        bits |= (uint32_t)(width - 1) << shift;
+        need = sh_left;
+        tied = sh_count != need;
+        if (!tied) break;  // the whole bucket is taken: lower digits decide nothing
         __syncthreads();
     }
-    // kept: key above the threshold, or equal to it and among its first `need`.
-    // Warps own contiguous index ranges; ranks come from counts per warp.
-    const int per = ((L + 31) / 32 + 31) / 32 * 32;
-    const int lo = min(L, warp * per), hi = min(L, lo + per);
-    int eq = 0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const bool is = j0 + lane < hi && key(j0 + lane) == prefix;
-        eq += __popc(__ballot_sync(0xffffffffu, is));
+
+    // Warps own contiguous runs of mask words.  Kept: above the threshold, or
+    // equal to it and among its first `need`.
+    const int words = (L + 31) / 32, per = (words + NW - 1) / NW;
+    const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
+    int equal = 0;
+    if (tied) {  // (uniform) ranks among equal keys are needed
+        for (int x = w0; x < w1; ++x) {
+            const int j = 32 * x + lane;
+            equal += __popc(__ballot_sync(0xffffffffu, j < L && (key_at(j) & bits) == prefix));
+        }
+        if (lane == 0) sh_warp[0][warp] = equal;
+        __syncthreads();
+        equal = 0;
+        for (int i = 0; i < warp; ++i) equal += sh_warp[0][i];
+        __syncthreads();
     }
-    if (lane == 0) sh_cnt[warp] = eq;
-    __syncthreads();
-    int eq0 = 0;
-    for (int i = 0; i < warp; ++i) eq0 += sh_cnt[i];
-    __syncthreads();
-    // walk: is token j0 + lane kept, given the warp's equal keys before j0
-    auto kept_mask = [&](int j0, int& eqs) -> uint32_t {
-        const uint32_t k = j0 + lane < hi ? key(j0 + lane) : 0u;
-        const uint32_t em = __ballot_sync(0xffffffffu, j0 + lane < hi && k == prefix);
-        const int rank = eqs + __popc(em & ((1u << lane) - 1u));
-        const bool kept = j0 + lane < hi && (k > prefix || (k == prefix && rank < need));
-        eqs += __popc(em);
-        return __ballot_sync(0xffffffffu, kept);
+    auto below = [&](int x) -> uint32_t {  // tokens of word x with index below keep
+        const int n = keep - 32 * x;
+        return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
     };
-    int holes = 0, movers = 0, eqs = eq0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const uint32_t km = kept_mask(j0, eqs);
-        const uint32_t below = j0 + 32 <= keep ? 0xffffffffu : (j0 >= keep ? 0u : (1u << (keep - j0)) - 1u);
-        const uint32_t live = j0 + 32 <= hi ? 0xffffffffu : (1u << (hi - j0)) - 1u;
-        holes += __popc(~km & below & live);
-        movers += __popc(km & ~below);
+    int holes = 0, moved = 0;
+    for (int x = w0; x < w1; ++x) {
+        const int j = 32 * x + lane;
+        const uint32_t k = j < L ? key_at(j) & bits : 0u;
+        const uint32_t same = __ballot_sync(0xffffffffu, j < L && k == prefix);
+        const int rank = equal + __popc(same & ((1u << lane) - 1u));
+        const uint32_t kept = __ballot_sync(0xffffffffu, j < L && (k > prefix || (k == prefix && rank < need)));
+        equal += __popc(same);
+        if (lane == 0) mask[x] = kept;
+        holes += __popc(~kept & below(x));  // (keep <= L: every index below keep is a token)
+        moved += __popc(kept & ~below(x));
     }
     if (lane == 0) {
-        sh_cnt[warp] = holes;
-        sh_cnt2[warp] = movers;
+        sh_warp[0][warp] = holes;
+        sh_warp[1][warp] = moved;
     }
-    __syncthreads();
-    int hole0 = 0, mover0 = 0;
+    __syncthreads();  // the keys are used up as well
+    holes = moved = 0;
     for (int i = 0; i < warp; ++i) {
-        hole0 += sh_cnt[i];
-        mover0 += sh_cnt2[i];
+        holes += sh_warp[0][i];
+        moved += sh_warp[1][i];
     }
-    // destinations of holes and sources of movers, by rank, then joined
-    int32_t* hole_at = map + keep;
-    int32_t* mover_at = map + 2 * keep;
-    eqs = eq0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const uint32_t km = kept_mask(j0, eqs);
-        const uint32_t below = j0 + 32 <= keep ? 0xffffffffu : (j0 >= keep ? 0u : (1u << (keep - j0)) - 1u);
-        const uint32_t live = j0 + 32 <= hi ? 0xffffffffu : (1u << (hi - j0)) - 1u;
-        const uint32_t hm = ~km & below & live, mm = km & ~below, lt = (1u << lane) - 1u;
-        const int j = j0 + lane;
-        if ((hm >> lane) & 1u) hole_at[hole0 + __popc(hm & lt)] = j;
-        else if (j < min(hi, keep)) map[j] = j;
-        if ((mm >> lane) & 1u) mover_at[mover0 + __popc(mm & lt)] = j;
-        hole0 += __popc(hm);
-        mover0 += __popc(mm);
+    __syncwarp();
+    for (int x = w0; x < w1; ++x) {
+        const uint32_t kept = mask[x], late = kept & ~below(x);
+        if (lane == 0) holes_before[x] = holes;
+        if ((late >> lane) & 1u) movers[moved + __popc(late & ((1u << lane) - 1u))] = 32 * x + lane;
+        holes += __popc(~kept & below(x));
+        moved += __popc(late);
     }
     __syncthreads();
-    int total = 0;
-    for (int i = 0; i < 32; ++i) total += sh_cnt[i];
-    for (int i = tid; i < total; i += kSelThreads) map[hole_at[i]] = mover_at[i];
+    const int32_t* from_tb = a.block_tables + (int64_t)e.s * a.max_blocks;
+    const int32_t* to_tb = a.new_block_tables + (int64_t)e.s * a.new_max_blocks;
+    int2* list = a.list + (int64_t)blockIdx.x * a.list_stride;
+    for (int i0 = 32 * warp; i0 < keep; i0 += NT) {
+        const int i = i0 + lane;
+        bool copy = false;
+        int src = i;
+        if (i < keep) {
+            const uint32_t kept = mask[i >> 5];
+            if (!((kept >> lane) & 1u)) src = movers[holes_before[i >> 5] + __popc(~kept & ((1u << lane) - 1u))];
+            if (src != i || wo != w) wo[i] = w[src];
+            if (po) po[i] = token_position(a, pos, src, L, e.c, e.seen);
+            copy = src != i || from_tb[i / a.block_size] != to_tb[i / a.block_size];
+        }
+        const uint32_t c = __ballot_sync(0xffffffffu, copy);
+        int at = 0;
+        if (lane == 0 && c) at = atomicAdd(&sh_rows, __popc(c));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(c & ((1u << lane) - 1u));
+        if (copy) list[at] = make_int2(i, src);  // (in any order: the rows are disjoint)
+    }
+    __syncthreads();
+    if (tid == 0) a.counts[blockIdx.x] = sh_rows;
 }
 
 // VB: bytes per vector of a row.
@@ -180,67 +267,119 @@ template <> struct VecOf<4> { using V = uint32_t; };
 template <> struct VecOf<2> { using V = uint16_t; };
 template <> struct VecOf<1> { using V = uint8_t; };
 
-constexpr int kMoveWarps = 8, kMoveRows = 64;  // destination rows per CTA
+constexpr int kMoveWarps = 4, kMoveRows = 32 * kMoveWarps;  // rows of a unit's list per CTA
+constexpr int kMoveCtas = 152 * 12;
 
+// A warp takes 32 rows: lane r translates row r's slots, then the lanes copy
+// the rows' K and V vectors, U of them in flight each.
 template <int VB>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictArgs a, int chunks) {
+__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictArgs a, int chunks, int64_t jobs) {
     using V = typename VecOf<VB>::V;
+    constexpr int U = 8;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int u = blockIdx.x / chunks, i0 = (blockIdx.x - u * chunks) * kMoveRows;
-    const EvictUnit e = evict_unit(a, u);
-    const int count = min(e.L, a.keep);
-    if (i0 >= count) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bs = a.block_size, Hkv = a.num_kv_heads;
-    const int32_t* map = e.L > a.keep ? a.map + (int64_t)u * a.map_stride : nullptr;
-    const int32_t* from_tb = a.block_tables + (int64_t)e.s * a.max_blocks;
-    const int32_t* to_tb = a.new_block_tables + (int64_t)e.s * a.new_max_blocks;
-    const int64_t rv = a.row_bytes / VB;
-    for (int i = i0 + warp; i < min(count, i0 + kMoveRows); i += kMoveWarps) {
-        const int src = map ? map[i] : i;
-        if (lane == 0) {
-            const float w = a.weights[e.row + src];
-            const int p = token_position(a, a.positions + e.row, src, e.L, e.c, e.seen);
-            a.weights_out[e.row + i] = w;
-            if (a.positions_out) a.positions_out[e.row + i] = p;
+    const uint32_t rv = (uint32_t)(a.row_bytes / VB), per = 2 * rv;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int u = (int)(job / chunks), first = (int)(job - (int64_t)u * chunks) * kMoveRows + 32 * warp;
+        const int s = u / Hkv, h = u - s * Hkv;
+        const int listed = a.counts ? __ldcg(a.counts + u) : -1;
+        const int rows = listed >= 0 ? listed : min(max(0, a.context_lens[s]), a.keep);
+        if (first >= rows) continue;
+        // this lane's row: its slots (equal ones: nothing to copy)
+        int from = 0, to = 0;
+        if (first + lane < rows) {
+            const int2 r = listed >= 0 ? __ldcg(a.list + (int64_t)u * a.list_stride + first + lane)
+                                       : make_int2(first + lane, first + lane);
+            from = a.block_tables[(int64_t)s * a.max_blocks + r.y / bs] * bs + r.y % bs;
+            to = a.new_block_tables[(int64_t)s * a.new_max_blocks + r.x / bs] * bs + r.x % bs;
         }
-        const int64_t fb = from_tb[src / bs], tb = to_tb[i / bs];
-        if (src == i && fb == tb) continue;
-        const int64_t fo = ((fb * bs + src % bs) * Hkv + e.h) * rv, to = ((tb * bs + i % bs) * Hkv + e.h) * rv;
-        for (int x = lane; x < rv; x += 32) {
-            const V kv = static_cast<const V*>(a.k_cache)[fo + x], vv = static_cast<const V*>(a.v_cache)[fo + x];
-            static_cast<V*>(a.k_cache)[to + x] = kv;
-            static_cast<V*>(a.v_cache)[to + x] = vv;
+        if (!__any_sync(0xffffffffu, from != to)) continue;
+        if (a.k_scales && from != to) {
+            const int64_t f = ((int64_t)(from / bs) * Hkv + h) * bs + from % bs, d = ((int64_t)(to / bs) * Hkv + h) * bs + to % bs;
+            a.k_scales[d] = a.k_scales[f];
+            a.v_scales[d] = a.v_scales[f];
         }
-        if (a.k_scales && lane < 2) {
-            float* sc = lane ? a.v_scales : a.k_scales;
-            sc[(tb * Hkv + e.h) * bs + i % bs] = sc[(fb * Hkv + e.h) * bs + src % bs];
+        const uint32_t n = min(32, rows - first) * per;
+        const V* k = static_cast<const V*>(a.k_cache);
+        const V* v = static_cast<const V*>(a.v_cache);
+        for (uint32_t e0 = 0; e0 < n; e0 += 32 * U) {
+            V x[U];
+            int64_t dst[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const uint32_t it = e0 + 32 * i + lane, r = min(it / per, 31u), c = it - r * per;
+                const int f = __shfl_sync(0xffffffffu, from, r), d = __shfl_sync(0xffffffffu, to, r);
+                const uint32_t col = c < rv ? c : c - rv;
+                dst[i] = it < n && f != d ? (((int64_t)d * Hkv + h) * rv + col) * 2 + (c < rv ? 0 : 1) : -1;
+                if (dst[i] >= 0) x[i] = (c < rv ? k : v)[((int64_t)f * Hkv + h) * rv + col];
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (dst[i] >= 0) static_cast<V*>(dst[i] & 1 ? a.v_cache : a.k_cache)[dst[i] >> 1] = x[i];
         }
     }
+}
+
+// Workspace: rows listed per unit, the lists, and (contexts beyond shared
+// memory) the movers.  Nothing where no sequence can exceed the budget.
+struct EvictSpace {
+    size_t counts = 0, list = 0, movers = 0;
+};
+EvictSpace evict_space(int64_t units, int32_t max_context, int32_t keep) {
+    EvictSpace w;
+    if (max_context <= keep) return w;
+    auto round = [](size_t b) { return (b + 255) / 256 * 256; };
+    w.counts = round((size_t)units * sizeof(int32_t));
+    w.list = round((size_t)units * keep * sizeof(int2));
+    if (max_context > kStageMax) w.movers = (size_t)units * keep * sizeof(int32_t);
+    return w;
+}
+
+template <int NT, bool STAGED>
+cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream) {
+    const size_t smem = select_smem(a.max_context);
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<NT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_smem(evict_select_kernel<NT, STAGED>, dim3((unsigned)units), dim3(NT), smem, stream, a);
 }
 
 }  // namespace
 
 size_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep) {
-    if (max_context <= keep) return 0;
-    return (size_t)num_seqs * num_kv_heads * 3 * keep * sizeof(int32_t);
+    const EvictSpace w = evict_space((int64_t)num_seqs * num_kv_heads, max_context, keep);
+    return w.counts + w.list + w.movers;
 }
 
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
+cudaError_t launch_evict(const EvictArgs& a, void* workspace, cudaStream_t stream) {
     const int64_t units = (int64_t)a.num_seqs * a.num_kv_heads;
+    const EvictSpace w = evict_space(units, a.max_context, a.keep);
     EvictArgs p = a;
-    p.map_stride = 3 * (int64_t)a.keep;
-    cudaError_t e = launch_pdl(evict_select_kernel, dim3((unsigned)units), dim3(kSelThreads), stream, p);
+    p.list_stride = a.keep;
+    if (w.list) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.counts = reinterpret_cast<int32_t*>(ws);
+        p.list = reinterpret_cast<int2*>(ws + w.counts);
+        p.movers = reinterpret_cast<int32_t*>(ws + w.counts + w.list);
+    }
+    // short contexts: several small CTAs per SM; long ones: a CTA of 1,024
+    // threads holds an SM's shared memory anyway
+    cudaError_t e = a.max_context > kStageMax ? launch_select<1024, false>(p, units, stream)
+                    : a.max_context > 8192    ? launch_select<1024, true>(p, units, stream)
+                    : a.max_context > 2048    ? launch_select<512, true>(p, units, stream)
+                                              : launch_select<256, true>(p, units, stream);
     if (e != cudaSuccess) return e;
     const int rows = std::min(a.keep, a.max_context);
     const int chunks = std::max(1, (rows + kMoveRows - 1) / kMoveRows);
-    const dim3 grid((unsigned)(units * chunks)), block(kMoveWarps * 32);
+    const int64_t jobs = units * chunks;
+    const dim3 grid((unsigned)std::min<int64_t>(jobs, kMoveCtas)), block(32 * kMoveWarps);
     const int64_t rb = a.row_bytes;
-    if (rb % 16 == 0) return launch_pdl(evict_move_kernel<16>, grid, block, stream, p, chunks);
-    if (rb % 8 == 0) return launch_pdl(evict_move_kernel<8>, grid, block, stream, p, chunks);
-    if (rb % 4 == 0) return launch_pdl(evict_move_kernel<4>, grid, block, stream, p, chunks);
-    if (rb % 2 == 0) return launch_pdl(evict_move_kernel<2>, grid, block, stream, p, chunks);
-    return launch_pdl(evict_move_kernel<1>, grid, block, stream, p, chunks);
+    if (rb % 16 == 0) return launch_pdl(evict_move_kernel<16>, grid, block, stream, p, chunks, jobs);
+    if (rb % 8 == 0) return launch_pdl(evict_move_kernel<8>, grid, block, stream, p, chunks, jobs);
+    if (rb % 4 == 0) return launch_pdl(evict_move_kernel<4>, grid, block, stream, p, chunks, jobs);
+    if (rb % 2 == 0) return launch_pdl(evict_move_kernel<2>, grid, block, stream, p, chunks, jobs);
+    return launch_pdl(evict_move_kernel<1>, grid, block, stream, p, chunks, jobs);
 }
 
 }  // namespace pa

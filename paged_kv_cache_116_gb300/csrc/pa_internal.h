@@ -253,11 +253,17 @@ struct EvictArgs {
     int32_t num_sink;
     int32_t num_recent;
     int64_t row_bytes;  // of one head's K (or V) row
-    int32_t* map;       // workspace
-    int64_t map_stride = 0;
+    // workspace (set by the launcher): rows to copy per (sequence, KV head),
+    // -1 for all by index; (destination, source) indexes; movers by rank
+    int32_t* counts = nullptr;
+    int2* list = nullptr;
+    int32_t* movers = nullptr;
+    int64_t list_stride = 0;
 };
+// Longest context (the select kernel's bit mask lives in shared memory).
+constexpr int32_t kEvictMaxContext = 1 << 19;
 size_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep);
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, void* workspace, cudaStream_t stream);
 
 // SMs of the current device.
 int sm_count();

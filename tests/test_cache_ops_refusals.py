@@ -116,7 +116,7 @@ def _evict(lib, **kw):
     (dict(pos=P(48), rec=P(32)), INVALID), (dict(seen=P(32)), INVALID), (dict(ks=ONE, vs=ONE), INVALID),
     (dict(dt=FP8), INVALID), (dict(dt=FP8, ks=ONE), INVALID), (dict(dt=9), INVALID), (dict(kc=P(24)), INVALID),
     (dict(wsb=8), WORKSPACE), (dict(ws=None), WORKSPACE), (dict(ws=P(24)), INVALID), (dict(hkv=0), INVALID),
-    (dict(mc=-1), INVALID), (dict(S=1 << 24), UNSUPPORTED)])
+    (dict(mc=-1), INVALID), (dict(S=1 << 24), UNSUPPORTED), (dict(mc=(1 << 19) + 1, stride=1 << 20), UNSUPPORTED)])
 def test_evict_refuses(lib, kw, status):
     assert _evict(lib, **kw) == status, lib.pa_last_error()
 

@@ -103,6 +103,9 @@ CASES = [
     ([33, 40], 2, 5, 16, "bf16", False, 17, 0, 5, "spread"),       # 10-byte rows
     ([600, 90, 91], 8, 128, 16, "bf16", True, 90, 2, 30, "ties"),
     ([64, 65], 3, 33, 8, "bf16", True, 40, 0, 0, "spread"),        # 33-byte rows of codes
+    ([20000, 9000], 1, 8, 32, "bf16", False, 3000, 4, 200, "ties"),
+    ([60000, 100], 1, 8, 64, "f16", False, 5000, 4, 200, "ties"),   # past the keys that shared memory holds
+    ([60000], 1, 8, 64, "f16", False, 50000, 0, 1000, "special"),
 ]
 
 
