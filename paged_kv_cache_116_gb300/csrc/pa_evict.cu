@@ -24,10 +24,9 @@
 //   (order-preserving integers of the weights, the held ones above all) are
 //   read once into shared memory; the keep-th largest is found by a radix
 //   selection of 11, 11 and 10 bits, which ends as soon as a digit's bucket is
-//   taken whole; one walk marks the kept tokens in a bit mask and counts holes
-//   and movers per warp, a second lists the movers by rank, and the threads
-//   then write each destination index's weight and position and list the
-//   rows to copy.
+//   taken whole; the kept tokens are marked in a bit mask, holes and movers are
+//   ranked by a prefix over its words, and the threads then write each
+//   destination index's weight and position and list the rows to copy.
 //   evict_move_kernel copies the listed rows, all of the GPU's warps over all
 //   units' lists.
 // Bound: the select kernel by the latency of its few passes over shared
@@ -88,7 +87,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     constexpr int NW = NT / 32, PER = kBins / NT;  // warps; buckets per thread
     extern __shared__ uint32_t dyn[];
     __shared__ uint32_t hist[kBins];
-    __shared__ int sh_warp[2][NW];
+    __shared__ int sh_warp[NW];
+    __shared__ uint64_t sh_both[NW];
     __shared__ int sh_digit, sh_left, sh_count, sh_rows;
     const int words_max = (a.max_context + 31) / 32;
     uint32_t* mask = dyn;
@@ -116,12 +116,12 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         return;
     }
     int* movers = STAGED ? reinterpret_cast<int*>(keys) : a.movers + (int64_t)blockIdx.x * a.list_stride;
-    auto key = [&](int j) -> uint32_t {
-        const int p = token_position(a, pos, j, L, e.c, e.seen);
-        if (p < a.num_sink || p >= e.seen - a.num_recent) return 0xffffffffu;
-        return weight_key(w[j]);
+    auto to_key = [&](int p, float x) -> uint32_t {
+        return p < a.num_sink || p >= e.seen - a.num_recent ? 0xffffffffu : weight_key(x);
     };
-    auto key_at = [&](int j) -> uint32_t { return STAGED ? keys[j] : key(j); };
+    auto key_at = [&](int j) -> uint32_t {
+        return STAGED ? keys[j] : to_key(token_position(a, pos, j, L, e.c, e.seen), w[j]);
+    };
     for (int b = tid; b < kBins; b += NT) hist[b] = 0;
     __syncthreads();
 
@@ -133,15 +133,32 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 1024 : 2048;
-        for (int j = tid; j < L; j += NT) {
-            uint32_t k;
-            if (pass == 0) {
-                k = key(j);
-                if (STAGED) keys[j] = k;
-            } else {
-                k = key_at(j);
+        if (pass == 0) {
+            constexpr int U = 8;  // tokens in flight per thread
+            for (int j0 = tid; j0 < L; j0 += NT * U) {
+                float x[U];
+                int p[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int j = j0 + i * NT;
+                    x[i] = j < L ? w[j] : 0.f;
+                    p[i] = j < L ? token_position(a, pos, j, L, e.c, e.seen) : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int j = j0 + i * NT;
+                    if (j >= L) break;
+                    const uint32_t k = to_key(p[i], x[i]);
+                    if (STAGED) keys[j] = k;
+                    atomicAdd(&hist[k >> shift], 1u);
+                }
             }
-            if ((k & bits) == prefix) atomicAdd(&hist[(k >> shift) & (width - 1)], 1u);
+        } else {
+#pragma unroll 4
+            for (int j = tid; j < L; j += NT) {
+                const uint32_t k = key_at(j);
+                if ((k & bits) == prefix) atomicAdd(&hist[(k >> shift) & (width - 1)], 1u);
+            }
         }
         __syncthreads();
         // buckets from the top: thread t holds PER of them
@@ -157,11 +174,11 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        if (lane == 31) sh_warp[0][warp] = incl;
+        if (lane == 31) sh_warp[warp] = incl;
         __syncthreads();
         int before = incl - sum;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) before += i < warp ? sh_warp[0][i] : 0;
+        for (int i = 0; i < NW; ++i) before += i < warp ? sh_warp[i] : 0;
         if (before < need && need <= before + sum) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -184,76 +201,108 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         __syncthreads();
     }
 
-    // Warps own contiguous runs of mask words.  Kept: above the threshold, or
-    // equal to it and among its first `need`.
-    const int words = (L + 31) / 32, per = (words + NW - 1) / NW;
-    const int w0 = min(words, warp * per), w1 = min(words, w0 + per);
-    int equal = 0;
-    if (tied) {  // (uniform) ranks among equal keys are needed
+    // Kept: above the threshold, or equal to it and among its first `need`.
+    // One bit per token, a warp per mask word.
+    const int words = (L + 31) / 32;
+    if (!tied) {
+#pragma unroll 4
+        for (int x = warp; x < words; x += NW) {
+            const int j = 32 * x + lane;
+            const uint32_t kept = __ballot_sync(0xffffffffu, j < L && (key_at(j) & bits) >= prefix);
+            if (lane == 0) mask[x] = kept;
+        }
+        __syncthreads();
+    } else {  // ranks among equal keys: warps own contiguous runs of words
+        const int per = (words + NW - 1) / NW, w0 = min(words, warp * per), w1 = min(words, w0 + per);
+        int equal = 0;
         for (int x = w0; x < w1; ++x) {
             const int j = 32 * x + lane;
-            equal += __popc(__ballot_sync(0xffffffffu, j < L && (key_at(j) & bits) == prefix));
+            equal += __popc(__ballot_sync(0xffffffffu, j < L && key_at(j) == prefix));
         }
-        if (lane == 0) sh_warp[0][warp] = equal;
+        if (lane == 0) sh_warp[warp] = equal;
         __syncthreads();
         equal = 0;
-        for (int i = 0; i < warp; ++i) equal += sh_warp[0][i];
+        for (int i = 0; i < warp; ++i) equal += sh_warp[i];
+        for (int x = w0; x < w1; ++x) {
+            const int j = 32 * x + lane;
+            const uint32_t k = j < L ? key_at(j) : 0u;
+            const uint32_t same = __ballot_sync(0xffffffffu, j < L && k == prefix);
+            const int rank = equal + __popc(same & ((1u << lane) - 1u));
+            const uint32_t kept = __ballot_sync(0xffffffffu, j < L && (k > prefix || (k == prefix && rank < need)));
+            equal += __popc(same);
+            if (lane == 0) mask[x] = kept;
+        }
         __syncthreads();
     }
-    auto below = [&](int x) -> uint32_t {  // tokens of word x with index below keep
+    // Holes below `keep` and movers from there on, ranked: a thread per run of
+    // words, a block-wide prefix of both counts (fields of 32 bits).
+    auto below = [&](int x) -> uint32_t {  // tokens of word x with index below keep (each is a token: keep < L)
         const int n = keep - 32 * x;
         return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
     };
-    int holes = 0, moved = 0;
-    for (int x = w0; x < w1; ++x) {
-        const int j = 32 * x + lane;
-        const uint32_t k = j < L ? key_at(j) & bits : 0u;
-        const uint32_t same = __ballot_sync(0xffffffffu, j < L && k == prefix);
-        const int rank = equal + __popc(same & ((1u << lane) - 1u));
-        const uint32_t kept = __ballot_sync(0xffffffffu, j < L && (k > prefix || (k == prefix && rank < need)));
-        equal += __popc(same);
-        if (lane == 0) mask[x] = kept;
-        holes += __popc(~kept & below(x));  // (keep <= L: every index below keep is a token)
-        moved += __popc(kept & ~below(x));
+    const int run = (words + NT - 1) / NT, x0 = min(words, tid * run), x1 = min(words, x0 + run);
+    uint64_t both = 0;
+    for (int x = x0; x < x1; ++x)
+        both += (uint64_t)__popc(~mask[x] & below(x)) | (uint64_t)__popc(mask[x] & ~below(x)) << 32;
+    uint64_t incl = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
     }
-    if (lane == 0) {
-        sh_warp[0][warp] = holes;
-        sh_warp[1][warp] = moved;
-    }
-    __syncthreads();  // the keys are used up as well
-    holes = moved = 0;
-    for (int i = 0; i < warp; ++i) {
-        holes += sh_warp[0][i];
-        moved += sh_warp[1][i];
-    }
-    __syncwarp();
-    for (int x = w0; x < w1; ++x) {
-        const uint32_t kept = mask[x], late = kept & ~below(x);
-        if (lane == 0) holes_before[x] = holes;
-        if ((late >> lane) & 1u) movers[moved + __popc(late & ((1u << lane) - 1u))] = 32 * x + lane;
-        holes += __popc(~kept & below(x));
-        moved += __popc(late);
+    if (lane == 31) sh_both[warp] = incl;
+    __syncthreads();
+    both = incl - both;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) both += i < warp ? sh_both[i] : 0;
+    int holes = (int)(uint32_t)both, moved = (int)(both >> 32);
+    for (int x = x0; x < x1; ++x) {
+        holes_before[x] = holes;
+        holes += __popc(~mask[x] & below(x));
+        for (uint32_t late = mask[x] & ~below(x); late; late &= late - 1) movers[moved++] = 32 * x + __ffs(late) - 1;
     }
     __syncthreads();
     const int32_t* from_tb = a.block_tables + (int64_t)e.s * a.max_blocks;
     const int32_t* to_tb = a.new_block_tables + (int64_t)e.s * a.new_max_blocks;
+    const int bs = a.block_size, sh = (bs & (bs - 1)) == 0 ? 31 - __clz(bs) : -1;
+    auto block_of = [&](int x) { return sh >= 0 ? x >> sh : x / bs; };
     int2* list = a.list + (int64_t)blockIdx.x * a.list_stride;
-    for (int i0 = 32 * warp; i0 < keep; i0 += NT) {
-        const int i = i0 + lane;
-        bool copy = false;
-        int src = i;
-        if (i < keep) {
+    constexpr int U = 4;  // destinations in flight per thread
+    for (int i0 = 32 * warp; i0 < keep; i0 += NT * U) {
+        int src[U], p[U], fb[U], tb[U];
+        int2 off[U];
+        float x[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * NT + lane;
+            src[q] = -1;
+            fb[q] = tb[q] = 0;
+            if (i >= keep) continue;
             const uint32_t kept = mask[i >> 5];
-            if (!((kept >> lane) & 1u)) src = movers[holes_before[i >> 5] + __popc(~kept & ((1u << lane) - 1u))];
-            if (src != i || wo != w) wo[i] = w[src];
-            if (po) po[i] = token_position(a, pos, src, L, e.c, e.seen);
-            copy = src != i || from_tb[i / a.block_size] != to_tb[i / a.block_size];
+            src[q] = (kept >> lane) & 1u ? i : movers[holes_before[i >> 5] + __popc(~kept & ((1u << lane) - 1u))];
+            x[q] = w[src[q]];
+            p[q] = token_position(a, pos, src[q], L, e.c, e.seen);
+            const int bf = block_of(src[q]), bt = block_of(i);
+            fb[q] = from_tb[bf];
+            tb[q] = to_tb[bt];
+            off[q] = make_int2(src[q] - bf * bs, i - bt * bs);
         }
-        const uint32_t c = __ballot_sync(0xffffffffu, copy);
-        int at = 0;
-        if (lane == 0 && c) at = atomicAdd(&sh_rows, __popc(c));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(c & ((1u << lane) - 1u));
-        if (copy) list[at] = make_int2(i, src);  // (in any order: the rows are disjoint)
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * NT + lane;
+            if (i0 + q * NT >= keep) break;  // (uniform for the warp)
+            if (src[q] >= 0) {
+                wo[i] = x[q];
+                if (po) po[i] = p[q];
+            }
+            const bool copy = src[q] >= 0 && (src[q] != i || fb[q] != tb[q]);
+            const uint32_t c = __ballot_sync(0xffffffffu, copy);
+            int at = 0;
+            if (lane == 0 && c) at = atomicAdd(&sh_rows, __popc(c));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(c & ((1u << lane) - 1u));
+            if (copy)  // source and destination slots (in any order: the rows are disjoint)
+                list[at] = make_int2(fb[q] * bs + off[q].x, tb[q] * bs + off[q].y);
+        }
     }
     __syncthreads();
     if (tid == 0) a.counts[blockIdx.x] = sh_rows;
@@ -267,40 +316,54 @@ template <> struct VecOf<4> { using V = uint32_t; };
 template <> struct VecOf<2> { using V = uint16_t; };
 template <> struct VecOf<1> { using V = uint8_t; };
 
-constexpr int kMoveWarps = 4, kMoveRows = 32 * kMoveWarps;  // rows of a unit's list per CTA
-constexpr int kMoveCtas = 152 * 12;
+constexpr int kWarpRows = 8, kMoveWarps = 4;
+constexpr int kMoveCtas = 152 * 16;  // wanted over all units
 
-// A warp takes 32 rows: lane r translates row r's slots, then the lanes copy
-// the rows' K and V vectors, U of them in flight each.
+// Each unit has `ctas` CTAs, whose warps take eight rows of its list in turn
+// (few enough that a short list spreads, and nobody visits what no list
+// holds); a warp's lanes copy the rows' K and V vectors, U of them in flight each.
 template <int VB>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictArgs a, int chunks, int64_t jobs) {
+__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictArgs a, int ctas) {
     using V = typename VecOf<VB>::V;
     constexpr int U = 8;
     pdl_wait_primary();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bs = a.block_size, Hkv = a.num_kv_heads;
     const uint32_t rv = (uint32_t)(a.row_bytes / VB), per = 2 * rv;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int u = (int)(job / chunks), first = (int)(job - (int64_t)u * chunks) * kMoveRows + 32 * warp;
-        const int s = u / Hkv, h = u - s * Hkv;
-        const int listed = a.counts ? __ldcg(a.counts + u) : -1;
-        const int rows = listed >= 0 ? listed : min(max(0, a.context_lens[s]), a.keep);
-        if (first >= rows) continue;
-        // this lane's row: its slots (equal ones: nothing to copy)
-        int from = 0, to = 0;
-        if (first + lane < rows) {
-            const int2 r = listed >= 0 ? __ldcg(a.list + (int64_t)u * a.list_stride + first + lane)
-                                       : make_int2(first + lane, first + lane);
-            from = a.block_tables[(int64_t)s * a.max_blocks + r.y / bs] * bs + r.y % bs;
-            to = a.new_block_tables[(int64_t)s * a.new_max_blocks + r.x / bs] * bs + r.x % bs;
+    const int u = blockIdx.x / ctas, s = u / Hkv, h = u - s * Hkv;
+    int first = ((blockIdx.x - u * ctas) * kMoveWarps + warp) * kWarpRows;
+    // the unit's rows: those listed, or (-1) all of them by index; the first
+    // list entries are read together with the count, not after it
+    auto listed_row = [&](int r) {
+        return a.counts && lane < kWarpRows && r < a.keep ? __ldcg(a.list + (int64_t)u * a.list_stride + r)
+                                                          : make_int2(0, 0);
+    };
+    int2 entry = listed_row(first + lane);
+    const int listed = a.counts ? __ldcg(a.counts + u) : -1;
+    const int rows = listed >= 0 ? listed : min(max(0, a.context_lens[s]), a.keep);
+    int2 ahead = entry;
+    const int stride = ctas * kMoveWarps * kWarpRows;
+    for (; first < rows; first += stride) {
+        const int r = first + lane;
+        entry = ahead;
+        ahead = listed_row(r + stride);
+        int from = 0, to = 0;  // this lane's row: its slots (equal ones: nothing to copy)
+        if (lane < kWarpRows && r < rows) {
+            if (listed < 0)
+                entry = make_int2(a.block_tables[(int64_t)s * a.max_blocks + r / bs] * bs + r % bs,
+                                  a.new_block_tables[(int64_t)s * a.new_max_blocks + r / bs] * bs + r % bs);
+            from = entry.x;
+            to = entry.y;
         }
         if (!__any_sync(0xffffffffu, from != to)) continue;
-        if (a.k_scales && from != to) {
-            const int64_t f = ((int64_t)(from / bs) * Hkv + h) * bs + from % bs, d = ((int64_t)(to / bs) * Hkv + h) * bs + to % bs;
-            a.k_scales[d] = a.k_scales[f];
-            a.v_scales[d] = a.v_scales[f];
+        const bool scaled = a.k_scales && from != to;
+        float ks = 0.f, vs = 0.f;  // stored after the rows' loads are out
+        if (scaled) {
+            const int64_t f = ((int64_t)(from / bs) * Hkv + h) * bs + from % bs;
+            ks = a.k_scales[f];
+            vs = a.v_scales[f];
         }
-        const uint32_t n = min(32, rows - first) * per;
+        const uint32_t n = min(kWarpRows, rows - first) * per;
         const V* k = static_cast<const V*>(a.k_cache);
         const V* v = static_cast<const V*>(a.v_cache);
         for (uint32_t e0 = 0; e0 < n; e0 += 32 * U) {
@@ -308,8 +371,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
             int64_t dst[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const uint32_t it = e0 + 32 * i + lane, r = min(it / per, 31u), c = it - r * per;
-                const int f = __shfl_sync(0xffffffffu, from, r), d = __shfl_sync(0xffffffffu, to, r);
+                const uint32_t it = e0 + 32 * i + lane, row = min(it / per, 31u), c = it - row * per;
+                const int f = __shfl_sync(0xffffffffu, from, row), d = __shfl_sync(0xffffffffu, to, row);
                 const uint32_t col = c < rv ? c : c - rv;
                 dst[i] = it < n && f != d ? (((int64_t)d * Hkv + h) * rv + col) * 2 + (c < rv ? 0 : 1) : -1;
                 if (dst[i] >= 0) x[i] = (c < rv ? k : v)[((int64_t)f * Hkv + h) * rv + col];
@@ -317,6 +380,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 if (dst[i] >= 0) static_cast<V*>(dst[i] & 1 ? a.v_cache : a.k_cache)[dst[i] >> 1] = x[i];
+        }
+        if (scaled) {
+            const int64_t d = ((int64_t)(to / bs) * Hkv + h) * bs + to % bs;
+            a.k_scales[d] = ks;
+            a.v_scales[d] = vs;
         }
     }
 }
@@ -370,16 +438,16 @@ cudaError_t launch_evict(const EvictArgs& a, void* workspace, cudaStream_t strea
                     : a.max_context > 2048    ? launch_select<512, true>(p, units, stream)
                                               : launch_select<256, true>(p, units, stream);
     if (e != cudaSuccess) return e;
-    const int rows = std::min(a.keep, a.max_context);
-    const int chunks = std::max(1, (rows + kMoveRows - 1) / kMoveRows);
-    const int64_t jobs = units * chunks;
-    const dim3 grid((unsigned)std::min<int64_t>(jobs, kMoveCtas)), block(32 * kMoveWarps);
+    const int rows = std::max(1, std::min(a.keep, a.max_context));
+    const int ctas = (int)std::max<int64_t>(
+        1, std::min<int64_t>(kMoveCtas / units, (rows + kMoveWarps * kWarpRows - 1) / (kMoveWarps * kWarpRows)));
+    const dim3 grid((unsigned)(units * ctas)), block(32 * kMoveWarps);
     const int64_t rb = a.row_bytes;
-    if (rb % 16 == 0) return launch_pdl(evict_move_kernel<16>, grid, block, stream, p, chunks, jobs);
-    if (rb % 8 == 0) return launch_pdl(evict_move_kernel<8>, grid, block, stream, p, chunks, jobs);
-    if (rb % 4 == 0) return launch_pdl(evict_move_kernel<4>, grid, block, stream, p, chunks, jobs);
-    if (rb % 2 == 0) return launch_pdl(evict_move_kernel<2>, grid, block, stream, p, chunks, jobs);
-    return launch_pdl(evict_move_kernel<1>, grid, block, stream, p, chunks, jobs);
+    if (rb % 16 == 0) return launch_pdl(evict_move_kernel<16>, grid, block, stream, p, ctas);
+    if (rb % 8 == 0) return launch_pdl(evict_move_kernel<8>, grid, block, stream, p, ctas);
+    if (rb % 4 == 0) return launch_pdl(evict_move_kernel<4>, grid, block, stream, p, ctas);
+    if (rb % 2 == 0) return launch_pdl(evict_move_kernel<2>, grid, block, stream, p, ctas);
+    return launch_pdl(evict_move_kernel<1>, grid, block, stream, p, ctas);
 }
 
 }  // namespace pa

@@ -254,7 +254,7 @@ struct EvictArgs {
     int32_t num_recent;
     int64_t row_bytes;  // of one head's K (or V) row
     // workspace (set by the launcher): rows to copy per (sequence, KV head),
-    // -1 for all by index; (destination, source) indexes; movers by rank
+    // -1 for all by index; their (source, destination) slots; movers by rank
     int32_t* counts = nullptr;
     int2* list = nullptr;
     int32_t* movers = nullptr;
