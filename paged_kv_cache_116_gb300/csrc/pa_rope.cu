@@ -25,8 +25,7 @@
 // A block takes `tpb` tokens: their sines and cosines go to shared memory
 // once and serve all heads; then every thread works 16-byte vectors, a
 // rotated item being the two vectors that hold both halves of 8 (16-bit) or
-// 4 (fp32) pairs, several items in flight per thread, the first ones fetched
-// while the angles are computed.
+// 4 (fp32) pairs, the same item for all of the block's tokens.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -81,129 +80,168 @@ __device__ __forceinline__ void store_vec(T* p, const RVec<T, VEC>& v) {
     *reinterpret_cast<RVec<T, VEC>*>(p) = v;
 }
 
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const RVec<T, VEC>& v, float (&x)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = Elt<T>::to_f(v.e[e]);
+}
+// Rotates the pairs held in a and b; cs: their cosines and sines.
+template <int VEC>
+__device__ __forceinline__ void rotate(float (&a)[VEC], float (&b)[VEC], const float2* cs, bool interleaved) {
+    if (VEC > 1 && interleaved) {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const float2 c0 = cs[e], c1 = cs[VEC / 2 + e];
+            const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
+            a[2 * e] = x0 * c0.x - y0 * c0.y;
+            a[2 * e + 1] = y0 * c0.x + x0 * c0.y;
+            b[2 * e] = x1 * c1.x - y1 * c1.y;
+            b[2 * e + 1] = y1 * c1.x + x1 * c1.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float2 c = cs[e];
+            const float x = a[e], y = b[e];
+            a[e] = x * c.x - y * c.y;
+            b[e] = y * c.x + x * c.y;
+        }
+    }
+}
+// VEC codes of x / sc, as the quantizing write rounds them.
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* d, const float (&x)[VEC], float sc) {
+    uint32_t w[(VEC + 3) / 4] = {};
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+        w[e / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[e], sc), __NV_SATFINITE, __NV_E4M3) << (8 * (e % 4));
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(d) = w[0];
+    else *d = (uint8_t)w[0];
+}
+
 // VEC: elements per vector (16 bytes, or 1 where sizes or alignment do not
 // allow it).  FP8: k and v rows are quantized into code pools.
+// Four CTAs per SM and two tokens in flight per thread: measured on 8,192
+// tokens of 32 + 8 heads x 128 (bf16) against one to four in flight and two to
+// six CTAs.
 template <typename T, int VEC, bool FP8>
-__global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs p) {
-    constexpr int U = 4;  // items in flight per thread
-    extern __shared__ float2 tab[];  // [tpb][rot / 2] cosine, sine
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeArgs p) {
+    constexpr int U = 2;  // tokens in flight per thread
+    extern __shared__ float2 tab[];  // [tpb][rot / 2] cosine, sine; then the tokens' slots
     pdl_wait_primary();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * p.tpb;
     const int nt = (int)min((int64_t)p.tpb, p.n - t0);
     const int half = p.rot_dim / 2, hd = p.head_dim, Hq = p.num_heads, Hkv = p.num_kv_heads;
-    const int R = half / VEC;                    // rotated items per head
-    const int per = R + (hd - p.rot_dim) / VEC;  // and the vectors passed through
-    const int n_rot = (Hq + (FP8 ? 0 : Hkv)) * per;
-    const int items = n_rot + (FP8 ? 0 : Hkv * (hd / VEC));
-    const int total = nt * items;
-    const T* q = static_cast<const T*>(p.q);
-    const T* k = static_cast<const T*>(p.k);
-    const T* v = static_cast<const T*>(p.v);
+    int64_t* slots = reinterpret_cast<int64_t*>(tab + (size_t)p.tpb * half);
+    for (int i = threadIdx.x; i < nt; i += kRopeThreads) slots[i] = p.slots[t0 + i];
+    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+        const int t = i / half, pr = i - t * half;
+        const int ax = p.pair_axis ? min(max(p.pair_axis[pr], 0), p.num_axes - 1) : 0;
+        const double fr = p.inv_freq[pr];
+        const uint64_t turns = (uint64_t)p.positions[(int64_t)ax * p.n + t0 + t] * turn_fraction(fr);
+        // the nearest 32-bit fraction, as half turns in [-1, 1)
+        const float x = (float)(int32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
+        float s, c;
+        sincospif(x, &s, &c);
+        if (!isfinite(fr)) s = c = __int_as_float(0x7fc00000);
+        tab[i] = make_float2(c, s);
+    }
+    __syncthreads();
 
-    bool ready = false;
-    auto angles = [&]() {
-        for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-            const int t = i / half, pr = i - t * half;
-            const int ax = p.pair_axis ? min(max(p.pair_axis[pr], 0), p.num_axes - 1) : 0;
-            const double fr = p.inv_freq[pr];
-            const uint64_t turns = (uint64_t)p.positions[(int64_t)ax * p.n + t0 + t] * turn_fraction(fr);
-            // the nearest 32-bit fraction, as half turns in [-1, 1)
-            const float x = (float)(int32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
-            float s, c;
-            sincospif(x, &s, &c);
-            if (!isfinite(fr)) s = c = __int_as_float(0x7fc00000);
-            tab[i] = make_float2(c, s);
+    // A token's items, two vectors each: per head of q and k those that hold
+    // both halves of VEC rotary pairs, then the rest of the head two by two;
+    // per head of v all of it two by two.  A thread finds its item once and
+    // works it for all tokens of the CTA.  Code pools: the items of a row are
+    // neighbouring lanes (a power of two of them), which share the row's
+    // maximum; the element-wise form (VEC 1) quantizes below instead.
+    constexpr bool kCodes = FP8 && VEC > 1, kRowsBelow = FP8 && VEC == 1;
+    const int R = half / VEC, per = R + ((hd - p.rot_dim) / VEC + 1) / 2;
+    const int n_rot = (Hq + (kRowsBelow ? 0 : Hkv)) * per, vper = (hd / VEC + 1) / 2;
+    const int items = n_rot + (kRowsBelow ? 0 : Hkv * vper);
+    for (int it = threadIdx.x; it < items; it += kRopeThreads) {
+        const bool is_v = it >= n_rot;
+        int head = is_v ? (it - n_rot) / vper : it / per;
+        const int r = is_v ? it - n_rot - head * vper : it - head * per;
+        const bool is_q = head < Hq && !is_v, turned = !is_v && r < R;
+        if (!is_v && !is_q) head -= Hq;
+        const T* src = static_cast<const T*>(is_v ? p.v : is_q ? p.q : p.k);
+        const int64_t stride = is_v ? p.v_stride : is_q ? p.q_stride : p.k_stride;  // between tokens
+        src += t0 * stride + (int64_t)head * hd;
+        const int64_t row = (int64_t)(is_q ? Hq : Hkv) * hd;  // of the destination
+        const int64_t dst = (is_q ? t0 * row : 0) + (int64_t)head * hd;
+        const int pr = r * VEC;  // the first pair
+        int o0, o1;
+        if (turned) {
+            o0 = p.interleaved ? 2 * pr : pr;
+            o1 = p.interleaved ? o0 + VEC : o0 + half;
+        } else {
+            o0 = is_v ? 2 * r * VEC : p.rot_dim + 2 * (r - R) * VEC;
+            o1 = o0 + VEC < hd ? o0 + VEC : -1;
         }
-        __syncthreads();
-        ready = true;
-    };
-
-    for (int base = 0; base < total; base += kRopeThreads * U) {
-        RVec<T, VEC> a[U], b[U];
-        T* dst[U];
-        int o0[U], o1[U], pr0[U];
+        for (int t = 0; t < nt; t += U) {
+            RVec<T, VEC> a[U], b[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int it = base + u * kRopeThreads + threadIdx.x;
-            dst[u] = nullptr;
-            if (it >= total) continue;
-            const int t = it / items;
-            int r = it - t * items;
-            const int64_t tok = t0 + t;
-            const T* src;
-            int e = -1;  // rotated item within the head, or -1
-            if (r < n_rot) {
-                const int head = r / per;
-                r -= head * per;
-                if (head < Hq) {
-                    src = q + tok * p.q_stride + (int64_t)head * hd;
-                    dst[u] = static_cast<T*>(p.q_out) + (tok * Hq + head) * hd;
-                } else {
-                    const int64_t slot = p.slots[tok];
-                    if (slot < 0) continue;
-                    src = k + tok * p.k_stride + (int64_t)(head - Hq) * hd;
-                    dst[u] = static_cast<T*>(p.k_cache) + (slot * Hkv + head - Hq) * hd;
-                }
-                if (r < R) e = r;
-                o0[u] = p.rot_dim + (r - R) * VEC;
-            } else {
-                const int64_t slot = p.slots[tok];
-                if (slot < 0) continue;
-                r = (r - n_rot) * VEC;  // element of the token's v row
-                src = v + tok * p.v_stride;
-                dst[u] = static_cast<T*>(p.v_cache) + slot * Hkv * hd;
-                o0[u] = r;
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= nt) break;
+                const T* s = src + (t + u) * stride;
+                a[u] = load_vec<T, VEC>(s + o0);
+                if (VEC > 1 || o1 >= 0) b[u] = load_vec<T, VEC>(s + o1);
             }
-            o1[u] = -1;
-            if (e >= 0) {
-                o0[u] = p.interleaved ? 2 * e * VEC : e * VEC;
-                o1[u] = p.interleaved ? o0[u] + VEC : o0[u] + half;
-                pr0[u] = t * half + e * VEC;
-                b[u] = load_vec<T, VEC>(src + o1[u]);
-            }
-            a[u] = load_vec<T, VEC>(src + o0[u]);
-        }
-        if (!ready) angles();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (dst[u] == nullptr) continue;
-            if (o1[u] >= 0) {
-                const float2* cs = tab + pr0[u];
-                if (VEC > 1 && p.interleaved) {
+            for (int u = 0; u < U; ++u) {
+                if (t + u >= nt) break;
+                const int64_t slot = is_q ? t + u : slots[t + u];
+                if (slot < 0) continue;  // a padding token's k or v
+                const float2* cs = tab + (t + u) * half + pr;
+                if (kCodes && !is_q) {
+                    float x[2][VEC];
+                    unpack<T, VEC>(a[u], x[0]);
+                    unpack<T, VEC>(b[u], x[1]);
+                    if (turned) rotate<VEC>(x[0], x[1], cs, p.interleaved);
+                    float amax = 0.f;
 #pragma unroll
-                    for (int e = 0; e < VEC / 2; ++e) {
-                        const float2 c0 = cs[e], c1 = cs[VEC / 2 + e];
-                        const float x0 = Elt<T>::to_f(a[u].e[2 * e]), y0 = Elt<T>::to_f(a[u].e[2 * e + 1]);
-                        const float x1 = Elt<T>::to_f(b[u].e[2 * e]), y1 = Elt<T>::to_f(b[u].e[2 * e + 1]);
-                        a[u].e[2 * e] = Elt<T>::from_f(x0 * c0.x - y0 * c0.y);
-                        a[u].e[2 * e + 1] = Elt<T>::from_f(y0 * c0.x + x0 * c0.y);
-                        b[u].e[2 * e] = Elt<T>::from_f(x1 * c1.x - y1 * c1.y);
-                        b[u].e[2 * e + 1] = Elt<T>::from_f(y1 * c1.x + x1 * c1.y);
+                    for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
+                    const uint32_t lanes = (per == 32 ? 0xffffffffu : (1u << per) - 1u) << (threadIdx.x & 31 & ~(per - 1));
+                    for (int o = 1; o < per; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+                    const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+                    uint8_t* d = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + dst + slot * row;
+                    store_codes<VEC>(d + o0, x[0], sc);
+                    store_codes<VEC>(d + o1, x[1], sc);
+                    if (r == 0) {
+                        const int64_t blk = slot / p.block_size, off = slot - blk * p.block_size;
+                        (is_v ? p.v_scales : p.k_scales)[(blk * Hkv + head) * p.block_size + off] = sc;
                     }
-                } else {
+                    continue;
+                }
+                T* d = static_cast<T*>(is_q ? p.q_out : is_v ? p.v_cache : p.k_cache) + dst + slot * row;
+                if (turned) {
+                    float x[2][VEC];
+                    unpack<T, VEC>(a[u], x[0]);
+                    unpack<T, VEC>(b[u], x[1]);
+                    rotate<VEC>(x[0], x[1], cs, p.interleaved);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        const float2 c = cs[e];
-                        const float x = Elt<T>::to_f(a[u].e[e]), y = Elt<T>::to_f(b[u].e[e]);
-                        a[u].e[e] = Elt<T>::from_f(x * c.x - y * c.y);
-                        b[u].e[e] = Elt<T>::from_f(y * c.x + x * c.y);
+                        a[u].e[e] = Elt<T>::from_f(x[0][e]);
+                        b[u].e[e] = Elt<T>::from_f(x[1][e]);
                     }
                 }
-                store_vec<T, VEC>(dst[u] + o1[u], b[u]);
+                store_vec<T, VEC>(d + o0, a[u]);
+                if (VEC > 1 || o1 >= 0) store_vec<T, VEC>(d + o1, b[u]);
             }
-            store_vec<T, VEC>(dst[u] + o0[u], a[u]);
         }
     }
 
-    if constexpr (FP8) {
-        if (!ready) angles();
+    if constexpr (kRowsBelow) {
+        const T* k = static_cast<const T*>(p.k);
+        const T* v = static_cast<const T*>(p.v);
         // one warp per (token, KV head, K|V) row: lane l holds pairs l, l+32,
         // ... of the rotated part and elements rot + l, ... of the rest
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         for (int row = warp; row < nt * Hkv * 2; row += kRopeThreads / 32) {
             const int is_v = row & 1, h = (row >> 1) % Hkv, t = (row >> 1) / Hkv;
-            const int64_t tok = t0 + t, slot = p.slots[tok];
+            const int64_t tok = t0 + t, slot = slots[t];
             if (slot < 0) continue;
             const T* src = is_v ? v + tok * p.v_stride + (int64_t)h * hd : k + tok * p.k_stride + (int64_t)h * hd;
             const int rot = is_v ? 0 : p.rot_dim, hf = rot / 2;
@@ -259,12 +297,18 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(T);
     const bool al = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
                       reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.q_out)) & 15) == 0;
-    const bool vec = al && a.head_dim % V == 0 && a.rot_dim % (2 * V) == 0 && a.q_stride % V == 0 &&
-                     a.k_stride % V == 0 && a.v_stride % V == 0;
+    const int row_items = a.head_dim / (2 * V);  // code pools: a power of two up to a warp
+    const bool vec = al && a.head_dim % (2 * V) == 0 && a.rot_dim % (2 * V) == 0 && a.q_stride % V == 0 &&
+                     a.k_stride % V == 0 && a.v_stride % V == 0 &&
+                     (!FP8 || ((row_items & (row_items - 1)) == 0 && row_items <= 32));
     RopeArgs p = a;
-    p.tpb = a.n >= 4 * 1216 ? 4 : (a.n >= 2 * 1216 ? 2 : 1);
+// Tokens per CTA: more spread the angles' and the items' setup over more
+    // tokens, as long as every SM keeps its four CTAs (8,192 tokens: 41 us
+    // with 4, 39 with 8, 40 with 16).
+    p.tpb = 8;
+    while (p.tpb > 1 && a.n < (int64_t)p.tpb * 152 * 4) p.tpb /= 2;
     const dim3 grid((unsigned)((a.n + p.tpb - 1) / p.tpb));
-    const size_t smem = (size_t)p.tpb * (a.rot_dim / 2) * sizeof(float2);
+    const size_t smem = (size_t)p.tpb * ((a.rot_dim / 2) * sizeof(float2) + sizeof(int64_t));
     return vec ? launch_pdl_smem(rope_write_kernel<T, V, FP8>, grid, dim3(kRopeThreads), smem, stream, p)
                : launch_pdl_smem(rope_write_kernel<T, 1, FP8>, grid, dim3(kRopeThreads), smem, stream, p);
 }
