@@ -370,11 +370,21 @@ def pa_varlen_fp8(out, q, k_codes, v_codes, k_scales, v_scales, block_tables, se
     return out
 
 
+def _raw(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 def _rope_rows(name, t, heads, hd):
     """Token stride (elements) of q, k or v [n, heads, hd]: heads contiguous, tokens at any stride."""
-    if not t.is_cuda or tuple(t.shape[1:]) != (heads, hd) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != hd):
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if not t.is_cuda or h != heads or d != hd or sd != 1 or (h > 1 and sh != hd):
         raise ValueError("%s must be a CUDA tensor [n, %d, %d] whose heads are contiguous" % (name, heads, hd))
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * hd)
+    return st if n > 1 else max(st, heads * hd)
 
 
 def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd):
@@ -395,8 +405,8 @@ def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv
             raise ValueError("q_out must be [n, heads, head_dim], and q, q_out, k and v of one dtype")
         qs = _rope_rows("q", q, hq, hd)
     ks, vs = _rope_rows("k", k, hkv, hd), _rope_rows("v", v, hkv, hd)
-    return (_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(positions), positions.shape[0], _ptr(inv_freq),
-            _ptr(pair_axis), 2 * inv_freq.numel()), n, hq
+    return (_raw(q_out), _raw(q), _raw(k), _raw(v), qs, ks, vs, _raw(positions), positions.shape[0], _raw(inv_freq),
+            _raw(pair_axis), 2 * inv_freq.numel()), n, hq
 
 
 def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, pair_axis=None,
@@ -410,8 +420,8 @@ def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
     args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
     if k.dtype != k_cache.dtype:
         raise ValueError("k and the cache must be of one dtype")
-    st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
-                                nb, bs, hq, hkv, hd, _dtype(k), _stream(stream))
+    st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_cache), _raw(v_cache),
+                                nb, bs, hq, hkv, hd, _dtype(k), _raw_stream(stream))
     _check(st, "pa_rope_write_kv")
     return q_out
 
@@ -423,9 +433,9 @@ def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_co
     nb, bs, hkv, hd = k_codes.shape
     args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
-    st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _ptr(slot_mapping), n, _ptr(k_codes),
-                                    _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
-                                    _stream(stream))
+    st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_codes),
+                                    _raw(v_codes), _raw(k_scales), _raw(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
+                                    _raw_stream(stream))
     _check(st, "pa_rope_write_kv_fp8")
     return q_out
 
@@ -449,7 +459,7 @@ def _i32(*ts):
 
 
 def _ws(workspace):
-    return _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _raw(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def pa_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype):
@@ -467,9 +477,9 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     nb, bs, hkv, hd = k_cache.shape
     S, hq, _ = q.shape
     stride = _weight_rows("weights", weights, S, hkv)
-    st = lib().pa_decode_weights(_ptr(out), _ptr(weights), stride, _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), S, hq, hkv, hd, nb,
-                                 bs, max_context, float(scale), _dtype(q), *_ws(workspace), _stream(stream))
+    st = lib().pa_decode_weights(_raw(out), _raw(weights), stride, _raw(q), _raw(k_cache), _raw(v_cache),
+                                 _raw(block_tables), block_tables.shape[1], _raw(context_lens), S, hq, hkv, hd, nb,
+                                 bs, max_context, float(scale), _dtype(q), *_ws(workspace), _raw_stream(stream))
     _check(st, "pa_decode_weights")
     return out
 
@@ -489,10 +499,10 @@ def pa_decode_weights_fp8(out, weights, q, k_codes, v_codes, k_scales, v_scales,
     S, hq, _ = q.shape
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     stride = _weight_rows("weights", weights, S, hkv)
-    st = lib().pa_decode_weights_fp8(_ptr(out), _ptr(weights), stride, _ptr(q), _ptr(k_codes), _ptr(v_codes),
-                                     _ptr(k_scales), _ptr(v_scales), _ptr(block_tables), block_tables.shape[1],
-                                     _ptr(context_lens), S, hq, hkv, hd, nb, bs, max_context, float(scale), _dtype(q),
-                                     *_ws(workspace), _stream(stream))
+    st = lib().pa_decode_weights_fp8(_raw(out), _raw(weights), stride, _raw(q), _raw(k_codes), _raw(v_codes),
+                                     _raw(k_scales), _raw(v_scales), _raw(block_tables), block_tables.shape[1],
+                                     _raw(context_lens), S, hq, hkv, hd, nb, bs, max_context, float(scale), _dtype(q),
+                                     *_ws(workspace), _raw_stream(stream))
     _check(st, "pa_decode_weights_fp8")
     return out
 
@@ -514,10 +524,10 @@ def pa_prompt_weights(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q,
     T, hq, _ = q.shape
     S = seq_lens.shape[0]
     stride = _weight_rows("weights", weights, S, hkv)
-    st = lib().pa_prompt_weights(_ptr(weights), stride, _ptr(q), _ptr(k_cache), _ptr(block_tables),
-                                 block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), S, T, max_q, hq, hkv, hd,
+    st = lib().pa_prompt_weights(_raw(weights), stride, _raw(q), _raw(k_cache), _raw(block_tables),
+                                 block_tables.shape[1], _raw(seq_lens), _raw(cu_seqlens_q), S, T, max_q, hq, hkv, hd,
                                  nb, bs, max_context, window, float(scale), 1 if causal else 0, _dtype(q),
-                                 *_ws(workspace), _stream(stream))
+                                 *_ws(workspace), _raw_stream(stream))
     _check(st, "pa_prompt_weights")
     return weights
 
@@ -539,10 +549,10 @@ def pa_prompt_weights_fp8(weights, q, k_codes, k_scales, block_tables, seq_lens,
     S = seq_lens.shape[0]
     _scale_pools(nb, hkv, bs, k_scales)
     stride = _weight_rows("weights", weights, S, hkv)
-    st = lib().pa_prompt_weights_fp8(_ptr(weights), stride, _ptr(q), _ptr(k_codes), _ptr(k_scales),
-                                     _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), _ptr(cu_seqlens_q), S,
+    st = lib().pa_prompt_weights_fp8(_raw(weights), stride, _raw(q), _raw(k_codes), _raw(k_scales),
+                                     _raw(block_tables), block_tables.shape[1], _raw(seq_lens), _raw(cu_seqlens_q), S,
                                      T, max_q, hq, hkv, hd, nb, bs, max_context, window, float(scale),
-                                     1 if causal else 0, _dtype(q), *_ws(workspace), _stream(stream))
+                                     1 if causal else 0, _dtype(q), *_ws(workspace), _raw_stream(stream))
     _check(st, "pa_prompt_weights_fp8")
     return weights
 
@@ -572,10 +582,10 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
             raise ValueError("%s must have the row stride of weights" % name)
     if k_scales is not None:
         _scale_pools(nb, hkv, bs, k_scales, v_scales)
-    st = lib().pa_evict(_ptr(weights_out), _ptr(positions_out), _ptr(new_lens), _ptr(weights), _ptr(positions),
-                        _ptr(recorded_lens), _ptr(seen_lens), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
-                        _ptr(v_scales), _ptr(block_tables), block_tables.shape[1], _ptr(new_block_tables),
-                        new_block_tables.shape[1], _ptr(context_lens), S, hkv, hd, nb, bs, max_context, keep,
-                        num_sink, num_recent, _pool_dtype(k_cache), *_ws(workspace), _stream(stream))
+    st = lib().pa_evict(_raw(weights_out), _raw(positions_out), _raw(new_lens), _raw(weights), _raw(positions),
+                        _raw(recorded_lens), _raw(seen_lens), stride, _raw(k_cache), _raw(v_cache), _raw(k_scales),
+                        _raw(v_scales), _raw(block_tables), block_tables.shape[1], _raw(new_block_tables),
+                        new_block_tables.shape[1], _raw(context_lens), S, hkv, hd, nb, bs, max_context, keep,
+                        num_sink, num_recent, _pool_dtype(k_cache), *_ws(workspace), _raw_stream(stream))
     _check(st, "pa_evict")
     return new_lens

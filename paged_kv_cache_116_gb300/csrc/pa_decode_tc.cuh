@@ -1097,31 +1097,56 @@ __global__ void __launch_bounds__(256) decode_merge_weights_kernel(const TcParam
     extern __shared__ int32_t mprefix[];  // [num_seqs + 1]
     __shared__ float2 ml[16];
     const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
-    tile_prefix(p.context_lens, S, mprefix, nullptr);
     if ((int)blockIdx.x < merge_blocks) {
+        tile_prefix(p.context_lens, S, mprefix, nullptr);
         merge_item<T, HD>(p, TW, mprefix, blockIdx.x);
         return;
     }
-    pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t W = (int64_t)mprefix[S] * Hkv;
-    const int64_t all = (int64_t)S * Hkv * chunks;
-    for (int64_t it = (int64_t)blockIdx.x - merge_blocks; it < all; it += (int64_t)gridDim.x - merge_blocks) {
-        const int64_t u = it / chunks;
+    const uint32_t all = (uint32_t)S * Hkv * chunks;
+    constexpr int K = kWeightChunk / 256;  // tokens per thread
+    bool waited = false;
+    for (uint32_t it = blockIdx.x - merge_blocks; it < all; it += gridDim.x - merge_blocks) {
+        const uint32_t u = it / (uint32_t)chunks, s = u / (uint32_t)Hkv, h = u - s * Hkv;
         const int t0 = (int)(it - u * chunks) * kWeightChunk;
-        const int s = (int)(u / Hkv), h = (int)(u - (int64_t)s * Hkv);
         const int L = p.context_lens[s];
         if (t0 >= L) continue;
+        if (!waited) {  // the lengths are older than the decode grid, its records and scores are not
+            tile_prefix(p.context_lens, S, mprefix, nullptr);
+            pdl_wait_primary();
+            waited = true;
+        } else {
+            __syncthreads();  // ml of the previous chunk is used up
+        }
+        const int64_t W = (int64_t)mprefix[S] * Hkv;
         const int nb = mprefix[s + 1] - mprefix[s];
         const int64_t u0 = (int64_t)mprefix[s] * Hkv + (int64_t)h * nb, u1 = u0 + nb;
-        auto owner = [&](int64_t f) -> int64_t { return ((f + 1) * TW + W - 1) / W - 1; };
-        const int64_t wf = owner(u0), wl = owner(u1 - 1);
-        __syncthreads();  // ml of the previous chunk is used up
-        if (wf == wl) {
-            if (threadIdx.x < G) ml[threadIdx.x] = __ldcg(&p.row_stats[(int64_t)s * p.num_heads + h * G + threadIdx.x]);
-        } else {
+        // the weights and the first four heads' scores are on their way while
+        // the pieces are joined
+        float* row = weights + (int64_t)u * stride;
+        const float* sc = p.scores + u0 * BS * G;
+        const bool quads = (G & 3) == 0;
+        float old[K];
+        float4 x[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int t = t0 + k * 256 + threadIdx.x;
+            old[k] = t < L - 1 ? row[t] : 0.f;
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < L) {
+                if (quads) x[k] = __ldcg(reinterpret_cast<const float4*>(sc + (int64_t)t * G));
+                else x[k].x = __ldcg(sc + (int64_t)t * G);
+            }
+        }
+        if (warp < G) {
+            auto owner = [&](int64_t f) -> int64_t { return ((f + 1) * TW + W - 1) / W - 1; };
+            const int64_t wf = owner(u0), wl = owner(u1 - 1);
             const int slot0 = u0 == wf * W / TW ? 0 : 1;
             for (int j = warp; j < G; j += 8) {
+                if (wf == wl) {  // worked whole by one warp
+                    if (lane == 0) ml[j] = __ldcg(&p.row_stats[(int64_t)s * p.num_heads + h * G + j]);
+                    continue;
+                }
                 float M = -INFINITY, l = 0.f;
                 for (int64_t w0 = wf; w0 <= wl; w0 += 32) {
                     const int64_t w = w0 + lane;
@@ -1141,26 +1166,27 @@ __global__ void __launch_bounds__(256) decode_merge_weights_kernel(const TcParam
             }
         }
         __syncthreads();
-        float* row = weights + u * stride;
-        const float* sc = p.scores + u0 * BS * G;
 #pragma unroll
-        for (int k = 0; k < kWeightChunk / 256; ++k) {
+        for (int k = 0; k < K; ++k) {
             const int t = t0 + k * 256 + threadIdx.x;
             if (t >= L) break;
-            const float* x = sc + (int64_t)t * G;
-            float w = 0.f;
-            if ((G & 3) == 0) {
+            const float* xs = sc + (int64_t)t * G;
+            float w;
+            if (quads) {
+                w = 0.f;
+                float4 v = x[k];
                 for (int j = 0; j < G; j += 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(x + j));
+                    if (j) v = __ldcg(reinterpret_cast<const float4*>(xs + j));
                     w = fmaf(exp2f(v.x - ml[j].x), ml[j].y, w);
                     w = fmaf(exp2f(v.y - ml[j + 1].x), ml[j + 1].y, w);
                     w = fmaf(exp2f(v.z - ml[j + 2].x), ml[j + 2].y, w);
                     w = fmaf(exp2f(v.w - ml[j + 3].x), ml[j + 3].y, w);
                 }
             } else {
-                for (int j = 0; j < G; ++j) w = fmaf(exp2f(__ldcg(x + j) - ml[j].x), ml[j].y, w);
+                w = exp2f(x[k].x - ml[0].x) * ml[0].y;
+                for (int j = 1; j < G; ++j) w = fmaf(exp2f(__ldcg(xs + j) - ml[j].x), ml[j].y, w);
             }
-            row[t] = t < L - 1 ? row[t] + w : w;
+            row[t] = old[k] + w;  // (the newest token starts from 0)
         }
     }
 }

@@ -407,9 +407,11 @@ EvictSpace evict_space(int64_t units, int32_t max_context, int32_t keep) {
 template <int NT, bool STAGED>
 cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream) {
     const size_t smem = select_smem(a.max_context);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<NT, STAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 32 * 1024) {  // (with the static arrays beyond what every kernel may have)
+        cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<NT, STAGED>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl_smem(evict_select_kernel<NT, STAGED>, dim3((unsigned)units), dim3(NT), smem, stream, a);
 }
 
