@@ -1010,9 +1010,10 @@ static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_
 // The prompt form's path (PA_OPT_VARLEN_KERNEL pins it), how its work is cut,
 // and its workspace.
 struct PromptWeightsPlan {
+    static constexpr size_t kCounters = 256;  // ahead of the rest (tensor-core path)
     bool tc = false;
     pa::WeightPlan cut;
-    size_t bytes() const { return cut.stats_bytes + cut.tile_stats_bytes + cut.partial_bytes; }
+    size_t bytes() const { return (tc ? kCounters : 0) + cut.stats_bytes + cut.tile_stats_bytes + cut.partial_bytes; }
 };
 static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
@@ -1065,11 +1066,13 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
                                      num_blocks, block_size, max_context, st);
         if (err != PA_OK) return err;
     }
-    a.stats = static_cast<float2*>(workspace);
-    a.tile_stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut.stats_bytes);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.next_item = reinterpret_cast<uint32_t*>(ws);
+    if (plan.tc) ws += PromptWeightsPlan::kCounters;
+    a.stats = reinterpret_cast<float2*>(ws);
+    a.tile_stats = reinterpret_cast<float*>(ws + plan.cut.stats_bytes);
     a.stat_tiles = plan.cut.stat_tiles;
-    a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cut.stats_bytes +
-                                         plan.cut.tile_stats_bytes);
+    a.partial = reinterpret_cast<float*>(ws + plan.cut.stats_bytes + plan.cut.tile_stats_bytes);
     a.key_splits = plan.cut.key_splits;
     a.row_splits = plan.cut.row_splits;
     a.few_rows = plan.cut.few_rows ? 1 : 0;

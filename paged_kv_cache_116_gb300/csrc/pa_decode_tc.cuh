@@ -1087,8 +1087,8 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, con
 // each thread then reads its tokens' scores (G contiguous floats) and updates
 // one weight per token.  x - M is taken before the division by L: a
 // log-sum-exp rounded to fp32 would cost |lse| 2^-24 in every weight.
-constexpr int kWeightChunk = 1024;
-constexpr int kWeightMaxCtas = 152 * 32;  // beyond this a CTA takes several chunks
+constexpr int kWeightChunk = 2048;
+constexpr int kWeightMaxCtas = 152 * 16;  // beyond this a CTA takes several chunks
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) decode_merge_weights_kernel(const TcParams p, const int64_t TW,

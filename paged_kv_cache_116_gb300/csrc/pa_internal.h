@@ -199,6 +199,7 @@ struct WeightArgs {
     int dtype;
     int kv_fp8;
     float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
+    uint32_t* next_item = nullptr;  // two counters (workspace)
     float* tile_stats = nullptr;
     int stat_tiles = 0;
     float* partial = nullptr;

@@ -61,8 +61,8 @@ __device__ __forceinline__ void work_prefix(const WeightArgs& a, int32_t* prefix
     __syncthreads();
 }
 
-// Work item -> (request, KV head, tile): a request's items are its heads'
-// tiles, head by head.
+// Work item -> (request, KV head, tile): a request's items are its tiles, all
+// heads of a tile before the next (the callers put the long tiles first).
 __device__ __forceinline__ void locate_work(const int32_t* prefix, int S, int Hkv, int64_t item, int& s, int& h,
                                             int& tile) {
     int lo = 0, hi = S - 1;
@@ -71,11 +71,10 @@ __device__ __forceinline__ void locate_work(const int32_t* prefix, int S, int Hk
         if ((int64_t)prefix[mid] * Hkv <= item) lo = mid;
         else hi = mid - 1;
     }
-    const int per = prefix[lo + 1] - prefix[lo];
     const int64_t rem = item - (int64_t)prefix[lo] * Hkv;
     s = lo;
-    h = (int)(rem / per);
-    tile = (int)(rem - (int64_t)h * per);
+    tile = (int)(rem / Hkv);
+    h = (int)(rem - (int64_t)tile * Hkv);
 }
 
 }  // namespace pa

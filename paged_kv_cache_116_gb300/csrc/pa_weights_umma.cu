@@ -26,17 +26,18 @@
 // crossed from L2 at 9.3 TB/s, which bounded the kernel (8,192-token prompt,
 // 32 / 8 heads: 0.93 ms).
 //
-// Where there are few stationary tiles the streamed axis is split over
-// gridDim.y: in pass 1 pass 2 joins the pieces' (maximum, sum) as it reads
-// them, in pass 2 the pieces' partial weights are added by a third kernel.
+// Where there are few stationary tiles the streamed axis is split: pass 1's
+// pieces of (maximum, sum) are joined by a small kernel, pass 2's partial
+// weights added by another.
 //
-// Roles (19 warps up to head_dim 128): four groups of four warps work the
-// accumulator tiles, one row or key per thread; one warp loads tiles by TMA
+// Roles (20 warps up to head_dim 128): four groups of four warps work the
+// accumulator tiles, one row or key per thread; two warps load tiles by TMA
 // (128-byte swizzle; keys through the block table, one 16-token group per
 // box); one warp per stationary tile issues its MMAs (one warp for both left
 // the tensor pipe idle while it waited: 590 of 1,090 cycles per accumulator).
-// Accumulators are (stationary tile x, parity of the streamed tile), 128
-// columns each.  In pass 1 a group owns one of them; in pass 2 it owns half of
+// Accumulators are (stationary tile x, parity of the streamed tile within its
+// item), 128 columns each; the parity decides which group adds what up, so it
+// may not depend on what a CTA worked before.  In pass 1 a group owns one of them; in pass 2 it owns half of
 // the columns of both tiles' accumulators of a parity, so that every column
 // statistic it reads from shared memory serves two keys.  Every wait is
 // bounded; on expiry the CTA sets a status bit, abandons its work, waits
@@ -84,7 +85,6 @@ constexpr int TM = 128;                       // rows of A and columns of B
 constexpr int GRP = 16;                       // keys per TMA box (two boxes of 8 with 8-token blocks)
 constexpr int NGRP = TM / GRP;
 constexpr uint64_t WAIT_NS = 2000000000ull;   // 2 s
-constexpr int kMaxCtas = 1 << 14;             // beyond this a CTA takes several items
 
 template <int HD>
 struct WGeo {
@@ -105,9 +105,12 @@ struct WGeo {
     static constexpr int JOIN_OFF = STAT_OFF + SRING * 2 * TM * 4;  // results handed over, float2[3][128]
     static constexpr int BAR_OFF = JOIN_OFF + 3 * TM * 8;
     // a_full, a_empty, b_full[RING], b_empty[RING], d_full[NWG],
-    // s_full[SRING], d_empty[NWG], s_empty[SRING], g_bar, j_full[3], j_empty[3]
-    static constexpr int NBAR = 2 + 2 * RING + 2 * NWG + 2 * SRING + 7;
-    static constexpr int ADDR_OFF = BAR_OFF + NBAR * 8;
+    // s_full[SRING], i_full[IRING], d_empty[NWG], s_empty[SRING],
+    // i_empty[IRING], g_bar, j_full[3], j_empty[3]
+    static constexpr int IRING = 4;  // work items handed to the CTA's warps
+    static constexpr int NBAR = 2 + 2 * RING + 2 * NWG + 2 * SRING + 2 * IRING + 7;
+    static constexpr int ITEM_OFF = BAR_OFF + NBAR * 8;  // int[IRING]
+    static constexpr int ADDR_OFF = ITEM_OFF + IRING * 4;
     static constexpr int PREF_OFF = ADDR_OFF + 16;
 };
 static_assert(1024 + WGeo<128>::PREF_OFF + (kWeightMaxSeqsPerLaunch + 1) * 4 <= 232448 &&
@@ -122,22 +125,30 @@ struct Item {
     int h;
     int a0, na;  // first stationary tile (query tile, or key tile in pass 2) and how many
     int b0, b1;  // streamed tiles
+    int z;       // piece of the streamed axis
 };
 
 // The statistics of one row (an index into a piece of p.stats), joined over
 // pass 1's key splits: (-M, 1 / l).
 __device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) {
     const int64_t part = (int64_t)p.total_q * p.num_heads;
-    float2 s = __ldcg(p.stats + row);
-    for (int z = 1; z < p.key_splits; ++z) {
-        const float2 o = __ldcg(p.stats + z * part + row);
-        const float mn = fmaxf(s.x, o.x);
-        if (mn == -INFINITY) {  // no key, or none with a number for a score
-            s.y += o.y;
-            continue;
+    constexpr int B = 8;  // pieces in flight
+    float2 s = make_float2(-INFINITY, 0.f);
+    for (int z0 = 0; z0 < p.key_splits; z0 += B) {
+        float2 o[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            o[b] = z0 + b < p.key_splits ? __ldcg(p.stats + (z0 + b) * part + row) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float mn = fmaxf(s.x, o[b].x);
+            if (mn == -INFINITY) {  // no key, or none with a number for a score
+                s.y += o[b].y;
+                continue;
+            }
+            s.y = s.y * exp2f(s.x - mn) + o[b].y * exp2f(o[b].x - mn);
+            s.x = mn;
         }
-        s.y = s.y * exp2f(s.x - mn) + o.y * exp2f(o.x - mn);
-        s.x = mn;
     }
     return make_float2(s.x == -INFINITY ? 0.f : -s.x, 1.f / s.y);
 }
@@ -150,7 +161,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     weights_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const WeightArgs p) {
     using Gm = WGeo<HD>;
-    constexpr int NA = Gm::NA, RING = Gm::RING;
+    constexpr int NA = Gm::NA, RING = Gm::RING, NTH = Gm::NTHREADS;
     constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr bool kKeysStream = PASS != kKeyWeights;
     extern __shared__ uint8_t smem_raw[];
@@ -162,9 +173,12 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     uint64_t* b_empty = b_full + RING;
     uint64_t* d_full = b_empty + RING;
     uint64_t* s_full = d_full + Gm::NWG;
-    uint64_t* d_empty = s_full + Gm::SRING;
+    uint64_t* i_full = s_full + Gm::SRING;
+    uint64_t* d_empty = i_full + Gm::IRING;
     uint64_t* s_empty = d_empty + Gm::NWG;
-    uint64_t* g_bar = s_empty + Gm::SRING;
+    uint64_t* i_empty = s_empty + Gm::SRING;
+    uint64_t* g_bar = i_empty + Gm::IRING;
+    volatile int* item_s = reinterpret_cast<volatile int*>(base + Gm::ITEM_OFF);
     uint64_t* j_full = g_bar + 1;
     uint64_t* j_empty = j_full + 3;
     float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);
@@ -184,11 +198,12 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             const uint64_t* b = bars + i;
             // a_empty, b_empty: one commit per issuing warp; from d_empty on
             // one arrival per warp: of the groups that work the accumulator
-            // or tile, of all groups (g_bar), of one group (j_*)
+            // or tile, of all warps (i_empty), of all groups (g_bar), of one
+            // group (j_*)
             const uint32_t groups =
                 b >= j_full ? 1 : b >= g_bar ? Gm::NWG : b < s_empty && PASS == kRowStats ? 1 : NA;
-            const bool per_mma = b == a_empty || (b >= b_empty && b < d_full);
-            mbar_init(bars + i, b >= d_empty ? 4 * groups : per_mma ? NA : 1u);
+            const bool per_mma = b == a_empty || (b >= b_empty && b < d_full), each_warp = b >= i_empty && b < g_bar;
+            mbar_init(bars + i, each_warp ? NTH / 32 : b >= d_empty ? 4 * groups : per_mma ? NA : 1u);
         }
         mbar_fence_init();
     }
@@ -201,7 +216,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         const int tiles = PASS == kRowStats ? (sq.rows + TT - 1) / TT : sq.rows ? (sq.L + TM - 1) / TM : 0;
         return (tiles + NA - 1) / NA;
     });
-    const int64_t items = (int64_t)prefix[p.num_seqs] * Hkv;
+    // an item is a piece of the streamed axis of a (request, KV head, group of
+    // stationary tiles)
+    const int splits = PASS == kRowStats ? p.key_splits : p.row_splits;
+    const int64_t items = (int64_t)prefix[p.num_seqs] * Hkv * splits;
     if (blockIdx.x >= items) return;  // uniform for the CTA
     if (warp == Gm::W_MMA) {
         tmem_alloc(const_cast<uint32_t*>(taddr_slot), Gm::TMEM_COLS);
@@ -227,7 +245,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     auto item_at = [&](int64_t it) -> Item {
         Item w;
         int s, tile;
-        locate_work(prefix, p.num_seqs, Hkv, it, s, w.h, tile);
+        const int64_t unit = it / splits;
+        w.z = (int)(it - unit * splits);
+        locate_work(prefix, p.num_seqs, Hkv, unit, s, w.h, tile);
         w.sq = weight_seq(p, s);
         const int q_tiles = (w.sq.rows + TT - 1) / TT, k_tiles = (w.sq.L + TM - 1) / TM;
         int n;
@@ -245,8 +265,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             w.b0 = 0;
             n = (max(seen, 0) + TM - 1) / TM;
         }
-        w.b1 = w.b0 + (int)((int64_t)n * (blockIdx.y + 1) / gridDim.y);
-        w.b0 += (int)((int64_t)n * blockIdx.y / gridDim.y);
+        w.b1 = w.b0 + (int)((int64_t)n * (w.z + 1) / splits);
+        w.b0 += (int)((int64_t)n * w.z / splits);
         return w;
     };
     // where query tile t of a request keeps its statistics: distinct for every
@@ -255,6 +275,35 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     auto stat_tile = [&](const WeightSeq& sq, int h, int t) -> int64_t {
         return (int64_t)h * p.stat_tiles + sq.row0 / TT + sq.s + t;
     };
+    // The CTA's items: its own number first, then whatever is next in the grid
+    // (items differ in length; dealt out in advance they left SMs idle).  The
+    // first producer draws them as it gets to them; every warp takes each in
+    // turn (-1: none left, or a wait ran out).
+    int n_item = 0;
+    auto next_item = [&]() -> int {
+        const int k = n_item % Gm::IRING;
+        const uint32_t ph = (uint32_t)(n_item / Gm::IRING) & 1u;
+        if (warp == Gm::W_PROD) {
+            int ok = 0;
+            if (lane == 0 && (ok = mbar_wait_ns(&i_empty[k], ph ^ 1u, WAIT_NS))) {
+                // (drawn only now: an item drawn ahead would wait for this CTA
+                // while others run dry, 0.66 against 0.60 ms on 8,192 tokens)
+                const int64_t it = n_item == 0 ? blockIdx.x : (int64_t)gridDim.x + atomicAdd(p.next_item + (PASS > 1), 1u);
+                item_s[k] = it < items ? (int)it : -1;
+                mbar_arrive(&i_full[k]);
+            }
+            if (!__shfl_sync(0xffffffffu, ok, 0)) return -1;
+        }
+        if (!mbar_wait_ns(&i_full[k], ph, WAIT_NS)) return -1;
+        const int it = item_s[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[k]);
+        ++n_item;
+        return it;
+    };
+    // (in pass 2 a group works both stationary tiles' accumulators of a parity;
+    // a lone tile, which only the last keys of a request are, keeps to the first)
+    constexpr bool spread_alone = PASS != kKeyWeights;
     auto fail = [&]() { atomicOr(&g_weights_status, kStatusTimeout); };
 
     if (warp >= Gm::W_PROD && warp < Gm::W_MMA) {
@@ -305,7 +354,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
+        for (int it; run && (it = next_item()) >= 0;) {
             const Item w = item_at(it);
             if (w.b0 >= w.b1) continue;
             const int mine = w.b0 + (nb + me) % Gm::NPROD;  // this warp's first tile of the item
@@ -359,18 +408,20 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         // ---------------- MMA issuer of stationary tile x
         const uint32_t x = lane0(warp - Gm::W_MMA);
         const uint32_t idesc = umma_idesc_f16(TM, TM, kBF16, false);
-        const uint32_t s_lo = lane0(smem_u32(base) >> 4 | 1u << 16), a_lo = s_lo + x * (Gm::TILE / 16);
+        const uint32_t s_lo = lane0(smem_u32(base) >> 4 | 1u << 16);
         const uint32_t d_x = lane0(tmem) + x * 2 * TM;
         int na = 0, nb = 0, nd[2] = {0, 0}, last = -1;  // items, streamed tiles, accumulators of each parity
         bool run = true;
-        for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
+        for (int it; run && (it = next_item()) >= 0;) {
             const Item w = item_at(it);
             if (w.b0 >= w.b1) continue;
             if (!(run = mbar_wait_ns(a_full, (uint32_t)na & 1u, WAIT_NS))) break;
             ++na;
-            const bool mine = (int)x < w.na;
+            const bool alone = NA == 2 && w.na == 1;  // one stationary tile: its tiles take all four accumulators in turn
+            const uint32_t a_lo = lane0(s_lo + (alone ? 0 : x) * (Gm::TILE / 16));
             for (int t = w.b0; t < w.b1; ++t, ++nb) {
-                const int slot = nb % RING, par = nb & 1, turn = par ? nd[1] : nd[0];
+                const int slot = nb % RING, par = (t - w.b0) & 1, turn = par ? nd[1] : nd[0];
+                const bool mine = alone ? spread_alone && ((t - w.b0) >> 1 & 1) == (int)x || !spread_alone && x == 0 : true;
                 run = mbar_wait_ns(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
                       (!mine || mbar_wait_ns(&d_empty[2 * x + par], ((uint32_t)turn & 1u) ^ 1u, WAIT_NS));
                 if (!__all_sync(0xffffffffu, run)) {
@@ -415,7 +466,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + par * TM;  // + 2 TM x
         const float sl = p.scale_log2;
         const int64_t part = (int64_t)p.total_q * p.num_heads;  // rows of one split's statistics
-        int nx = 0, n_meet = 0, n_join = 0;  // streamed tiles; barriers gone through
+        int nx = 0, n_meet = 0;              // streamed tiles; barriers gone through
+        int n_join[3] = {0, 0, 0};           // handovers through each buffer
         int n_d[2] = {0, 0};                 // accumulators of x worked by this group
         bool run = true;
         auto release = [&](int x) {
@@ -428,16 +480,17 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             tc_fence_after();
             return ok;
         };
-        // a giving group hands its values to the receiving one through buffer j
+        // a giving group hands its values to the receiving one through buffer j;
+        // the turns of each buffer are counted by all groups
         auto give = [&](int j, float2 v) -> bool {
-            if (!mbar_wait_ns(&j_empty[j], ((uint32_t)n_join++ & 1u) ^ 1u, WAIT_NS)) return false;
+            if (!mbar_wait_ns(&j_empty[j], ((uint32_t)n_join[j] & 1u) ^ 1u, WAIT_NS)) return false;
             join_s[j * TM + m] = v;
             __syncwarp();
             if (lane == 0) mbar_arrive(&j_full[j]);
             return true;
         };
-        auto take = [&](int j, uint32_t turn, float2& v) -> bool {
-            if (!mbar_wait_ns(&j_full[j], turn & 1u, WAIT_NS)) return false;
+        auto take = [&](int j, float2& v) -> bool {
+            if (!mbar_wait_ns(&j_full[j], (uint32_t)n_join[j] & 1u, WAIT_NS)) return false;
             v = join_s[j * TM + m];
             __syncwarp();
             if (lane == 0) mbar_arrive(&j_empty[j]);
@@ -448,12 +501,6 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(g_bar);
             return mbar_wait_ns(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
-        };
-        // statistics of query tile t's row r, joined over pass 1's splits: (-M, 1 / l)
-        auto row_stat = [&](const Item& w, int t, int r) -> float2 {
-            const int tok = t * TT + r / G;
-            if (r >= TT * G || tok >= w.sq.rows) return make_float2(0.f, 0.f);
-            return joined_stat(p, (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + r % G);
         };
         // exp2(x - M) / l of `n` accumulators' columns [q, q + 16) for this
         // thread's keys, added to v[]: column c counts where lo[] <= c < end
@@ -487,28 +534,27 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         auto store_weight = [&](const Item& w, int key, float v) {
             if (key >= w.sq.L) return;
             const int64_t row = (int64_t)w.sq.s * Hkv + w.h;
-            if (PASS == kKeyWeights && gridDim.y > 1) {
-                p.partial[((int64_t)blockIdx.y * p.num_seqs * Hkv + row) * p.max_context + key] = v;
+            if (PASS == kKeyWeights && splits > 1) {
+                p.partial[((int64_t)w.z * p.num_seqs * Hkv + row) * p.max_context + key] = v;
             } else {
                 float* dst = p.weights + row * p.weights_stride + key;
                 *dst = key < w.sq.L - w.sq.n ? *dst + v : v;
             }
         };
-        for (int64_t it = blockIdx.x; it < items && run; it += gridDim.x) {
+        for (int it; run && (it = next_item()) >= 0;) {
             const Item w = item_at(it);
             if constexpr (PASS == kRowStats) {
-                if (hi >= w.na) {
-                    nx += w.b1 - w.b0;
-                    continue;
-                }
-                const int x = hi;
+                // a lone stationary tile is worked by all groups, every fourth
+                // streamed tile each; else group hi, par works tile hi's
+                const bool alone = NA == 2 && w.na == 1;
+                const int x = alone ? 0 : hi;
                 const int tok = (w.a0 + x) * TT + m / G, g = m % G;
                 const bool valid = m < TT * G && tok < w.sq.rows;
                 const int last = p.causal ? w.sq.L - w.sq.rows + tok : w.sq.L - 1;  // last key the row sees
                 float m_used = -INFINITY, l = 0.f;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
-                    if ((nx & 1) != par) continue;
-                    if (!(run = acquire(x))) break;
+                    if (((t - w.b0) & 1) != par || (alone && ((t - w.b0) >> 1 & 1) != hi)) continue;
+                    if (!(run = acquire(hi))) break;
                     // rows that hold no query are never stored; they take the
                     // unmasked path with their warp
                     const int vis = valid ? min(last - t * TM, TM - 1) : TM - 1;
@@ -526,7 +572,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                         for (int q = 0; q < TM / 32; ++q) {
                             float a[32];
-                            tmem_ld32(acc + 2 * TM * x + 32 * q, a);
+                            tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
                             tmem_wait_ld();
                             if (full) {
 #pragma unroll
@@ -550,7 +596,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                         for (int q = 0; q < TM / 32; ++q) {
                             float a[32];
-                            tmem_ld32(acc + 2 * TM * x + 32 * q, a);
+                            tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -577,34 +623,43 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         settle(max_pass());
                     }
                     l = fmaf(l, alpha, sum);
-                    release(x);
+                    release(hi);
                 }
                 if (!run) break;
-                if (par == 1) {
-                    run = give(x, make_float2(m_used, l));
+                // group 2 hi gets 2 hi + 1's; group 0 those of all others where the tile is alone
+                const bool taker = alone ? wg == 0 : par == 0;
+                if (!taker) {
+                    run = give(wg - 1, make_float2(m_used, l));
                 } else {
-                    float2 o;
-                    if (!(run = take(x, (uint32_t)n_join++, o))) break;
-                    const float mn = fmaxf(m_used, o.x);
-                    if (mn == -INFINITY) {
-                        l += o.y;
-                    } else {
-                        l = l * exp2f(m_used - mn) + o.y * exp2f(o.x - mn);
-                        m_used = mn;
+                    for (int g = wg; g < (alone ? Gm::NWG - 1 : wg + 1) && run; ++g) {
+                        float2 o;
+                        if (!(run = take(g, o))) break;
+                        const float mn = fmaxf(m_used, o.x);
+                        if (mn == -INFINITY) {
+                            l += o.y;
+                        } else {
+                            l = l * exp2f(m_used - mn) + o.y * exp2f(o.x - mn);
+                            m_used = mn;
+                        }
                     }
-                    if (gridDim.y == 1 && !p.few_rows) {  // final: -M and 1 / l by column
+                }
+#pragma unroll
+                for (int g = 0; g < 3; ++g) n_join[g] += alone || g != 1;
+                if (!run) break;
+                if (taker) {
+                    if (splits == 1) {  // final: -M and 1 / l by column
                         float* st = p.tile_stats + stat_tile(w.sq, w.h, w.a0 + x) * 2 * TM;
                         st[m] = valid && m_used != -INFINITY ? -m_used : 0.f;
                         st[TM + m] = valid ? 1.f / l : 0.f;
                     } else if (valid) {
-                        p.stats[(int64_t)blockIdx.y * part + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + g] =
+                        p.stats[(int64_t)w.z * part + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + g] =
                             make_float2(m_used, l);
                     }
                 }
             } else if constexpr (PASS == kKeyWeights) {
                 float total[2] = {0.f, 0.f};
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
-                    if ((nx & 1) != par) continue;
+                    if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
                     const float* nm = stat_s + sl * 2 * TM + hi * HC;
                     const float* il = nm + TM;
@@ -652,12 +707,15 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 } else {
                     for (int g = 0; g < Gm::NWG - 1 && run; ++g) {
                         float2 o;
-                        if (!(run = take(g, (uint32_t)n_join, o))) break;
+                        if (!(run = take(g, o))) break;
                         total[0] += o.x;
                         total[1] += o.y;
                     }
-                    ++n_join;
-                    if (!run) break;
+                }
+#pragma unroll
+                for (int g = 0; g < 3; ++g) ++n_join[g];
+                if (!run) break;
+                if (wg == 0) {
                     store_weight(w, w.a0 * TM + m, total[0]);
                     if (w.na == 2) store_weight(w, (w.a0 + 1) * TM + m, total[1]);
                 }
@@ -666,19 +724,22 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 // few rows: the item's query tiles stay, their statistics with them
                 if (!(run = meet())) break;  // the previous item's are used up
                 if (wg < NA) {
-                    const float2 st = row_stat(w, wg, m);
-                    stat_s[wg * 2 * TM + m] = st.x;
-                    stat_s[wg * 2 * TM + TM + m] = st.y;
+                    const float* st = p.tile_stats + stat_tile(w.sq, w.h, wg) * 2 * TM;
+                    const bool have = wg < w.na;
+                    stat_s[wg * 2 * TM + m] = have ? __ldcg(st + m) : 0.f;
+                    stat_s[wg * 2 * TM + TM + m] = have ? __ldcg(st + TM + m) : 0.f;
                 }
                 if (!(run = meet())) break;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
-                    if ((nx & 1) != par) continue;
+                    if (((t - w.b0) & 1) != par) continue;
                     const int key = t * TM + m;
                     float v = 0.f;
+                    const int turn = NA == 2 && w.na == 1 ? (t - w.b0) >> 1 & 1 : 0;  // a lone tile's accumulators rotate
 #pragma unroll
                     for (int x = 0; x < NA; ++x) {
                         if (x >= w.na) break;
-                        if (!(run = acquire(x))) break;
+                        const int ax = x + turn;
+                        if (!(run = acquire(ax))) break;
                         const int end = min(TT, w.sq.rows - x * TT) * G;
                         const int lo[2] = {p.causal ? (key - (w.sq.L - w.sq.rows) - x * TT) * G : 0, 0};
                         const bool full = __all_sync(0xffffffffu, lo[0] <= 0 && end == TT * G);
@@ -687,9 +748,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                         for (int q = 0; q < HC / 16; ++q) {
                             float a[2][16];
-                            tmem_ld16(acc + 2 * TM * x + hi * HC + 16 * q, a[0]);
+                            tmem_ld16(acc + 2 * TM * ax + hi * HC + 16 * q, a[0]);
                             tmem_wait_ld();
-                            if (q == HC / 16 - 1) release(x);
+                            if (q == HC / 16 - 1) release(ax);
                             const float* nm = stat_s + x * 2 * TM + hi * HC + 16 * q;
                             add_columns(std::integral_constant<int, 1>(), a, nm, nm + TM, hi * HC + 16 * q, full, lo, end,
                                         vx, v2);
@@ -700,12 +761,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     }
                     if (!run) break;
                     if (NA == 2) {  // the other half of the columns
-                        if (hi == 1) {
-                            if (!(run = give(par, make_float2(v, 0.f)))) break;
-                            continue;
-                        }
-                        float2 o;
-                        if (!(run = take(par, (uint32_t)n_join++, o))) break;
+                        float2 o = make_float2(v, 0.f);
+                        if (!(run = hi == 1 ? give(par, o) : take(par, o))) break;
+                        ++(par ? n_join[1] : n_join[0]);
+                        if (hi == 1) continue;
                         v += o.x;
                     }
                     store_weight(w, key, v);
@@ -810,9 +869,11 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
     }
     const size_t smem = weights_smem<HD>(a.num_seqs);
     const dim3 block(WGeo<HD>::NTHREADS);
+    cudaError_t e = cudaMemsetAsync(a.next_item, 0, 2 * sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
     auto k1 = weights_umma_kernel<T, HD, kRowStats>;
     auto k2 = a.few_rows ? weights_umma_kernel<T, HD, kFewRows> : weights_umma_kernel<T, HD, kKeyWeights>;
-    cudaError_t e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     constexpr int NA = WGeo<HD>::NA;
@@ -820,16 +881,18 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
     const int64_t q_items = (rows / (NA * TT) + a.num_seqs) * a.num_kv_heads;
     const int64_t k_items = a.few_rows ? (int64_t)a.num_seqs * a.num_kv_heads
                                        : (int64_t)a.num_seqs * a.num_kv_heads * ((a.max_context + NA * TM - 1) / (NA * TM));
-    auto ctas = [](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(n, kMaxCtas)); };
-    e = launch_pdl_smem(k1, dim3(ctas(q_items), (unsigned)a.key_splits), block, smem, stream, tmQ, tmK, a);
+    // one CTA fits an SM, and works its share of the items
+    const int64_t sms = sm_count();
+    auto ctas = [&](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(n, sms)); };
+    e = launch_pdl_smem(k1, dim3(ctas(q_items * a.key_splits)), block, smem, stream, tmQ, tmK, a);
     if (e != cudaSuccess) return e;
-    if (!a.few_rows && a.key_splits > 1) {
+    if (a.key_splits > 1) {
         const int64_t tiles = (rows / TT + a.num_seqs) * a.num_kv_heads;
-        e = launch_pdl_smem(stats_join_kernel, dim3(ctas(tiles)), dim3(TM), (size_t)(a.num_seqs + 1) * sizeof(int32_t),
+        e = launch_pdl_smem(stats_join_kernel, dim3((unsigned)std::min<int64_t>(tiles, sms * 8)), dim3(TM), (size_t)(a.num_seqs + 1) * sizeof(int32_t),
                             stream, a);
         if (e != cudaSuccess) return e;
     }
-    e = launch_pdl_smem(k2, dim3(ctas(k_items), (unsigned)a.row_splits), block, smem, stream, tmQ, tmK, a);
+    e = launch_pdl_smem(k2, dim3(ctas(k_items * a.row_splits)), block, smem, stream, tmQ, tmK, a);
     if (e != cudaSuccess || a.few_rows || a.row_splits == 1) return e;
     const int64_t wrows = (int64_t)a.num_seqs * a.num_kv_heads;
     return launch_pdl(weights_join_kernel,
@@ -844,35 +907,36 @@ bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, 
            (block_size == 8 || (block_size % GRP == 0 && block_size <= 256)) && group >= 1 && group <= TM;
 }
 
-// How the work is cut.  A CTA holds an SM; where there are fewer items than
-// two per SM the streamed axis is split, into pieces of at least four tiles.
+// How the work is cut: pieces of the streamed axis, where there are few
+// stationary tiles.  Pieces of fewer than 16 tiles spend much of their time
+// starting (2,048-token prompt: 103 us with pieces of 4 or more, 85 us so).
+// Items of unequal length (causal tiles) are cut so that there are two per SM
+// for the scheduling to even out (8,192 tokens: 560 us, 568 with four per SM,
+// 626 with eight); few rows over long contexts are equal pieces, as many as
+// make three whole rounds over the SMs.
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                              int32_t num_kv_heads, int32_t head_dim, int32_t max_context, int32_t window) {
-    constexpr int64_t kWant = 2 * 152, kMinTiles = 4;
+    constexpr int64_t kSms = 152, kMinTiles = 16;
     const int G = num_heads / num_kv_heads, TT = TM / G, NA = head_dim <= 128 ? 2 : 1;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    auto pieces = [&](int64_t items, int64_t tiles, int64_t most) {
-        return (int)std::max<int64_t>(1, std::min({up(kWant, items), tiles / kMinTiles, most}));
-    };
     WeightPlan w;
     const int64_t rows = window > 0 ? std::min<int64_t>(total_q, (int64_t)num_seqs * window) : total_q;
     const int32_t row_max = window > 0 ? std::min(max_q, window) : max_q;  // of one request
     const int64_t k_tiles = up(max_context, TM), q_tiles = up(row_max, TT);
-    w.key_splits = pieces(std::max<int64_t>(1, up(rows, NA * TT)) * num_kv_heads, k_tiles, 32);
     w.few_rows = q_tiles <= NA;
-    if (w.few_rows) {
-        w.row_splits = pieces((int64_t)num_seqs * num_kv_heads, k_tiles, 256);
-    } else {
-        w.row_splits = pieces((int64_t)num_seqs * num_kv_heads * up(k_tiles, NA), q_tiles, 8);
-    }
-    // partial statistics (several key splits, or few rows: pass 2 joins them
-    // itself), and the statistics by query tile that pass 2 streams
+    auto pieces = [&](int64_t items, int64_t tiles, int64_t most) {
+        const int64_t want = w.few_rows ? 3 * kSms / items : up(2 * kSms, items);
+        return (int)std::max<int64_t>(1, std::min({want, tiles / kMinTiles, most}));
+    };
+    const int64_t units = (int64_t)num_seqs * num_kv_heads;
+    w.key_splits = pieces(w.few_rows ? units : std::max<int64_t>(1, up(rows, NA * TT)) * num_kv_heads, k_tiles, 64);
+    w.row_splits = w.few_rows ? pieces(units, k_tiles, 256) : pieces(units * up(k_tiles, NA), q_tiles, 8);
+    // partial statistics (several key splits), and the statistics by query
+    // tile that pass 2 reads
     auto round = [](size_t b) { return (b + 255) / 256 * 256; };
-    if (w.few_rows || w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
-    if (!w.few_rows) {
-        w.stat_tiles = total_q / TT + num_seqs + 1;
-        w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
-    }
+    if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
+    w.stat_tiles = total_q / TT + num_seqs + 1;
+    w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
     w.partial_bytes = !w.few_rows && w.row_splits > 1
                           ? (size_t)w.row_splits * std::min(num_seqs, kWeightMaxSeqsPerLaunch) * num_kv_heads *
                                 max_context * sizeof(float)
