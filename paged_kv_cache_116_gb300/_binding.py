@@ -375,15 +375,18 @@ def _raw(t):
 
 
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    """The stream's handle (of the current stream without making a Stream object of it)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _rope_rows(name, t, heads, hd):
+def _rope_rows(name, t, n, heads, hd):
     """Token stride (elements) of q, k or v [n, heads, hd]: heads contiguous, tokens at any stride."""
-    n, h, d = t.shape
+    m, h, d = t.shape
     st, sh, sd = t.stride()
-    if not t.is_cuda or h != heads or d != hd or sd != 1 or (h > 1 and sh != hd):
-        raise ValueError("%s must be a CUDA tensor [n, %d, %d] whose heads are contiguous" % (name, heads, hd))
+    if not t.is_cuda or m != n or h != heads or d != hd or sd != 1 or (h > 1 and sh != hd):
+        raise ValueError("%s must be a CUDA tensor [%d, %d, %d] whose heads are contiguous" % (name, n, heads, hd))
     return st if n > 1 else max(st, heads * hd)
 
 
@@ -396,15 +399,16 @@ def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv
         raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
     if pair_axis is not None and (pair_axis.dtype != torch.int32 or pair_axis.numel() != inv_freq.numel()):
         raise ValueError("pair_axis must be int32 with one entry per frequency")
-    if k.shape[0] != n or v.shape[0] != n or slot_mapping.shape[0] != n or k.dtype != v.dtype:
-        raise ValueError("q, k, v, positions and slot_mapping must hold the same number of tokens, k and v one dtype")
+    dt = k.dtype
+    if slot_mapping.shape[0] != n or v.dtype != dt:
+        raise ValueError("positions and slot_mapping must hold one entry per token, k and v one dtype")
     hq, qs = 0, 0
     if q is not None:
         hq = q.shape[1]
-        if tuple(q_out.shape) != (n, hq, hd) or q.dtype != k.dtype or q_out.dtype != k.dtype:
+        if q_out.shape != (n, hq, hd) or q.dtype != dt or q_out.dtype != dt:
             raise ValueError("q_out must be [n, heads, head_dim], and q, q_out, k and v of one dtype")
-        qs = _rope_rows("q", q, hq, hd)
-    ks, vs = _rope_rows("k", k, hkv, hd), _rope_rows("v", v, hkv, hd)
+        qs = _rope_rows("q", q, n, hq, hd)
+    ks, vs = _rope_rows("k", k, n, hkv, hd), _rope_rows("v", v, n, hkv, hd)
     return (_raw(q_out), _raw(q), _raw(k), _raw(v), qs, ks, vs, _raw(positions), positions.shape[0], _raw(inv_freq),
             _raw(pair_axis), 2 * inv_freq.numel()), n, hq
 
@@ -442,14 +446,15 @@ def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_co
 
 def _scale_pools(nb, hkv, bs, *scales):
     for s in scales:
-        if tuple(s.shape) != (nb, hkv, bs) or s.dtype != torch.float32:
+        if s.shape != (nb, hkv, bs) or s.dtype != torch.float32:
             raise ValueError("scales must be float32 [num_blocks, num_kv_heads, block_size]")
 
 
 def _weight_rows(name, t, S, hkv, dtype=torch.float32):
-    if t.dim() != 3 or tuple(t.shape[:2]) != (S, hkv) or t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != S or shape[1] != hkv or t.dtype != dtype:
         raise ValueError("%s must be %s [num_seqs, num_kv_heads, weights_stride]" % (name, dtype))
-    return t.shape[2]
+    return shape[2]
 
 
 def _i32(*ts):

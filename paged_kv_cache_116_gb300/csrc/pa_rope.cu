@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
     const int R = half / VEC, per = R + ((hd - p.rot_dim) / VEC + 1) / 2;
     const int n_rot = (Hq + (kRowsBelow ? 0 : Hkv)) * per, vper = (hd / VEC + 1) / 2;
     const int items = n_rot + (kRowsBelow ? 0 : Hkv * vper);
-    for (int it = threadIdx.x; it < items; it += kRopeThreads) {
+    for (int it = blockIdx.y * kRopeThreads + threadIdx.x; it < items; it += gridDim.y * kRopeThreads) {
         const bool is_v = it >= n_rot;
         int head = is_v ? (it - n_rot) / vper : it / per;
         const int r = is_v ? it - n_rot - head * vper : it - head * per;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
         // one warp per (token, KV head, K|V) row: lane l holds pairs l, l+32,
         // ... of the rotated part and elements rot + l, ... of the rest
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        for (int row = warp; row < nt * Hkv * 2; row += kRopeThreads / 32) {
+        for (int row = blockIdx.y * (kRopeThreads / 32) + warp; row < nt * Hkv * 2; row += gridDim.y * (kRopeThreads / 32)) {
             const int is_v = row & 1, h = (row >> 1) % Hkv, t = (row >> 1) / Hkv;
             const int64_t tok = t0 + t, slot = slots[t];
             if (slot < 0) continue;
@@ -307,7 +307,11 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
     // with 4, 39 with 8, 40 with 16).
     p.tpb = 8;
     while (p.tpb > 1 && a.n < (int64_t)p.tpb * 152 * 4) p.tpb /= 2;
-    const dim3 grid((unsigned)((a.n + p.tpb - 1) / p.tpb));
+    // few tokens: their items over several CTAs each, which repeat the angles
+    const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
+    const int items = (a.num_heads + 2 * a.num_kv_heads) * (a.head_dim / (vec ? 2 * V : 2));
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(2 * 152 / ctas, (items + kRopeThreads - 1) / kRopeThreads));
+    const dim3 grid((unsigned)ctas, (unsigned)parts);
     const size_t smem = (size_t)p.tpb * ((a.rot_dim / 2) * sizeof(float2) + sizeof(int64_t));
     return vec ? launch_pdl_smem(rope_write_kernel<T, V, FP8>, grid, dim3(kRopeThreads), smem, stream, p)
                : launch_pdl_smem(rope_write_kernel<T, 1, FP8>, grid, dim3(kRopeThreads), smem, stream, p);
