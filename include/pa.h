@@ -538,10 +538,12 @@ PA_API pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weight
  *   q, cu_seqlens_q, seq_lens, block_tables, total_q, max_q, causal: as for pa_varlen
  *   window:    >= 0
  *   workspace: pa_prompt_weights_workspace_size(...) bytes, 16-byte aligned
- * bf16/f16 with head_dim 64, 128 or 256, block_size 8 or a multiple of 16 up
- * to 256 and at most 128 query heads per KV head run on the tcgen05 kernels
- * (PA_OPT_VARLEN_KERNEL pins a kernel as it does for pa_varlen), the rest on
- * the CUDA cores.
+ * bf16/f16 with head_dim 64, 128 or 256 and at most 128 query heads per KV
+ * head run on the tcgen05 kernels (PA_OPT_VARLEN_KERNEL pins a kernel as it
+ * does for pa_varlen), the rest on the CUDA cores.  Caches whose block_size is
+ * neither 8 nor a multiple of 16 up to 256, and quantized ones, are first laid
+ * out densely in the workspace, which then holds num_seqs * max_context keys
+ * in the query's type.
  */
 PA_API size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

@@ -1013,7 +1013,8 @@ struct PromptWeightsPlan {
     static constexpr size_t kCounters = 256;  // ahead of the rest (tensor-core path)
     bool tc = false;
     pa::WeightPlan cut;
-    size_t bytes() const { return (tc ? kCounters : 0) + cut.stats_bytes + cut.tile_stats_bytes + cut.partial_bytes; }
+    size_t bytes() const { return (tc ? kCounters : 0) + cut.dense_bytes + cut.scale_bytes + cut.stats_bytes + cut.tile_stats_bytes +
+               cut.partial_bytes; }
 };
 static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
@@ -1021,9 +1022,10 @@ static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, 
     PromptWeightsPlan p;
     if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return p;
     const int G = num_heads / num_kv_heads;
-    p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, block_size, G, fp8);
+    p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, G);
     if (p.tc)
-        p.cut = pa::weights_umma_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, max_context, window);
+        p.cut = pa::weights_umma_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size,
+                                      max_context, window, fp8);
     else
         p.cut.stats_bytes = (size_t)total_q * num_heads * sizeof(float2);
     return p;
@@ -1054,8 +1056,8 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     const PromptWeightsPlan plan = prompt_weights_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim,
                                                        block_size, max_context, window, dtype, k_scales != nullptr);
     if (g_options[PA_OPT_VARLEN_KERNEL] == 2 && !plan.tc)
-        return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 caches, head_dim 64/128/256, block_size "
-                                        "8 or a multiple of 16 up to 256 and at most 128 query heads per KV head");
+        return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 queries, head_dim 64/128/256 and at "
+                                        "most 128 query heads per KV head");
     if (!workspace || workspace_bytes < plan.bytes())
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                           std::to_string(plan.bytes()) + " needed");
@@ -1069,6 +1071,11 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.next_item = reinterpret_cast<uint32_t*>(ws);
     if (plan.tc) ws += PromptWeightsPlan::kCounters;
+    a.dense_stride = plan.cut.dense_stride;
+    a.dense_keys = ws;
+    ws += plan.cut.dense_bytes;
+    a.key_scales = reinterpret_cast<float*>(ws);
+    ws += plan.cut.scale_bytes;
     a.stats = reinterpret_cast<float2*>(ws);
     a.tile_stats = reinterpret_cast<float*>(ws + plan.cut.stats_bytes);
     a.stat_tiles = plan.cut.stat_tiles;

@@ -200,6 +200,9 @@ struct WeightArgs {
     int kv_fp8;
     float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
     uint32_t* next_item = nullptr;  // two counters (workspace)
+    void* dense_keys = nullptr;     // [num_seqs, dense_stride, num_kv_heads, head_dim] of the query's type
+    float* key_scales = nullptr;    // [num_seqs, num_kv_heads, dense_stride], times scale_log2
+    int dense_stride = 0;
     float* tile_stats = nullptr;
     int stat_tiles = 0;
     float* partial = nullptr;
@@ -219,11 +222,13 @@ struct WeightPlan {
     int row_splits = 1;
     bool few_rows = false;  // row_splits then cuts the keys, without partial weights
     int stat_tiles = 0;     // tile_stats: [num_kv_heads, stat_tiles, 2, 128]
-    size_t stats_bytes = 0, tile_stats_bytes = 0, partial_bytes = 0;
+    int dense_stride = 0;   // tokens per request of a dense copy of the keys; 0: read in place
+    size_t stats_bytes = 0, tile_stats_bytes = 0, partial_bytes = 0, dense_bytes = 0, scale_bytes = 0;
 };
-bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, bool kv_fp8);
+bool weights_umma_supported(int dtype, int head_dim, int group);
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
-                             int32_t num_kv_heads, int32_t head_dim, int32_t max_context, int32_t window);
+                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_context,
+                             int32_t window, bool kv_fp8);
 cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream);
 uint32_t weights_umma_status(bool clear);
 

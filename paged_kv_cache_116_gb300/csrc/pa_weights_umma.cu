@@ -1,7 +1,6 @@
 // pa_weights_umma.cu -- attention weights of a request's cached tokens on the
 // 5th-generation tensor cores (tcgen05.mma, accumulators in tensor memory):
-// bf16/f16, head_dim 64, 128 or 256, block_size 8 or a multiple of 16 up to
-// 256.  The definition stands at the head of pa_weights_simt.cu; the two
+// bf16/f16 queries, head_dim 64, 128 or 256.  The definition stands at the head of pa_weights_simt.cu; the two
 // passes over Q K^T are here one kernel in two forms:
 //
 //   pass 1 (row statistics)  stationary A = 128 query rows, streamed B = the
@@ -25,6 +24,11 @@
 // tile feeds two MMAs.  With one (and two CTAs per SM) the streamed tiles
 // crossed from L2 at 9.3 TB/s, which bounded the kernel (8,192-token prompt,
 // 32 / 8 heads: 0.93 ms).
+//
+// Pools with block_size 8 or a multiple of 16 up to 256 are read in place.
+// Others, and code pools, are first laid out densely in the workspace, codes
+// as their exact values in the query's type; a code row's scale multiplies the
+// fp32 score (of the key's column in pass 1, of its lane in pass 2).
 //
 // Where there are few stationary tiles the streamed axis is split: pass 1's
 // pieces of (maximum, sum) are joined by a small kernel, pass 2's partial
@@ -155,8 +159,9 @@ __device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) 
 
 enum Pass { kRowStats = 1, kKeyWeights = 2, kFewRows = 3 };
 
-// T: the element type of q and the pool.
-template <typename T, int HD, int PASS>
+// T: the element type of q and the keys.  SC: keys have scales
+// (p.key_scales, the score's scale in them).
+template <typename T, int HD, int PASS, bool SC>
 __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     weights_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const WeightArgs p) {
@@ -182,6 +187,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     uint64_t* j_full = g_bar + 1;
     uint64_t* j_empty = j_full + 3;
     float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);
+    // keys streamed with their scales: kScaleRing x [128] behind the stationary statistics
+    constexpr int kScaleRing = 4, kRing = PASS == kKeyWeights ? Gm::SRING : kScaleRing;
+    float* scale_s = stat_s + NA * 2 * TM;
+    static_assert(kScaleRing * TM + NA * 2 * TM <= Gm::SRING * 2 * TM, "scales fit behind the statistics");
     float2* join_s = reinterpret_cast<float2*>(base + Gm::JOIN_OFF);
     volatile uint32_t* taddr_slot = reinterpret_cast<volatile uint32_t*>(base + Gm::ADDR_OFF);
     int32_t* prefix = reinterpret_cast<int32_t*>(base + Gm::PREF_OFF);
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         // ---------------- producer `me` of every NPROD-th streamed tile; the first also loads the stationary ones
         const int me = warp - Gm::W_PROD;
         const uint64_t pol = l2_policy_evict_last();  // keys are read twice, query tiles by every key tile
-        const int bsz = p.block_size, halves = bsz == 8 ? 2 : 1;
+        const int bsz = p.block_size, halves = !p.dense_stride && bsz == 8 ? 2 : 1;
         const int nbox = NGRP * halves;  // boxes along the keys of a tile
         int na = 0, nb = 0;
         bool run = true;
@@ -318,6 +327,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         // group holds no context, the first half's; never read past it)
         auto key_row = [&](const Item& w, int kt) -> int32_t {
             if (lane >= nbox) return 0;
+            if (p.dense_stride) return w.sq.s * p.dense_stride + kt * TM + lane * GRP;
             const int32_t* table = p.block_tables + (int64_t)w.sq.s * p.max_blocks;
             int tok = kt * TM + lane * (GRP / halves);
             if (halves == 2 && (lane & 1) && tok >= w.sq.L) tok -= 8;
@@ -382,6 +392,14 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     expect(&b_full[slot], key_groups(w, t) * group_bytes);
                     load_keys(w, t, row, dst, &b_full[slot]);
                     if (t + Gm::NPROD < w.b1) row = key_row(w, t + Gm::NPROD);
+                    if constexpr (SC) {
+                        const int sl = nb % kScaleRing;
+                        if (!(run = wait(&s_empty[sl], (uint32_t)(nb / kScaleRing & 1) ^ 1u))) break;
+                        expect(&s_full[sl], TM * 4);
+                        if (lane == 0)
+                            bulk_g2s(scale_s + sl * TM, p.key_scales + ((int64_t)w.sq.s * Hkv + w.h) * p.dense_stride + t * TM,
+                                     TM * 4, &s_full[sl]);
+                    }
                 } else {
                     expect(&b_full[slot], query_bytes);
                     load_queries(w, t, dst, &b_full[slot]);
@@ -397,12 +415,12 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         if (!run) {  // copies in flight land before the CTA's shared memory is given up
             if (me == 0 && na) mbar_wait_ns(a_full, (uint32_t)(na - 1) & 1u, WAIT_NS);
             for (int j = max(0, nb - RING); j <= nb; ++j)
-                if ((j + me) % Gm::NPROD == 0 && j < nb + (PASS == kKeyWeights))
+                if ((j + me) % Gm::NPROD == 0 && j < nb + (PASS == kKeyWeights || SC))
                     mbar_wait_ns(&b_full[j % RING], (uint32_t)(j / RING) & 1u, WAIT_NS);
-            if (PASS == kKeyWeights)
-                for (int j = max(0, nb - Gm::SRING); j < nb; ++j)
+            if (PASS == kKeyWeights || SC)
+                for (int j = max(0, nb - kRing); j < nb; ++j)
                     if ((j + me) % Gm::NPROD == 0)
-                        mbar_wait_ns(&s_full[j % Gm::SRING], (uint32_t)(j / Gm::SRING) & 1u, WAIT_NS);
+                        mbar_wait_ns(&s_full[j % kRing], (uint32_t)(j / kRing) & 1u, WAIT_NS);
         }
     } else if (warp >= Gm::W_MMA) {
         // ---------------- MMA issuer of stationary tile x
@@ -496,6 +514,11 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(&j_empty[j]);
             return true;
         };
+        // this warp is done with what slot sl of the statistics (or scales) ring holds
+        auto used = [&](int sl_) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[sl_]);
+        };
         // a bounded barrier of all groups
         auto meet = [&]() -> bool {
             __syncwarp();
@@ -504,17 +527,18 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         };
         // exp2(x - M) / l of `n` accumulators' columns [q, q + 16) for this
         // thread's keys, added to v[]: column c counts where lo[] <= c < end
-        auto add_columns = [&](auto count, const float (&a)[2][16], const float* nm, const float* il, int c0, bool full,
-                               const int (&lo)[2], int end, float (&v)[2], unsigned long long (&v2)[2]) {
+        auto add_columns = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm, const float* il,
+                               int c0, bool full, const int (&lo)[2], int end, float (&v)[2],
+                               unsigned long long (&v2)[2]) {
             constexpr int N = decltype(count)::value;
             if (full) {
-                const unsigned long long sv = f32x2_pack(sl, sl);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);
                     const float4 i4 = *reinterpret_cast<const float4*>(il + 4 * j);
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
+                        const unsigned long long sv = f32x2_pack(ks[k], ks[k]);
                         float x0, x1, x2, x3;
                         f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j], a[k][4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
                         f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j + 2], a[k][4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
@@ -528,7 +552,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                     for (int k = 0; k < N; ++k)
                         if (c0 + j >= lo[k] && c0 + j < end)
-                            v[k] = fmaf(fast_exp2(fmaf(a[k][j], sl, nm[j])), il[j], v[k]);
+                            v[k] = fmaf(fast_exp2(fmaf(a[k][j], ks[k], nm[j])), il[j], v[k]);
             }
         };
         auto store_weight = [&](const Item& w, int key, float v) {
@@ -553,7 +577,20 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 const int last = p.causal ? w.sq.L - w.sq.rows + tok : w.sq.L - 1;  // last key the row sees
                 float m_used = -INFINITY, l = 0.f;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
-                    if (((t - w.b0) & 1) != par || (alone && ((t - w.b0) >> 1 & 1) != hi)) continue;
+                    if (!SC) {
+                        if (((t - w.b0) & 1) != par || (alone && ((t - w.b0) >> 1 & 1) != hi)) continue;
+                    } else {
+                        if (((t - w.b0) & 1) != par) continue;
+                    }
+                    const float* ks = scale_s + nx % kScaleRing * TM;  // the tile's key scales (SC)
+                    if constexpr (SC) {
+                        const int sl_ = nx % kScaleRing;
+                        if (!(run = mbar_wait_ns(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
+                        if (alone && ((t - w.b0) >> 1 & 1) != hi) {  // another group's; it is counted all the same
+                            used(sl_);
+                            continue;
+                        }
+                    }
                     if (!(run = acquire(hi))) break;
                     // rows that hold no query are never stored; they take the
                     // unmasked path with their warp
@@ -577,14 +614,15 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             if (full) {
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
+                                    const float2 k2 = SC ? *reinterpret_cast<const float2*>(ks + 32 * q + 2 * j) : make_float2(sl, sl);
                                     float x0, x1;
-                                    f32x2_unpack(fma_f32x2(f32x2_pack(a[2 * j], a[2 * j + 1]), sv, nv), x0, x1);
+                                    f32x2_unpack(fma_f32x2(f32x2_pack(a[2 * j], a[2 * j + 1]), SC ? f32x2_pack(k2.x, k2.y) : sv, nv), x0, x1);
                                     s2 = add_f32x2(s2, f32x2_pack(fast_exp2(x0), fast_exp2(x1)));
                                 }
                             } else {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
-                                    sum += 32 * q + j <= vis ? fast_exp2(fmaf(a[j], sl, neg)) : 0.f;
+                                    sum += 32 * q + j <= vis ? fast_exp2(fmaf(a[j], SC ? ks[32 * q + j] : sl, neg)) : 0.f;
                             }
                         }
                         float s0, s1;
@@ -600,7 +638,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             tmem_wait_ld();
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (32 * q + j <= vis) mt = fmaxf(mt, a[j] * sl);
+                                if (32 * q + j <= vis) mt = fmaxf(mt, a[j] * (SC ? ks[32 * q + j] : sl));
                         }
                         return mt;
                     };
@@ -624,6 +662,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     }
                     l = fmaf(l, alpha, sum);
                     release(hi);
+                    if constexpr (SC) used(nx % kScaleRing);
                 }
                 if (!run) break;
                 // group 2 hi gets 2 hi + 1's; group 0 those of all others where the tile is alone
@@ -657,7 +696,14 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     }
                 }
             } else if constexpr (PASS == kKeyWeights) {
-                float total[2] = {0.f, 0.f};
+                float total[2] = {0.f, 0.f}, ks[2] = {sl, sl};
+                if constexpr (SC) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int key = (w.a0 + x) * TM + m;
+                        ks[x] = key < w.sq.L ? __ldcg(p.key_scales + ((int64_t)w.sq.s * Hkv + w.h) * p.dense_stride + key) : 0.f;
+                    }
+                }
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
@@ -689,8 +735,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             release(0);
                             if (w.na == 2) release(NA - 1);
                         }
-                        if (w.na == 2) add_columns(Both(), a, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
-                        else add_columns(One(), a, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                        if (w.na == 2) add_columns(Both(), a, ks, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                        else add_columns(One(), a, ks, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
                     }
 #pragma unroll
                     for (int x = 0; x < NA; ++x) {
@@ -698,8 +744,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         f32x2_unpack(v2[x], s0, s1);
                         total[x] += v[x] + (s0 + s1);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[sl]);
+                    used(sl);
                 }
                 if (!run) break;
                 if (wg > 0) {
@@ -733,7 +778,13 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if (((t - w.b0) & 1) != par) continue;
                     const int key = t * TM + m;
-                    float v = 0.f;
+                    float v = 0.f, ks[2] = {sl, 0.f};
+                    if constexpr (SC) {
+                        const int sl_ = nx % kScaleRing;
+                        if (!(run = mbar_wait_ns(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
+                        ks[0] = scale_s[sl_ * TM + m];
+                        used(sl_);
+                    }
                     const int turn = NA == 2 && w.na == 1 ? (t - w.b0) >> 1 & 1 : 0;  // a lone tile's accumulators rotate
 #pragma unroll
                     for (int x = 0; x < NA; ++x) {
@@ -752,7 +803,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             tmem_wait_ld();
                             if (q == HC / 16 - 1) release(ax);
                             const float* nm = stat_s + x * 2 * TM + hi * HC + 16 * q;
-                            add_columns(std::integral_constant<int, 1>(), a, nm, nm + TM, hi * HC + 16 * q, full, lo, end,
+                            add_columns(std::integral_constant<int, 1>(), a, ks, nm, nm + TM, hi * HC + 16 * q, full, lo, end,
                                         vx, v2);
                         }
                         float s0, s1;
@@ -777,6 +828,56 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == Gm::W_MMA) tmem_dealloc(tmem, Gm::TMEM_COLS);
+}
+
+// Lays a batch's keys out densely, request s's token t at row s * dense_stride
+// + t: codes become their exact values in T and their scales, times the
+// score's, a row per (request, KV head); 16-bit keys are copied.  A thread
+// moves 16 bytes of pool.  Bound: HBM.
+template <typename T, bool FP8>
+__global__ void __launch_bounds__(256) dense_keys_kernel(const WeightArgs p, T* __restrict__ keys, float* __restrict__ scales) {
+    constexpr int E = FP8 ? 16 : 8;  // elements per 16 bytes
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int row = p.num_kv_heads * p.head_dim, chunks = row / E, bs = p.block_size;
+    for (int s = blockIdx.y; s < p.num_seqs; s += gridDim.y) {
+        const WeightSeq sq = weight_seq(p, s);
+        if (sq.rows == 0) continue;
+        const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
+        const int64_t all = (int64_t)sq.L * chunks;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+            const int t = (int)(i / chunks), c = (int)(i - (int64_t)t * chunks);
+            const int64_t blk = table[t / bs];
+            const int off = t % bs;
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.k_cache) + (blk * bs + off) * chunks + c);
+            uint4* dst = reinterpret_cast<uint4*>(keys + ((int64_t)s * p.dense_stride + t) * row + c * E);
+            if constexpr (FP8) {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16x2x2(w[k], lo, hi);
+                    if constexpr (std::is_same<T, __half>::value) {
+                        o[2 * k] = lo;
+                        o[2 * k + 1] = hi;
+                    } else {  // every code is a bf16 value as well
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                        o[2 * k] = pack2<T>(a.x, a.y);
+                        o[2 * k + 1] = pack2<T>(b.x, b.y);
+                    }
+                }
+                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                if (c < p.num_kv_heads)
+                    scales[((int64_t)s * p.num_kv_heads + c) * p.dense_stride + t] =
+                        p.scale_log2 * __ldcg(p.k_scales + (blk * p.num_kv_heads + c) * bs + off);
+            } else {
+                *dst = v;
+            }
+        }
+    }
 }
 
 // Joins pass 1's key splits into the statistics that pass 2 streams: a thread
@@ -851,9 +952,24 @@ bool encode_map(CUtensorMap* m, const void* ptr, int dtype, const cuuint64_t (&d
     return true;
 }
 
-template <typename T, int HD>
-cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream) {
+template <typename T, int HD, bool SC>
+cudaError_t launch_umma(const WeightArgs& args, int32_t num_blocks, std::string* err, cudaStream_t stream) {
+    WeightArgs a = args;
     const int G = a.num_heads / a.num_kv_heads, TT = TM / G;
+    const int64_t sms = sm_count();
+    cudaError_t e = cudaMemsetAsync(a.next_item, 0, 2 * sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
+    int64_t k_rows = (int64_t)num_blocks * a.block_size;
+    if (a.dense_stride) {
+        T* keys = static_cast<T*>(a.dense_keys);
+        const int64_t per = ((int64_t)a.max_context * a.num_kv_heads * HD / (SC ? 16 : 8) + 255) / 256;
+        const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(per, std::max<int64_t>(1, 8 * sms / a.num_seqs))),
+                        (unsigned)a.num_seqs);
+        e = launch_pdl(dense_keys_kernel<T, SC>, grid, dim3(256), stream, a, keys, a.key_scales);
+        if (e != cudaSuccess) return e;
+        a.k_cache = keys;
+        k_rows = (int64_t)a.num_seqs * a.dense_stride;
+    }
     CUtensorMap tmQ, tmK;
     {
         cuuint64_t dims[3] = {(cuuint64_t)HD, (cuuint64_t)a.num_heads, (cuuint64_t)a.total_q};
@@ -862,17 +978,15 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
         if (!encode_map(&tmQ, a.q, a.dtype, dims, strides, box, err)) return cudaErrorInvalidValue;
     }
     {
-        cuuint64_t dims[3] = {64, (cuuint64_t)a.num_kv_heads * (HD / 64), (cuuint64_t)num_blocks * a.block_size};
+        cuuint64_t dims[3] = {64, (cuuint64_t)a.num_kv_heads * (HD / 64), (cuuint64_t)k_rows};
         cuuint64_t strides[2] = {128, (cuuint64_t)a.num_kv_heads * HD * 2};
-        cuuint32_t box[3] = {64, 1, (cuuint32_t)(a.block_size == 8 ? 8 : GRP)};
+        cuuint32_t box[3] = {64, 1, (cuuint32_t)(!a.dense_stride && a.block_size == 8 ? 8 : GRP)};
         if (!encode_map(&tmK, a.k_cache, a.dtype, dims, strides, box, err)) return cudaErrorInvalidValue;
     }
     const size_t smem = weights_smem<HD>(a.num_seqs);
     const dim3 block(WGeo<HD>::NTHREADS);
-    cudaError_t e = cudaMemsetAsync(a.next_item, 0, 2 * sizeof(uint32_t), stream);
-    if (e != cudaSuccess) return e;
-    auto k1 = weights_umma_kernel<T, HD, kRowStats>;
-    auto k2 = a.few_rows ? weights_umma_kernel<T, HD, kFewRows> : weights_umma_kernel<T, HD, kKeyWeights>;
+    auto k1 = weights_umma_kernel<T, HD, kRowStats, SC>;
+    auto k2 = a.few_rows ? weights_umma_kernel<T, HD, kFewRows, SC> : weights_umma_kernel<T, HD, kKeyWeights, SC>;
     e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -881,15 +995,14 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
     const int64_t q_items = (rows / (NA * TT) + a.num_seqs) * a.num_kv_heads;
     const int64_t k_items = a.few_rows ? (int64_t)a.num_seqs * a.num_kv_heads
                                        : (int64_t)a.num_seqs * a.num_kv_heads * ((a.max_context + NA * TM - 1) / (NA * TM));
-    // one CTA fits an SM, and works its share of the items
-    const int64_t sms = sm_count();
+    // one CTA fits an SM, and draws its share of the items
     auto ctas = [&](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(n, sms)); };
     e = launch_pdl_smem(k1, dim3(ctas(q_items * a.key_splits)), block, smem, stream, tmQ, tmK, a);
     if (e != cudaSuccess) return e;
     if (a.key_splits > 1) {
         const int64_t tiles = (rows / TT + a.num_seqs) * a.num_kv_heads;
-        e = launch_pdl_smem(stats_join_kernel, dim3((unsigned)std::min<int64_t>(tiles, sms * 8)), dim3(TM), (size_t)(a.num_seqs + 1) * sizeof(int32_t),
-                            stream, a);
+        e = launch_pdl_smem(stats_join_kernel, dim3((unsigned)std::min<int64_t>(tiles, sms * 8)), dim3(TM),
+                            (size_t)(a.num_seqs + 1) * sizeof(int32_t), stream, a);
         if (e != cudaSuccess) return e;
     }
     e = launch_pdl_smem(k2, dim3(ctas(k_items * a.row_splits)), block, smem, stream, tmQ, tmK, a);
@@ -900,11 +1013,18 @@ cudaError_t launch_umma(const WeightArgs& a, int32_t num_blocks, std::string* er
                       stream, a);
 }
 
+template <typename T, bool SC>
+cudaError_t launch_hd(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream) {
+    return a.head_dim == 64    ? launch_umma<T, 64, SC>(a, num_blocks, err, stream)
+           : a.head_dim == 128 ? launch_umma<T, 128, SC>(a, num_blocks, err, stream)
+                               : launch_umma<T, 256, SC>(a, num_blocks, err, stream);
+}
+
 }  // namespace
 
-bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, bool kv_fp8) {
-    return !kv_fp8 && (dtype == 1 || dtype == 2) && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
-           (block_size == 8 || (block_size % GRP == 0 && block_size <= 256)) && group >= 1 && group <= TM;
+bool weights_umma_supported(int dtype, int head_dim, int group) {
+    return (dtype == 1 || dtype == 2) && (head_dim == 64 || head_dim == 128 || head_dim == 256) && group >= 1 &&
+           group <= TM;
 }
 
 // How the work is cut: pieces of the streamed axis, where there are few
@@ -915,7 +1035,8 @@ bool weights_umma_supported(int dtype, int head_dim, int block_size, int group, 
 // 626 with eight); few rows over long contexts are equal pieces, as many as
 // make three whole rounds over the SMs.
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
-                             int32_t num_kv_heads, int32_t head_dim, int32_t max_context, int32_t window) {
+                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_context,
+                             int32_t window, bool kv_fp8) {
     constexpr int64_t kSms = 152, kMinTiles = 16;
     const int G = num_heads / num_kv_heads, TT = TM / G, NA = head_dim <= 128 ? 2 : 1;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
@@ -937,6 +1058,13 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
     w.stat_tiles = total_q / TT + num_seqs + 1;
     w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
+    // pools that no box fits, and code pools, are laid out densely first
+    if (kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256))) {
+        w.dense_stride = (int)(k_tiles * TM);
+        const size_t tokens = (size_t)std::min(num_seqs, kWeightMaxSeqsPerLaunch) * w.dense_stride;
+        w.dense_bytes = tokens * num_kv_heads * head_dim * 2;
+        if (kv_fp8) w.scale_bytes = tokens * num_kv_heads * sizeof(float);
+    }
     w.partial_bytes = !w.few_rows && w.row_splits > 1
                           ? (size_t)w.row_splits * std::min(num_seqs, kWeightMaxSeqsPerLaunch) * num_kv_heads *
                                 max_context * sizeof(float)
@@ -945,13 +1073,15 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
 }
 
 cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream) {
+    if (a.dense_stride && (int64_t)a.num_seqs * a.dense_stride > INT32_MAX) {
+        *err = "the dense key layout's rows do not fit in int32";
+        return cudaErrorInvalidValue;
+    }
     if (a.dtype == 1)
-        return a.head_dim == 64    ? launch_umma<__nv_bfloat16, 64>(a, num_blocks, err, stream)
-               : a.head_dim == 128 ? launch_umma<__nv_bfloat16, 128>(a, num_blocks, err, stream)
-                                   : launch_umma<__nv_bfloat16, 256>(a, num_blocks, err, stream);
-    return a.head_dim == 64    ? launch_umma<__half, 64>(a, num_blocks, err, stream)
-           : a.head_dim == 128 ? launch_umma<__half, 128>(a, num_blocks, err, stream)
-                               : launch_umma<__half, 256>(a, num_blocks, err, stream);
+        return a.kv_fp8 ? launch_hd<__nv_bfloat16, true>(a, num_blocks, err, stream)
+                        : launch_hd<__nv_bfloat16, false>(a, num_blocks, err, stream);
+    return a.kv_fp8 ? launch_hd<__half, true>(a, num_blocks, err, stream)
+                    : launch_hd<__half, false>(a, num_blocks, err, stream);
 }
 
 uint32_t weights_umma_status(bool clear) {

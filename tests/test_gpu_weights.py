@@ -214,6 +214,11 @@ PROMPT = [
     ([70, 5], [90, 700], 128, 1, 64, 16, "bf16", 0, True, False),
     ([40, 129], [40, 260], 4, 2, 256, 8, "f16", 0, True, False),
     ([33, 1], [9000, 2500], 32, 8, 128, 256, "bf16", 32, True, False),
+    ([900, 40], [1300, 2000], 8, 2, 128, 16, "bf16", 0, True, True),
+    ([40, 33], [6000, 300], 32, 8, 128, 16, "f16", 32, True, True),
+    ([200, 31], [260, 500], 6, 2, 64, 24, "bf16", 0, True, True),
+    ([50, 130], [500, 140], 4, 2, 256, 16, "f16", 0, False, True),
+    ([300, 20], [400, 900], 12, 2, 128, 1, "bf16", 0, True, False),
 ]
 
 
