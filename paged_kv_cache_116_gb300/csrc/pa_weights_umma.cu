@@ -234,18 +234,6 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         tmem_alloc(const_cast<uint32_t*>(taddr_slot), Gm::TMEM_COLS);
         tmem_relinquish();
     }
-    if (PASS != kRowStats && TT * G < TM) {
-        // rows of a query tile past its T G (token, head) pairs get no TMA
-        // data: zeros, so that their columns are finite and weigh 0
-        const int pad = TM - TT * G, per = Gm::CH * pad * 8;
-        const int first = PASS == kFewRows ? 0 : NA, count = PASS == kFewRows ? NA : RING;
-        for (int e = threadIdx.x; e < count * per; e += Gm::NTHREADS) {
-            const int tile = first + e / per, r0 = e % per, c = r0 / (pad * 8), r = r0 - c * pad * 8;
-            *reinterpret_cast<uint4*>(base + tile * Gm::TILE + c * Gm::CHB + (TT * G + r / 8) * 128 + (r & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -528,10 +516,11 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         // exp2(x - M) / l of `n` accumulators' columns [q, q + 16) for this
         // thread's keys, added to v[]: column c counts where lo[] <= c < end
         auto add_columns = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm, const float* il,
-                               int c0, bool full, const int (&lo)[2], int end, float (&v)[2],
+                               int c0, bool whole, const int (&lo)[2], int end, float (&v)[2],
                                unsigned long long (&v2)[2]) {
             constexpr int N = decltype(count)::value;
-            if (full) {
+            // columns past the tile's T G rows hold whatever was there
+            if (whole && c0 + 16 <= TT * G) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);

@@ -268,3 +268,81 @@ def test_prompt_weights_many_requests(pa):
         k = torch.stack([b.k[b.tables[s, 0].long(), :2, 0] for s in range(S)]).double()
         want = torch.softmax(torch.einsum("sgd,std->sgt", q.double(), k) * 0.125, -1).sum(1)
         assert bool(((w.cpu()[:, 0].double() - want).abs() <= 1e-4 * want).all()), form
+
+
+def test_prompt_weights_infinite_key(pa):
+    """A key every query gives a score of -infinity weighs 0, whatever the group size pads a query tile with."""
+    b = Batch([200], 1, 128, 16, "f16", 3)
+    b.k.clamp_(min=0.01)
+    b.k[b.tables[0, 2].long(), 5, 0, 7] = -float("inf")  # token 37
+    b.to(DEV)
+    q = torch.rand((150, 6, 128), generator=torch.Generator().manual_seed(3)).clamp(min=0.01).to(torch.float16)
+    before = torch.zeros((1, 1, 200))
+    w = before.to(DEV)
+    _prompt(pa, b, q.to(DEV), [0, 150], 0, 0.05, w)
+    b.k[b.tables[0, 2].long(), 5, 0, 7] = -60000.0  # finite for the reference: the weight underflows to 0 as well
+    want, rtol = prompt_exact(b, q, [0, 150], 0, 0.05, True, before)
+    got = w.cpu()
+    assert float(got[0, 0, 37]) == 0.0
+    want[0, 0, 37] = 0.0
+    b.k[b.tables[0, 2].long(), 5, 0, 7] = 0.01
+    _, rtol = prompt_exact(b, q, [0, 150], 0, 0.05, True, before)
+    assert bool(((got.double() - want).abs() <= rtol * want).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pinned_kernels_and_grids_agree(pa, fp8):
+    """The CUDA-core and the tensor-core forms, and decode grids of other sizes, within the tolerance."""
+    b = Batch([700, 33, 90], 2, 128, 16, "bf16", 23, fp8).to(DEV)
+    new, cu = [64, 1, 90], [0, 64, 65, 155]
+    gen = torch.Generator().manual_seed(4)
+    q1 = torch.randn((3, 8, 128), generator=gen).to(torch.bfloat16)
+    qp = torch.randn((cu[-1], 8, 128), generator=gen).to(torch.bfloat16)
+    before = _start_weights(3, 2, 700, 4)
+    _, want1, r1 = decode_exact(b, q1, 0.09, before)
+    wantp, rp = prompt_exact(b, qp, cu, 40, 0.09, True, before)
+    try:
+        for kernel, ctas in ((1, 0), (2, 0), (2, 3), (2, 400)):
+            pa.pa_set_option(pa.PA_OPT_DECODE_KERNEL, kernel)
+            pa.pa_set_option(pa.PA_OPT_VARLEN_KERNEL, kernel)
+            pa.pa_set_option(pa.PA_OPT_DECODE_CTAS, ctas)
+            w = before.to(DEV)
+            _decode(pa, b, q1.to(DEV), w, 0.09)
+            _check_weights(w.cpu(), want1, before, b, r1)
+            w = before.to(DEV)
+            _prompt(pa, b, qp.to(DEV), cu, 40, 0.09, w)
+            _check_weights(w.cpu(), wantp, before, b, rp)
+    finally:
+        for o in (pa.PA_OPT_DECODE_KERNEL, pa.PA_OPT_VARLEN_KERNEL, pa.PA_OPT_DECODE_CTAS):
+            pa.pa_set_option(o, 0)
+
+
+def test_check_mode_refuses_bad_batches(pa):
+    """Check mode: indexes are validated on the host, nothing is launched, the weights stay as they are."""
+    b = Batch([50, 20], 2, 128, 16, "bf16", 23).to(DEV)
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device=DEV)
+    w = torch.full((2, 2, 50), 3.0, device=DEV)
+    pa.pa_set_check_mode(True)
+    try:
+        for bad in ("length", "block"):
+            lens, tables = b.dlens.clone(), b.dtables.clone()
+            if bad == "length":
+                lens[1] = 51
+            else:
+                tables[0, 1] = b.num_blocks
+            keep = b.dlens, b.dtables
+            b.dlens, b.dtables = lens, tables
+            with pytest.raises(pa.PAError) as e:
+                _decode(pa, b, q, w, 0.1)
+            assert e.value.status == 3
+            with pytest.raises(pa.PAError) as e:
+                _prompt(pa, b, q, [0, 1, 2], 0, 0.1, w)
+            assert e.value.status == 3
+            b.dlens, b.dtables = keep
+        with pytest.raises(pa.PAError) as e:
+            _prompt(pa, b, torch.zeros((71, 8, 128), dtype=torch.bfloat16, device=DEV), [0, 50, 71], 0, 0.1, w)
+        assert e.value.status == 3  # more new tokens than context
+        _decode(pa, b, q, w, 0.1)
+    finally:
+        pa.pa_set_check_mode(False)
+    assert float(w[0, 0, 49]) != 3.0 and float(w[1, 0, 20]) == 3.0
