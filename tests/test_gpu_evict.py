@@ -197,3 +197,32 @@ def test_evict_graph(pa):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(*outs))
         assert torch.equal(_bits(pools[0]), _bits(b.dk)) and torch.equal(_bits(pools[1]), _bits(b.dv))
+
+
+def test_evict_check_mode(pa):
+    """A block written for one sequence and read by another, a block given twice, lengths that do not fit."""
+    b = Batch([80, 80], 2, 64, 16, "bf16", 13, extra_blocks=6).to(DEV)
+    w = _weights(2, 2, 80, "spread", 6)
+    fresh = torch.arange(b.num_blocks - 6, b.num_blocks, dtype=torch.int32).view(2, 3)
+    pa.pa_set_check_mode(True)
+    try:
+        for bad in ("read", "twice", "range"):
+            nt = fresh.clone()
+            if bad == "read":
+                nt[0, 0] = b.tables[1, 0]
+            elif bad == "twice":
+                nt[0, 0] = nt[1, 1]
+            else:
+                nt[1, 2] = b.num_blocks
+            with pytest.raises(pa.PAError) as e:
+                _run(pa, b, w, 40, 2, 8, nt)
+            assert e.value.status == 3
+        pos = torch.zeros((2, 2, 80), dtype=torch.int32)
+        for rec, seen in (([81, 0], [90, 90]), ([10, 10], [79, 90])):
+            with pytest.raises(pa.PAError) as e:
+                _run(pa, b, w, 40, 2, 8, fresh, pos=pos, rec=rec, seen=seen)
+            assert e.value.status == 3
+        got = _run(pa, b, w, 40, 2, 8, fresh)
+    finally:
+        pa.pa_set_check_mode(False)
+    _check(b, w, got, 40, 2, 8, fresh)

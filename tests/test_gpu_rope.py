@@ -171,3 +171,35 @@ def test_in_place_q_stream_and_graph(pa):
     pa.pa_rope_write_kv(ref, dq, *args, pair_axis=ax)
     torch.cuda.synchronize()
     assert torch.equal(out, ref) and torch.equal(kc, kref)
+
+
+def test_check_mode(pa):
+    (q, k, v), (dq, dk, dv), pos, inv, axis, slots, blocks = _inputs(8, 4, 2, 64, 16, "bf16", 2, 64, 100, 9)
+    kc, vc = (torch.zeros((blocks, 16, 2, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = torch.zeros((8, 4, 64), dtype=torch.bfloat16, device=DEV)
+    twice, far, ax = slots.clone(), slots.clone(), axis.clone()
+    twice[4], far[4], ax[3] = twice[5], blocks * 16, 2
+    pa.pa_set_check_mode(True)
+    try:
+        for sl, a in ((twice, axis), (far, axis), (slots, ax)):
+            with pytest.raises(pa.PAError) as e:
+                pa.pa_rope_write_kv(out, dq, dk, dv, pos.to(DEV), inv.to(DEV), sl.to(DEV), kc, vc, pair_axis=a.to(DEV))
+            assert e.value.status == 3
+        assert not bool(out.any()) and not bool(kc.any())
+        pa.pa_rope_write_kv(out, dq, dk, dv, pos.to(DEV), inv.to(DEV), slots.to(DEV), kc, vc, pair_axis=axis.to(DEV))
+    finally:
+        pa.pa_set_check_mode(False)
+    assert bool(kc.any())
+
+
+def test_binding_refuses(pa):
+    (q, k, v), (dq, dk, dv), pos, inv, axis, slots, blocks = _inputs(8, 4, 2, 64, 16, "bf16", 1, 64, 100, 9)
+    kc, vc = (torch.zeros((blocks, 16, 2, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = torch.zeros((8, 4, 64), dtype=torch.bfloat16, device=DEV)
+    good = [out, dq, dk, dv, pos.to(DEV), inv.to(DEV), slots.to(DEV), kc, vc]
+    for i, bad in ((0, out[:, :2]), (1, dq.float()), (2, dk[:4]), (3, dv.transpose(1, 2)), (4, pos.to(DEV).int()),
+                   (5, inv.to(DEV).float()), (6, slots.to(DEV)[:4]), (2, k)):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises((ValueError, TypeError)):
+            pa.pa_rope_write_kv(*args)
