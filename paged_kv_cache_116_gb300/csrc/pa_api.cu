@@ -813,6 +813,8 @@ static pa_status rope_impl(void* q_out, const void* q, const void* k, const void
     if (num_axes < 1) return fail(PA_ERR_INVALID_ARG, "num_axes must be positive");
     if (rot_dim < 2 || rot_dim % 2 || rot_dim > head_dim)
         return fail(PA_ERR_INVALID_ARG, "rot_dim must be even and in [2, head_dim]");
+    if (((int64_t)num_heads + 2 * (int64_t)num_kv_heads) * head_dim > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "a token's q, k and v must be at most 2^31 - 1 elements");
     if (n == 0) return PA_OK;
     if ((num_heads && (!q_out || !q)) || !k || !v || !positions || !inv_freq || !slot_mapping || !k_cache || !v_cache ||
         (fp8 && (!k_scales || !v_scales)))
@@ -1020,7 +1022,9 @@ static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, 
                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                                              int32_t max_context, int32_t window, int dtype, bool fp8) {
     PromptWeightsPlan p;
-    if (num_seqs <= 0 || total_q <= 0 || num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads) return p;
+    if (num_seqs <= 0 || total_q <= 0 || max_q <= 0 || max_context <= 0 || block_size <= 0 || window < 0 ||
+        num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads)
+        return p;
     const int G = num_heads / num_kv_heads;
     p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, G);
     if (p.tc)
@@ -1042,7 +1046,7 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     if (g != PA_OK) return g;
     if (num_seqs < 0 || total_q < 0 || max_q < 0 || max_blocks < 0 || max_context < 0 || window < 0)
         return fail(PA_ERR_INVALID_ARG, "sizes must be non-negative");
-    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (num_seqs == 0 || total_q == 0 || max_q == 0 || max_context == 0) return PA_OK;
     if (!weights || !q || !k_cache || !block_tables || !seq_lens || !cu_seqlens_q)
         return fail(PA_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(q) || !aligned16(k_cache)) return fail(PA_ERR_INVALID_ARG, "q and the cache must be 16-byte aligned");
@@ -1058,6 +1062,8 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     if (g_options[PA_OPT_VARLEN_KERNEL] == 2 && !plan.tc)
         return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 queries, head_dim 64/128/256 and at "
                                         "most 128 query heads per KV head");
+    if (plan.tc && plan.cut.dense_stride < 0)
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * max_context keys laid out densely must fit in int32");
     if (!workspace || workspace_bytes < plan.bytes())
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                           std::to_string(plan.bytes()) + " needed");

@@ -67,7 +67,7 @@ __device__ __forceinline__ EvictUnit evict_unit(const EvictArgs& a, int u) {
     EvictUnit e;
     e.s = u / a.num_kv_heads;
     e.h = u - e.s * a.num_kv_heads;
-    e.L = max(0, a.context_lens[e.s]);
+    e.L = min(max(0, a.context_lens[e.s]), a.max_context);  // (shared memory holds no more)
     e.c = a.recorded_lens ? min(max(0, a.recorded_lens[e.s]), e.L) : 0;
     e.seen = a.seen_lens ? a.seen_lens[e.s] : e.L;
     e.row = ((int64_t)e.s * a.num_kv_heads + e.h) * a.stride;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
     };
     int2 entry = listed_row(first + lane);
     const int listed = a.counts ? __ldcg(a.counts + u) : -1;
-    const int rows = listed >= 0 ? listed : min(max(0, a.context_lens[s]), a.keep);
+    const int rows = listed >= 0 ? listed : min(max(0, a.context_lens[s]), min(a.keep, a.max_context));
     int2 ahead = entry;
     const int stride = ctas * kMoveWarps * kWarpRows;
     for (; first < rows; first += stride) {

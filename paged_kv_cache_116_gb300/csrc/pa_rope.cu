@@ -302,7 +302,7 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
                      a.k_stride % V == 0 && a.v_stride % V == 0 &&
                      (!FP8 || ((row_items & (row_items - 1)) == 0 && row_items <= 32));
     RopeArgs p = a;
-// Tokens per CTA: more spread the angles' and the items' setup over more
+    // Tokens per CTA: more spread the angles' and the items' setup over more
     // tokens, as long as every SM keeps its four CTAs (8,192 tokens: 41 us
     // with 4, 39 with 8, 40 with 16).
     p.tpb = 8;

@@ -1049,8 +1049,8 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
     // pools that no box fits, and code pools, are laid out densely first
     if (kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256))) {
-        w.dense_stride = (int)(k_tiles * TM);
-        const size_t tokens = (size_t)std::min(num_seqs, kWeightMaxSeqsPerLaunch) * w.dense_stride;
+        const size_t tokens = (size_t)std::min(num_seqs, kWeightMaxSeqsPerLaunch) * (size_t)(k_tiles * TM);
+        w.dense_stride = tokens <= INT32_MAX ? (int)(k_tiles * TM) : -1;  // (refused)
         w.dense_bytes = tokens * num_kv_heads * head_dim * 2;
         if (kv_fp8) w.scale_bytes = tokens * num_kv_heads * sizeof(float);
     }
@@ -1062,10 +1062,6 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
 }
 
 cudaError_t launch_weights_umma(const WeightArgs& a, int32_t num_blocks, std::string* err, cudaStream_t stream) {
-    if (a.dense_stride && (int64_t)a.num_seqs * a.dense_stride > INT32_MAX) {
-        *err = "the dense key layout's rows do not fit in int32";
-        return cudaErrorInvalidValue;
-    }
     if (a.dtype == 1)
         return a.kv_fp8 ? launch_hd<__nv_bfloat16, true>(a, num_blocks, err, stream)
                         : launch_hd<__nv_bfloat16, false>(a, num_blocks, err, stream);

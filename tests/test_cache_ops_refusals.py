@@ -125,3 +125,23 @@ def test_evict_nothing_to_do(lib):
     assert _evict(lib, S=0, w=None) == 0
     assert lib.pa_evict_workspace_size(4, 2, 100, 100) == 0  # nothing can exceed the budget
     assert lib.pa_evict_workspace_size(0, 2, 100, 50) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_empty_contexts_and_huge_sizes(lib, fp8):
+    """max_context 0: no request holds a token.  Sizes beyond int32 are refused before any launch."""
+    assert _prompt(lib, fp8, mc=0, stride=0) == 0
+    assert _prompt(lib, fp8, mq=0) == 0
+    assert _prompt(lib, fp8, mc=1 << 30, stride=1 << 30, bs=12, wsb=1 << 62) == UNSUPPORTED
+    assert _rope(lib, fp8, hkv=1 << 22, hq=1 << 23, ks=1 << 40, vs=1 << 40, qs=1 << 40, nb=1, bs=1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("name, count", [
+    ("pa_decode_weights_workspace_size", 7), ("pa_decode_weights_fp8_workspace_size", 7),
+    ("pa_prompt_weights_workspace_size", 10), ("pa_prompt_weights_fp8_workspace_size", 10),
+    ("pa_evict_workspace_size", 4)])
+def test_workspace_sizes_answer_any_numbers(lib, name, count):
+    """Zeros, negatives and the largest integers: a number comes back, nothing divides by zero."""
+    gen = __import__("random").Random(1)
+    for _ in range(4000):
+        getattr(lib, name)(*[gen.choice((-2 ** 31, -1, 0, 1, 7, 16, 64, 128, 1000, 2 ** 31 - 1)) for _ in range(count)])
