@@ -303,10 +303,10 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
                      (!FP8 || ((row_items & (row_items - 1)) == 0 && row_items <= 32));
     RopeArgs p = a;
     // Tokens per CTA: more spread the angles' and the items' setup over more
-    // tokens, as long as every SM keeps its four CTAs (8,192 tokens: 41 us
-    // with 4, 39 with 8, 40 with 16).
-    p.tpb = 8;
-    while (p.tpb > 1 && a.n < (int64_t)p.tpb * 152 * 4) p.tpb /= 2;
+    // tokens; the batch in one wave of four CTAs per SM (8,192 tokens: 37.5 us
+    // with 14, 39.5 in two waves of 8; 1,999 code-pool tokens: 9.5 us with 4,
+    // 11.5 with 2).
+    p.tpb = (int)std::min<int64_t>(16, (a.n + 152 * 4 - 1) / (152 * 4));
     // few tokens: their items over several CTAs each, which repeat the angles
     const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
     const int items = (a.num_heads + 2 * a.num_kv_heads) * (a.head_dim / (vec ? 2 * V : 2));
