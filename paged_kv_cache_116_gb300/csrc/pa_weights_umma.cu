@@ -102,11 +102,11 @@ struct WGeo {
     static constexpr int CHB = TM * 128;      // bytes of one chunk of a tile
     static constexpr int TILE = CH * CHB;
     static constexpr int RING_OFF = NA * TILE;
-    // pass 2: the streamed query tiles' statistics, SRING x {-M, 1 / l}[128];
-    // few rows: the stationary ones', [NA]{-M, 1 / l}[128]
+    // pass 2: the streamed query tiles' statistics, [SRING][128]; few rows:
+    // the stationary ones', [NA][128]
     static constexpr int SRING = 8;
     static constexpr int STAT_OFF = RING_OFF + RING * TILE;
-    static constexpr int JOIN_OFF = STAT_OFF + SRING * 2 * TM * 4;  // results handed over, float2[3][128]
+    static constexpr int JOIN_OFF = STAT_OFF + SRING * TM * 4;  // results handed over, float2[3][128]
     static constexpr int BAR_OFF = JOIN_OFF + 3 * TM * 8;
     // a_full, a_empty, b_full[RING], b_empty[RING], d_full[NWG],
     // s_full[SRING], i_full[IRING], d_empty[NWG], s_empty[SRING],
@@ -132,9 +132,17 @@ struct Item {
     int z;       // piece of the streamed axis
 };
 
-// The statistics of one row (an index into a piece of p.stats), joined over
-// pass 1's key splits: (-M, 1 / l).
-__device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) {
+// What pass 2 needs of a row: its weights are exp2(x + statistic), the
+// statistic being -(M + log2 l).  One number per column costs pass 2 half the
+// shared-memory reads of -M and 1 / l and an addition instead of an FMA (8,192
+// tokens: 498 against 521 us); its rounding, 2^-24 of its size, is that of a
+// score.  A row with only scores of -infinity (l = 0) gets +infinity, hence
+// NaN weights, as its softmax has.
+__device__ __forceinline__ float row_stat(float m, float l) { return (m == -INFINITY ? 0.f : -m) - log2f(l); }
+
+// The statistic of one row (an index into a piece of p.stats), joined over
+// pass 1's key splits.
+__device__ __forceinline__ float joined_stat(const WeightArgs& p, int64_t row) {
     const int64_t part = (int64_t)p.total_q * p.num_heads;
     constexpr int B = 8;  // pieces in flight
     float2 s = make_float2(-INFINITY, 0.f);
@@ -154,7 +162,7 @@ __device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) 
             s.x = mn;
         }
     }
-    return make_float2(s.x == -INFINITY ? 0.f : -s.x, 1.f / s.y);
+    return row_stat(s.x, s.y);
 }
 
 enum Pass { kRowStats = 1, kKeyWeights = 2, kFewRows = 3 };
@@ -189,8 +197,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);
     // keys streamed with their scales: kScaleRing x [128] behind the stationary statistics
     constexpr int kScaleRing = 4, kRing = PASS == kKeyWeights ? Gm::SRING : kScaleRing;
-    float* scale_s = stat_s + NA * 2 * TM;
-    static_assert(kScaleRing * TM + NA * 2 * TM <= Gm::SRING * 2 * TM, "scales fit behind the statistics");
+    float* scale_s = stat_s + NA * TM;
+    static_assert(kScaleRing + NA <= Gm::SRING, "scales fit behind the statistics");
     float2* join_s = reinterpret_cast<float2*>(base + Gm::JOIN_OFF);
     volatile uint32_t* taddr_slot = reinterpret_cast<volatile uint32_t*>(base + Gm::ADDR_OFF);
     int32_t* prefix = reinterpret_cast<int32_t*>(base + Gm::PREF_OFF);
@@ -393,10 +401,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     load_queries(w, t, dst, &b_full[slot]);
                     const int sl = nb % Gm::SRING;
                     if (!(run = wait(&s_empty[sl], (uint32_t)(nb / Gm::SRING & 1) ^ 1u))) break;
-                    expect(&s_full[sl], 2 * TM * 4);
+                    expect(&s_full[sl], TM * 4);
                     if (lane == 0)
-                        bulk_g2s(stat_s + sl * 2 * TM, p.tile_stats + stat_tile(w.sq, w.h, t) * 2 * TM, 2 * TM * 4,
-                                 &s_full[sl]);
+                        bulk_g2s(stat_s + sl * TM, p.tile_stats + stat_tile(w.sq, w.h, t) * TM, TM * 4, &s_full[sl]);
                 }
             }
         }
@@ -513,35 +520,39 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(g_bar);
             return mbar_wait_ns(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
         };
-        // exp2(x - M) / l of `n` accumulators' columns [q, q + 16) for this
-        // thread's keys, added to v[]: column c counts where lo[] <= c < end
-        auto add_columns = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm, const float* il,
-                               int c0, bool whole, const int (&lo)[2], int end, float (&v)[2],
+        // exp2(x + statistic) of 16 columns of one or both stationary tiles'
+        // accumulators, added to v[] and v2[] of this thread's keys
+        auto add_whole = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm,
+                             unsigned long long (&v2)[2]) {
+            constexpr int N = decltype(count)::value;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const unsigned long long sv = f32x2_pack(ks[k], ks[k]);
+                    float x0, x1, x2, x3;
+                    f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j], a[k][4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
+                    f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j + 2], a[k][4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
+                    v2[k] = add_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), v2[k]);
+                    v2[k] = add_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), v2[k]);
+                }
+            }
+        };
+        // the same where a mask may cut: column c0 + j counts if lo[] <= c0 + j < end
+        auto add_columns = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm, int c0, bool whole, const int (&lo)[2], int end, float (&v)[2],
                                unsigned long long (&v2)[2]) {
             constexpr int N = decltype(count)::value;
             // columns past the tile's T G rows hold whatever was there
             if (whole && c0 + 16 <= TT * G) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);
-                    const float4 i4 = *reinterpret_cast<const float4*>(il + 4 * j);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        const unsigned long long sv = f32x2_pack(ks[k], ks[k]);
-                        float x0, x1, x2, x3;
-                        f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j], a[k][4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
-                        f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j + 2], a[k][4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
-                        v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), f32x2_pack(i4.x, i4.y), v2[k]);
-                        v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), f32x2_pack(i4.z, i4.w), v2[k]);
-                    }
-                }
+                add_whole(count, a, ks, nm, v2);
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
                     for (int k = 0; k < N; ++k)
                         if (c0 + j >= lo[k] && c0 + j < end)
-                            v[k] = fmaf(fast_exp2(fmaf(a[k][j], ks[k], nm[j])), il[j], v[k]);
+                            v[k] += fast_exp2(fmaf(a[k][j], ks[k], nm[j]));
             }
         };
         auto store_weight = [&](const Item& w, int key, float v) {
@@ -595,12 +606,15 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         sum = 0.f;
                         unsigned long long s2 = f32x2_pack(0.f, 0.f);
                         const unsigned long long sv = f32x2_pack(sl, sl), nv = f32x2_pack(neg, neg);
-#pragma unroll
-                        for (int q = 0; q < TM / 32; ++q) {
-                            float a[32];
-                            tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
-                            tmem_wait_ld();
-                            if (full) {
+                        // (rolled, and the masked form apart: the four groups' loops
+                        // otherwise wait for instructions, 575 against 521 us
+                        // with both passes so, 8,192 tokens)
+                        if (full) {
+#pragma unroll 1
+                            for (int q = 0; q < TM / 32; ++q) {
+                                float a[32];
+                                tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
+                                tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) {
                                     const float2 k2 = SC ? *reinterpret_cast<const float2*>(ks + 32 * q + 2 * j) : make_float2(sl, sl);
@@ -608,7 +622,13 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                                     f32x2_unpack(fma_f32x2(f32x2_pack(a[2 * j], a[2 * j + 1]), SC ? f32x2_pack(k2.x, k2.y) : sv, nv), x0, x1);
                                     s2 = add_f32x2(s2, f32x2_pack(fast_exp2(x0), fast_exp2(x1)));
                                 }
-                            } else {
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int q = 0; q < TM / 32; ++q) {
+                                float a[32];
+                                tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
+                                tmem_wait_ld();
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
                                     sum += 32 * q + j <= vis ? fast_exp2(fmaf(a[j], SC ? ks[32 * q + j] : sl, neg)) : 0.f;
@@ -620,7 +640,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     };
                     auto max_pass = [&]() -> float {
                         float mt = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < TM / 32; ++q) {
                             float a[32];
                             tmem_ld32(acc + 2 * TM * hi + 32 * q, a);
@@ -675,10 +695,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 for (int g = 0; g < 3; ++g) n_join[g] += alone || g != 1;
                 if (!run) break;
                 if (taker) {
-                    if (splits == 1) {  // final: -M and 1 / l by column
-                        float* st = p.tile_stats + stat_tile(w.sq, w.h, w.a0 + x) * 2 * TM;
-                        st[m] = valid && m_used != -INFINITY ? -m_used : 0.f;
-                        st[TM + m] = valid ? 1.f / l : 0.f;
+                    if (splits == 1) {
+                        p.tile_stats[stat_tile(w.sq, w.h, w.a0 + x) * TM + m] = valid ? row_stat(m_used, l) : 0.f;
                     } else if (valid) {
                         p.stats[(int64_t)w.z * part + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + g] =
                             make_float2(m_used, l);
@@ -696,8 +714,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
-                    const float* nm = stat_s + sl * 2 * TM + hi * HC;
-                    const float* il = nm + TM;
+                    const float* nm = stat_s + sl * TM + hi * HC;
                     if (!(run = mbar_wait_ns(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS) && acquire(0) &&
                                 (w.na < 2 || acquire(NA - 1))))
                         break;
@@ -714,7 +731,21 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     unsigned long long v2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
                     using Both = std::integral_constant<int, NA>;
                     using One = std::integral_constant<int, 1>;
-#pragma unroll
+                    if (NA == 2 && full && w.na == 2 && TT * G == TM) {
+#pragma unroll 2
+                        for (int q = 0; q < HC / 16; ++q) {
+                            float a[2][16];
+                            tmem_ld16(acc + hi * HC + 16 * q, a[0]);
+                            tmem_ld16(acc + 2 * TM + hi * HC + 16 * q, a[1]);
+                            tmem_wait_ld();
+                            if (q == HC / 16 - 1) {
+                                release(0);
+                                release(NA - 1);
+                            }
+                            add_whole(Both(), a, ks, nm + 16 * q, v2);
+                        }
+                    } else {
+#pragma unroll 1
                     for (int q = 0; q < HC / 16; ++q) {
                         float a[2][16];
                         tmem_ld16(acc + hi * HC + 16 * q, a[0]);
@@ -724,8 +755,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             release(0);
                             if (w.na == 2) release(NA - 1);
                         }
-                        if (w.na == 2) add_columns(Both(), a, ks, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
-                        else add_columns(One(), a, ks, nm + 16 * q, il + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                        if (w.na == 2) add_columns(Both(), a, ks, nm + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                        else add_columns(One(), a, ks, nm + 16 * q, hi * HC + 16 * q, full, lo, end, v, v2);
+                    }
                     }
 #pragma unroll
                     for (int x = 0; x < NA; ++x) {
@@ -758,10 +790,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 // few rows: the item's query tiles stay, their statistics with them
                 if (!(run = meet())) break;  // the previous item's are used up
                 if (wg < NA) {
-                    const float* st = p.tile_stats + stat_tile(w.sq, w.h, wg) * 2 * TM;
-                    const bool have = wg < w.na;
-                    stat_s[wg * 2 * TM + m] = have ? __ldcg(st + m) : 0.f;
-                    stat_s[wg * 2 * TM + TM + m] = have ? __ldcg(st + TM + m) : 0.f;
+                    const float* st = p.tile_stats + stat_tile(w.sq, w.h, wg) * TM;
+                    stat_s[wg * TM + m] = wg < w.na ? __ldcg(st + m) : 0.f;
                 }
                 if (!(run = meet())) break;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
@@ -785,15 +815,26 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         const bool full = __all_sync(0xffffffffu, lo[0] <= 0 && end == TT * G);
                         float vx[2] = {0.f, 0.f};
                         unsigned long long v2[2] = {f32x2_pack(0.f, 0.f), 0};
-#pragma unroll
-                        for (int q = 0; q < HC / 16; ++q) {
-                            float a[2][16];
-                            tmem_ld16(acc + 2 * TM * ax + hi * HC + 16 * q, a[0]);
-                            tmem_wait_ld();
-                            if (q == HC / 16 - 1) release(ax);
-                            const float* nm = stat_s + x * 2 * TM + hi * HC + 16 * q;
-                            add_columns(std::integral_constant<int, 1>(), a, ks, nm, nm + TM, hi * HC + 16 * q, full, lo, end,
-                                        vx, v2);
+                        const float* nm = stat_s + x * TM + hi * HC;
+                        if (full && TT * G == TM) {
+#pragma unroll 1
+                            for (int q = 0; q < HC / 16; ++q) {
+                                float a[2][16];
+                                tmem_ld16(acc + 2 * TM * ax + hi * HC + 16 * q, a[0]);
+                                tmem_wait_ld();
+                                if (q == HC / 16 - 1) release(ax);
+                                add_whole(std::integral_constant<int, 1>(), a, ks, nm + 16 * q, v2);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int q = 0; q < HC / 16; ++q) {
+                                float a[2][16];
+                                tmem_ld16(acc + 2 * TM * ax + hi * HC + 16 * q, a[0]);
+                                tmem_wait_ld();
+                                if (q == HC / 16 - 1) release(ax);
+                                add_columns(std::integral_constant<int, 1>(), a, ks, nm + 16 * q,
+                                            hi * HC + 16 * q, full, lo, end, vx, v2);
+                            }
                         }
                         float s0, s1;
                         f32x2_unpack(v2[0], s0, s1);
@@ -883,11 +924,8 @@ __global__ void __launch_bounds__(TM) stats_join_kernel(const WeightArgs p) {
         locate_work(prefix, p.num_seqs, p.num_kv_heads, it, s, h, tile);
         const WeightSeq sq = weight_seq(p, s);
         const int tok = tile * TT + m / G;
-        float2 v = make_float2(0.f, 0.f);
-        if (m < TT * G && tok < sq.rows) v = joined_stat(p, (int64_t)(sq.row0 + tok) * p.num_heads + h * G + m % G);
-        float* st = p.tile_stats + ((int64_t)h * p.stat_tiles + sq.row0 / TT + s + tile) * 2 * TM;
-        st[m] = v.x;
-        st[TM + m] = v.y;
+        p.tile_stats[((int64_t)h * p.stat_tiles + sq.row0 / TT + s + tile) * TM + m] =
+            m < TT * G && tok < sq.rows ? joined_stat(p, (int64_t)(sq.row0 + tok) * p.num_heads + h * G + m % G) : 0.f;
     }
 }
 
@@ -1046,7 +1084,7 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
     w.stat_tiles = total_q / TT + num_seqs + 1;
-    w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
+    w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * TM * sizeof(float);
     // pools that no box fits, and code pools, are laid out densely first
     if (kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256))) {
         const size_t tokens = (size_t)std::min(num_seqs, kWeightMaxSeqsPerLaunch) * (size_t)(k_tiles * TM);
