@@ -838,7 +838,7 @@ def main():
                     "<FP8>" if fp8 else "", call) if tc_decode else "attn_simt_kernel (%s, CUDA-core path)" % call),
                 "achieved": achieved, "peak": peaks["hbm_gbs"], "unit": "GB/s", "frac": achieved / peaks["hbm_gbs"],
                 "peak_kind": kind + " hbm_gbs", "algorithmic_bytes": alg,
-                "traffic": traffic_record(tkey, "pa_decode_tc.cu") if tc_decode else None,
+                "traffic": traffic_record(tkey, "pa_decode_tc.cuh") if tc_decode else None,
                 "kernel_us": kern_ms * 1e3, "kernel_us_median_of_51": kern_med_us}
     elif fp8 and w.dtype in ("bf16", "f16") and hd == 128 and (bs == 8 or (bs % 16 == 0 and bs <= 256)):
         # the mixed step over a code cache on the tensor cores (codes turned

@@ -21,9 +21,15 @@
 // the G query heads of a KV head (row t G + g).
 //
 // Up to head_dim 128 a CTA keeps two stationary tiles, so that every streamed
-// tile feeds two MMAs.  With one (and two CTAs per SM) the streamed tiles
-// crossed from L2 at 9.3 TB/s, which bounded the kernel (8,192-token prompt,
-// 32 / 8 heads: 0.93 ms).
+// tile feeds two MMAs: with one the streamed tiles crossed from L2 twice as
+// often, a third more time in all (8,192-token prompt, 32 / 8 heads of 128).
+//
+// Bound: the groups' work on the columns, by issue slots and the exponential
+// unit (32 per cycle and SM, 512 cycles per accumulator, as many as its MMAs
+// take); a pass spends about 1,070 cycles per accumulator, 250 us on 8,192
+// tokens with 32 / 8 heads (550 GFLOP in both passes: 1.10 PFLOP/s).  With a
+// short window over long contexts: the two reads of the keys (4 x 32,768 keys
+// of 8 heads, 32 rows: 55-65 us per pass, 4.6 TB/s).
 //
 // Pools with block_size 8 or a multiple of 16 up to 256 are read in place.
 // Others, and code pools, are first laid out densely in the workspace, codes
@@ -37,8 +43,8 @@
 // Roles (20 warps up to head_dim 128): four groups of four warps work the
 // accumulator tiles, one row or key per thread; two warps load tiles by TMA
 // (128-byte swizzle; keys through the block table, one 16-token group per
-// box); one warp per stationary tile issues its MMAs (one warp for both left
-// the tensor pipe idle while it waited: 590 of 1,090 cycles per accumulator).
+// box); one warp per stationary tile issues its MMAs (one warp for both: 3 % slower
+// on 8,192 tokens).
 // Accumulators are (stationary tile x, parity of the streamed tile within its
 // item), 128 columns each; the parity decides which group adds what up, so it
 // may not depend on what a CTA worked before.  In pass 1 a group owns one of them; in pass 2 it owns half of
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             int ok = 0;
             if (lane == 0 && (ok = mbar_wait_ns(&i_empty[k], ph ^ 1u, WAIT_NS))) {
                 // (drawn only now: an item drawn ahead would wait for this CTA
-                // while others run dry, 0.66 against 0.60 ms on 8,192 tokens)
+                // while others run dry, 10 % more time on 8,192 tokens)
                 const int64_t it = n_item == 0 ? blockIdx.x : (int64_t)gridDim.x + atomicAdd(p.next_item + (PASS > 1), 1u);
                 item_s[k] = it < items ? (int)it : -1;
                 mbar_arrive(&i_full[k]);
@@ -863,7 +869,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 // Lays a batch's keys out densely, request s's token t at row s * dense_stride
 // + t: codes become their exact values in T and their scales, times the
 // score's, a row per (request, KV head); 16-bit keys are copied.  A thread
-// moves 16 bytes of pool.  Bound: HBM.
+// moves 16 bytes of pool.  Bound: HBM; read and written once it costs less
+// than boxes of 12 or 1 rows would (4 x 32,768 code keys of 8 heads: about a
+// third of the call's 235 us).
 template <typename T, bool FP8>
 __global__ void __launch_bounds__(256) dense_keys_kernel(const WeightArgs p, T* __restrict__ keys, float* __restrict__ scales) {
     constexpr int E = FP8 ? 16 : 8;  // elements per 16 bytes
@@ -1056,10 +1064,10 @@ bool weights_umma_supported(int dtype, int head_dim, int group) {
 
 // How the work is cut: pieces of the streamed axis, where there are few
 // stationary tiles.  Pieces of fewer than 16 tiles spend much of their time
-// starting (2,048-token prompt: 103 us with pieces of 4 or more, 85 us so).
+// starting (2,048-token prompt: 1.2 x the time with pieces of 4 or more).
 // Items of unequal length (causal tiles) are cut so that there are two per SM
-// for the scheduling to even out (8,192 tokens: 560 us, 568 with four per SM,
-// 626 with eight); few rows over long contexts are equal pieces, as many as
+// for the scheduling to even out (8,192 tokens: 1 % slower with four per SM,
+// 12 % with eight); few rows over long contexts are equal pieces, as many as
 // make three whole rounds over the SMs.
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_context,
