@@ -992,10 +992,9 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
 // the running state by the log-sum-exp rule, in warp order.  Warps with
 // empty ranges (only when the batch has fewer tiles than the decode grid
 // has warps) hold no record.
-template <typename T, int HD>
+template <typename T, int HD, int B = HD <= 128 ? 8 : 4>  // B: records per batch
 __device__ __forceinline__ void merge_item(const TcParams& p, const int64_t TW, const int32_t* mprefix, int block) {
     constexpr int E = HD / 16;             // output elements per lane
-    constexpr int B = HD <= 128 ? 8 : 4;   // records per batch
     const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
     const int64_t item = (int64_t)block * 16 + (threadIdx.x >> 4);
     if (item >= (int64_t)S * Hkv * G) return;
@@ -1086,12 +1085,14 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, con
 // does, joins their (m, l) -- one warp per head, lanes over the pieces -- and
 // each thread then reads its tokens' scores (G contiguous floats) and updates
 // one weight per token.  x - M is taken before the division by L: a
-// log-sum-exp rounded to fp32 would cost |lse| 2^-24 in every weight.
-constexpr int kWeightChunk = 2048;
+// log-sum-exp rounded to fp32 would cost |lse| 2^-24 in every weight.  Smaller
+// batches of records and four tokens per thread let three CTAs share an SM
+// (two with eight of each: 2 us more on every batch of 70-200 us).
+constexpr int kWeightChunk = 1024;
 constexpr int kWeightMaxCtas = 152 * 16;  // beyond this a CTA takes several chunks
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) decode_merge_weights_kernel(const TcParams p, const int64_t TW,
+__global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcParams p, const int64_t TW,
                                                                    float* __restrict__ weights, int64_t stride,
                                                                    int merge_blocks, int chunks) {
     extern __shared__ int32_t mprefix[];  // [num_seqs + 1]
@@ -1099,7 +1100,7 @@ __global__ void __launch_bounds__(256) decode_merge_weights_kernel(const TcParam
     const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
     if ((int)blockIdx.x < merge_blocks) {
         tile_prefix(p.context_lens, S, mprefix, nullptr);
-        merge_item<T, HD>(p, TW, mprefix, blockIdx.x);
+        merge_item<T, HD, HD <= 128 ? 4 : 2>(p, TW, mprefix, blockIdx.x);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
