@@ -30,11 +30,15 @@
 //   evict_move_kernel copies the listed rows, all of the GPU's warps over all
 //   units' lists.
 // Bound: the select kernel by the latency of its few passes over shared
-// memory, the move kernel by HBM (each listed row is read and written once).
+// memory (512 heads of 1,040 tokens: 11 us, of which 2 us each for loading,
+// the two digits, ranking and writing; 64 heads of 32,768: 21 us, a third of
+// it the first pass), the move kernel by HBM (each listed row is read and
+// written once: 262,144 rows of 2 x 256 bytes at 4.8 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -86,7 +90,7 @@ template <int NT, bool STAGED>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     constexpr int NW = NT / 32, PER = kBins / NT;  // warps; buckets per thread
     extern __shared__ uint32_t dyn[];
-    __shared__ uint32_t hist[kBins];
+    __shared__ alignas(16) uint32_t hist[kBins];
     __shared__ int sh_warp[NW];
     __shared__ uint64_t sh_both[NW];
     __shared__ int sh_digit, sh_left, sh_count, sh_rows;
@@ -162,12 +166,19 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         }
         __syncthreads();
         // buckets from the top: thread t holds PER of them
+        // (as vectors, whose lanes fall into different banks)
+        using BV = typename std::conditional<PER == 2, uint2, uint4>::type;
+        constexpr int VE = sizeof(BV) / 4, NV = PER / VE;
         int mine[PER], sum = 0;
+        BV* own = reinterpret_cast<BV*>(hist + kBins - (tid + 1) * PER);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            mine[i] = (int)hist[kBins - 1 - (tid * PER + i)];
-            sum += mine[i];
+        for (int v = 0; v < NV; ++v) {
+            const BV b = own[v];
+            memcpy(mine + v * VE, &b, sizeof(b));
+            own[v] = BV{};
         }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) sum += mine[i];
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -176,22 +187,19 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
         }
         if (lane == 31) sh_warp[warp] = incl;
         __syncthreads();
-        int before = incl - sum;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) before += i < warp ? sh_warp[i] : 0;
+        int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? sh_warp[lane] : 0);
         if (before < need && need <= before + sum) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                if (before < need && need <= before + mine[i]) {
+                const int n = mine[PER - 1 - i];
+                if (before < need && need <= before + n) {
                     sh_digit = kBins - 1 - (tid * PER + i);
                     sh_left = need - before;
-                    sh_count = mine[i];
+                    sh_count = n;
                 }
-                before += mine[i];
+                before += n;
             }
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) hist[kBins - 1 - (tid * PER + i)] = 0;
         __syncthreads();
         prefix |= (uint32_t)sh_digit << shift;
         bits |= (uint32_t)(width - 1) << shift;
@@ -321,9 +329,10 @@ constexpr int kMoveCtas = 152 * 16;  // wanted over all units
 
 // Each unit has `ctas` CTAs, whose warps take eight rows of its list in turn
 // (few enough that a short list spreads, and nobody visits what no list
-// holds); a warp's lanes copy the rows' K and V vectors, U of them in flight each.
+// holds); a warp's lanes copy the rows' K and V vectors, U of them in flight
+// each, six CTAs per SM (five: 2 us more on moves of 35-50 us; eight spill).
 template <int VB>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const EvictArgs a, int ctas) {
+__global__ void __launch_bounds__(kMoveWarps * 32, 6) evict_move_kernel(const EvictArgs a, int ctas) {
     using V = typename VecOf<VB>::V;
     constexpr int U = 8;
     pdl_wait_primary();
