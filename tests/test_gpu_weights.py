@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_ops import Batch, DTYPES, decode_exact, prompt_exact
+from cache_ops import Batch, DTYPES, decode_exact, prompt_exact, weight_rtol
 from helpers import within_tol
 
 pytestmark = pytest.mark.gpu
@@ -346,3 +346,90 @@ def test_check_mode_refuses_bad_batches(pa):
     finally:
         pa.pa_set_check_mode(False)
     assert float(w[0, 0, 49]) != 3.0 and float(w[1, 0, 20]) == 3.0
+
+
+def test_prompt_weights_more_requests_than_a_launch(pa):
+    """Over 4,096 requests with long ones on both sides of the cut; the CUDA-core form answers for all of them."""
+    S, hkv, hd = 4105, 2, 64
+    new = [1] * S
+    lens = [2 + s % 5 for s in range(S)]
+    for s, n in ((0, 200), (4095, 150), (4096, 180), (4104, 300)):
+        new[s], lens[s] = n, n + s % 3
+    cu = np.concatenate(([0], np.cumsum(new))).tolist()
+    b = Batch(lens, hkv, hd, 16, "bf16", 31).to(DEV)
+    q = torch.randn((cu[-1], 4, hd), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    before = _start_weights(S, hkv, 301, 2)
+    got, ref = before.to(DEV), before.to(DEV)
+    _prompt(pa, b, q, cu, 0, 0.1, got)
+    try:
+        pa.pa_set_option(pa.PA_OPT_VARLEN_KERNEL, 1)
+        _prompt(pa, b, q, cu, 0, 0.1, ref)
+    finally:
+        pa.pa_set_option(pa.PA_OPT_VARLEN_KERNEL, 0)
+    mag = float(q.float().norm(dim=-1).max() * b.k.float().nan_to_num().norm(dim=-1).max()) * 0.1 * 1.45
+    rtol = 2 * weight_rtol(hd, mag, 301, 600)  # both are off
+    for s in range(S):
+        lens_s = lens[s]
+        assert torch.equal(got[s, :, lens_s:], ref[s, :, lens_s:])
+    assert bool(((got - ref).abs() <= rtol * ref.abs()).all()), float(((got - ref).abs() / ref.abs()).max())
+
+
+def test_prompt_weights_graphs_share_a_workspace_and_streams_do_not(pa):
+    """Two captured calls on one workspace, replayed in turn; then the same two and an attention step at once on three
+    streams with memory of their own.  Every run gives the eager call's bits."""
+    b = Batch([700, 90, 1500], 4, 64, 16, "bf16", 41).to(DEV)
+    cu, mq, mc = [0, 600, 640, 1000], 600, 1500
+    gen = torch.Generator().manual_seed(3)
+    q = [torch.randn((1000, 8, 64), generator=gen).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    dcu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    size = [pa.pa_prompt_weights_workspace_size(3, 1000, mq, 8, 4, 64, 16, mc, win, torch.bfloat16) for win in (0, 16)]
+
+    def call(i, w, ws):
+        pa.pa_prompt_weights(w, q[i], b.dk, b.dtables, b.dlens, dcu, mq, mc, (0, 16)[i], 0.125, workspace=ws)
+
+    want = [torch.zeros((3, 4, mc), device=DEV) for _ in range(2)]
+    got = [torch.zeros((3, 4, mc), device=DEV) for _ in range(2)]
+    shared = torch.empty(max(size), dtype=torch.uint8, device=DEV)
+    for i in range(2):
+        call(i, want[i], shared)
+        want[i].zero_()
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, capture_error_mode="thread_local"):
+            call(i, got[i], shared)
+        graphs.append(g)
+    for _ in range(3):
+        for i in range(2):
+            graphs[i].replay()
+    own = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in size]
+    for _ in range(3):
+        for i in range(2):
+            call(i, want[i], own[i])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    def attend(out, ws):
+        pa.pa_varlen(out, q[0], b.dk, b.dv, b.dtables, b.dlens, dcu, mq, mc, 0.125, workspace=ws)
+
+    n = pa.pa_varlen_workspace_size(3, 1000, mq, 8, 4, 64, 16, mc, torch.bfloat16)
+    vws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+    ref, out = torch.empty_like(q[0]), torch.empty_like(q[0])
+    attend(ref, vws)
+    for t in got + want:
+        t.zero_()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i, got[i], own[i])
+        with torch.cuda.stream(streams[2]):
+            attend(out, vws)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            call(i, want[i], shared)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(out, ref)
