@@ -868,13 +868,14 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 
 // Lays a batch's keys out densely, request s's token t at row s * dense_stride
 // + t: codes become their exact values in T and their scales, times the
-// score's, a row per (request, KV head); 16-bit keys are copied.  A thread
-// moves 16 bytes of pool.  Bound: HBM; read and written once it costs less
-// than boxes of 12 or 1 rows would (4 x 32,768 code keys of 8 heads: about a
-// third of the call's 235 us).
+// score's, a row per (request, KV head); 16-bit keys are copied.  A CTA takes
+// 16 tokens at a time, a thread 16 bytes of pool, four in flight.  Bound: HBM
+// (4 x 32,768 code keys of 8 heads: 403 MB in 77 us, 5.2 TB/s; with one load
+// in flight 95 us).
+constexpr int kDenseTokens = 16;
 template <typename T, bool FP8>
 __global__ void __launch_bounds__(256) dense_keys_kernel(const WeightArgs p, T* __restrict__ keys, float* __restrict__ scales) {
-    constexpr int E = FP8 ? 16 : 8;  // elements per 16 bytes
+    constexpr int E = FP8 ? 16 : 8, U = 4;  // elements per 16 bytes
     pdl_wait_primary();
     pdl_launch_dependents();
     const int row = p.num_kv_heads * p.head_dim, chunks = row / E, bs = p.block_size;
@@ -882,37 +883,51 @@ __global__ void __launch_bounds__(256) dense_keys_kernel(const WeightArgs p, T* 
         const WeightSeq sq = weight_seq(p, s);
         if (sq.rows == 0) continue;
         const int32_t* table = p.block_tables + (int64_t)s * p.max_blocks;
-        const int64_t all = (int64_t)sq.L * chunks;
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-            const int t = (int)(i / chunks), c = (int)(i - (int64_t)t * chunks);
-            const int64_t blk = table[t / bs];
-            const int off = t % bs;
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.k_cache) + (blk * bs + off) * chunks + c);
-            uint4* dst = reinterpret_cast<uint4*>(keys + ((int64_t)s * p.dense_stride + t) * row + c * E);
-            if constexpr (FP8) {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[8];
+        for (int t0 = blockIdx.x * kDenseTokens; t0 < sq.L; t0 += gridDim.x * kDenseTokens) {
+            const int n = min(kDenseTokens, sq.L - t0) * chunks;
+            for (int e0 = threadIdx.x; e0 < n; e0 += 256 * U) {
+                uint4 v[U];
+                float sc[U];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t lo, hi;
-                    e4m3x4_to_f16x2x2(w[k], lo, hi);
-                    if constexpr (std::is_same<T, __half>::value) {
-                        o[2 * k] = lo;
-                        o[2 * k + 1] = hi;
-                    } else {  // every code is a bf16 value as well
-                        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                        o[2 * k] = pack2<T>(a.x, a.y);
-                        o[2 * k + 1] = pack2<T>(b.x, b.y);
+                for (int u = 0; u < U; ++u) {
+                    const int e = e0 + 256 * u;
+                    if (e >= n) break;
+                    const int r = e / chunks, c = e - r * chunks, b = (t0 + r) / bs, off = t0 + r - b * bs;
+                    const int64_t blk = table[b];
+                    v[u] = __ldcg(reinterpret_cast<const uint4*>(p.k_cache) + (blk * bs + off) * chunks + c);
+                    if (FP8 && c < p.num_kv_heads) sc[u] = __ldcg(p.k_scales + (blk * p.num_kv_heads + c) * bs + off);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int e = e0 + 256 * u;
+                    if (e >= n) break;
+                    const int r = e / chunks, c = e - r * chunks, t = t0 + r;
+                    uint4* dst = reinterpret_cast<uint4*>(keys + ((int64_t)s * p.dense_stride + t) * row + c * E);
+                    if constexpr (FP8) {
+                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t lo, hi;
+                            e4m3x4_to_f16x2x2(w[k], lo, hi);
+                            if constexpr (std::is_same<T, __half>::value) {
+                                o[2 * k] = lo;
+                                o[2 * k + 1] = hi;
+                            } else {  // every code is a bf16 value as well
+                                const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+                                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                                o[2 * k] = pack2<T>(a.x, a.y);
+                                o[2 * k + 1] = pack2<T>(b.x, b.y);
+                            }
+                        }
+                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        if (c < p.num_kv_heads)
+                            scales[((int64_t)s * p.num_kv_heads + c) * p.dense_stride + t] = p.scale_log2 * sc[u];
+                    } else {
+                        *dst = v[u];
                     }
                 }
-                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                if (c < p.num_kv_heads)
-                    scales[((int64_t)s * p.num_kv_heads + c) * p.dense_stride + t] =
-                        p.scale_log2 * __ldcg(p.k_scales + (blk * p.num_kv_heads + c) * bs + off);
-            } else {
-                *dst = v;
             }
         }
     }
@@ -997,7 +1012,7 @@ cudaError_t launch_umma(const WeightArgs& args, int32_t num_blocks, std::string*
     int64_t k_rows = (int64_t)num_blocks * a.block_size;
     if (a.dense_stride) {
         T* keys = static_cast<T*>(a.dense_keys);
-        const int64_t per = ((int64_t)a.max_context * a.num_kv_heads * HD / (SC ? 16 : 8) + 255) / 256;
+        const int64_t per = (a.max_context + kDenseTokens - 1) / kDenseTokens;
         const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(per, std::max<int64_t>(1, 8 * sms / a.num_seqs))),
                         (unsigned)a.num_seqs);
         e = launch_pdl(dense_keys_kernel<T, SC>, grid, dim3(256), stream, a, keys, a.key_scales);

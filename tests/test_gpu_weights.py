@@ -433,3 +433,29 @@ def test_prompt_weights_graphs_share_a_workspace_and_streams_do_not(pa):
             call(i, want[i], shared)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 3.0])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weights_at_any_scale(pa, scale, fp8):
+    """A negative scale turns the order of the scores round, zero makes them equal, a large one leaves one key each."""
+    b = Batch([900, 40, 333], 2, 128, 16, "f16", 51, fp8).to(DEV)
+    new, cu = [700, 5, 40], [0, 700, 705, 745]
+    gen = torch.Generator().manual_seed(6)
+    q1 = torch.randn((3, 8, 128), generator=gen).to(torch.float16)
+    qp = torch.randn((cu[-1], 8, 128), generator=gen).to(torch.float16)
+    before = _start_weights(3, 2, 900, 5)
+    _, want, rtol = decode_exact(b, q1, scale, before)
+    w = before.to(DEV)
+    _decode(pa, b, q1.to(DEV), w, scale)
+    _close(w.cpu(), want, rtol)
+    for window in (0, 16):
+        want, rtol = prompt_exact(b, qp, cu, window, scale, True, before)
+        w = before.to(DEV)
+        _prompt(pa, b, qp.to(DEV), cu, window, scale, w)
+        _close(w.cpu(), want, rtol)
+
+
+def _close(got, want, rtol):
+    """As _check_weights, and of up to 4,096 terms each may be lost below the smallest normal number."""
+    assert bool(((got.double() - want).abs() <= (rtol + 2.0 ** -23) * want.abs() + 4096 * 2.0 ** -126).all())
