@@ -39,7 +39,7 @@
 namespace pa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;  // at most
 
 // inv_freq / (2 pi) as a fraction of a turn in 64 bits (two's complement).
 // freq = m 2^e with a 53-bit integer m: F = m * (2^64 / (2 pi)) * 2^e, whole
@@ -122,7 +122,7 @@ __device__ __forceinline__ void store_codes(uint8_t* d, const float (&x)[VEC], f
 
 // VEC: elements per vector (16 bytes, or 1 where sizes or alignment do not
 // allow it).  FP8: k and v rows are quantized into code pools.
-// Four CTAs per SM and two tokens in flight per thread: measured on 8,192
+// 1,024 threads per SM and two tokens in flight per thread: measured on 8,192
 // tokens of 32 + 8 heads x 128 (bf16) against one to four in flight and two to
 // six CTAs.
 template <typename T, int VEC, bool FP8>
@@ -135,8 +135,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
     const int nt = (int)min((int64_t)p.tpb, p.n - t0);
     const int half = p.rot_dim / 2, hd = p.head_dim, Hq = p.num_heads, Hkv = p.num_kv_heads;
     int64_t* slots = reinterpret_cast<int64_t*>(tab + (size_t)p.tpb * half);
-    for (int i = threadIdx.x; i < nt; i += kRopeThreads) slots[i] = p.slots[t0 + i];
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+    const int NT = blockDim.x;
+    for (int i = threadIdx.x; i < nt; i += NT) slots[i] = p.slots[t0 + i];
+    for (int i = threadIdx.x; i < nt * half; i += NT) {
         const int t = i / half, pr = i - t * half;
         const int ax = p.pair_axis ? min(max(p.pair_axis[pr], 0), p.num_axes - 1) : 0;
         const double fr = p.inv_freq[pr];
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
     const int R = half / VEC, per = R + ((hd - p.rot_dim) / VEC + 1) / 2;
     const int n_rot = (Hq + (kRowsBelow ? 0 : Hkv)) * per, vper = (hd / VEC + 1) / 2;
     const int items = n_rot + (kRowsBelow ? 0 : Hkv * vper);
-    for (int it = blockIdx.y * kRopeThreads + threadIdx.x; it < items; it += gridDim.y * kRopeThreads) {
+    for (int it = blockIdx.y * NT + threadIdx.x; it < items; it += gridDim.y * NT) {
         const bool is_v = it >= n_rot;
         int head = is_v ? (it - n_rot) / vper : it / per;
         const int r = is_v ? it - n_rot - head * vper : it - head * per;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
         // one warp per (token, KV head, K|V) row: lane l holds pairs l, l+32,
         // ... of the rotated part and elements rot + l, ... of the rest
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        for (int row = blockIdx.y * (kRopeThreads / 32) + warp; row < nt * Hkv * 2; row += gridDim.y * (kRopeThreads / 32)) {
+        for (int row = blockIdx.y * (NT / 32) + warp; row < nt * Hkv * 2; row += gridDim.y * (NT / 32)) {
             const int is_v = row & 1, h = (row >> 1) % Hkv, t = (row >> 1) / Hkv;
             const int64_t tok = t0 + t, slot = slots[t];
             if (slot < 0) continue;
@@ -302,19 +303,25 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
                      a.k_stride % V == 0 && a.v_stride % V == 0 &&
                      (!FP8 || ((row_items & (row_items - 1)) == 0 && row_items <= 32));
     RopeArgs p = a;
-    // Tokens per CTA: more spread the angles' and the items' setup over more
-    // tokens; the batch in one wave of four CTAs per SM (8,192 tokens: 37.5 us
-    // with 14, 39.5 in two waves of 8; 1,999 code-pool tokens: 9.5 us with 4,
-    // 11.5 with 2).
-    p.tpb = (int)std::min<int64_t>(16, (a.n + 152 * 4 - 1) / (152 * 4));
-    // few tokens: their items over several CTAs each, which repeat the angles
-    const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
+    // Threads per CTA: the number that the items of a token fill best (128
+    // items left half of 256 threads idle: 1,999 code-pool tokens 9.5 us, 7.5
+    // so).  Tokens per CTA: more spread the angles' and the items' setup over
+    // more tokens; the batch in one wave of 1,024 threads per SM (8,192 tokens:
+    // 37 us so, 39.5 in two waves).  Few tokens: their items over several CTAs
+    // each, which repeat the angles.
     const int items = (a.num_heads + 2 * a.num_kv_heads) * (a.head_dim / (vec ? 2 * V : 2));
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(2 * 152 / ctas, (items + kRopeThreads - 1) / kRopeThreads));
+    auto filled = [&](int n) { return (int64_t)((items + n - 1) / n) * n; };
+    int threads = 128;
+    for (int n = 160; n <= kRopeThreads; n += 32)
+        if (filled(n) < filled(threads)) threads = n;
+    const int64_t slots = 152 * (1024 / threads);
+    p.tpb = (int)std::min<int64_t>(16, (a.n + slots - 1) / slots);
+    const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / 2 / ctas, (items + threads - 1) / threads));
     const dim3 grid((unsigned)ctas, (unsigned)parts);
     const size_t smem = (size_t)p.tpb * ((a.rot_dim / 2) * sizeof(float2) + sizeof(int64_t));
-    return vec ? launch_pdl_smem(rope_write_kernel<T, V, FP8>, grid, dim3(kRopeThreads), smem, stream, p)
-               : launch_pdl_smem(rope_write_kernel<T, 1, FP8>, grid, dim3(kRopeThreads), smem, stream, p);
+    return vec ? launch_pdl_smem(rope_write_kernel<T, V, FP8>, grid, dim3((unsigned)threads), smem, stream, p)
+               : launch_pdl_smem(rope_write_kernel<T, 1, FP8>, grid, dim3((unsigned)threads), smem, stream, p);
 }
 
 }  // namespace
