@@ -463,6 +463,15 @@ def _i32(*ts):
             raise TypeError("block tables, lengths and cu_seqlens_q must be int32")
 
 
+def _same_batch(q, pool, lens, *tables):
+    """A batch's parts fit each other: q's head_dim and type and the pools', a table row and a length per sequence."""
+    if q is not None and (q.shape[2] != pool.shape[3] or (pool.dtype != torch.uint8 and pool.dtype != q.dtype)):
+        raise ValueError("q and the cache must be of one head_dim and dtype (codes: uint8)")
+    for t in tables:
+        if t.shape[0] != lens.shape[0]:
+            raise ValueError("block tables must have one row per sequence")
+
+
 def _ws(workspace):
     return _raw(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
 
@@ -479,8 +488,11 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     weights [S, Hkv, stride] fp32; the newest token's entry is set."""
     _dev(out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace)
     _i32(block_tables, context_lens)
+    _same_batch(q, k_cache, context_lens, block_tables)
     nb, bs, hkv, hd = k_cache.shape
     S, hq, _ = q.shape
+    if out.shape != q.shape or context_lens.shape[0] != S or v_cache.shape != k_cache.shape:
+        raise ValueError("out must have q's shape, context_lens one entry per query, the pools one shape")
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_decode_weights(_raw(out), _raw(weights), stride, _raw(q), _raw(k_cache), _raw(v_cache),
                                  _raw(block_tables), block_tables.shape[1], _raw(context_lens), S, hq, hkv, hd, nb,
@@ -500,8 +512,11 @@ def pa_decode_weights_fp8(out, weights, q, k_codes, v_codes, k_scales, v_scales,
     """pa_decode_weights over a quantized cache: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
     _dev(out, weights, q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, workspace)
     _i32(block_tables, context_lens)
+    _same_batch(q, k_codes, context_lens, block_tables)
     nb, bs, hkv, hd = k_codes.shape
     S, hq, _ = q.shape
+    if out.shape != q.shape or context_lens.shape[0] != S or v_codes.shape != k_codes.shape:
+        raise ValueError("out must have q's shape, context_lens one entry per query, the pools one shape")
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_decode_weights_fp8(_raw(out), _raw(weights), stride, _raw(q), _raw(k_codes), _raw(v_codes),
@@ -525,9 +540,12 @@ def pa_prompt_weights(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q,
     weights [S, Hkv, stride] fp32 for tokens cached before the step, set for new ones.  q [T, Hq, hd]."""
     _dev(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q, workspace)
     _i32(block_tables, seq_lens, cu_seqlens_q)
+    _same_batch(q, k_cache, seq_lens, block_tables)
     nb, bs, hkv, hd = k_cache.shape
     T, hq, _ = q.shape
     S = seq_lens.shape[0]
+    if cu_seqlens_q.shape[0] != S + 1:
+        raise ValueError("cu_seqlens_q must hold one entry more than there are sequences")
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_prompt_weights(_raw(weights), stride, _raw(q), _raw(k_cache), _raw(block_tables),
                                  block_tables.shape[1], _raw(seq_lens), _raw(cu_seqlens_q), S, T, max_q, hq, hkv, hd,
@@ -549,9 +567,12 @@ def pa_prompt_weights_fp8(weights, q, k_codes, k_scales, block_tables, seq_lens,
     """pa_prompt_weights over a quantized cache's keys: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
     _dev(weights, q, k_codes, k_scales, block_tables, seq_lens, cu_seqlens_q, workspace)
     _i32(block_tables, seq_lens, cu_seqlens_q)
+    _same_batch(q, k_codes, seq_lens, block_tables)
     nb, bs, hkv, hd = k_codes.shape
     T, hq, _ = q.shape
     S = seq_lens.shape[0]
+    if cu_seqlens_q.shape[0] != S + 1:
+        raise ValueError("cu_seqlens_q must hold one entry more than there are sequences")
     _scale_pools(nb, hkv, bs, k_scales)
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_prompt_weights_fp8(_raw(weights), stride, _raw(q), _raw(k_codes), _raw(k_scales),
@@ -577,8 +598,11 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
     _dev(new_lens, weights_out, positions_out, weights, k_cache, v_cache, block_tables, new_block_tables, context_lens,
          positions, recorded_lens, seen_lens, k_scales, v_scales, workspace)
     _i32(new_lens, block_tables, new_block_tables, context_lens, recorded_lens, seen_lens)
+    _same_batch(None, k_cache, context_lens, block_tables, new_block_tables)
     nb, bs, hkv, hd = k_cache.shape
     S = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or new_lens.shape[0] != S:
+        raise ValueError("the pools must be of one shape and dtype, new_lens must hold one entry per sequence")
     stride = _weight_rows("weights", weights, S, hkv)
     rows = [("weights_out", weights_out, torch.float32), ("positions_out", positions_out, torch.int32),
             ("positions", positions, torch.int32)]

@@ -459,3 +459,31 @@ def test_weights_at_any_scale(pa, scale, fp8):
 def _close(got, want, rtol):
     """As _check_weights, and of up to 4,096 terms each may be lost below the smallest normal number."""
     assert bool(((got.double() - want).abs() <= (rtol + 2.0 ** -23) * want.abs() + 4096 * 2.0 ** -126).all())
+
+
+def test_bindings_refuse_parts_that_do_not_fit(pa):
+    b = Batch([50, 20], 2, 128, 16, "bf16", 23).to(DEV)
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device=DEV)
+    w, cu = torch.zeros((2, 2, 50), device=DEV), torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    ws, out = torch.empty(1 << 24, dtype=torch.uint8, device=DEV), torch.empty_like(q)
+    good = dict(out=out, weights=w, q=q, k_cache=b.dk, v_cache=b.dv, block_tables=b.dtables, context_lens=b.dlens,
+                max_context=50, scale=0.1, workspace=ws)
+    for bad in (dict(q=q.float(), out=out.float()), dict(q=q[..., :64].contiguous()), dict(out=out[:1]),
+                dict(block_tables=b.dtables[:1]), dict(context_lens=b.dlens[:1]), dict(v_cache=b.dv[:2]),
+                dict(weights=w[:1]), dict(weights=w.double())):
+        with pytest.raises(ValueError):
+            pa.pa_decode_weights(**{**good, **bad})
+    good = dict(weights=w, q=q, k_cache=b.dk, block_tables=b.dtables, seq_lens=b.dlens, cu_seqlens_q=cu, max_q=1,
+                max_context=50, window=0, scale=0.1, workspace=ws)
+    for bad in (dict(q=q.half()), dict(cu_seqlens_q=cu[:2]), dict(block_tables=b.dtables[:1]),
+                dict(weights=w[:, :1].contiguous())):
+        with pytest.raises(ValueError):
+            pa.pa_prompt_weights(**{**good, **bad})
+    good = dict(new_lens=torch.zeros(2, dtype=torch.int32, device=DEV), weights_out=w.clone(), positions_out=None,
+                weights=w, k_cache=b.dk, v_cache=b.dv, block_tables=b.dtables, new_block_tables=b.dtables,
+                context_lens=b.dlens, max_context=50, keep=10, num_sink=0, num_recent=1, workspace=ws)
+    for bad in (dict(new_block_tables=b.dtables[:1]), dict(v_cache=b.dv.half()),
+                dict(weights_out=w[..., :40].contiguous())):
+        with pytest.raises(ValueError):
+            pa.pa_evict(**{**good, **bad})
+    assert not bool(w.any())
