@@ -1071,6 +1071,88 @@ __device__ __forceinline__ void merge_item(const TcParams& p, const int64_t TW, 
     }
 }
 
+// The same for a unit in very many pieces (a few sequences over all the GPU's
+// warps): a CTA per (unit, query head), whose sixteen half warps fold a
+// contiguous sixteenth of the records each, one of them then their results in
+// order.
+template <typename T, int HD>
+__device__ __forceinline__ void merge_many(const TcParams& p, const int64_t TW, const int32_t* mprefix, int64_t item) {
+    constexpr int E = HD / 16, B = 4, W16 = 16;  // output elements per lane, records per batch, half warps
+    __shared__ float part_o[W16][HD];
+    __shared__ float2 part_ml[W16];
+    const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group, hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
+    const int j = (int)(item % G);
+    const int64_t u = item / G;
+    const int s = (int)(u / Hkv), h = (int)(u - (int64_t)s * Hkv);
+    const int nb = mprefix[s + 1] - mprefix[s];
+    if (nb == 0) return;  // (uniform for the CTA, as the next)
+    const int64_t W = (int64_t)mprefix[S] * Hkv;
+    const int64_t u0 = (int64_t)mprefix[s] * Hkv + (int64_t)h * nb, u1 = u0 + nb;
+    auto owner = [&](int64_t f) -> int64_t { return ((f + 1) * TW + W - 1) / W - 1; };
+    const int64_t wf = owner(u0), wl = owner(u1 - 1), n = wl - wf + 1;
+    if (n == 1) return;  // held whole by one warp
+    const int slot0 = u0 == wf * W / TW ? 0 : 1;
+    const float* rec0 = p.ws_part + (int64_t)j * (HD + 4) + hl * E;
+    const int64_t rstride = (int64_t)G * (HD + 4);
+    pdl_wait_primary();
+    float M = -INFINITY, L = 0.f, o[E];
+#pragma unroll
+    for (int t = 0; t < E; ++t) o[t] = 0.f;
+    const int64_t end = wf + n * (hw + 1) / W16;
+    for (int64_t w0 = wf + n * hw / W16; w0 < end; w0 += B) {
+        float m[B], l[B];
+        float4 a[B][E / 4];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int64_t w = w0 + b;
+            const bool ok = w < end && !(W < TW && w * W / TW == (w + 1) * W / TW);
+            const float* r = rec0 + (w * 2 + (w == wf ? slot0 : 0)) * rstride;
+            m[b] = ok ? __ldcg(r - hl * E + HD) : -INFINITY;
+            l[b] = ok ? __ldcg(r - hl * E + HD + 1) : 0.f;
+#pragma unroll
+            for (int t = 0; t < E / 4; ++t)
+                a[b][t] = ok ? __ldcg(reinterpret_cast<const float4*>(r) + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float Mn = M;
+#pragma unroll
+        for (int b = 0; b < B; ++b) Mn = fmaxf(Mn, m[b]);
+        const float Ms = Mn == -INFINITY ? 0.f : Mn;  // nothing but absent records, or scores without a number
+        const float c = exp2f(M - Ms);
+        L *= c;
+#pragma unroll
+        for (int t = 0; t < E; ++t) o[t] *= c;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float e = exp2f(m[b] - Ms);
+            L = fmaf(e, l[b], L);
+#pragma unroll
+            for (int t = 0; t < E / 4; ++t) {
+                o[4 * t + 0] = fmaf(e, a[b][t].x, o[4 * t + 0]);
+                o[4 * t + 1] = fmaf(e, a[b][t].y, o[4 * t + 1]);
+                o[4 * t + 2] = fmaf(e, a[b][t].z, o[4 * t + 2]);
+                o[4 * t + 3] = fmaf(e, a[b][t].w, o[4 * t + 3]);
+            }
+        }
+        M = Mn;
+    }
+#pragma unroll
+    for (int t = 0; t < E; ++t) part_o[hw][hl * E + t] = o[t];
+    if (hl == 0) part_ml[hw] = make_float2(M, L);
+    __syncthreads();
+    if (threadIdx.x >= HD) return;
+    float Mn = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W16; ++i) Mn = fmaxf(Mn, part_ml[i].x);
+    float sum = 0.f, v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W16; ++i) {
+        const float e = exp2f(part_ml[i].x - Mn);
+        sum = fmaf(e, part_ml[i].y, sum);
+        v = fmaf(e, part_o[i][threadIdx.x], v);
+    }
+    static_cast<T*>(p.out)[((int64_t)s * p.num_heads + (int64_t)h * G + j) * HD + threadIdx.x] = Elt<T>::from_f(v / sum);
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, const int64_t TW) {
     extern __shared__ int32_t mprefix[];   // [num_seqs + 1]
@@ -1091,7 +1173,7 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, con
 constexpr int kWeightChunk = 1024;
 constexpr int kWeightMaxCtas = 152 * 16;  // beyond this a CTA takes several chunks
 
-template <typename T, int HD>
+template <typename T, int HD, bool MANY>
 __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcParams p, const int64_t TW,
                                                                    float* __restrict__ weights, int64_t stride,
                                                                    int merge_blocks, int chunks) {
@@ -1100,7 +1182,8 @@ __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcPa
     const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
     if ((int)blockIdx.x < merge_blocks) {
         tile_prefix(p.context_lens, S, mprefix, nullptr);
-        merge_item<T, HD, HD <= 128 ? 4 : 2>(p, TW, mprefix, blockIdx.x);
+        if constexpr (MANY) merge_many<T, HD>(p, TW, mprefix, blockIdx.x);
+        else merge_item<T, HD, HD <= 128 ? 4 : 2>(p, TW, mprefix, blockIdx.x);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1325,12 +1408,17 @@ cudaError_t launch_typed(const AttnArgs& a, int32_t num_blocks, int grid, void* 
     mcfg.blockDim = dim3(256);
     mcfg.dynamicSmemBytes = (size_t)(a.num_seqs + 1) * sizeof(int32_t);
     if constexpr (SCORES) {
-        const int merge_blocks = (int)mcfg.gridDim.x;
+        // (units in more than 32 pieces; the call on 3 x 16,000 tokens of 2 KV
+        // heads x 64: 22 us, 50 with the half-warp merge; 1 x 32,768 of 8 x
+        // 128: 34 and 65)
+        const bool many = tw > 32 * (int64_t)a.num_seqs * a.num_kv_heads;
+        const int merge_blocks = many ? (int)items : (int)mcfg.gridDim.x;
         const int chunks = std::max(1, (a.max_context + kWeightChunk - 1) / kWeightChunk);
         const int64_t all = (int64_t)a.num_seqs * a.num_kv_heads * chunks;
         mcfg.gridDim.x = (unsigned)(merge_blocks + std::min<int64_t>(all, kWeightMaxCtas));
-        return cudaLaunchKernelEx(&mcfg, decode_merge_weights_kernel<T, HD>, p, tw, weights->weights,
-                                  weights->stride, merge_blocks, chunks);
+        return cudaLaunchKernelEx(&mcfg, many ? decode_merge_weights_kernel<T, HD, true>
+                                              : decode_merge_weights_kernel<T, HD, false>,
+                                  p, tw, weights->weights, weights->stride, merge_blocks, chunks);
     }
     return cudaLaunchKernelEx(&mcfg, decode_merge_kernel<T, HD>, p, tw);
 }

@@ -62,6 +62,9 @@ DECODE = [
     ([40, 0, 3], 34, 2, 128, 16, "bf16", False),    # more query heads than the tensor-core kernel takes
     ([50, 120], 4, 4, 100, 16, "f16", False),       # a head_dim it does not take
     ([5000], 32, 8, 128, 16, "bf16", False),        # one long sequence, split
+    ([16000, 3], 12, 2, 64, 8, "bf16", False),      # few units in hundreds of pieces
+    ([9000, 70], 4, 1, 256, 16, "f16", False),
+    ([12000], 8, 1, 128, 16, "bf16", True),
     ([3500, 12, 1, 800], 32, 8, 128, 16, "bf16", True),
     ([100, 37], 12, 2, 256, 16, "f16", True),
     ([60, 19], 8, 8, 128, 8, "f16", True),
