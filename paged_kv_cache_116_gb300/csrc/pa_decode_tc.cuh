@@ -77,6 +77,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_launch.cuh"
 
 namespace pa {
 namespace {
@@ -1336,7 +1337,7 @@ int grid_for(const void* kfn, int32_t num_seqs, int32_t num_kv_heads, int32_t ma
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const size_t smem = smem_bytes<HD, FP8>(num_seqs);
-    cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    allow_smem(kfn, smem_bytes<HD, FP8>(kDecodeMaxSeqsPerLaunch));
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kfn, Pipe<HD, FP8>::NW * 32, smem);
     if (occ < 1) occ = 1;
     int64_t grid = (int64_t)sms * occ;
@@ -1383,7 +1384,7 @@ cudaError_t launch_typed(const AttnArgs& a, int32_t num_blocks, int grid, void* 
 
     const void* kfn = kernel_ptr<T, HD, NT, FP8, PAIR, GATHER, SCORES>();
     const size_t smem = smem_bytes<HD, FP8>(a.num_seqs);
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(kfn, smem_bytes<HD, FP8>(kDecodeMaxSeqsPerLaunch));
     if (e != cudaSuccess) return e;
     // programmatic dependent launch: the grid may be scheduled while the
     // previous kernel on the stream finishes; the kernel waits for it first

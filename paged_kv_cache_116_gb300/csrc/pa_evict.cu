@@ -85,6 +85,11 @@ size_t select_smem(int32_t max_context) {
     return words * 8 + (max_context <= kStageMax ? (size_t)max_context * 4 : 0);
 }
 
+// Longest context of the select kernel's forms, by threads.
+constexpr int select_max(int threads, bool staged) {
+    return !staged ? kEvictMaxContext : threads == 256 ? 2048 : threads == 512 ? 8192 : kStageMax;
+}
+
 // NT threads; STAGED: the context fits in shared memory.
 template <int NT, bool STAGED>
 __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
@@ -415,13 +420,13 @@ EvictSpace evict_space(int64_t units, int32_t max_context, int32_t keep) {
 
 template <int NT, bool STAGED>
 cudaError_t launch_select(const EvictArgs& a, int64_t units, cudaStream_t stream) {
-    const size_t smem = select_smem(a.max_context);
-    if (smem > 32 * 1024) {  // (with the static arrays beyond what every kernel may have)
-        cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<NT, STAGED>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t most = select_smem(select_max(NT, STAGED));
+    if (most > 32 * 1024) {  // (with the static arrays beyond what every kernel may have)
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<NT, STAGED>), most);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl_smem(evict_select_kernel<NT, STAGED>, dim3((unsigned)units), dim3(NT), smem, stream, a);
+    return launch_pdl_smem(evict_select_kernel<NT, STAGED>, dim3((unsigned)units), dim3(NT), select_smem(a.max_context),
+                           stream, a);
 }
 
 }  // namespace
@@ -444,10 +449,10 @@ cudaError_t launch_evict(const EvictArgs& a, void* workspace, cudaStream_t strea
     }
     // short contexts: several small CTAs per SM; long ones: a CTA of 1,024
     // threads holds an SM's shared memory anyway
-    cudaError_t e = a.max_context > kStageMax ? launch_select<1024, false>(p, units, stream)
-                    : a.max_context > 8192    ? launch_select<1024, true>(p, units, stream)
-                    : a.max_context > 2048    ? launch_select<512, true>(p, units, stream)
-                                              : launch_select<256, true>(p, units, stream);
+    cudaError_t e = a.max_context > select_max(1024, true)  ? launch_select<1024, false>(p, units, stream)
+                    : a.max_context > select_max(512, true) ? launch_select<1024, true>(p, units, stream)
+                    : a.max_context > select_max(256, true) ? launch_select<512, true>(p, units, stream)
+                                                            : launch_select<256, true>(p, units, stream);
     if (e != cudaSuccess) return e;
     const int rows = std::max(1, std::min(a.keep, a.max_context));
     const int ctas = (int)std::max<int64_t>(

@@ -9,6 +9,14 @@
 
 namespace pa {
 
+// Raises a kernel's limit of dynamic shared memory to the most that any of its
+// launches asks for.  The limit belongs to the kernel, not to the launch: set
+// to one call's own size, a smaller call of another host thread would lower it
+// before this one's launch, which is then refused.
+inline cudaError_t allow_smem(const void* kernel, size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                             Args&&... args) {

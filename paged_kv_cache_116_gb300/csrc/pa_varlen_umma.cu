@@ -79,6 +79,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_launch.cuh"
 
 namespace pa {
 namespace {
@@ -1267,8 +1268,8 @@ cudaError_t um_launch(const AttnArgs& a, int32_t num_blocks, void* workspace, st
     const int64_t dgroups = dec_route ? (a.num_seqs + DG - 1) / DG : 0;
     p.dec_ctas = (int32_t)dgroups;
     const size_t smem = um_smem_bytes<HD>(workspace ? 0 : a.num_seqs);
-    cudaError_t e = cudaFuncSetAttribute(varlen_umma_kernel<T, HD, FP8>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&varlen_umma_kernel<T, HD, FP8>),
+                               um_smem_bytes<HD>(kMaxSeqsSmem));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1037,8 +1037,9 @@ cudaError_t launch_umma(const WeightArgs& args, int32_t num_blocks, std::string*
     const dim3 block(WGeo<HD>::NTHREADS);
     auto k1 = weights_umma_kernel<T, HD, kRowStats, SC>;
     auto k2 = a.few_rows ? weights_umma_kernel<T, HD, kFewRows, SC> : weights_umma_kernel<T, HD, kKeyWeights, SC>;
-    e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr int kMost = kWeightMaxSeqsPerLaunch;
+    e = allow_smem(reinterpret_cast<const void*>(k1), weights_smem<HD>(kMost));
+    if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(k2), weights_smem<HD>(kMost));
     if (e != cudaSuccess) return e;
     constexpr int NA = WGeo<HD>::NA;
     const int64_t rows = a.window > 0 ? std::min<int64_t>(a.total_q, (int64_t)a.num_seqs * a.window) : a.total_q;
