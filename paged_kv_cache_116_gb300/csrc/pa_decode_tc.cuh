@@ -64,7 +64,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -72,12 +71,12 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 #include <string>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_tmap.cuh"
 
 namespace pa {
 namespace {
@@ -1278,50 +1277,24 @@ __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcPa
 
 // ---------------------------------------------------------------- host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 // The cache as a 3-D tensor: 128 bytes (64 16-bit elements, or 128 E4M3
 // codes) x (Hkv * CH) 128-byte chunks of a token row x num_blocks *
 // block_size token rows; one box = one chunk of one KV head over the 16 (or
 // 8) rows of a block.
 bool make_kv_map(CUtensorMap* m, const void* cache, int dtype, bool fp8, int num_blocks, int block_size,
                  int num_kv_heads, int head_dim, std::string* err) {
-    auto fn = encode_fn();
-    if (!fn) {
-        *err = "cuTensorMapEncodeTiled is not available from the driver";
-        return false;
-    }
     const int elt = fp8 ? 1 : 2;
     const int ch = head_dim * elt / 128, inner = 128 / elt;
     cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)num_kv_heads * ch, (cuuint64_t)num_blocks * block_size};
     cuuint64_t strides[2] = {128, (cuuint64_t)num_kv_heads * head_dim * elt};
     cuuint32_t box[3] = {(cuuint32_t)inner, 1, (cuuint32_t)(block_size == 8 ? 8 : BS)};
-    cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType ty = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                        : (dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
     // L2 fills of 256 bytes suit a 16-bit head row (two 128-byte chunks); a
     // code row is one 128-byte chunk, and a 256-byte fill would drag in the
     // neighbouring head's row
     const CUtensorMapL2promotion promo = fp8 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    CUresult r = fn(m, ty, 3, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
-        return false;
-    }
-    return true;
+    return encode_tiled_3d(m, ty, cache, dims, strides, box, promo, err);
 }
 
 template <typename T, int HD, int NT, bool FP8, bool PAIR = false, bool GATHER = false, bool SCORES = false>

@@ -65,7 +65,6 @@
 // exclusive prefix in shared memory) and finds its work, in request order,
 // by binary search.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -73,13 +72,13 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 #include <string>
 #include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_tmap.cuh"
 
 namespace pa {
 namespace {
@@ -1160,39 +1159,12 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* __rest
 
 // ---------------------------------------------------------------- host side
 
-PFN_cuTensorMapEncodeTiled_v12000 um_encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 // dtype: 1 bf16, 2 f16, 3 E4M3 codes (bytes)
 bool um_encode(CUtensorMap* m, const void* base, int dtype, const cuuint64_t dims[3], const cuuint64_t strides[2],
                const cuuint32_t box[3], std::string* err) {
-    auto fn = um_encode_fn();
-    if (!fn) {
-        *err = "cuTensorMapEncodeTiled is not available from the driver";
-        return false;
-    }
-    cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType ty = dtype == 3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : (dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
-    CUresult r = fn(m, ty, 3,
-                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
-        return false;
-    }
-    return true;
+    return encode_tiled_3d(m, ty, base, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, err);
 }
 
 // Workspace layout of a planned launch: plan header, prefill items (one per

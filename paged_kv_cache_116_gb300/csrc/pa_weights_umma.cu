@@ -53,19 +53,18 @@
 // bounded; on expiry the CTA sets a status bit, abandons its work, waits
 // (bounded) for its loads in flight and frees its tensor memory.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
-#include <mutex>
 #include <string>
 #include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_tmap.cuh"
 #include "pa_weights.cuh"
 
 namespace pa {
@@ -970,36 +969,10 @@ __global__ void __launch_bounds__(256) weights_join_kernel(const WeightArgs p) {
 
 // ---------------------------------------------------------------- host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
 bool encode_map(CUtensorMap* m, const void* ptr, int dtype, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
                 const cuuint32_t (&box)[3], std::string* err) {
-    auto fn = encode_fn();
-    if (!fn) {
-        *err = "cuTensorMapEncodeTiled is not available from the driver";
-        return false;
-    }
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUtensorMapDataType ty = dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUresult r = fn(m, ty, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
-        return false;
-    }
-    return true;
+    return encode_tiled_3d(m, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ptr, dims,
+                           strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, err);
 }
 
 template <typename T, int HD, bool SC>

@@ -156,3 +156,34 @@ def test_threads_with_launches_of_different_size(pa, make, monkeypatch):
         got = c(st)
         st.synchronize()
         assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("make", [_evict, _prompt, _decode_weights, _decode, _varlen])
+@pytest.mark.parametrize("ctas", [0, 3])
+def test_first_call_of_a_thread(pa, make, ctas):
+    """A thread that has made no CUDA call yet: its first is the library's (with a pinned decode grid nothing is asked
+    of the device on the way)."""
+    pa.pa_set_option(pa.PA_OPT_DECODE_CTAS, ctas)
+    try:
+        _first_call(make(pa, False))
+    finally:
+        pa.pa_set_option(pa.PA_OPT_DECODE_CTAS, 0)
+
+
+def _first_call(call):
+    want = call().clone()
+    torch.cuda.synchronize()
+    stream, got = torch.cuda.current_stream(), []
+
+    def work():
+        try:
+            got.append(call(stream))
+        except Exception as e:  # noqa: BLE001 (reported by the test's thread)
+            got.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert torch.is_tensor(got[0]), got[0]
+    assert torch.equal(got[0], want)
