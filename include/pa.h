@@ -112,11 +112,13 @@ PA_API pa_status pa_set_check_mode(int on);
 PA_API pa_status pa_device_status(int clear);
 
 /* Exercises that failure path without a fault (library self-test; the pages
- * have no counterpart): one CTA waits on a shared-memory barrier that nothing
- * completes, with the same bounded wait the decode kernel uses, gives up
- * after `polls` polls (1 .. 2^20), sets the timeout bit and returns; a
- * following pa_device_status reports PA_ERR_TIMEOUT (and clears it on
- * request).  Nothing else is touched and the context stays usable. */
+ * have no counterpart): the warps of one CTA wait on shared-memory barriers
+ * that nothing completes, with the kernels' own bounded waits (the decode
+ * kernel's for `polls` polls, 1 .. 2^20; those of handed-out work items for a
+ * fraction of a millisecond), give up, set the timeout bit if each of them
+ * reported its expiry, and return; a following pa_device_status reports
+ * PA_ERR_TIMEOUT (and clears it on request).  Nothing else is touched and the
+ * context stays usable. */
 PA_API pa_status pa_selftest_wait_timeout(int32_t polls, void* stream);
 
 /*

@@ -122,6 +122,12 @@ __device__ __forceinline__ bool mbar_wait_ns(uint64_t* bar, uint32_t parity, uin
         if (global_ns() - t0 > limit_ns) return false;
     }
 }
+// The same by a whole warp, with one answer for all lanes: lanes that gave up
+// while others saw the barrier complete would part before the warp's next
+// collective instruction.
+__device__ __forceinline__ bool mbar_wait_ns_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_ns(bar, parity, limit_ns));
+}
 
 // Order this thread's generic-proxy shared-memory accesses before later
 // async-proxy (TMA) accesses of the same memory.

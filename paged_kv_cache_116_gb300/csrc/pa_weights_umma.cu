@@ -63,6 +63,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_items.cuh"
 #include "pa_launch.cuh"
 #include "pa_tmap.cuh"
 #include "pa_weights.cuh"
@@ -288,33 +289,25 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     // The CTA's items: its own number first, then whatever is next in the grid
     // (items differ in length; dealt out in advance they left SMs idle).  The
     // first producer draws them as it gets to them; every warp takes each in
-    // turn (-1: none left, or a wait ran out).
-    int n_item = 0;
-    auto next_item = [&]() -> int {
-        const int k = n_item % Gm::IRING;
-        const uint32_t ph = (uint32_t)(n_item / Gm::IRING) & 1u;
-        if (warp == Gm::W_PROD) {
-            int ok = 0;
-            if (lane == 0 && (ok = mbar_wait_ns(&i_empty[k], ph ^ 1u, WAIT_NS))) {
-                // (drawn only now: an item drawn ahead would wait for this CTA
-                // while others run dry, 10 % more time on 8,192 tokens)
-                const int64_t it = n_item == 0 ? blockIdx.x : (int64_t)gridDim.x + atomicAdd(p.next_item + (PASS > 1), 1u);
-                item_s[k] = it < items ? (int)it : -1;
-                mbar_arrive(&i_full[k]);
-            }
-            if (!__shfl_sync(0xffffffffu, ok, 0)) return -1;
+    // turn.
+    auto fail = [&]() { atomicOr(&g_weights_status, kStatusTimeout); };
+    ItemRing<Gm::IRING> ring{i_full, i_empty, item_s};
+    auto next_item = [&](bool& run) -> int {
+        const int it = ring.next(warp == Gm::W_PROD, WAIT_NS, [&]() -> int {
+            // (drawn only now: an item drawn ahead would wait for this CTA
+            // while others run dry, 10 % more time on 8,192 tokens)
+            const int64_t i = ring.n == 0 ? blockIdx.x : (int64_t)gridDim.x + atomicAdd(p.next_item + (PASS > 1), 1u);
+            return i < items ? (int)i : kItemsDone;
+        });
+        if (it == kItemsExpired) {  // the other items are lost: reported here, in whatever role
+            run = false;
+            if (lane == 0) fail();
         }
-        if (!mbar_wait_ns(&i_full[k], ph, WAIT_NS)) return -1;
-        const int it = item_s[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&i_empty[k]);
-        ++n_item;
         return it;
     };
     // (in pass 2 a group works both stationary tiles' accumulators of a parity;
     // a lone tile, which only the last keys of a request are, keeps to the first)
     constexpr bool spread_alone = PASS != kKeyWeights;
-    auto fail = [&]() { atomicOr(&g_weights_status, kStatusTimeout); };
 
     if (warp >= Gm::W_PROD && warp < Gm::W_MMA) {
         // ---------------- producer `me` of every NPROD-th streamed tile; the first also loads the stationary ones
@@ -365,7 +358,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        for (int it; run && (it = next_item()) >= 0;) {
+        for (int it; run && (it = next_item(run)) >= 0;) {
             const Item w = item_at(it);
             if (w.b0 >= w.b1) continue;
             const int mine = w.b0 + (nb + me) % Gm::NPROD;  // this warp's first tile of the item
@@ -430,22 +423,19 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         const uint32_t d_x = lane0(tmem) + x * 2 * TM;
         int na = 0, nb = 0, nd[2] = {0, 0}, last = -1;  // items, streamed tiles, accumulators of each parity
         bool run = true;
-        for (int it; run && (it = next_item()) >= 0;) {
+        for (int it; run && (it = next_item(run)) >= 0;) {
             const Item w = item_at(it);
             if (w.b0 >= w.b1) continue;
-            if (!(run = mbar_wait_ns(a_full, (uint32_t)na & 1u, WAIT_NS))) break;
+            if (!(run = mbar_wait_ns_warp(a_full, (uint32_t)na & 1u, WAIT_NS))) break;
             ++na;
             const bool alone = NA == 2 && w.na == 1;  // one stationary tile: its tiles take all four accumulators in turn
             const uint32_t a_lo = lane0(s_lo + (alone ? 0 : x) * (Gm::TILE / 16));
             for (int t = w.b0; t < w.b1; ++t, ++nb) {
                 const int slot = nb % RING, par = (t - w.b0) & 1, turn = par ? nd[1] : nd[0];
                 const bool mine = alone ? spread_alone && ((t - w.b0) >> 1 & 1) == (int)x || !spread_alone && x == 0 : true;
-                run = mbar_wait_ns(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
-                      (!mine || mbar_wait_ns(&d_empty[2 * x + par], ((uint32_t)turn & 1u) ^ 1u, WAIT_NS));
-                if (!__all_sync(0xffffffffu, run)) {
-                    run = false;
-                    break;
-                }
+                run = mbar_wait_ns_warp(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
+                      (!mine || mbar_wait_ns_warp(&d_empty[2 * x + par], ((uint32_t)turn & 1u) ^ 1u, WAIT_NS));
+                if (!run) break;
                 tc_fence_after();
                 const uint32_t b_lo = lane0(s_lo + (Gm::RING_OFF + slot * Gm::TILE) / 16);
                 // the accumulator's lanes are query rows, or keys
@@ -494,21 +484,21 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(&d_empty[2 * x + par]);
         };
         auto acquire = [&](int x) -> bool {
-            const bool ok = mbar_wait_ns(&d_full[2 * x + par], (uint32_t)n_d[x]++ & 1u, WAIT_NS);
+            const bool ok = mbar_wait_ns_warp(&d_full[2 * x + par], (uint32_t)n_d[x]++ & 1u, WAIT_NS);
             tc_fence_after();
             return ok;
         };
         // a giving group hands its values to the receiving one through buffer j;
         // the turns of each buffer are counted by all groups
         auto give = [&](int j, float2 v) -> bool {
-            if (!mbar_wait_ns(&j_empty[j], ((uint32_t)n_join[j] & 1u) ^ 1u, WAIT_NS)) return false;
+            if (!mbar_wait_ns_warp(&j_empty[j], ((uint32_t)n_join[j] & 1u) ^ 1u, WAIT_NS)) return false;
             join_s[j * TM + m] = v;
             __syncwarp();
             if (lane == 0) mbar_arrive(&j_full[j]);
             return true;
         };
         auto take = [&](int j, float2& v) -> bool {
-            if (!mbar_wait_ns(&j_full[j], (uint32_t)n_join[j] & 1u, WAIT_NS)) return false;
+            if (!mbar_wait_ns_warp(&j_full[j], (uint32_t)n_join[j] & 1u, WAIT_NS)) return false;
             v = join_s[j * TM + m];
             __syncwarp();
             if (lane == 0) mbar_arrive(&j_empty[j]);
@@ -523,7 +513,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         auto meet = [&]() -> bool {
             __syncwarp();
             if (lane == 0) mbar_arrive(g_bar);
-            return mbar_wait_ns(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
+            return mbar_wait_ns_warp(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
         };
         // exp2(x + statistic) of 16 columns of one or both stationary tiles'
         // accumulators, added to v[] and v2[] of this thread's keys
@@ -570,7 +560,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 *dst = key < w.sq.L - w.sq.n ? *dst + v : v;
             }
         };
-        for (int it; run && (it = next_item()) >= 0;) {
+        for (int it; run && (it = next_item(run)) >= 0;) {
             const Item w = item_at(it);
             if constexpr (PASS == kRowStats) {
                 // a lone stationary tile is worked by all groups, every fourth
@@ -590,7 +580,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     const float* ks = scale_s + nx % kScaleRing * TM;  // the tile's key scales (SC)
                     if constexpr (SC) {
                         const int sl_ = nx % kScaleRing;
-                        if (!(run = mbar_wait_ns(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
+                        if (!(run = mbar_wait_ns_warp(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
                         if (alone && ((t - w.b0) >> 1 & 1) != hi) {  // another group's; it is counted all the same
                             used(sl_);
                             continue;
@@ -720,7 +710,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
                     const float* nm = stat_s + sl * TM + hi * HC;
-                    if (!(run = mbar_wait_ns(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS) && acquire(0) &&
+                    if (!(run = mbar_wait_ns_warp(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS) && acquire(0) &&
                                 (w.na < 2 || acquire(NA - 1))))
                         break;
                     // column c (query row) counts for key k where lo[k] <= c < end
@@ -805,7 +795,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     float v = 0.f, ks[2] = {sl, 0.f};
                     if constexpr (SC) {
                         const int sl_ = nx % kScaleRing;
-                        if (!(run = mbar_wait_ns(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
+                        if (!(run = mbar_wait_ns_warp(&s_full[sl_], (uint32_t)(nx / kScaleRing) & 1u, WAIT_NS))) break;
                         ks[0] = scale_s[sl_ * TM + m];
                         used(sl_);
                     }
