@@ -381,6 +381,19 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _pools(k, v, dtype, codes=False):
+    """K and V pools of one shape and type: the rows' dtype, or E4M3 codes.  (The library takes both pools' size from
+    the first, and the width of a row from the call.)"""
+    if (k.dtype not in _CODES) if codes else (k.dtype != dtype):
+        raise ValueError("the pools must hold E4M3 codes (uint8)" if codes else
+                         "the pools must be of the dtype of q, k and v (codes: use the _fp8 call)")
+    if v is not None and (v.shape != k.shape or v.dtype != k.dtype):
+        raise ValueError("the pools must be of one shape and dtype")
+
+
 def _rope_rows(name, t, n, heads, hd):
     """Token stride (elements) of q, k or v [n, heads, hd]: heads contiguous, tokens at any stride."""
     m, h, d = t.shape
@@ -394,6 +407,8 @@ def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv
     _dev(q_out, positions, inv_freq, slot_mapping, pair_axis)
     if positions.dim() == 1:
         positions = positions[None]
+    if positions.dim() != 2 or slot_mapping.dim() != 1 or (q is not None and q_out is None):
+        raise ValueError("positions must be [num_axes, n], slot_mapping [n], and a q needs its q_out")
     n = positions.shape[1]
     if positions.dtype != torch.int64 or inv_freq.dtype != torch.float64 or slot_mapping.dtype != torch.int64:
         raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
@@ -422,8 +437,7 @@ def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
     _dev(k_cache, v_cache)
     nb, bs, hkv, hd = k_cache.shape
     args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
-    if k.dtype != k_cache.dtype:
-        raise ValueError("k and the cache must be of one dtype")
+    _pools(k_cache, v_cache, k.dtype)
     st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_cache), _raw(v_cache),
                                 nb, bs, hq, hkv, hd, _dtype(k), _raw_stream(stream))
     _check(st, "pa_rope_write_kv")
@@ -436,6 +450,7 @@ def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_co
     _dev(k_codes, v_codes, k_scales, v_scales)
     nb, bs, hkv, hd = k_codes.shape
     args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
+    _pools(k_codes, v_codes, None, True)
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_codes),
                                     _raw(v_codes), _raw(k_scales), _raw(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
@@ -464,9 +479,9 @@ def _i32(*ts):
 
 
 def _same_batch(q, pool, lens, *tables):
-    """A batch's parts fit each other: q's head_dim and type and the pools', a table row and a length per sequence."""
-    if q is not None and (q.shape[2] != pool.shape[3] or (pool.dtype != torch.uint8 and pool.dtype != q.dtype)):
-        raise ValueError("q and the cache must be of one head_dim and dtype (codes: uint8)")
+    """A batch's parts fit each other: q's head_dim and the pools', a table row and a length per sequence."""
+    if q is not None and q.shape[2] != pool.shape[3]:
+        raise ValueError("q and the cache must be of one head_dim")
     for t in tables:
         if t.shape[0] != lens.shape[0]:
             raise ValueError("block tables must have one row per sequence")
@@ -491,8 +506,9 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     _same_batch(q, k_cache, context_lens, block_tables)
     nb, bs, hkv, hd = k_cache.shape
     S, hq, _ = q.shape
-    if out.shape != q.shape or context_lens.shape[0] != S or v_cache.shape != k_cache.shape:
-        raise ValueError("out must have q's shape, context_lens one entry per query, the pools one shape")
+    _pools(k_cache, v_cache, q.dtype)
+    if out.shape != q.shape or out.dtype != q.dtype or context_lens.shape[0] != S:
+        raise ValueError("out must have q's shape and dtype, context_lens one entry per query")
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_decode_weights(_raw(out), _raw(weights), stride, _raw(q), _raw(k_cache), _raw(v_cache),
                                  _raw(block_tables), block_tables.shape[1], _raw(context_lens), S, hq, hkv, hd, nb,
@@ -515,8 +531,9 @@ def pa_decode_weights_fp8(out, weights, q, k_codes, v_codes, k_scales, v_scales,
     _same_batch(q, k_codes, context_lens, block_tables)
     nb, bs, hkv, hd = k_codes.shape
     S, hq, _ = q.shape
-    if out.shape != q.shape or context_lens.shape[0] != S or v_codes.shape != k_codes.shape:
-        raise ValueError("out must have q's shape, context_lens one entry per query, the pools one shape")
+    _pools(k_codes, v_codes, q.dtype, True)
+    if out.shape != q.shape or out.dtype != q.dtype or context_lens.shape[0] != S:
+        raise ValueError("out must have q's shape and dtype, context_lens one entry per query")
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_decode_weights_fp8(_raw(out), _raw(weights), stride, _raw(q), _raw(k_codes), _raw(v_codes),
@@ -541,6 +558,7 @@ def pa_prompt_weights(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q,
     _dev(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q, workspace)
     _i32(block_tables, seq_lens, cu_seqlens_q)
     _same_batch(q, k_cache, seq_lens, block_tables)
+    _pools(k_cache, None, q.dtype)
     nb, bs, hkv, hd = k_cache.shape
     T, hq, _ = q.shape
     S = seq_lens.shape[0]
@@ -568,6 +586,7 @@ def pa_prompt_weights_fp8(weights, q, k_codes, k_scales, block_tables, seq_lens,
     _dev(weights, q, k_codes, k_scales, block_tables, seq_lens, cu_seqlens_q, workspace)
     _i32(block_tables, seq_lens, cu_seqlens_q)
     _same_batch(q, k_codes, seq_lens, block_tables)
+    _pools(k_codes, None, q.dtype, True)
     nb, bs, hkv, hd = k_codes.shape
     T, hq, _ = q.shape
     S = seq_lens.shape[0]
