@@ -461,7 +461,7 @@ def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_co
 
 def _scale_pools(nb, hkv, bs, *scales):
     for s in scales:
-        if s.shape != (nb, hkv, bs) or s.dtype != torch.float32:
+        if s is None or s.shape != (nb, hkv, bs) or s.dtype != torch.float32:
             raise ValueError("scales must be float32 [num_blocks, num_kv_heads, block_size]")
 
 
@@ -620,15 +620,18 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
     _same_batch(None, k_cache, context_lens, block_tables, new_block_tables)
     nb, bs, hkv, hd = k_cache.shape
     S = context_lens.shape[0]
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or new_lens.shape[0] != S:
-        raise ValueError("the pools must be of one shape and dtype, new_lens must hold one entry per sequence")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the pools must be of one shape and dtype")
+    for t in (context_lens, new_lens, recorded_lens, seen_lens):
+        if t is not None and t.shape != (S,):
+            raise ValueError("context_lens, new_lens, recorded_lens and seen_lens hold one entry per sequence")
     stride = _weight_rows("weights", weights, S, hkv)
     rows = [("weights_out", weights_out, torch.float32), ("positions_out", positions_out, torch.int32),
             ("positions", positions, torch.int32)]
     for name, t, dt in rows:
         if t is not None and _weight_rows(name, t, S, hkv, dt) != stride:
             raise ValueError("%s must have the row stride of weights" % name)
-    if k_scales is not None:
+    if k_scales is not None or v_scales is not None:
         _scale_pools(nb, hkv, bs, k_scales, v_scales)
     st = lib().pa_evict(_raw(weights_out), _raw(positions_out), _raw(new_lens), _raw(weights), _raw(positions),
                         _raw(recorded_lens), _raw(seen_lens), stride, _raw(k_cache), _raw(v_cache), _raw(k_scales),

@@ -123,3 +123,34 @@ def test_parts_that_do_not_fit_are_refused(lib, call, kw):
     with pytest.raises(ValueError):
         call(**kw)
     assert lib.reached == 0
+
+
+def _evict(**kw):
+    a = dict(new_lens=_t(S, dtype=I32), weights_out=_t(S, HKV, MC, dtype=F32), positions_out=None,
+             weights=_t(S, HKV, MC, dtype=F32), k_cache=_pool(), v_cache=_pool(), block_tables=_t(S, 3, dtype=I32),
+             new_block_tables=_t(S, 3, dtype=I32), context_lens=_t(S, dtype=I32), max_context=MC, keep=8, num_sink=0,
+             num_recent=0, workspace=_t(64, dtype=U8), stream=STREAM)
+    a.update(kw)
+    B.pa_evict(**a)
+
+
+_RECORDED = dict(positions=_t(S, HKV, MC, dtype=I32), recorded_lens=_t(S, dtype=I32), seen_lens=_t(S, dtype=I32))
+_CODE_POOLS = dict(k_cache=_pool(U8), v_cache=_pool(U8), k_scales=_scales(), v_scales=_scales())
+
+
+@pytest.mark.parametrize("kw", [{}, _RECORDED, _CODE_POOLS])
+def test_evict_reaches_the_library(lib, kw):
+    _evict(**kw)
+    assert lib.reached == 1
+
+
+@pytest.mark.parametrize("kw", [
+    {**_RECORDED, "recorded_lens": _t(S - 1, dtype=I32)}, {**_RECORDED, "seen_lens": _t(1, dtype=I32)},
+    {**_RECORDED, "seen_lens": _t(S, 2, dtype=I32)}, dict(new_lens=_t(S, 2, dtype=I32)),
+    {**_CODE_POOLS, "v_scales": None}, {**_CODE_POOLS, "k_scales": None},
+    {**_CODE_POOLS, "v_scales": _scales(2)}])
+def test_evict_refuses_lengths_and_scales_that_do_not_fit(lib, kw):
+    """A length per sequence: a shorter array would be read past its end."""
+    with pytest.raises(ValueError):
+        _evict(**kw)
+    assert lib.reached == 0
