@@ -374,11 +374,30 @@ def _raw(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream):
-    """The stream's handle (of the current stream without making a Stream object of it)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_device_count = None
+
+
+def _devices():
+    """How many devices there are (asked once)."""
+    global _device_count
+    if _device_count is None:
+        _device_count = torch.cuda.device_count()
+    return _device_count
+
+
+def _raw_stream(stream, *ts):
+    """The stream's handle (of the current stream without making a Stream object of it), for a call on these tensors:
+    all on the current device, where the library launches (looked at where there is another one: 1 us of 10 per
+    call)."""
+    dev = _current_device()
+    if (_device_count or _devices()) > 1:
+        for t in ts:
+            if t is not None and t.get_device() != dev:
+                raise ValueError("the tensors must be on the current device (%d)" % dev)
+        if stream is not None and stream.device_index != dev:
+            raise ValueError("the stream must be of the current device (%d)" % dev)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -439,7 +458,9 @@ def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
     args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
     _pools(k_cache, v_cache, k.dtype)
     st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_cache), _raw(v_cache),
-                                nb, bs, hq, hkv, hd, _dtype(k), _raw_stream(stream))
+                                nb, bs, hq, hkv, hd, _dtype(k),
+                                _raw_stream(stream, q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
+                                            v_cache, pair_axis))
     _check(st, "pa_rope_write_kv")
     return q_out
 
@@ -454,7 +475,8 @@ def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_co
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_codes),
                                     _raw(v_codes), _raw(k_scales), _raw(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
-                                    _raw_stream(stream))
+                                    _raw_stream(stream, q_out, q, k, v, positions, inv_freq, slot_mapping, k_codes,
+                                                v_codes, k_scales, v_scales, pair_axis))
     _check(st, "pa_rope_write_kv_fp8")
     return q_out
 
@@ -512,7 +534,9 @@ def pa_decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_l
     stride = _weight_rows("weights", weights, S, hkv)
     st = lib().pa_decode_weights(_raw(out), _raw(weights), stride, _raw(q), _raw(k_cache), _raw(v_cache),
                                  _raw(block_tables), block_tables.shape[1], _raw(context_lens), S, hq, hkv, hd, nb,
-                                 bs, max_context, float(scale), _dtype(q), *_ws(workspace), _raw_stream(stream))
+                                 bs, max_context, float(scale), _dtype(q), *_ws(workspace),
+                                 _raw_stream(stream, out, weights, q, k_cache, v_cache, block_tables, context_lens,
+                                             workspace))
     _check(st, "pa_decode_weights")
     return out
 
@@ -539,7 +563,9 @@ def pa_decode_weights_fp8(out, weights, q, k_codes, v_codes, k_scales, v_scales,
     st = lib().pa_decode_weights_fp8(_raw(out), _raw(weights), stride, _raw(q), _raw(k_codes), _raw(v_codes),
                                      _raw(k_scales), _raw(v_scales), _raw(block_tables), block_tables.shape[1],
                                      _raw(context_lens), S, hq, hkv, hd, nb, bs, max_context, float(scale), _dtype(q),
-                                     *_ws(workspace), _raw_stream(stream))
+                                     *_ws(workspace),
+                                     _raw_stream(stream, out, weights, q, k_codes, v_codes, k_scales, v_scales,
+                                                 block_tables, context_lens, workspace))
     _check(st, "pa_decode_weights_fp8")
     return out
 
@@ -568,7 +594,9 @@ def pa_prompt_weights(weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q,
     st = lib().pa_prompt_weights(_raw(weights), stride, _raw(q), _raw(k_cache), _raw(block_tables),
                                  block_tables.shape[1], _raw(seq_lens), _raw(cu_seqlens_q), S, T, max_q, hq, hkv, hd,
                                  nb, bs, max_context, window, float(scale), 1 if causal else 0, _dtype(q),
-                                 *_ws(workspace), _raw_stream(stream))
+                                 *_ws(workspace),
+                                 _raw_stream(stream, weights, q, k_cache, block_tables, seq_lens, cu_seqlens_q,
+                                             workspace))
     _check(st, "pa_prompt_weights")
     return weights
 
@@ -597,7 +625,9 @@ def pa_prompt_weights_fp8(weights, q, k_codes, k_scales, block_tables, seq_lens,
     st = lib().pa_prompt_weights_fp8(_raw(weights), stride, _raw(q), _raw(k_codes), _raw(k_scales),
                                      _raw(block_tables), block_tables.shape[1], _raw(seq_lens), _raw(cu_seqlens_q), S,
                                      T, max_q, hq, hkv, hd, nb, bs, max_context, window, float(scale),
-                                     1 if causal else 0, _dtype(q), *_ws(workspace), _raw_stream(stream))
+                                     1 if causal else 0, _dtype(q), *_ws(workspace),
+                                     _raw_stream(stream, weights, q, k_codes, k_scales, block_tables, seq_lens,
+                                                 cu_seqlens_q, workspace))
     _check(st, "pa_prompt_weights_fp8")
     return weights
 
@@ -637,6 +667,9 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
                         _raw(recorded_lens), _raw(seen_lens), stride, _raw(k_cache), _raw(v_cache), _raw(k_scales),
                         _raw(v_scales), _raw(block_tables), block_tables.shape[1], _raw(new_block_tables),
                         new_block_tables.shape[1], _raw(context_lens), S, hkv, hd, nb, bs, max_context, keep,
-                        num_sink, num_recent, _pool_dtype(k_cache), *_ws(workspace), _raw_stream(stream))
+                        num_sink, num_recent, _pool_dtype(k_cache), *_ws(workspace),
+                        _raw_stream(stream, new_lens, weights_out, positions_out, weights, k_cache, v_cache,
+                                    block_tables, new_block_tables, context_lens, positions, recorded_lens, seen_lens,
+                                    k_scales, v_scales, workspace))
     _check(st, "pa_evict")
     return new_lens

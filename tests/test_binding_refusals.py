@@ -34,10 +34,12 @@ class _Lib:
 def lib(monkeypatch):
     fake = _Lib()
     monkeypatch.setattr(B, "lib", lambda: fake)
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_device_count", 2)
     return fake
 
 
-STREAM = types.SimpleNamespace(cuda_stream=0)
+STREAM = types.SimpleNamespace(cuda_stream=0, device_index=0)
 I32, F32, U8, F8 = torch.int32, torch.float32, torch.uint8, torch.float8_e4m3fn
 NB, BS, HKV, HQ, HD, S, N, MC = 6, 16, 2, 8, 64, 3, 5, 40
 
@@ -153,4 +155,37 @@ def test_evict_refuses_lengths_and_scales_that_do_not_fit(lib, kw):
     """A length per sequence: a shorter array would be read past its end."""
     with pytest.raises(ValueError):
         _evict(**kw)
+    assert lib.reached == 0
+
+
+def _on(device, t):
+    t._on = device
+    return t
+
+
+@pytest.mark.parametrize("call, kw", [
+    (_decode, dict(v=_on(1, _pool()))), (_decode, dict(tables=_on(1, _t(S, 3, dtype=I32)))),
+    (_prompt, dict(q=_on(1, _t(N, HQ, HD)))), (_rope, dict(k=_on(1, _t(N, HKV, HD)))),
+    (_rope, dict(pos=_on(1, _t(1, N, dtype=torch.int64)))), (_rope, dict(vc=_on(1, _pool()))),
+    (_evict, dict(k_cache=_on(1, _pool()))), (_evict, dict(weights=_on(1, _t(S, HKV, MC, dtype=F32))))])
+def test_tensors_of_another_device_are_refused(lib, call, kw):
+    with pytest.raises(ValueError, match="device"):
+        call(**kw)
+    assert lib.reached == 0
+
+
+@pytest.mark.parametrize("call", [_decode, _prompt, _rope, _evict])
+def test_a_current_device_other_than_the_tensors_is_refused(lib, monkeypatch, call):
+    """The library launches on the current device."""
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="device"):
+        call()
+    assert lib.reached == 0
+
+
+@pytest.mark.parametrize("call", [_decode, _prompt, _rope])
+def test_a_stream_of_another_device_is_refused(lib, monkeypatch, call):
+    monkeypatch.setattr(STREAM, "device_index", 1)
+    with pytest.raises(ValueError, match="device"):
+        call()
     assert lib.reached == 0
