@@ -214,9 +214,12 @@ __host__ __device__ constexpr bool tma_block_size(int bs) { return bs == 8 || (b
 // give; the stage's barrier then counts one arrival per lane.  SCORES: each
 // tile's fp32 scores are also stored (4 bytes per key and query head, in
 // whole 32-byte sectors, most of them still in L2 when they are read back);
-// over a code cache the query then enters the mma unscaled -- exact in f16
-// for f16 and for bf16 above f16's subnormals -- and the scale multiplies
-// the fp32 score, since a score is worth a weight's whole precision here.
+// over a code cache the query then enters the mma without the softmax scale,
+// which multiplies the fp32 score, since a score is worth a weight's whole
+// precision here.  An f16 query is exact in the f16 mma; a bf16 query head is
+// brought there by the power of two that puts its largest element into
+// [2^14, 2^15) (exact for elements down to 2^-28 of the largest, nothing
+// leaves f16's range), which the fp32 scores are divided by.
 template <typename T, int HD, int NT, bool FP8, bool PAIR, bool GATHER = false, bool SCORES = false>
 __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -443,6 +446,9 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
     // dims kb0 + 4kk + 2, +3), and head dims [g HD/8, (g+1) HD/8) of value
     // rows 2c4, 2c4+1, 2c4+8, 2c4+9 (m-tile mt, row g + 8hi: dim vb0 + 2mt + hi).
     const int kb0 = c4 * (HD / 4), vb0 = g * (HD / 8);
+    // SCORES over codes, bf16: query heads 2c4, 2c4+1 (of 8) entered times 1 / qsc
+    constexpr bool kFitQuery = FP8 && SCORES && std::is_same<T, __nv_bfloat16>::value;
+    float qsc[kFitQuery ? NT : 1][2];
 
     // the new token's K/V rows of unit (cs, ch), and the pool block of position L-1
     auto load_new_rows = [&]() {
@@ -459,31 +465,65 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
     };
 
     auto begin_unit = [&]() {
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
+        if constexpr (kFitQuery) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int hh = nt * 8 + g;
+                uint32_t w[HD / 8] = {};  // this lane's elements, two each
+                float top = 0.f;
                 if (hh < G) {
-                    const T* qrow = qbase + ((int64_t)cs * p.num_heads + ch * G + hh) * HD;
-                    if constexpr (FP8) {
-                        float x[4];
+                    const uint4* qrow =
+                        reinterpret_cast<const uint4*>(qbase + ((int64_t)cs * p.num_heads + ch * G + hh) * HD + kb0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[e] = Elt<T>::to_f(qrow[kb0 + 4 * kk + e]);
-                            if constexpr (!SCORES) x[e] *= p.scale_log2;
-                        }
-                        qb[kk][nt][0] = pack2<__half>(x[0], x[1]);
-                        qb[kk][nt][1] = pack2<__half>(x[2], x[3]);
-                    } else {
-                        const T* qp = qrow + kk * 16 + 2 * c4;
-                        qb[kk][nt][0] = *reinterpret_cast<const uint32_t*>(qp);
-                        qb[kk][nt][1] = *reinterpret_cast<const uint32_t*>(qp + 8);
+                    for (int d = 0; d < HD / 32; ++d) {
+                        const uint4 v = qrow[d];
+                        w[4 * d] = v.x, w[4 * d + 1] = v.y, w[4 * d + 2] = v.z, w[4 * d + 3] = v.w;
                     }
-                } else {
-                    qb[kk][nt][0] = qb[kk][nt][1] = 0u;
                 }
+#pragma unroll
+                for (int d = 0; d < HD / 8; ++d)  // (bf16: the upper half of an fp32)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[d] << 16)),
+                                           fabsf(__uint_as_float(w[d] & 0xffff0000u))));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // exponent field of the factor: 127 + 14 - (e - 127), at most
+                // 2^73 (smaller elements weigh nothing); an infinite row keeps 1
+                const uint32_t e = top == INFINITY ? 127u : min(268u - (__float_as_uint(top) >> 23), 200u);
+                const float fit = __uint_as_float(e << 23), inv = __uint_as_float((254u - e) << 23);
+                qsc[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c4);
+                qsc[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c4 + 4);
+#pragma unroll
+                for (int d = 0; d < HD / 8; ++d)
+                    qb[d / 2][nt][d % 2] = pack2<__half>(__uint_as_float(w[d] << 16) * fit,
+                                                         __uint_as_float(w[d] & 0xffff0000u) * fit);
             }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int hh = nt * 8 + g;
+                    if (hh < G) {
+                        const T* qrow = qbase + ((int64_t)cs * p.num_heads + ch * G + hh) * HD;
+                        if constexpr (FP8) {
+                            float x[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                x[e] = Elt<T>::to_f(qrow[kb0 + 4 * kk + e]);
+                                if constexpr (!SCORES) x[e] *= p.scale_log2;
+                            }
+                            qb[kk][nt][0] = pack2<__half>(x[0], x[1]);
+                            qb[kk][nt][1] = pack2<__half>(x[2], x[3]);
+                        } else {
+                            const T* qp = qrow + kk * 16 + 2 * c4;
+                            qb[kk][nt][0] = *reinterpret_cast<const uint32_t*>(qp);
+                            qb[kk][nt][1] = *reinterpret_cast<const uint32_t*>(qp + 8);
+                        }
+                    } else {
+                        qb[kk][nt][0] = qb[kk][nt][1] = 0u;
+                    }
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mrow[nt][0] = mrow[nt][1] = -INFINITY;
@@ -843,6 +883,10 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (kFitQuery) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] *= qsc[nt][e & 1];
+            }
             const float x0 = ok0 ? sc[nt][0] * sm0 : -INFINITY;
             const float x1 = ok0 ? sc[nt][1] * sm0 : -INFINITY;
             const float x2 = ok1 ? sc[nt][2] * sm1 : -INFINITY;
