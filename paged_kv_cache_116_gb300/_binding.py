@@ -422,20 +422,21 @@ def _rope_rows(name, t, n, heads, hd):
     return st if n > 1 else max(st, heads * hd)
 
 
-def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd):
-    _dev(q_out, positions, inv_freq, slot_mapping, pair_axis)
-    if positions.dim() == 1:
-        positions = positions[None]
-    if positions.dim() != 2 or slot_mapping.dim() != 1 or (q is not None and q_out is None):
-        raise ValueError("positions must be [num_axes, n], slot_mapping [n], and a q needs its q_out")
-    n = positions.shape[1]
+def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, k_pool, v_pool, codes):
+    _dev(q_out, positions, inv_freq, slot_mapping, pair_axis, k_pool, v_pool)
+    shape = positions.shape
+    if len(shape) not in (1, 2) or (q is not None and q_out is None):
+        raise ValueError("positions must be [num_axes, n] or [n], and a q needs its q_out")
+    n, axes = shape[-1], shape[0] if len(shape) == 2 else 1
+    _, _, hkv, hd = k_pool.shape
     if positions.dtype != torch.int64 or inv_freq.dtype != torch.float64 or slot_mapping.dtype != torch.int64:
         raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
     if pair_axis is not None and (pair_axis.dtype != torch.int32 or pair_axis.numel() != inv_freq.numel()):
         raise ValueError("pair_axis must be int32 with one entry per frequency")
     dt = k.dtype
-    if slot_mapping.shape[0] != n or v.dtype != dt:
+    if slot_mapping.shape != (n,) or v.dtype != dt:
         raise ValueError("positions and slot_mapping must hold one entry per token, k and v one dtype")
+    _pools(k_pool, v_pool, dt, codes)
     hq, qs = 0, 0
     if q is not None:
         hq = q.shape[1]
@@ -443,7 +444,7 @@ def _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv
             raise ValueError("q_out must be [n, heads, head_dim], and q, q_out, k and v of one dtype")
         qs = _rope_rows("q", q, n, hq, hd)
     ks, vs = _rope_rows("k", k, n, hkv, hd), _rope_rows("v", v, n, hkv, hd)
-    return (_raw(q_out), _raw(q), _raw(k), _raw(v), qs, ks, vs, _raw(positions), positions.shape[0], _raw(inv_freq),
+    return (_raw(q_out), _raw(q), _raw(k), _raw(v), qs, ks, vs, _raw(positions), axes, _raw(inv_freq),
             _raw(pair_axis), 2 * inv_freq.numel()), n, hq
 
 
@@ -453,10 +454,8 @@ def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
 
     positions [num_axes, n] (or [n]) int64, inv_freq [rot_dim / 2] float64, pair_axis [rot_dim / 2] int32 (None: one
     axis), all on the device.  Tokens of q, k and v may lie at any stride; q None: keys and values only."""
-    _dev(k_cache, v_cache)
+    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, k_cache, v_cache, False)
     nb, bs, hkv, hd = k_cache.shape
-    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
-    _pools(k_cache, v_cache, k.dtype)
     st = lib().pa_rope_write_kv(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_cache), _raw(v_cache),
                                 nb, bs, hq, hkv, hd, _dtype(k),
                                 _raw_stream(stream, q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
@@ -468,10 +467,9 @@ def pa_rope_write_kv(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
 def pa_rope_write_kv_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_codes, v_codes, k_scales, v_scales,
                          pair_axis=None, interleaved=False, stream=None):
     """pa_rope_write_kv into a quantized cache: codes [NB, bs, Hkv, hd] uint8, scales [NB, Hkv, bs] fp32."""
-    _dev(k_codes, v_codes, k_scales, v_scales)
+    _dev(k_scales, v_scales)
+    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, k_codes, v_codes, True)
     nb, bs, hkv, hd = k_codes.shape
-    args, n, hq = _rope_args(q_out, q, k, v, positions, inv_freq, slot_mapping, pair_axis, hkv, hd)
-    _pools(k_codes, v_codes, None, True)
     _scale_pools(nb, hkv, bs, k_scales, v_scales)
     st = lib().pa_rope_write_kv_fp8(*args, 1 if interleaved else 0, _raw(slot_mapping), n, _raw(k_codes),
                                     _raw(v_codes), _raw(k_scales), _raw(v_scales), nb, bs, hq, hkv, hd, _dtype(k),
@@ -653,7 +651,7 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("the pools must be of one shape and dtype")
     for t in (context_lens, new_lens, recorded_lens, seen_lens):
-        if t is not None and t.shape != (S,):
+        if t is not None and t.numel() != S:
             raise ValueError("context_lens, new_lens, recorded_lens and seen_lens hold one entry per sequence")
     stride = _weight_rows("weights", weights, S, hkv)
     rows = [("weights_out", weights_out, torch.float32), ("positions_out", positions_out, torch.int32),
