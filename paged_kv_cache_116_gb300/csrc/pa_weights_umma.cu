@@ -433,8 +433,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             for (int t = w.b0; t < w.b1; ++t, ++nb) {
                 const int slot = nb % RING, par = (t - w.b0) & 1, turn = par ? nd[1] : nd[0];
                 const bool mine = alone ? spread_alone && ((t - w.b0) >> 1 & 1) == (int)x || !spread_alone && x == 0 : true;
-                run = mbar_wait_ns_warp(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
-                      (!mine || mbar_wait_ns_warp(&d_empty[2 * x + par], ((uint32_t)turn & 1u) ^ 1u, WAIT_NS));
+                run = __all_sync(0xffffffffu, mbar_wait_ns(&b_full[slot], (uint32_t)(nb / RING) & 1u, WAIT_NS) &&
+                                                  (!mine || mbar_wait_ns(&d_empty[2 * x + par],
+                                                                         ((uint32_t)turn & 1u) ^ 1u, WAIT_NS)));
                 if (!run) break;
                 tc_fence_after();
                 const uint32_t b_lo = lane0(s_lo + (Gm::RING_OFF + slot * Gm::TILE) / 16);
@@ -483,8 +484,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[2 * x + par]);
         };
+        // (each lane's own answer: the warp's is the vote of all, one for the waits of a tile)
         auto acquire = [&](int x) -> bool {
-            const bool ok = mbar_wait_ns_warp(&d_full[2 * x + par], (uint32_t)n_d[x]++ & 1u, WAIT_NS);
+            const bool ok = mbar_wait_ns(&d_full[2 * x + par], (uint32_t)n_d[x]++ & 1u, WAIT_NS);
             tc_fence_after();
             return ok;
         };
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                             continue;
                         }
                     }
-                    if (!(run = acquire(hi))) break;
+                    if (!(run = __all_sync(0xffffffffu, acquire(hi)))) break;
                     // rows that hold no query are never stored; they take the
                     // unmasked path with their warp
                     const int vis = valid ? min(last - t * TM, TM - 1) : TM - 1;
@@ -710,9 +712,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
                     const float* nm = stat_s + sl * TM + hi * HC;
-                    if (!(run = mbar_wait_ns_warp(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS) && acquire(0) &&
-                                (w.na < 2 || acquire(NA - 1))))
-                        break;
+                    bool ok = mbar_wait_ns(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS);
+                    ok = acquire(0) && ok;
+                    if (w.na == 2) ok = acquire(NA - 1) && ok;
+                    if (!(run = __all_sync(0xffffffffu, ok))) break;
                     // column c (query row) counts for key k where lo[k] <= c < end
                     const int end = min(TT, w.sq.rows - t * TT) * G;
                     int lo[2];
@@ -804,7 +807,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     for (int x = 0; x < NA; ++x) {
                         if (x >= w.na) break;
                         const int ax = x + turn;
-                        if (!(run = acquire(ax))) break;
+                        if (!(run = __all_sync(0xffffffffu, acquire(ax)))) break;
                         const int end = min(TT, w.sq.rows - x * TT) * G;
                         const int lo[2] = {p.causal ? (key - (w.sq.L - w.sq.rows) - x * TT) * G : 0, 0};
                         const bool full = __all_sync(0xffffffffu, lo[0] <= 0 && end == TT * G);
