@@ -1031,7 +1031,8 @@ static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, 
         p.cut = pa::weights_umma_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size,
                                       max_context, window, fp8);
     else
-        p.cut.stats_bytes = (size_t)total_q * num_heads * sizeof(float2);
+        p.cut.stats_bytes =
+            (size_t)pa::weight_stat_rows(num_seqs, total_q, window).rows * num_heads * sizeof(float2);
     return p;
 }
 
@@ -1082,6 +1083,9 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     ws += plan.cut.dense_bytes;
     a.key_scales = reinterpret_cast<float*>(ws);
     ws += plan.cut.scale_bytes;
+    const pa::WeightStatRows sr = pa::weight_stat_rows(num_seqs, total_q, window);
+    a.stat_rows = sr.rows;
+    a.stat_pitch = sr.pitch;
     a.stats = reinterpret_cast<float2*>(ws);
     a.tile_stats = reinterpret_cast<float*>(ws + plan.cut.stats_bytes);
     a.stat_tiles = plan.cut.stat_tiles;

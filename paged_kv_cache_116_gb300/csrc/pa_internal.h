@@ -198,7 +198,9 @@ struct WeightArgs {
     float scale_log2;
     int dtype;
     int kv_fp8;
-    float2* stats;  // [total_q, num_heads]: each row's maximum (log2 domain) and 1 / sum
+    float2* stats;  // [stat_rows, num_heads]: each counted row's maximum (log2 domain) and 1 / sum
+    int stat_rows = 0;
+    int stat_pitch = 0;  // WeightStatRows::pitch
     uint32_t* next_item = nullptr;  // two counters (workspace)
     void* dense_keys = nullptr;     // [num_seqs, dense_stride, num_kv_heads, head_dim] of the query's type
     float* key_scales = nullptr;    // [num_seqs, num_kv_heads, dense_stride], times scale_log2
@@ -212,9 +214,20 @@ struct WeightArgs {
 };
 // Requests one launch handles (their tile counts' prefix lives in shared memory).
 constexpr int kWeightMaxSeqsPerLaunch = 4096;
+// Rows of statistics a launch holds.  A window much shorter than the new
+// tokens counts few of them: request s of the launch then has `pitch` rows
+// from s * pitch on; otherwise (pitch 0) they lie as q's rows do.
+struct WeightStatRows {
+    int32_t rows, pitch;
+};
+inline WeightStatRows weight_stat_rows(int32_t num_seqs, int32_t total_q, int32_t window) {
+    const int64_t seqs = num_seqs < kWeightMaxSeqsPerLaunch ? num_seqs : kWeightMaxSeqsPerLaunch;
+    if (window > 0 && seqs * window < total_q) return {(int32_t)(seqs * window), window};
+    return {total_q, 0};
+}
 cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
 // The same on the tensor cores (pa_weights_umma.cu), which cut the work as
-// their plan says.  stats then holds key_splits pieces of [total_q, num_heads]
+// their plan says.  stats then holds key_splits pieces of [stat_rows, num_heads]
 // (maximum, sum), partial row_splits pieces of [num_seqs, num_kv_heads,
 // max_context].
 struct WeightPlan {

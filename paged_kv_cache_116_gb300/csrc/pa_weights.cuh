@@ -13,7 +13,8 @@ struct WeightSeq {
     int L;       // keys
     int n;       // new tokens
     int rows;    // of them counted: the last min(n, window)
-    int row0;    // row of q (and of stats) of the first counted one
+    int row0;    // row of q of the first counted one
+    int stat0;   // row of its statistics
 };
 
 __device__ __forceinline__ WeightSeq weight_seq(const WeightArgs& a, int s) {
@@ -29,6 +30,7 @@ __device__ __forceinline__ WeightSeq weight_seq(const WeightArgs& a, int s) {
     if (q.L <= 0) q.L = q.n = 0;
     q.rows = a.window > 0 ? min(q.n, a.window) : q.n;
     q.row0 = end - q.rows;
+    q.stat0 = a.stat_pitch ? s * a.stat_pitch : q.row0;
     return q;
 }
 

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(NTH) row_stats_kernel(const WeightArgs a) {
             for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
             const int r = r0 + ty + 16 * i;
             if (tx == 0 && r < sq.rows * G)
-                a.stats[(int64_t)(sq.row0 + r / G) * a.num_heads + h * G + r % G] =
+                a.stats[(int64_t)(sq.stat0 + r / G) * a.num_heads + h * G + r % G] =
                     make_float2(m[i] == -INFINITY ? 0.f : m[i], 1.f / l[i]);
         }
     }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(NTH) key_weights_kernel(const WeightArgs a) {
             for (int i = 0; i < 4; ++i) {
                 const int r = r0 + ty + 16 * i, vis = visible(a, sq, r, G);
                 if (vis <= k0) continue;
-                const float2 st = a.stats[(int64_t)(sq.row0 + r / G) * a.num_heads + h * G + r % G];
+                const float2 st = a.stats[(int64_t)(sq.stat0 + r / G) * a.num_heads + h * G + r % G];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (k0 + tx + 16 * j < vis) sum[j] = fmaf(exp2f(x[i][j] - st.x), st.y, sum[j]);

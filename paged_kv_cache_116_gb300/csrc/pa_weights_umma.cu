@@ -149,7 +149,7 @@ __device__ __forceinline__ float row_stat(float m, float l) { return (m == -INFI
 // The statistic of one row (an index into a piece of p.stats), joined over
 // pass 1's key splits.
 __device__ __forceinline__ float joined_stat(const WeightArgs& p, int64_t row) {
-    const int64_t part = (int64_t)p.total_q * p.num_heads;
+    const int64_t part = (int64_t)p.stat_rows * p.num_heads;
     constexpr int B = 8;  // pieces in flight
     float2 s = make_float2(-INFINITY, 0.f);
     for (int z0 = 0; z0 < p.key_splits; z0 += B) {
@@ -282,9 +282,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     };
     // where query tile t of a request keeps its statistics: distinct for every
     // (request, tile), since a request's ceil(rows / T) tiles fit between its
-    // floor(row0 / T) + s and the next request's
+    // floor(stat0 / T) + s and the next request's
     auto stat_tile = [&](const WeightSeq& sq, int h, int t) -> int64_t {
-        return (int64_t)h * p.stat_tiles + sq.row0 / TT + sq.s + t;
+        return (int64_t)h * p.stat_tiles + sq.stat0 / TT + sq.s + t;
     };
     // The CTA's items: its own number first, then whatever is next in the grid
     // (items differ in length; dealt out in advance they left SMs idle).  The
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
         constexpr int HC = TM / NA;  // columns of a group in pass 2
         const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + par * TM;  // + 2 TM x
         const float sl = p.scale_log2;
-        const int64_t part = (int64_t)p.total_q * p.num_heads;  // rows of one split's statistics
+        const int64_t part = (int64_t)p.stat_rows * p.num_heads;  // rows of one split's statistics
         int nx = 0, n_meet = 0;              // streamed tiles; barriers gone through
         int n_join[3] = {0, 0, 0};           // handovers through each buffer
         int n_d[2] = {0, 0};                 // accumulators of x worked by this group
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     if (splits == 1) {
                         p.tile_stats[stat_tile(w.sq, w.h, w.a0 + x) * TM + m] = valid ? row_stat(m_used, l) : 0.f;
                     } else if (valid) {
-                        p.stats[(int64_t)w.z * part + (int64_t)(w.sq.row0 + tok) * p.num_heads + w.h * G + g] =
+                        p.stats[(int64_t)w.z * part + (int64_t)(w.sq.stat0 + tok) * p.num_heads + w.h * G + g] =
                             make_float2(m_used, l);
                     }
                 }
@@ -939,8 +939,8 @@ __global__ void __launch_bounds__(TM) stats_join_kernel(const WeightArgs p) {
         locate_work(prefix, p.num_seqs, p.num_kv_heads, it, s, h, tile);
         const WeightSeq sq = weight_seq(p, s);
         const int tok = tile * TT + m / G;
-        p.tile_stats[((int64_t)h * p.stat_tiles + sq.row0 / TT + s + tile) * TM + m] =
-            m < TT * G && tok < sq.rows ? joined_stat(p, (int64_t)(sq.row0 + tok) * p.num_heads + h * G + m % G) : 0.f;
+        p.tile_stats[((int64_t)h * p.stat_tiles + sq.stat0 / TT + s + tile) * TM + m] =
+            m < TT * G && tok < sq.rows ? joined_stat(p, (int64_t)(sq.stat0 + tok) * p.num_heads + h * G + m % G) : 0.f;
     }
 }
 
@@ -1072,8 +1072,9 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     // partial statistics (several key splits), and the statistics by query
     // tile that pass 2 reads
     auto round = [](size_t b) { return (b + 255) / 256 * 256; };
-    if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * total_q * num_heads * sizeof(float2));
-    w.stat_tiles = total_q / TT + num_seqs + 1;
+    const int64_t stat_rows = weight_stat_rows(num_seqs, total_q, window).rows;
+    if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * stat_rows * num_heads * sizeof(float2));
+    w.stat_tiles = (int)(stat_rows / TT) + std::min(num_seqs, kWeightMaxSeqsPerLaunch) + 1;
     w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * TM * sizeof(float);
     // pools that no box fits, and code pools, are laid out densely first
     if (kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256))) {
