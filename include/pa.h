@@ -496,7 +496,10 @@ PA_API pa_status pa_rope_write_kv_fp8(void* q_out, const void* q, const void* k,
  *              belonging to sequence s as its block-table row does;
  *              weights_stride >= max_context
  *   workspace: pa_decode_weights_workspace_size(...) bytes, 16-byte aligned;
- *              its content on entry does not matter
+ *              its content on entry does not matter.  On the tensor cores it
+ *              holds 4 * num_heads bytes per token of max_context, of as many
+ *              sequences as take 4 GiB, one at least; the others follow in
+ *              further launches
  * The other arguments and the kernels' conditions are pa_decode's.  Weights
  * are per sequence, so sequences may share blocks.
  */
@@ -544,8 +547,9 @@ PA_API pa_status pa_decode_weights_fp8(void* out, float* weights, int64_t weight
  * head run on the tcgen05 kernels (PA_OPT_VARLEN_KERNEL pins a kernel as it
  * does for pa_varlen), the rest on the CUDA cores.  Caches whose block_size is
  * neither 8 nor a multiple of 16 up to 256, and quantized ones, are first laid
- * out densely in the workspace, which then holds num_seqs * max_context keys
- * in the query's type.
+ * out densely in the workspace, which then holds max_context keys (at most
+ * 2^29) of as many requests as take 4 GiB, one at least, in the query's type;
+ * the others follow in further launches.
  */
 PA_API size_t pa_prompt_weights_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

@@ -926,6 +926,7 @@ static size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 // row statistics.
 struct DecodeWeightsSpace {
     bool tc = false;
+    int seqs = 0;  // sequences per launch (tensor-core path)
     int grid = 0;
     size_t records = 0, stats = 0, scores = 0;
     size_t total() const { return records + stats + scores; }
@@ -938,10 +939,12 @@ static DecodeWeightsSpace decode_weights_space(int32_t num_seqs, int32_t num_hea
     w.tc = use_decode_tc(dtype, head_dim, block_size, G, fp8, sel);
     w.stats = align256((size_t)num_seqs * num_heads * sizeof(float2));
     if (w.tc) {
-        w.grid = pa::decode_weights_grid(num_seqs, num_kv_heads, head_dim, block_size, max_context, dtype, G,
+        const size_t scores = pa::decode_weights_scores(num_heads, max_context);
+        w.seqs = pa::seqs_per_launch(num_seqs, (double)scores, pa::kDecodeMaxSeqsPerLaunch);
+        w.scores = w.seqs * scores;
+        w.grid = pa::decode_weights_grid(w.seqs, num_kv_heads, head_dim, block_size, max_context, dtype, G,
                                          g_options[PA_OPT_DECODE_CTAS], fp8);
         w.records = align256(pa::decode_tc_workspace(num_seqs, num_kv_heads, G, head_dim, w.grid, fp8));
-        w.scores = pa::decode_weights_scores(num_seqs, num_heads, max_context);
     }
     return w;
 }
@@ -993,8 +996,8 @@ static pa_status decode_weights_impl(void* out, float* weights, int64_t weights_
         }
         return PA_OK;
     }
-    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kDecodeMaxSeqsPerLaunch) {
-        const int32_t cnt = std::min(num_seqs - s0, pa::kDecodeMaxSeqsPerLaunch);
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += sp.seqs) {
+        const int32_t cnt = std::min(num_seqs - s0, sp.seqs);
         pa::AttnArgs c = decode_part(a, s0, cnt);
         pa::DecodeWeights w;
         w.weights = weights + (int64_t)s0 * num_kv_heads * weights_stride;
@@ -1027,12 +1030,14 @@ static PromptWeightsPlan prompt_weights_plan(int32_t num_seqs, int32_t total_q, 
         return p;
     const int G = num_heads / num_kv_heads;
     p.tc = g_options[PA_OPT_VARLEN_KERNEL] != 1 && pa::weights_umma_supported(dtype, head_dim, G);
-    if (p.tc)
+    if (p.tc) {
         p.cut = pa::weights_umma_plan(num_seqs, total_q, max_q, num_heads, num_kv_heads, head_dim, block_size,
                                       max_context, window, fp8);
-    else
+    } else {
+        p.cut.seqs = std::min(num_seqs, pa::kWeightMaxSeqsPerLaunch);
         p.cut.stats_bytes =
-            (size_t)pa::weight_stat_rows(num_seqs, total_q, window).rows * num_heads * sizeof(float2);
+            (size_t)pa::weight_stat_rows(p.cut.seqs, total_q, window).rows * num_heads * sizeof(float2);
+    }
     return p;
 }
 
@@ -1064,7 +1069,7 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
         return fail(PA_ERR_UNSUPPORTED, "the tcgen05 weight kernels take bf16/f16 queries, head_dim 64/128/256 and at "
                                         "most 128 query heads per KV head");
     if (plan.tc && plan.cut.dense_stride < 0)
-        return fail(PA_ERR_UNSUPPORTED, "num_seqs * max_context keys laid out densely must fit in int32");
+        return fail(PA_ERR_UNSUPPORTED, "max_context must be at most 2^29 where the keys are laid out densely");
     if (!workspace || workspace_bytes < plan.bytes())
         return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace_bytes) + " bytes, " +
                                           std::to_string(plan.bytes()) + " needed");
@@ -1083,7 +1088,7 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     ws += plan.cut.dense_bytes;
     a.key_scales = reinterpret_cast<float*>(ws);
     ws += plan.cut.scale_bytes;
-    const pa::WeightStatRows sr = pa::weight_stat_rows(num_seqs, total_q, window);
+    const pa::WeightStatRows sr = pa::weight_stat_rows(plan.cut.seqs, total_q, window);
     a.stat_rows = sr.rows;
     a.stat_pitch = sr.pitch;
     a.stats = reinterpret_cast<float2*>(ws);
@@ -1093,8 +1098,8 @@ static pa_status prompt_weights_impl(float* weights, int64_t weights_stride, con
     a.key_splits = plan.cut.key_splits;
     a.row_splits = plan.cut.row_splits;
     a.few_rows = plan.cut.few_rows ? 1 : 0;
-    for (int32_t s0 = 0; s0 < num_seqs; s0 += pa::kWeightMaxSeqsPerLaunch) {
-        const pa::WeightArgs c = weights_part(a, s0, std::min(num_seqs - s0, pa::kWeightMaxSeqsPerLaunch));
+    for (int32_t s0 = 0; s0 < num_seqs; s0 += plan.cut.seqs) {
+        const pa::WeightArgs c = weights_part(a, s0, std::min(num_seqs - s0, plan.cut.seqs));
         std::string err;
         cudaError_t e = plan.tc ? pa::launch_weights_umma(c, num_blocks, &err, st)
                                 : pa::launch_weights_simt(c, st);

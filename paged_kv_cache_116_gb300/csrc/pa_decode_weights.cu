@@ -74,9 +74,8 @@ int decode_weights_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim
                      : grid_nt<__half, 1>(s, num_kv_heads, head_dim, block_size, max_context, ctas_override, kv_fp8);
 }
 
-size_t decode_weights_scores(int32_t num_seqs, int32_t num_heads, int32_t max_context) {
-    const int64_t s = std::min(num_seqs, kDecodeMaxSeqsPerLaunch);
-    return (size_t)(s * num_heads) * ((max_context + BS - 1) / BS * BS) * sizeof(float);
+size_t decode_weights_scores(int32_t num_heads, int32_t max_context) {
+    return (size_t)num_heads * (((size_t)max_context + BS - 1) / BS * BS) * sizeof(float);
 }
 
 cudaError_t launch_decode_weights(const AttnArgs& a, int32_t num_blocks, int grid_ctas, void* workspace,

@@ -18,6 +18,20 @@ inline int elt_size(int dtype) { return dtype == 0 ? 4 : (dtype == 3 ? 1 : 2); }
 // larger batches into launches of at most this many sequences.
 constexpr int kDecodeMaxSeqsPerLaunch = 4096;
 
+// What a launch of the weight operators may keep per token of max_context in
+// the workspace (the scores of a decode, a dense copy of the keys of a
+// prompt): these grow with sequences times max_context whatever the lengths
+// are, so batches beyond it are worked in several launches, of one sequence at
+// least.  1.5 % of the GPU's memory; 32 heads' scores over 131,072 tokens are
+// 17 MB a sequence, the keys of 8 heads of 128 are 268 MB.
+constexpr int64_t kScratchBytes = (int64_t)4 << 30;
+inline int32_t seqs_per_launch(int32_t num_seqs, double bytes_per_seq, int32_t most) {
+    const int32_t n = num_seqs < most ? num_seqs : most;
+    if (n * bytes_per_seq <= kScratchBytes) return n;
+    const double fit = kScratchBytes / bytes_per_seq;  // (below n)
+    return fit < 1 ? 1 : (int32_t)fit;
+}
+
 // Most layers one pa_copy_blocks call takes (their pointers travel in the
 // kernel's parameter block).  Equal to PA_MAX_LAYERS of pa.h.
 #define PA_MAX_LAYERS_INTERNAL 128
@@ -124,12 +138,13 @@ uint32_t decode_tc_status(bool clear);
 struct DecodeWeights {
     float* weights;  // [num_seqs, num_kv_heads, stride]
     int64_t stride;
-    float* scores;      // decode_weights_scores(...) bytes
+    float* scores;      // decode_weights_scores(...) bytes per sequence of the launch
     float2* row_stats;  // [num_seqs, num_heads]
 };
 int decode_weights_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                         int32_t max_context, int dtype, int32_t group, int64_t ctas_override, bool kv_fp8);
-size_t decode_weights_scores(int32_t num_seqs, int32_t num_heads, int32_t max_context);
+// Bytes of one sequence's scores.
+size_t decode_weights_scores(int32_t num_heads, int32_t max_context);
 cudaError_t launch_decode_weights(const AttnArgs& a, int32_t num_blocks, int grid_ctas, void* workspace,
                                   const DecodeWeights& w, std::string* err, cudaStream_t stream);
 uint32_t decode_weights_status(bool clear);
@@ -220,9 +235,8 @@ constexpr int kWeightMaxSeqsPerLaunch = 4096;
 struct WeightStatRows {
     int32_t rows, pitch;
 };
-inline WeightStatRows weight_stat_rows(int32_t num_seqs, int32_t total_q, int32_t window) {
-    const int64_t seqs = num_seqs < kWeightMaxSeqsPerLaunch ? num_seqs : kWeightMaxSeqsPerLaunch;
-    if (window > 0 && seqs * window < total_q) return {(int32_t)(seqs * window), window};
+inline WeightStatRows weight_stat_rows(int32_t seqs, int32_t total_q, int32_t window) {
+    if (window > 0 && (int64_t)seqs * window < total_q) return {seqs * window, window};
     return {total_q, 0};
 }
 cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
@@ -231,6 +245,7 @@ cudaError_t launch_weights_simt(const WeightArgs& a, cudaStream_t stream);
 // (maximum, sum), partial row_splits pieces of [num_seqs, num_kv_heads,
 // max_context].
 struct WeightPlan {
+    int seqs = 0;           // requests per launch
     int key_splits = 1;
     int row_splits = 1;
     bool few_rows = false;  // row_splits then cuts the keys, without partial weights

@@ -1057,36 +1057,40 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     constexpr int64_t kSms = 152, kMinTiles = 16;
     const int G = num_heads / num_kv_heads, TT = TM / G, NA = head_dim <= 128 ? 2 : 1;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    auto round = [](size_t b) { return (b + 255) / 256 * 256; };
     WeightPlan w;
-    const int64_t rows = window > 0 ? std::min<int64_t>(total_q, (int64_t)num_seqs * window) : total_q;
     const int32_t row_max = window > 0 ? std::min(max_q, window) : max_q;  // of one request
     const int64_t k_tiles = up(max_context, TM), q_tiles = up(row_max, TT);
+    // pools that no box fits, and code pools, are laid out densely first, of as
+    // many requests at a time as the scratch space takes
+    const bool dense = kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256));
+    const int64_t stride = k_tiles * TM, key_bytes = (int64_t)num_kv_heads * head_dim * 2;
+    const int64_t scale_bytes = kv_fp8 ? num_kv_heads * (int64_t)sizeof(float) : 0;
+    w.seqs = seqs_per_launch(num_seqs, dense ? (double)stride * (key_bytes + scale_bytes) : 0, kWeightMaxSeqsPerLaunch);
+    if (dense) {
+        // (several requests' tokens fit in int32 because their bytes fit in
+        // the scratch space, at 128 each or more)
+        w.dense_stride = stride <= (1 << 29) ? (int)stride : -1;  // (refused)
+        w.dense_bytes = (size_t)w.seqs * stride * key_bytes;
+        w.scale_bytes = (size_t)w.seqs * stride * scale_bytes;
+    }
+    const int64_t rows = window > 0 ? std::min<int64_t>(total_q, (int64_t)w.seqs * window) : total_q;
     w.few_rows = q_tiles <= NA;
     auto pieces = [&](int64_t items, int64_t tiles, int64_t most) {
         const int64_t want = w.few_rows ? 3 * kSms / items : up(2 * kSms, items);
         return (int)std::max<int64_t>(1, std::min({want, tiles / kMinTiles, most}));
     };
-    const int64_t units = (int64_t)num_seqs * num_kv_heads;
+    const int64_t units = (int64_t)w.seqs * num_kv_heads;
     w.key_splits = pieces(w.few_rows ? units : std::max<int64_t>(1, up(rows, NA * TT)) * num_kv_heads, k_tiles, 64);
     w.row_splits = w.few_rows ? pieces(units, k_tiles, 256) : pieces(units * up(k_tiles, NA), q_tiles, 8);
     // partial statistics (several key splits), and the statistics by query
     // tile that pass 2 reads
-    auto round = [](size_t b) { return (b + 255) / 256 * 256; };
-    const int64_t stat_rows = weight_stat_rows(num_seqs, total_q, window).rows;
+    const int64_t stat_rows = weight_stat_rows(w.seqs, total_q, window).rows;
     if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * stat_rows * num_heads * sizeof(float2));
-    w.stat_tiles = (int)(stat_rows / TT) + std::min(num_seqs, kWeightMaxSeqsPerLaunch) + 1;
+    w.stat_tiles = (int)(stat_rows / TT) + w.seqs + 1;
     w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * TM * sizeof(float);
-    // pools that no box fits, and code pools, are laid out densely first
-    if (kv_fp8 || !(block_size == 8 || (block_size % GRP == 0 && block_size <= 256))) {
-        const size_t tokens = (size_t)std::min(num_seqs, kWeightMaxSeqsPerLaunch) * (size_t)(k_tiles * TM);
-        w.dense_stride = tokens <= INT32_MAX ? (int)(k_tiles * TM) : -1;  // (refused)
-        w.dense_bytes = tokens * num_kv_heads * head_dim * 2;
-        if (kv_fp8) w.scale_bytes = tokens * num_kv_heads * sizeof(float);
-    }
-    w.partial_bytes = !w.few_rows && w.row_splits > 1
-                          ? (size_t)w.row_splits * std::min(num_seqs, kWeightMaxSeqsPerLaunch) * num_kv_heads *
-                                max_context * sizeof(float)
-                          : 0;
+    if (!w.few_rows && w.row_splits > 1)
+        w.partial_bytes = (size_t)w.row_splits * units * max_context * sizeof(float);
     return w;
 }
 

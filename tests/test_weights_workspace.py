@@ -36,3 +36,32 @@ def test_a_window_beyond_the_prompt_changes_nothing(lib, dtype):
     for window in (300, 4096, 2 ** 31 - 1):
         a = lib.pa_prompt_weights_workspace_size(3, 600, 300, 8, 2, 128, 16, 400, window, dtype)
         assert a == lib.pa_prompt_weights_workspace_size(3, 600, 300, 8, 2, 128, 16, 400, 0, dtype)
+
+
+GIB = 1 << 30
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_dense_keys_of_many_long_requests_are_laid_out_in_parts(lib, fp8):
+    """Blocks that no box fits, and codes: a copy of the keys of as many requests at a time as some GiB hold."""
+    def size(seqs, context, bs=12):
+        fn = lib.pa_prompt_weights_fp8_workspace_size if fp8 else lib.pa_prompt_weights_workspace_size
+        return fn(seqs, seqs, 1, 32, 8, 128, bs, context, 0, BF16)
+
+    one = 131072 * 8 * 128 * 2
+    assert one < size(1, 131072) < 1.1 * one
+    assert size(64, 131072) <= 4.5 * GIB
+    assert size(100000, 131072) <= 4.5 * GIB
+    # one request is never cut: what it needs is asked for
+    assert size(2, 1 << 23) >= (1 << 23) * 8 * 128 * 2
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_of_many_long_sequences_are_kept_in_parts(lib, fp8):
+    def size(seqs, context):
+        fn = lib.pa_decode_weights_fp8_workspace_size if fp8 else lib.pa_decode_weights_workspace_size
+        return fn(seqs, 32, 8, 128, 16, context, BF16)
+
+    assert size(1, 131072) >= 131072 * 32 * 4
+    assert size(4096, 131072) <= 4.5 * GIB
+    assert size(2, 1 << 29) >= (1 << 29) * 32 * 4
