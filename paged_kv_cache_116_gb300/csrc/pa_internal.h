@@ -249,7 +249,7 @@ struct WeightPlan {
     int key_splits = 1;
     int row_splits = 1;
     bool few_rows = false;  // row_splits then cuts the keys, without partial weights
-    int stat_tiles = 0;     // tile_stats: [num_kv_heads, stat_tiles, 128]
+    int stat_tiles = 0;     // tile_stats: [num_kv_heads, stat_tiles, 2, 128]
     int dense_stride = 0;   // tokens per request of a dense copy of the keys; 0: read in place
     size_t stats_bytes = 0, tile_stats_bytes = 0, partial_bytes = 0, dense_bytes = 0, scale_bytes = 0;
 };

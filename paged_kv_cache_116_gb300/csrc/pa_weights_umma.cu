@@ -108,11 +108,11 @@ struct WGeo {
     static constexpr int CHB = TM * 128;      // bytes of one chunk of a tile
     static constexpr int TILE = CH * CHB;
     static constexpr int RING_OFF = NA * TILE;
-    // pass 2: the streamed query tiles' statistics, [SRING][128]; few rows:
-    // the stationary ones', [NA][128]
+    // pass 2: the streamed query tiles' statistics, SRING x {-M, 1 / l}[128];
+    // few rows: the stationary ones', [NA]{-M, 1 / l}[128]
     static constexpr int SRING = 8;
     static constexpr int STAT_OFF = RING_OFF + RING * TILE;
-    static constexpr int JOIN_OFF = STAT_OFF + SRING * TM * 4;  // results handed over, float2[3][128]
+    static constexpr int JOIN_OFF = STAT_OFF + SRING * 2 * TM * 4;  // results handed over, float2[3][128]
     static constexpr int BAR_OFF = JOIN_OFF + 3 * TM * 8;
     // a_full, a_empty, b_full[RING], b_empty[RING], d_full[NWG],
     // s_full[SRING], i_full[IRING], d_empty[NWG], s_empty[SRING],
@@ -138,17 +138,22 @@ struct Item {
     int z;       // piece of the streamed axis
 };
 
-// What pass 2 needs of a row: its weights are exp2(x + statistic), the
-// statistic being -(M + log2 l).  One number per column costs pass 2 half the
-// shared-memory reads of -M and 1 / l and an addition instead of an FMA (8,192
-// tokens: 498 against 521 us); its rounding, 2^-24 of its size, is that of a
-// score.  A row with only scores of -infinity (l = 0) gets +infinity, hence
-// NaN weights, as its softmax has.
-__device__ __forceinline__ float row_stat(float m, float l) { return (m == -INFINITY ? 0.f : -m) - log2f(l); }
+// What pass 2 needs of a row, (-M, 1 / l): its weights are exp2(x - M) / l.
+// One number -(M + log2 l) would spare half of pass 2's reads of statistics
+// (8,192 tokens: 517 instead of 533 us), but its rounding, 2^-24 of its size,
+// would be in every weight of the row: against 64 bits the whole prompt's
+// weights are off by 3.4e-7 in norm (one number: 3.9e-7), 16 chunks' by
+// 1.6e-7 (1.9e-7).  What is left is the tensor cores' accumulation, which cuts
+// where fp32 addition rounds: neither exp2f in place of ex2.approx nor
+// compensated sums of the tiles change it.  A row with only scores of
+// -infinity (l = 0) gets 1 / l infinite, hence NaN weights, as its softmax has.
+__device__ __forceinline__ float2 row_stat(float m, float l) {
+    return make_float2(m == -INFINITY ? 0.f : -m, 1.f / l);
+}
 
-// The statistic of one row (an index into a piece of p.stats), joined over
+// The statistics of one row (an index into a piece of p.stats), joined over
 // pass 1's key splits.
-__device__ __forceinline__ float joined_stat(const WeightArgs& p, int64_t row) {
+__device__ __forceinline__ float2 joined_stat(const WeightArgs& p, int64_t row) {
     const int64_t part = (int64_t)p.stat_rows * p.num_heads;
     constexpr int B = 8;  // pieces in flight
     float2 s = make_float2(-INFINITY, 0.f);
@@ -203,8 +208,8 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
     float* stat_s = reinterpret_cast<float*>(base + Gm::STAT_OFF);
     // keys streamed with their scales: kScaleRing x [128] behind the stationary statistics
     constexpr int kScaleRing = 4, kRing = PASS == kKeyWeights ? Gm::SRING : kScaleRing;
-    float* scale_s = stat_s + NA * TM;
-    static_assert(kScaleRing + NA <= Gm::SRING, "scales fit behind the statistics");
+    float* scale_s = stat_s + NA * 2 * TM;
+    static_assert(kScaleRing + 2 * NA <= 2 * Gm::SRING, "scales fit behind the statistics");
     float2* join_s = reinterpret_cast<float2*>(base + Gm::JOIN_OFF);
     volatile uint32_t* taddr_slot = reinterpret_cast<volatile uint32_t*>(base + Gm::ADDR_OFF);
     int32_t* prefix = reinterpret_cast<int32_t*>(base + Gm::PREF_OFF);
@@ -399,9 +404,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                     load_queries(w, t, dst, &b_full[slot]);
                     const int sl = nb % Gm::SRING;
                     if (!(run = wait(&s_empty[sl], (uint32_t)(nb / Gm::SRING & 1) ^ 1u))) break;
-                    expect(&s_full[sl], TM * 4);
+                    expect(&s_full[sl], 2 * TM * 4);
                     if (lane == 0)
-                        bulk_g2s(stat_s + sl * TM, p.tile_stats + stat_tile(w.sq, w.h, t) * TM, TM * 4, &s_full[sl]);
+                        bulk_g2s(stat_s + sl * 2 * TM, p.tile_stats + stat_tile(w.sq, w.h, t) * 2 * TM, 2 * TM * 4,
+                                 &s_full[sl]);
                 }
             }
         }
@@ -517,22 +523,24 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
             if (lane == 0) mbar_arrive(g_bar);
             return mbar_wait_ns_warp(g_bar, (uint32_t)n_meet++ & 1u, WAIT_NS);
         };
-        // exp2(x + statistic) of 16 columns of one or both stationary tiles'
-        // accumulators, added to v[] and v2[] of this thread's keys
+        // exp2(x - M) / l of 16 columns of one or both stationary tiles'
+        // accumulators, added to v[] and v2[] of this thread's keys (nm: the
+        // columns' -M, TM further on their 1 / l)
         auto add_whole = [&](auto count, const float (&a)[2][16], const float (&ks)[2], const float* nm,
                              unsigned long long (&v2)[2]) {
             constexpr int N = decltype(count)::value;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float4 n4 = *reinterpret_cast<const float4*>(nm + 4 * j);
+                const float4 i4 = *reinterpret_cast<const float4*>(nm + TM + 4 * j);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     const unsigned long long sv = f32x2_pack(ks[k], ks[k]);
                     float x0, x1, x2, x3;
                     f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j], a[k][4 * j + 1]), sv, f32x2_pack(n4.x, n4.y)), x0, x1);
                     f32x2_unpack(fma_f32x2(f32x2_pack(a[k][4 * j + 2], a[k][4 * j + 3]), sv, f32x2_pack(n4.z, n4.w)), x2, x3);
-                    v2[k] = add_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), v2[k]);
-                    v2[k] = add_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), v2[k]);
+                    v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x0), fast_exp2(x1)), f32x2_pack(i4.x, i4.y), v2[k]);
+                    v2[k] = fma_f32x2(f32x2_pack(fast_exp2(x2), fast_exp2(x3)), f32x2_pack(i4.z, i4.w), v2[k]);
                 }
             }
         };
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
 #pragma unroll
                     for (int k = 0; k < N; ++k)
                         if (c0 + j >= lo[k] && c0 + j < end)
-                            v[k] += fast_exp2(fmaf(a[k][j], ks[k], nm[j]));
+                            v[k] = fmaf(fast_exp2(fmaf(a[k][j], ks[k], nm[j])), nm[TM + j], v[k]);
             }
         };
         auto store_weight = [&](const Item& w, int key, float v) {
@@ -693,7 +701,10 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 if (!run) break;
                 if (taker) {
                     if (splits == 1) {
-                        p.tile_stats[stat_tile(w.sq, w.h, w.a0 + x) * TM + m] = valid ? row_stat(m_used, l) : 0.f;
+                        float* st = p.tile_stats + stat_tile(w.sq, w.h, w.a0 + x) * 2 * TM;
+                        const float2 v = valid ? row_stat(m_used, l) : make_float2(0.f, 0.f);
+                        st[m] = v.x;
+                        st[TM + m] = v.y;
                     } else if (valid) {
                         p.stats[(int64_t)w.z * part + (int64_t)(w.sq.stat0 + tok) * p.num_heads + w.h * G + g] =
                             make_float2(m_used, l);
@@ -711,7 +722,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
                     if (((t - w.b0) & 1) != par) continue;
                     const int sl = nx % Gm::SRING;
-                    const float* nm = stat_s + sl * TM + hi * HC;
+                    const float* nm = stat_s + sl * 2 * TM + hi * HC;
                     bool ok = mbar_wait_ns(&s_full[sl], (uint32_t)(nx / Gm::SRING) & 1u, WAIT_NS);
                     ok = acquire(0) && ok;
                     if (w.na == 2) ok = acquire(NA - 1) && ok;
@@ -788,8 +799,9 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                 // few rows: the item's query tiles stay, their statistics with them
                 if (!(run = meet())) break;  // the previous item's are used up
                 if (wg < NA) {
-                    const float* st = p.tile_stats + stat_tile(w.sq, w.h, wg) * TM;
-                    stat_s[wg * TM + m] = wg < w.na ? __ldcg(st + m) : 0.f;
+                    const float* st = p.tile_stats + stat_tile(w.sq, w.h, wg) * 2 * TM;
+                    stat_s[wg * 2 * TM + m] = wg < w.na ? __ldcg(st + m) : 0.f;
+                    stat_s[wg * 2 * TM + TM + m] = wg < w.na ? __ldcg(st + TM + m) : 0.f;
                 }
                 if (!(run = meet())) break;
                 for (int t = w.b0; t < w.b1; ++t, ++nx) {
@@ -813,7 +825,7 @@ __global__ void __launch_bounds__(WGeo<HD>::NTHREADS, 1)
                         const bool full = __all_sync(0xffffffffu, lo[0] <= 0 && end == TT * G);
                         float vx[2] = {0.f, 0.f};
                         unsigned long long v2[2] = {f32x2_pack(0.f, 0.f), 0};
-                        const float* nm = stat_s + x * TM + hi * HC;
+                        const float* nm = stat_s + x * 2 * TM + hi * HC;
                         if (full && TT * G == TM) {
 #pragma unroll 1
                             for (int q = 0; q < HC / 16; ++q) {
@@ -939,8 +951,11 @@ __global__ void __launch_bounds__(TM) stats_join_kernel(const WeightArgs p) {
         locate_work(prefix, p.num_seqs, p.num_kv_heads, it, s, h, tile);
         const WeightSeq sq = weight_seq(p, s);
         const int tok = tile * TT + m / G;
-        p.tile_stats[((int64_t)h * p.stat_tiles + sq.stat0 / TT + s + tile) * TM + m] =
-            m < TT * G && tok < sq.rows ? joined_stat(p, (int64_t)(sq.stat0 + tok) * p.num_heads + h * G + m % G) : 0.f;
+        const bool row = m < TT * G && tok < sq.rows;
+        const float2 v = row ? joined_stat(p, (int64_t)(sq.stat0 + tok) * p.num_heads + h * G + m % G) : make_float2(0.f, 0.f);
+        float* st = p.tile_stats + ((int64_t)h * p.stat_tiles + sq.stat0 / TT + s + tile) * 2 * TM;
+        st[m] = v.x;
+        st[TM + m] = v.y;
     }
 }
 
@@ -1088,7 +1103,7 @@ WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, i
     const int64_t stat_rows = weight_stat_rows(w.seqs, total_q, window).rows;
     if (w.key_splits > 1) w.stats_bytes = round((size_t)w.key_splits * stat_rows * num_heads * sizeof(float2));
     w.stat_tiles = (int)(stat_rows / TT) + w.seqs + 1;
-    w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * TM * sizeof(float);
+    w.tile_stats_bytes = (size_t)w.stat_tiles * num_kv_heads * 2 * TM * sizeof(float);
     if (!w.few_rows && w.row_splits > 1)
         w.partial_bytes = (size_t)w.row_splits * units * max_context * sizeof(float);
     return w;
