@@ -109,8 +109,11 @@ __device__ __forceinline__ void scores(const WeightArgs& a, const WeightSeq& sq,
             const int t = min(k0 + tx + 16 * j, sq.L - 1);
             m *= a.k_scales[((int64_t)table[t / a.block_size] * a.num_kv_heads + h) * a.block_size + t % a.block_size];
         }
+        // rounded here: contracted with a subtraction of the maximum in one pass
+        // and not in the other, a row's weights would be off by half a unit of
+        // its scores (1e-4 at scores of 4,000)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i][j] *= m;
+        for (int i = 0; i < 4; ++i) x[i][j] = __fmul_rn(x[i][j], m);
     }
 }
 

@@ -19,7 +19,7 @@ def _equal_keys(lens, hkv, hd, bs, dtype, fp8):
     return b.to(DEV)
 
 
-@pytest.mark.parametrize("kernel", [0])
+@pytest.mark.parametrize("kernel", [0, 1])
 @pytest.mark.parametrize("new, lens, hq, hkv, hd, bs, dtype, window, fp8", [
     ([61, 1], [61, 37], 8, 2, 128, 16, "bf16", 0, False), ([61, 23], [75, 23], 12, 2, 64, 16, "f16", 0, False),
     ([61, 50], [61, 70], 8, 2, 128, 16, "bf16", 7, False), ([300], [301], 4, 2, 256, 16, "bf16", 0, False),
