@@ -489,9 +489,12 @@ PA_API pa_status pa_rope_write_kv_fp8(void* q_out, const void* q, const void* k,
  *   w(j) = sum over the query heads h of KV head kv of p_h(j),   j < L,
  *   weights[s, kv, j] += w(j) for j < L - 1, and = w(j) for j = L - 1
  * (the newest token, whose query this is, has no history).  out is
- * pa_decode's.  Entries from L on are left as they are, and a sequence with
- * L = 0 gets a zero row of out and no weights.  Weights are fp32, summed in a
- * fixed order: the same inputs give the same bits.
+ * pa_decode's up to rounding: the same formula and types (probabilities enter
+ * P V in the query's type on the tensor cores, as there; the weights come from
+ * the fp32 scores), the pieces of a sequence joined in another order.  Entries
+ * from L on are left as they are, and a sequence with L = 0 gets a zero row of
+ * out and no weights.  Weights are fp32, summed in a fixed order: the same
+ * inputs give the same bits.
  *   weights:   device fp32 [num_seqs, num_kv_heads, weights_stride], row s
  *              belonging to sequence s as its block-table row does;
  *              weights_stride >= max_context
@@ -514,8 +517,11 @@ PA_API pa_status pa_decode_weights(void* out, float* weights, int64_t weights_st
 
 /*
  * pa_decode_weights_fp8 -- the same over a quantized cache (see
- * pa_decode_fp8).  The query enters the products unscaled, so on the
- * tensor-core path |q| must lie inside the f16 range.
+ * pa_decode_fp8).  On the tensor-core path the query enters the f16 products
+ * exactly, by a power of two per head where it is bf16 (elements below 2^-28
+ * of the head's largest lose bits), and the scale multiplies the fp32 scores;
+ * pa_decode_fp8 rounds the scaled query to f16, so out may differ from its by
+ * that rounding of the scores.
  */
 PA_API size_t pa_decode_weights_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                                    int32_t head_dim, int32_t block_size, int32_t max_context,
