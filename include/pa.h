@@ -439,8 +439,10 @@ PA_API pa_status pa_decode_noalloc(void* out, const void* q, const void* k_cache
  * The pair is elements (i, i + rot_dim / 2) of each head, or (2i, 2i + 1)
  * with interleaved != 0; elements from rot_dim on pass through.  Several axes
  * (time, height, width) give each pair the position of its axis; one axis is
- * ordinary rotary embedding.  Angles are exact in the position: whole turns
- * are dropped in integer arithmetic, so far positions lose nothing.
+ * ordinary rotary embedding.  Whole turns are dropped in integer arithmetic:
+ * an angle is off by at most |position| max(1, |inv_freq|) 2^-63 turns, and by
+ * the rounding of what is left to fp32 (2^-26 turns, the larger part up to
+ * positions of 2^37).
  * q_out gets every token's rotated query heads; k (rotated) and v go to row
  * slot_mapping[t] of the pools as pa_write_kv puts them, and a negative slot
  * skips that write (q_out is still written).  Slots must be distinct (check

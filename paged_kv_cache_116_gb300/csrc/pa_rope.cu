@@ -17,9 +17,10 @@
 // radian).  Here inv_freq[i] / (2 pi) becomes a 64-bit fraction of a turn F
 // by one integer product of its significand with 2^64 / (2 pi); the
 // position's turn is the low 64 bits of position * F (whole turns drop out of
-// the wrap-around, negative positions included), exact to 2^-64 turns per
-// position step, and sincospif takes its upper 32 bits.  No fp64 instruction
-// is spent on it.
+// the wrap-around, negative positions included), and sincospif takes its upper
+// 32 bits.  F is off by less than 1 + freq units of 2^-64 turns, which the
+// position multiplies: below fp32's rounding of the angle (2^-26 turns) up to
+// 2^37, 2^-18 turns at 2^45.  No fp64 instruction is spent on it.
 //
 // Bound: HBM.  q, k and v are read once and q_out and the rows written once.
 // A block takes `tpb` tokens: their sines and cosines go to shared memory
