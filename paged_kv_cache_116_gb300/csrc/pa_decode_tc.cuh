@@ -1215,7 +1215,7 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, con
 // batches of records and four tokens per thread let three CTAs share an SM
 // (two with eight of each: 2 us more on every batch of 70-200 us).
 constexpr int kWeightChunk = 1024;
-constexpr int kWeightMaxCtas = 152 * 16;  // beyond this a CTA takes several chunks
+constexpr int kWeightMaxCtas = kSms * 16;  // beyond this a CTA takes several chunks
 
 template <typename T, int HD, bool MANY>
 __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcParams p, const int64_t TW,

@@ -330,7 +330,7 @@ template <> struct VecOf<2> { using V = uint16_t; };
 template <> struct VecOf<1> { using V = uint8_t; };
 
 constexpr int kWarpRows = 8, kMoveWarps = 4;
-constexpr int kMoveCtas = 152 * 16;  // wanted over all units
+constexpr int kMoveCtas = kSms * 16;  // wanted over all units
 
 // Each unit has `ctas` CTAs, whose warps take eight rows of its list in turn
 // (few enough that a short list spreads, and nobody visits what no list

@@ -36,6 +36,11 @@ inline int32_t seqs_per_launch(int32_t num_seqs, double bytes_per_seq, int32_t m
 // kernel's parameter block).  Equal to PA_MAX_LAYERS of pa.h.
 #define PA_MAX_LAYERS_INTERNAL 128
 
+// SMs of a GB300: what the rules that cut work into CTAs count on.  Not asked of
+// the device, since some of them size workspaces and those answers are also
+// given where there is none (sm_count() bounds the grids of persistent kernels).
+constexpr int kSms = 152;
+
 // Number of polls a bounded mbarrier wait makes before giving up.
 constexpr uint32_t kMaxPolls = 1u << 24;
 

@@ -315,7 +315,7 @@ cudaError_t launch_rope_typed(const RopeArgs& a, cudaStream_t stream) {
     int threads = 128;
     for (int n = 160; n <= kRopeThreads; n += 32)
         if (filled(n) < filled(threads)) threads = n;
-    const int64_t slots = 152 * (1024 / threads);
+    const int64_t slots = kSms * (1024 / threads);
     p.tpb = (int)std::min<int64_t>(16, (a.n + slots - 1) / slots);
     const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(slots / 2 / ctas, (items + threads - 1) / threads));

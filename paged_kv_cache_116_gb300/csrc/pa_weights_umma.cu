@@ -1069,7 +1069,7 @@ bool weights_umma_supported(int dtype, int head_dim, int group) {
 WeightPlan weights_umma_plan(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_context,
                              int32_t window, bool kv_fp8) {
-    constexpr int64_t kSms = 152, kMinTiles = 16;
+    constexpr int64_t kMinTiles = 16;
     const int G = num_heads / num_kv_heads, TT = TM / G, NA = head_dim <= 128 ? 2 : 1;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     auto round = [](size_t b) { return (b + 255) / 256 * 256; };
