@@ -5,7 +5,9 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <exception>
 #include <string>
+#include <unordered_map>
 #include <unordered_set>
 #include <vector>
 
@@ -31,9 +33,18 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool valid_dtype(int d) { return d == PA_F32 || d == PA_BF16 || d == PA_F16; }
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+// The answer of a check that ran out of host memory (no exception leaves a C
+// entry point).
+pa_status no_host_memory() { return fail(PA_ERR_INVALID_ARG, "check mode: no host memory for the index arrays"); }
+
 template <typename T>
 bool to_host(std::vector<T>& dst, const T* src, int64_t n, cudaStream_t st, pa_status* err) {
-    dst.resize((size_t)std::max<int64_t>(n, 0));
+    try {
+        dst.resize((size_t)std::max<int64_t>(n, 0));
+    } catch (const std::exception&) {
+        *err = no_host_memory();
+        return false;
+    }
     if (n <= 0) return true;
     cudaError_t e = cudaMemcpyAsync(dst.data(), src, sizeof(T) * (size_t)n, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -95,13 +106,17 @@ pa_status check_slots(const int64_t* slot_mapping, int64_t n, int32_t num_blocks
     if (!to_host(sm, slot_mapping, n, st, &err)) return err;
     const int64_t slots = (int64_t)num_blocks * block_size;
     std::unordered_set<int64_t> seen;
-    for (int64_t i = 0; i < n; ++i) {
-        if (sm[i] < 0) continue;
-        if (sm[i] >= slots)
-            return fail(PA_ERR_INDEX, "token " + std::to_string(i) + ": slot " + std::to_string(sm[i]) +
-                                          " outside the pool");
-        if (!seen.insert(sm[i]).second)
-            return fail(PA_ERR_INDEX, "slot " + std::to_string(sm[i]) + " written twice in one call");
+    try {
+        for (int64_t i = 0; i < n; ++i) {
+            if (sm[i] < 0) continue;
+            if (sm[i] >= slots)
+                return fail(PA_ERR_INDEX, "token " + std::to_string(i) + ": slot " + std::to_string(sm[i]) +
+                                              " outside the pool");
+            if (!seen.insert(sm[i]).second)
+                return fail(PA_ERR_INDEX, "slot " + std::to_string(sm[i]) + " written twice in one call");
+        }
+    } catch (const std::exception&) {
+        return no_host_memory();
     }
     return PA_OK;
 }
@@ -138,7 +153,8 @@ pa_status check_evict(const int32_t* recorded_lens, const int32_t* seen_lens, co
     if (!to_host(lens, context_lens, num_seqs, st, &err)) return err;
     err = check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
     if (err != PA_OK) return err;
-    for (int32_t L : lens) kept.push_back(std::min(L, keep));
+    if (!to_host(kept, context_lens, num_seqs, st, &err)) return err;
+    for (int32_t& L : kept) L = std::min(L, keep);
     err = check_tables(new_block_tables, num_seqs, new_max_blocks, kept, num_blocks, block_size, max_context, st);
     if (err != PA_OK) return err;
     if (recorded_lens && !to_host(rec, recorded_lens, num_seqs, st, &err)) return err;
@@ -152,26 +168,34 @@ pa_status check_evict(const int32_t* recorded_lens, const int32_t* seen_lens, co
     if (!to_host(from, block_tables, (int64_t)num_seqs * max_blocks, st, &err) ||
         !to_host(to, new_block_tables, (int64_t)num_seqs * new_max_blocks, st, &err))
         return err;
-    // who reads a block: its (sequence, logical block), or several
+    // who reads and who writes a block: its (sequence, logical block), or several
     constexpr int64_t kNobody = -1, kSeveral = -2;
-    std::vector<int64_t> reader((size_t)num_blocks, kNobody), writer((size_t)num_blocks, kNobody);
-    for (int32_t s = 0; s < num_seqs; ++s)
-        for (int64_t b = 0; b * block_size < lens[s]; ++b) {
-            int64_t& r = reader[from[(size_t)s * max_blocks + b]];
-            r = r == kNobody ? ((int64_t)s << 32 | b) : kSeveral;
-        }
-    for (int32_t s = 0; s < num_seqs; ++s)
-        for (int64_t b = 0; b * block_size < kept[s]; ++b) {
-            const int32_t id = to[(size_t)s * new_max_blocks + b];
-            const int64_t me = (int64_t)s << 32 | b;
-            if (id == from[(size_t)s * max_blocks + b] && lens[s] <= keep) continue;  // in place, nothing dropped
-            if (writer[id] != kNobody)
-                return fail(PA_ERR_INDEX, "block " + std::to_string(id) + " is the destination of two blocks");
-            writer[id] = me;
-            if (reader[id] != kNobody && reader[id] != me)
-                return fail(PA_ERR_INDEX, "block " + std::to_string(id) +
-                                              " is written for one sequence and read for another logical block");
-        }
+    struct Users {
+        int64_t reader = kNobody, writer = kNobody;
+    };
+    std::unordered_map<int32_t, Users> users;
+    try {
+        for (int32_t s = 0; s < num_seqs; ++s)
+            for (int64_t b = 0; b * block_size < lens[s]; ++b) {
+                int64_t& r = users[from[(size_t)s * max_blocks + b]].reader;
+                r = r == kNobody ? ((int64_t)s << 32 | b) : kSeveral;
+            }
+        for (int32_t s = 0; s < num_seqs; ++s)
+            for (int64_t b = 0; b * block_size < kept[s]; ++b) {
+                const int32_t id = to[(size_t)s * new_max_blocks + b];
+                const int64_t me = (int64_t)s << 32 | b;
+                if (id == from[(size_t)s * max_blocks + b] && lens[s] <= keep) continue;  // in place, nothing dropped
+                Users& u = users[id];
+                if (u.writer != kNobody)
+                    return fail(PA_ERR_INDEX, "block " + std::to_string(id) + " is the destination of two blocks");
+                u.writer = me;
+                if (u.reader != kNobody && u.reader != me)
+                    return fail(PA_ERR_INDEX, "block " + std::to_string(id) +
+                                                  " is written for one sequence and read for another logical block");
+            }
+    } catch (const std::exception&) {
+        return no_host_memory();
+    }
     return PA_OK;
 }
 
