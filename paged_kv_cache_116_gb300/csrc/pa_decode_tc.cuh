@@ -1197,11 +1197,21 @@ __device__ __forceinline__ void merge_many(const TcParams& p, const int64_t TW, 
     static_cast<T*>(p.out)[((int64_t)s * p.num_heads + (int64_t)h * G + j) * HD + threadIdx.x] = Elt<T>::from_f(v / sum);
 }
 
+// The merge grids do not end before the decode grid: the kernel after them on
+// the stream, launched as their dependent, waits for them only, and may write
+// what the decode still reads.  Half warps without records to join do not
+// wait, and in a batch of whole units nobody else does, so one CTA always
+// waits at its end.
+__device__ __forceinline__ void end_after_decode() {
+    if (blockIdx.x == 0) pdl_wait_primary();
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, const int64_t TW) {
     extern __shared__ int32_t mprefix[];   // [num_seqs + 1]
     tile_prefix(p.context_lens, p.num_seqs, mprefix, nullptr);
     merge_item<T, HD>(p, TW, mprefix, blockIdx.x);
+    end_after_decode();
 }
 
 // SCORES: the weights w(t) = sum over the group's heads j of
@@ -1228,6 +1238,7 @@ __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcPa
         tile_prefix(p.context_lens, S, mprefix, nullptr);
         if constexpr (MANY) merge_many<T, HD>(p, TW, mprefix, blockIdx.x);
         else merge_item<T, HD, HD <= 128 ? 4 : 2>(p, TW, mprefix, blockIdx.x);
+        end_after_decode();
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
