@@ -523,7 +523,9 @@ PA_API pa_status pa_decode_weights(void* out, float* weights, int64_t weights_st
  * exactly, by a power of two per head where it is bf16 (elements below 2^-28
  * of the head's largest lose bits), and the scale multiplies the fp32 scores;
  * pa_decode_fp8 rounds the scaled query to f16, so out may differ from its by
- * that rounding of the scores.
+ * that rounding of the scores.  As there, probabilities times value scales
+ * enter P V as f16 numbers, so value rows whose largest element is below 1e-3
+ * lose bits in out (not in the weights).
  */
 PA_API size_t pa_decode_weights_fp8_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads,
                                                    int32_t head_dim, int32_t block_size, int32_t max_context,
