@@ -37,6 +37,9 @@
  *     human-readable reason for the last non-OK status of the calling thread.
  *   - Block-table rows are padded to max_blocks; entries at or past
  *     ceil(len / block_size) are never read.
+ *   - Entry points may be called from several host threads at once, with
+ *     streams, results and workspaces of their own (pa_decode_noalloc, whose
+ *     scratch is the library's, and the options excepted).
  */
 #ifndef PA_H_
 #define PA_H_
