@@ -1208,17 +1208,14 @@ __device__ __forceinline__ void merge_many(const TcParams& p, const int64_t TW, 
 // the stream, launched as their dependent, waits for them only, and may write
 // what the decode still reads.  Half warps without records to join do not
 // wait, and in a batch of whole units nobody else does, so one CTA always
-// waits at its end.
-__device__ __forceinline__ void end_after_decode() {
-    if (blockIdx.x == 0) pdl_wait_primary();
-}
-
+// waits at its end (with the weights: one of theirs; a merging one cost 0.9 of
+// 94 us).
 template <typename T, int HD>
 __global__ void __launch_bounds__(256) decode_merge_kernel(const TcParams p, const int64_t TW) {
     extern __shared__ int32_t mprefix[];   // [num_seqs + 1]
     tile_prefix(p.context_lens, p.num_seqs, mprefix, nullptr);
     merge_item<T, HD>(p, TW, mprefix, blockIdx.x);
-    end_after_decode();
+    if (blockIdx.x == 0) pdl_wait_primary();
 }
 
 // SCORES: the weights w(t) = sum over the group's heads j of
@@ -1245,7 +1242,6 @@ __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcPa
         tile_prefix(p.context_lens, S, mprefix, nullptr);
         if constexpr (MANY) merge_many<T, HD>(p, TW, mprefix, blockIdx.x);
         else merge_item<T, HD, HD <= 128 ? 4 : 2>(p, TW, mprefix, blockIdx.x);
-        end_after_decode();
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1335,6 +1331,7 @@ __global__ void __launch_bounds__(256, 3) decode_merge_weights_kernel(const TcPa
             row[t] = old[k] + w;  // (the newest token starts from 0)
         }
     }
+    if (!waited && blockIdx.x == gridDim.x - 1) pdl_wait_primary();
 }
 
 // ---------------------------------------------------------------- host side
