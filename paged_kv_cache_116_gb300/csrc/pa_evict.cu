@@ -33,7 +33,7 @@
 // memory (512 heads of 1,040 tokens: 11 us, of which 2 us each for loading,
 // the two digits, ranking and writing; 64 heads of 32,768: 21 us, a third of
 // it the first pass), the move kernel by HBM (each listed row is read and
-// written once: 262,144 rows of 2 x 256 bytes at 4.8 TB/s).
+// written once: 262,144 rows of 2 x 256 bytes in 43 us, 6.2 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -26,10 +26,10 @@
 //
 // Bound: the groups' work on the columns, by issue slots and the exponential
 // unit (32 per cycle and SM, 512 cycles per accumulator, as many as its MMAs
-// take); a pass spends about 1,070 cycles per accumulator, 250 us on 8,192
-// tokens with 32 / 8 heads (550 GFLOP in both passes: 1.10 PFLOP/s).  With a
+// take); a pass spends about 1,120 cycles per accumulator, 255 and 268 us on
+// 8,192 tokens with 32 / 8 heads (550 GFLOP in both: 1.05 PFLOP/s).  With a
 // short window over long contexts: the two reads of the keys (4 x 32,768 keys
-// of 8 heads, 32 rows: 55-65 us per pass, 4.6 TB/s).
+// of 8 heads, 32 rows: 61 and 71 us, 3.9-4.5 TB/s).
 //
 // Pools with block_size 8 or a multiple of 16 up to 256 are read in place.
 // Others, and code pools, are first laid out densely in the workspace, codes
