@@ -29,7 +29,10 @@ inline int32_t seqs_per_launch(int32_t num_seqs, double bytes_per_seq, int32_t m
     const int32_t n = num_seqs < most ? num_seqs : most;
     if (n * bytes_per_seq <= kScratchBytes) return n;
     const double fit = kScratchBytes / bytes_per_seq;  // (below n)
-    return fit < 1 ? 1 : (int32_t)fit;
+    if (fit < 2) return 1;
+    // parts of one size: the last is not a single long sequence
+    const int64_t parts = ((int64_t)num_seqs + (int64_t)fit - 1) / (int64_t)fit;
+    return (int32_t)((num_seqs + parts - 1) / parts);
 }
 
 // Most layers one pa_copy_blocks call takes (their pointers travel in the

@@ -65,3 +65,12 @@ def test_scores_of_many_long_sequences_are_kept_in_parts(lib, fp8):
     assert size(1, 131072) >= 131072 * 32 * 4
     assert size(4096, 131072) <= 4.5 * GIB
     assert size(2, 1 << 29) >= (1 << 29) * 32 * 4
+
+
+@pytest.mark.parametrize("seqs", [129, 200, 256, 300, 4096])
+def test_parts_are_of_one_size(lib, seqs):
+    """129 sequences of 33 MB are two parts of 65 and 64, not 128 and a single one."""
+    per = 262144 * 32 * 4
+    parts = -(-seqs // ((4 * GIB) // per))
+    space = lib.pa_decode_weights_workspace_size(seqs, 32, 8, 128, 16, 262144, BF16)
+    assert 0 <= space - -(-seqs // parts) * per < 64 << 20  # (and the split records)
