@@ -637,6 +637,141 @@ PA_API pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* n
                           int32_t max_context, int32_t keep, int32_t num_sink, int32_t num_recent, int dtype,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---- Latent cache and shared prefixes --------------------------------------
+ * Attention that reads few cached bytes for many query rows: every query head
+ * shares one latent vector a token (latent attention, in its absorbed form),
+ * or sequences of a batch share the leading blocks of their tables, as the
+ * copies of a prompt do before their first write (pa_copy_blocks).  The pages
+ * describe the paged cache underneath ("分页 KV Cache", §块表与 slot mapping
+ * and §分页注意力; "KV cache：容量推导、分页与回收", §共享前缀后为什么需要引用计数) and
+ * have no counterpart for these.
+ *
+ * A latent cache is one pool [num_blocks, block_size, latent_dim + rope_dim],
+ * addressed through block tables and slots like any other: row t holds
+ * [c_t | r_t], the latent vector that every head's key and value are made of
+ * and a rotated part that all keys share.  With the key's projection of head
+ * h absorbed into the query (q[h] = [W_h^T q_h | rotated part]), a head's key
+ * is the whole row and its value the row's latent part; the value's
+ * projection is applied to the result by the caller.
+ */
+
+/*
+ * pa_latent_write -- one row a token into a latent cache, and the queries'
+ * rotated parts.  For token t and x = kv[t]:
+ *   c = x[0 : latent_dim] * norm_weight / sqrt(mean(x[0 : latent_dim]^2) + eps)
+ *       (norm_weight NULL: as it is, bit for bit),
+ *   row slot_mapping[t] of the cache receives [c | rotated x[latent_dim :]],
+ *   q_out[t, h] receives q[t, h] rotated (rope_dim elements each),
+ * by the angles positions[t] * inv_freq[i]; pairs and accuracy of the angles
+ * are those of pa_rope_write_kv.  Sums, norms and rotations are fp32, rounded
+ * once.  A negative slot skips the row (q_out is still written); slots must be
+ * distinct (check mode rejects duplicates).
+ *   kv:            device, token t at kv + t * kv_stride elements
+ *   q, q_out:      device, head h of token t at t * q_stride +
+ *                  h * q_head_stride elements (q_out likewise): slices of
+ *                  wider heads need no copy.  Heads and tokens may not
+ *                  overlap.  q_out may be q with the same strides, otherwise
+ *                  no overlap
+ *   norm_weight:   device [latent_dim] of dtype, or NULL
+ *   positions:     device int64 [n], any sign
+ *   inv_freq:      device double [rope_dim / 2]
+ *   cache:         device [num_blocks, block_size, latent_dim + rope_dim],
+ *                  16-byte aligned
+ *   rope_dim:      even, 2 <= rope_dim <= 256; latent_dim <= 4096
+ *   num_heads:     0: the cache's rows only (q and q_out are then ignored)
+ * Moves 16-byte vectors where sizes, strides and addresses allow it, else
+ * single elements.
+ */
+PA_API pa_status pa_latent_write(void* q_out, int64_t q_out_stride, int64_t q_out_head_stride, const void* q,
+                                 int64_t q_stride, int64_t q_head_stride, const void* kv, int64_t kv_stride,
+                                 const void* norm_weight, float eps, const int64_t* positions, const double* inv_freq,
+                                 int32_t rope_dim, int interleaved, const int64_t* slot_mapping, int64_t n,
+                                 void* cache, int32_t num_blocks, int32_t block_size, int32_t num_heads,
+                                 int32_t latent_dim, int dtype, void* stream);
+
+/*
+ * pa_latent_decode -- one query per sequence over a latent cache: for
+ * sequence s and head h,
+ *   out[s, h] = sum over t < L of softmax_t(scale * q[s, h] . row_t) c_t,
+ * L = context_lens[s], rows read through block_tables[s].  context_lens[s] ==
+ * 0 gives a zero row.  The work is split by lengths alone, so relabelling
+ * physical blocks gives bit-identical output.
+ *   out:       device [num_seqs, num_heads, latent_dim] of dtype
+ *   q:         device [num_seqs, num_heads, latent_dim + rope_dim] of dtype
+ *   cache:     device [num_blocks, block_size, latent_dim + rope_dim] of
+ *              dtype; all three 16-byte aligned
+ *   rope_dim:  >= 0; latent_dim + rope_dim <= 576
+ *   workspace: pa_latent_decode_workspace_size(...) bytes, 16-byte aligned;
+ *              its content on entry does not matter
+ * bf16/f16 with latent_dim 512, rope_dim 64 and block_size 8 or a multiple of
+ * 16 run on the tensor cores (tcgen05, two SMs per tile; probabilities enter
+ * the second product in the query's type, sums are fp32), the rest in fp32 on
+ * the CUDA cores.  PA_OPT_DECODE_KERNEL pins a kernel as it does for
+ * pa_decode.
+ */
+PA_API size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t latent_dim,
+                                              int32_t rope_dim, int32_t block_size, int32_t max_context, int dtype);
+PA_API pa_status pa_latent_decode(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                                  int32_t max_blocks, const int32_t* context_lens, int32_t num_seqs,
+                                  int32_t num_heads, int32_t latent_dim, int32_t rope_dim, int32_t num_blocks,
+                                  int32_t block_size, int32_t max_context, float scale, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * pa_latent_varlen -- the same for a step of new tokens (prompts, chunks,
+ * single tokens mixed), as pa_varlen does it: request i's queries are rows
+ * cu_seqlens_q[i] .. cu_seqlens_q[i+1]-1, new token j is at position
+ * seq_lens[i] - n_i + j and, with causal != 0, attends to positions 0..that
+ * position; with causal == 0 to all seq_lens[i].
+ *   out, q:    device [total_q, num_heads, latent_dim], [total_q, num_heads,
+ *              latent_dim + rope_dim]
+ *   workspace: pa_latent_varlen_workspace_size(...) bytes
+ * The other arguments are pa_varlen's and pa_latent_decode's;
+ * PA_OPT_VARLEN_KERNEL pins a kernel.
+ */
+PA_API size_t pa_latent_varlen_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                              int32_t latent_dim, int32_t rope_dim, int32_t block_size,
+                                              int32_t max_context, int dtype);
+PA_API pa_status pa_latent_varlen(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                                  int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                                  int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                  int32_t latent_dim, int32_t rope_dim, int32_t num_blocks, int32_t block_size,
+                                  int32_t max_context, float scale, int causal, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * pa_decode_shared -- pa_decode for a batch whose sequences share leading
+ * blocks: group g is sequences group_starts[g] .. group_starts[g+1]-1, and
+ * the first prefix_lens[g] tokens of its members lie in the same physical
+ * blocks, in the same order (the members' table rows begin alike).  The
+ * prefix is read once for all members, the rest of each context as pa_decode
+ * reads it, and the parts are joined by their log-sum-exp: out is pa_decode's
+ * up to rounding.  Sequences outside the groups, and groups of prefix 0, are
+ * worked as pa_decode works them.
+ *   group_starts: device int32 [num_groups + 1], non-decreasing, in
+ *                 [0, num_seqs]
+ *   prefix_lens:  device int32 [num_groups], multiples of block_size, at most
+ *                 every member's context length (it may be all of it).  Check
+ *                 mode rejects others, and members that do not share the
+ *                 blocks
+ *   workspace:    pa_decode_shared_workspace_size(...) bytes, 16-byte aligned;
+ *                 its content on entry does not matter
+ * num_groups == 0 is pa_decode.  The other arguments, the error behaviour and
+ * PA_OPT_DECODE_KERNEL are pa_decode's.  Where pa_decode runs on the CUDA
+ * cores (and for block sizes that no TMA box fits) nothing is shared and the
+ * call is pa_decode.
+ */
+PA_API size_t pa_decode_shared_workspace_size(int32_t num_seqs, int32_t num_groups, int32_t num_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                              int32_t max_context, int dtype);
+PA_API pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+                                  const int32_t* group_starts, const int32_t* prefix_lens, int32_t num_groups,
+                                  int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

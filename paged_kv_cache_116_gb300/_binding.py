@@ -27,7 +27,9 @@ EXPORTS = ("pa_status_string", "pa_last_error", "pa_set_option", "pa_get_option"
            "pa_rope_write_kv", "pa_rope_write_kv_fp8", "pa_decode_weights_workspace_size", "pa_decode_weights",
            "pa_decode_weights_fp8_workspace_size", "pa_decode_weights_fp8", "pa_prompt_weights_workspace_size",
            "pa_prompt_weights", "pa_prompt_weights_fp8_workspace_size", "pa_prompt_weights_fp8",
-           "pa_evict_workspace_size", "pa_evict")
+           "pa_evict_workspace_size", "pa_evict", "pa_latent_write", "pa_latent_decode_workspace_size",
+           "pa_latent_decode", "pa_latent_varlen_workspace_size", "pa_latent_varlen",
+           "pa_decode_shared_workspace_size", "pa_decode_shared")
 
 
 class PAError(RuntimeError):
@@ -97,6 +99,16 @@ def lib():
         "pa_evict_workspace_size": ([i32, i32, i32, i32], sz),
         "pa_evict": ([vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
                       i32, i32, i32, i32, ci, vp, sz, vp], ci),
+        "pa_latent_write": ([vp, i64, i64, vp, i64, i64, vp, i64, vp, cf, vp, vp, i32, ci, vp, i64, vp, i32, i32, i32,
+                             i32, ci, vp], ci),
+        "pa_latent_decode_workspace_size": ([i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_latent_decode": ([vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, cf, ci, vp, sz, vp], ci),
+        "pa_latent_varlen_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_latent_varlen": ([vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, cf, ci, ci, vp,
+                              sz, vp], ci),
+        "pa_decode_shared_workspace_size": ([i32, i32, i32, i32, i32, i32, i32, ci], sz),
+        "pa_decode_shared": ([vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, cf, ci, vp,
+                              sz, vp], ci),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -671,3 +683,152 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
                                     k_scales, v_scales, workspace))
     _check(st, "pa_evict")
     return new_lens
+
+
+def _heads_of(name, t, n, rope_dim, dtype):
+    """Token and head stride (elements) of q or q_out [n, heads, rope_dim], heads and tokens at any stride."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[0] != n or t.shape[2] != rope_dim or t.dtype != dtype or \
+            (t.stride(2) != 1 and rope_dim > 1):
+        raise ValueError("%s must be a CUDA tensor [%d, heads, %d] of kv's dtype, its last axis contiguous"
+                         % (name, n, rope_dim))
+    return t.stride(0), t.stride(1)
+
+
+def pa_latent_write(kv, positions, inv_freq, slot_mapping, latent_cache, norm_weight=None, eps=1e-6, q=None,
+                    q_out=None, interleaved=False, stream=None):
+    """Write one row a token into latent_cache [NB, bs, latent_dim + rope_dim]: kv [n, latent_dim + rope_dim] with its
+    latent part normalised (norm_weight [latent_dim], None: as it is) and its last rope_dim = 2 * len(inv_freq)
+    elements rotated; q [n, H, rope_dim] is rotated into q_out by the same angles.
+
+    positions, slot_mapping [n] int64, inv_freq float64, all on the device.  Tokens of kv, and tokens and heads of q
+    and q_out, may lie at any stride (slices of wider heads)."""
+    _dev(positions, inv_freq, slot_mapping, latent_cache, norm_weight)
+    if latent_cache.dim() != 3 or kv.dim() != 2 or positions.dim() != 1:
+        raise ValueError("latent_cache must be [num_blocks, block_size, row], kv [n, row] and positions [n]")
+    nb, bs, row = latent_cache.shape
+    n, dt, rope_dim = positions.shape[0], kv.dtype, 2 * inv_freq.numel()
+    if positions.dtype != torch.int64 or inv_freq.dtype != torch.float64 or slot_mapping.dtype != torch.int64:
+        raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
+    if not kv.is_cuda or kv.shape != (n, row) or kv.stride(1) != 1 or slot_mapping.shape != (n,):
+        raise ValueError("kv must be a CUDA tensor [n, latent_dim + rope_dim] with contiguous rows, and positions and "
+                         "slot_mapping hold one entry per token")
+    if latent_cache.dtype != dt or rope_dim >= row or (q is None) != (q_out is None):
+        raise ValueError("latent_cache must be of kv's dtype and wider than rope_dim, and a q needs its q_out")
+    if norm_weight is not None and (norm_weight.dtype != dt or norm_weight.shape != (row - rope_dim,)):
+        raise ValueError("norm_weight must be [latent_dim] of kv's dtype")
+    heads, qs, qo = 0, (0, 0), (0, 0)
+    if q is not None:
+        heads = q.shape[1]
+        qs, qo = _heads_of("q", q, n, rope_dim, dt), _heads_of("q_out", q_out, n, rope_dim, dt)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    st = lib().pa_latent_write(_raw(q_out), *qo, _raw(q), *qs, _raw(kv), kv.stride(0) if n > 1 else row,
+                               _raw(norm_weight), float(eps), _raw(positions), _raw(inv_freq), rope_dim,
+                               1 if interleaved else 0, _raw(slot_mapping), n, _raw(latent_cache), nb, bs, heads,
+                               row - rope_dim, _dtype(kv),
+                               _raw_stream(stream, kv, positions, inv_freq, slot_mapping, latent_cache, norm_weight, q,
+                                           q_out))
+    _check(st, "pa_latent_write")
+    return latent_cache
+
+
+def _latent_args(out, q, latent_cache, block_tables, lens):
+    if q.dim() != 3 or out.dim() != 3 or latent_cache.dim() != 3 or block_tables.dim() != 2 or lens.dim() != 1:
+        raise ValueError("q and out must be [rows, heads, dims], latent_cache [num_blocks, block_size, row], block "
+                         "tables [num_seqs, max_blocks] and lengths [num_seqs]")
+    row, lat = latent_cache.shape[2], out.shape[2]
+    if q.shape[2] != row or lat > row or out.shape[:2] != q.shape[:2]:
+        raise ValueError("q must be [rows, heads, latent_dim + rope_dim] as the cache's rows, out [rows, heads, "
+                         "latent_dim]")
+    if out.dtype != q.dtype or latent_cache.dtype != q.dtype:
+        raise ValueError("out and latent_cache must be of q's dtype")
+    if block_tables.shape[0] != lens.shape[0]:
+        raise ValueError("block tables must have one row per sequence")
+    return lat, row - lat
+
+
+def pa_latent_decode_workspace_size(num_seqs, num_heads, latent_dim, rope_dim, block_size, max_context, dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_latent_decode_workspace_size(num_seqs, num_heads, latent_dim, rope_dim, block_size, max_context,
+                                                 code)
+
+
+def pa_latent_decode(out, q, latent_cache, block_tables, context_lens, max_context, scale, workspace=None,
+                     stream=None):
+    """One query per sequence over a latent cache [NB, bs, latent_dim + rope_dim]: every head's key is the whole row,
+    its value the row's latent part.  q [S, H, latent_dim + rope_dim], out [S, H, latent_dim]."""
+    _dev(out, q, latent_cache, block_tables, context_lens, workspace)
+    _i32(block_tables, context_lens)
+    lat, rot = _latent_args(out, q, latent_cache, block_tables, context_lens)
+    nb, bs, _ = latent_cache.shape
+    S, H, _ = q.shape
+    if context_lens.shape[0] != S:
+        raise ValueError("context_lens must hold one entry per query")
+    st = lib().pa_latent_decode(_raw(out), _raw(q), _raw(latent_cache), _raw(block_tables), block_tables.shape[1],
+                                _raw(context_lens), S, H, lat, rot, nb, bs, max_context, float(scale), _dtype(q),
+                                *_ws(workspace),
+                                _raw_stream(stream, out, q, latent_cache, block_tables, context_lens, workspace))
+    _check(st, "pa_latent_decode")
+    return out
+
+
+def pa_latent_varlen_workspace_size(num_seqs, total_q, max_q, num_heads, latent_dim, rope_dim, block_size, max_context,
+                                    dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_latent_varlen_workspace_size(num_seqs, total_q, max_q, num_heads, latent_dim, rope_dim, block_size,
+                                                 max_context, code)
+
+
+def pa_latent_varlen(out, q, latent_cache, block_tables, seq_lens, cu_seqlens_q, max_q, max_context, scale,
+                     causal=True, workspace=None, stream=None):
+    """pa_latent_decode for prompts and chunks: q [T, H, latent_dim + rope_dim], out [T, H, latent_dim];
+    cu_seqlens_q [S+1]; seq_lens [S]."""
+    _dev(out, q, latent_cache, block_tables, seq_lens, cu_seqlens_q, workspace)
+    _i32(block_tables, seq_lens, cu_seqlens_q)
+    lat, rot = _latent_args(out, q, latent_cache, block_tables, seq_lens)
+    nb, bs, _ = latent_cache.shape
+    T, H, _ = q.shape
+    S = seq_lens.shape[0]
+    if cu_seqlens_q.shape != (S + 1,):
+        raise ValueError("cu_seqlens_q must hold one entry more than there are sequences")
+    st = lib().pa_latent_varlen(_raw(out), _raw(q), _raw(latent_cache), _raw(block_tables), block_tables.shape[1],
+                                _raw(seq_lens), _raw(cu_seqlens_q), S, T, max_q, H, lat, rot, nb, bs, max_context,
+                                float(scale), 1 if causal else 0, _dtype(q), *_ws(workspace),
+                                _raw_stream(stream, out, q, latent_cache, block_tables, seq_lens, cu_seqlens_q,
+                                            workspace))
+    _check(st, "pa_latent_varlen")
+    return out
+
+
+def pa_decode_shared_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, block_size, max_context,
+                                    dtype):
+    code = DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else dtype
+    return lib().pa_decode_shared_workspace_size(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, block_size,
+                                                 max_context, code)
+
+
+def pa_decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, max_context,
+                     scale, workspace=None, stream=None):
+    """pa_decode for sequences that share leading blocks: group g is sequences group_starts[g] .. group_starts[g+1]-1,
+    whose first prefix_lens[g] tokens (a multiple of block_size) lie in the same blocks and are read once for all.
+    group_starts [groups + 1], prefix_lens [groups] int32."""
+    _dev(out, q, k_cache, v_cache, block_tables, context_lens, group_starts, prefix_lens, workspace)
+    _i32(block_tables, context_lens)
+    if group_starts.dtype != torch.int32 or prefix_lens.dtype != torch.int32:
+        raise TypeError("group_starts and prefix_lens must be int32")
+    _same_batch(q, k_cache, context_lens, block_tables)
+    _pools(k_cache, v_cache, q.dtype)
+    nb, bs, hkv, hd = k_cache.shape
+    S, hq, _ = q.shape
+    groups = prefix_lens.numel()
+    if out.shape != q.shape or out.dtype != q.dtype or context_lens.shape[0] != S:
+        raise ValueError("out must have q's shape and dtype, context_lens one entry per query")
+    if group_starts.numel() != groups + 1:
+        raise ValueError("group_starts must hold one entry more than there are groups")
+    st = lib().pa_decode_shared(_raw(out), _raw(q), _raw(k_cache), _raw(v_cache), _raw(block_tables),
+                                block_tables.shape[1], _raw(context_lens), _raw(group_starts), _raw(prefix_lens),
+                                groups, S, hq, hkv, hd, nb, bs, max_context, float(scale), _dtype(q), *_ws(workspace),
+                                _raw_stream(stream, out, q, k_cache, v_cache, block_tables, context_lens, group_starts,
+                                            prefix_lens, workspace))
+    _check(st, "pa_decode_shared")
+    return out

@@ -265,6 +265,7 @@ pa_status pa_device_status(int clear) {
     const uint32_t bits =
         pa::decode_tc_status(clear != 0) | pa::decode_weights_status(clear != 0) |
                           pa::varlen_umma_status(clear != 0) | pa::weights_umma_status(clear != 0) |
+                          pa::latent_umma_status(clear != 0) |
                           pa::selftest_status(clear != 0);
     if (bits & 1u) return fail(PA_ERR_TIMEOUT, "a kernel's bounded barrier wait ran out");
     return PA_OK;
@@ -1309,6 +1310,267 @@ pa_status pa_evict(float* weights_out, int32_t* positions_out, int32_t* new_lens
     a.row_bytes = (int64_t)head_dim * pa::elt_size(dtype);
     cudaError_t e = pa::launch_evict(a, workspace, st);
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_evict launch");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ latent cache
+
+extern "C" pa_status pa_latent_write(void* q_out, int64_t q_out_stride, int64_t q_out_head_stride, const void* q,
+                                     int64_t q_stride, int64_t q_head_stride, const void* kv, int64_t kv_stride,
+                                     const void* norm_weight, float eps, const int64_t* positions,
+                                     const double* inv_freq, int32_t rope_dim, int interleaved,
+                                     const int64_t* slot_mapping, int64_t n, void* cache, int32_t num_blocks,
+                                     int32_t block_size, int32_t num_heads, int32_t latent_dim, int dtype,
+                                     void* stream) {
+    if (num_heads < 0 || latent_dim <= 0 || rope_dim < 2 || rope_dim % 2 || rope_dim > 256)
+        return fail(PA_ERR_INVALID_ARG, "latent_dim must be positive, rope_dim even and in [2, 256], num_heads >= 0");
+    if (latent_dim > 4096) return fail(PA_ERR_UNSUPPORTED, "latent_dim must be at most 4096");
+    pa_status g = check_geometry(std::max(num_heads, 1), 1, latent_dim + rope_dim, num_blocks, block_size, dtype);
+    if (g != PA_OK) return g;
+    if (n < 0) return fail(PA_ERR_INVALID_ARG, "n must be non-negative");
+    if (n == 0) return PA_OK;
+    if (n > (int64_t)INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "n must fit in int32");
+    if (!kv || !positions || !inv_freq || !slot_mapping || !cache || (num_heads && (!q || !q_out)))
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    const int elt = pa::elt_size(dtype);
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(kv) | reinterpret_cast<uintptr_t>(norm_weight) |
+                           (num_heads ? reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) : 0);
+    if (addr % (uintptr_t)elt) return fail(PA_ERR_INVALID_ARG, "pointers must be aligned to their type");
+    if (!aligned16(cache)) return fail(PA_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+    if (kv_stride < latent_dim + rope_dim)
+        return fail(PA_ERR_INVALID_ARG, "kv_stride may not be smaller than a token's row");
+    // no element of q_out twice: heads within tokens, or tokens within heads
+    const int64_t qt = n > 1 ? q_out_stride : rope_dim, qh = num_heads > 1 ? q_out_head_stride : rope_dim;
+    if (num_heads && !(qh >= rope_dim && (n == 1 || qt >= (num_heads - 1) * qh + rope_dim)) &&
+        !(qt >= rope_dim && (num_heads == 1 || qh >= (n - 1) * qt + rope_dim)))
+        return fail(PA_ERR_INVALID_ARG, "strides of q_out must keep heads and tokens apart");
+    if (num_heads && (q_stride < 0 || q_head_stride < 0))
+        return fail(PA_ERR_INVALID_ARG, "strides must be non-negative");
+    cudaStream_t st = as_stream(stream);
+    if (check_mode()) {
+        pa_status err = check_slots(slot_mapping, n, num_blocks, block_size, st);
+        if (err != PA_OK) return err;
+    }
+    pa::LatentWriteArgs a{};
+    a.q_out = num_heads ? q_out : nullptr;
+    a.q = num_heads ? q : nullptr;
+    a.kv = kv;
+    a.q_out_stride = num_heads && n > 1 ? q_out_stride : 0;
+    a.q_out_head_stride = num_heads > 1 ? q_out_head_stride : 0;
+    a.q_stride = num_heads && n > 1 ? q_stride : 0;
+    a.q_head_stride = num_heads > 1 ? q_head_stride : 0;
+    a.kv_stride = n > 1 ? kv_stride : 0;
+    a.norm_weight = norm_weight;
+    a.eps = eps;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.rope_dim = rope_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.slots = slot_mapping;
+    a.n = n;
+    a.cache = cache;
+    a.num_heads = num_heads;
+    a.latent_dim = latent_dim;
+    cudaError_t e = pa::launch_latent_write(a, dtype, st);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_latent_write launch");
+}
+
+// The kernel of a latent attention call (`want`: the pinned one, 0 automatic).
+static bool use_latent_umma(int64_t want, int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size,
+                            pa_status* st) {
+    const bool ok = pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size);
+    *st = PA_OK;
+    if (want == 2 && !ok)
+        *st = fail(PA_ERR_UNSUPPORTED, "the tensor-core latent kernel takes bf16/f16, latent_dim 512, rope_dim 64 and "
+                                       "block_size 8 or a multiple of 16");
+    return ok && want != 1;
+}
+
+static size_t latent_workspace(int64_t want, int64_t total_q, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+                               int32_t block_size, int dtype) {
+    if (total_q <= 0 || num_heads <= 0 || want == 1 ||
+        !pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size))
+        return 0;
+    return pa::latent_umma_workspace(total_q * num_heads);
+}
+
+// cu == nullptr: one query per sequence.
+static pa_status latent_impl(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                             int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu, int32_t num_seqs,
+                             int32_t total_q, int32_t max_q, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+                             int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int causal,
+                             int dtype, bool varlen, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* name = varlen ? "pa_latent_varlen" : "pa_latent_decode";
+    if (latent_dim <= 0 || rope_dim < 0) return fail(PA_ERR_INVALID_ARG, "latent_dim must be positive, rope_dim >= 0");
+    if ((int64_t)latent_dim + rope_dim > INT32_MAX) return fail(PA_ERR_UNSUPPORTED, "rows of at most 576 elements");
+    pa_status g = check_geometry(num_heads, 1, latent_dim + rope_dim, num_blocks, block_size, dtype);
+    if (g != PA_OK) return g;
+    if (num_seqs < 0 || total_q < 0 || max_q < 0 || max_blocks < 0 || max_context < 0)
+        return fail(PA_ERR_INVALID_ARG, "sizes must be non-negative");
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (!out || !q || !cache || !block_tables || !seq_lens || (varlen && !cu))
+        return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(cache))
+        return fail(PA_ERR_INVALID_ARG, "out, q and the cache must be 16-byte aligned");
+    if (!pa::latent_simt_supported(dtype, latent_dim + rope_dim))
+        return fail(PA_ERR_UNSUPPORTED, "latent_dim + rope_dim must be at most 576");
+    pa_status sel;
+    const bool tc = use_latent_umma(g_options[varlen ? PA_OPT_VARLEN_KERNEL : PA_OPT_DECODE_KERNEL], dtype, latent_dim,
+                                    rope_dim, block_size, &sel);
+    if (sel != PA_OK) return sel;
+    const int64_t rows = (int64_t)total_q * num_heads;
+    if (!tc && num_heads > 4 * 65535) return fail(PA_ERR_UNSUPPORTED, "too many heads");
+    if (tc && (rows > INT32_MAX - 128 ||
+               (rows / 128 + num_seqs) * (((int64_t)max_context + 127) / 128) > INT32_MAX))
+        return fail(PA_ERR_UNSUPPORTED, "too many query rows for one call");
+    cudaStream_t st = as_stream(stream);
+    if (check_mode()) {
+        pa_status err = PA_OK;
+        if (varlen) {
+            err = check_varlen(block_tables, max_blocks, seq_lens, cu, num_seqs, total_q, max_q, num_blocks,
+                               block_size, max_context, st);
+        } else {
+            std::vector<int32_t> lens;
+            if (!to_host(lens, seq_lens, num_seqs, st, &err)) return err;
+            err = check_tables(block_tables, num_seqs, max_blocks, lens, num_blocks, block_size, max_context, st);
+        }
+        if (err != PA_OK) return err;
+    }
+    pa::LatentArgs a{};
+    a.out = out;
+    a.q = q;
+    a.cache = cache;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.cu = cu;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.num_heads = num_heads;
+    a.latent_dim = latent_dim;
+    a.rope_dim = rope_dim;
+    a.block_size = block_size;
+    a.max_context = max_context;
+    a.scale = scale;
+    a.causal = causal ? 1 : 0;
+    a.dtype = dtype;
+    std::string err;
+    cudaError_t e;
+    if (tc) {
+        const size_t need = pa::latent_umma_workspace(rows);
+        if (workspace_bytes < need || !workspace)
+            return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace ? workspace_bytes : 0) +
+                                              " bytes, " + std::to_string(need) + " needed");
+        if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+        e = pa::launch_latent_umma(a, num_blocks, workspace, &err, st);
+    } else {
+        e = pa::launch_latent_simt(a, st);
+    }
+    if (e != cudaSuccess)
+        return err.empty() ? cuda_fail(e, name) : fail(PA_ERR_CUDA, std::string(name) + ": " + err);
+    return PA_OK;
+}
+
+extern "C" {
+
+size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+                                       int32_t block_size, int32_t max_context, int dtype) {
+    (void)max_context;
+    return latent_workspace(g_options[PA_OPT_DECODE_KERNEL], num_seqs, num_heads, latent_dim, rope_dim, block_size,
+                            dtype);
+}
+
+pa_status pa_latent_decode(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                           int32_t max_blocks, const int32_t* context_lens, int32_t num_seqs, int32_t num_heads,
+                           int32_t latent_dim, int32_t rope_dim, int32_t num_blocks, int32_t block_size,
+                           int32_t max_context, float scale, int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    return latent_impl(out, q, cache, block_tables, max_blocks, context_lens, nullptr, num_seqs, num_seqs, 1,
+                       num_heads, latent_dim, rope_dim, num_blocks, block_size, max_context, scale, 1, dtype, false,
+                       workspace, workspace_bytes, stream);
+}
+
+size_t pa_latent_varlen_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
+                                       int32_t latent_dim, int32_t rope_dim, int32_t block_size, int32_t max_context,
+                                       int dtype) {
+    (void)max_q, (void)max_context;
+    return num_seqs <= 0 ? 0 : latent_workspace(g_options[PA_OPT_VARLEN_KERNEL], total_q, num_heads, latent_dim,
+                                                rope_dim, block_size, dtype);
+}
+
+pa_status pa_latent_varlen(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                           int32_t max_blocks, const int32_t* seq_lens, const int32_t* cu_seqlens_q, int32_t num_seqs,
+                           int32_t total_q, int32_t max_q, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+                           int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int causal,
+                           int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    return latent_impl(out, q, cache, block_tables, max_blocks, seq_lens, cu_seqlens_q, num_seqs, total_q, max_q,
+                       num_heads, latent_dim, rope_dim, num_blocks, block_size, max_context, scale, causal, dtype,
+                       true, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ shared prefixes
+
+// Check-mode validation of the groups: their ranges, whole blocks, within the
+// members' contexts, one run of blocks for all members.
+static pa_status check_groups(const int32_t* group_starts, const int32_t* prefix_lens, int32_t num_groups,
+                              const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t block_size, cudaStream_t st) {
+    pa_status err = PA_OK;
+    std::vector<int32_t> starts, prefix, lens, bt;
+    if (!to_host(starts, group_starts, (int64_t)num_groups + 1, st, &err) ||
+        !to_host(prefix, prefix_lens, num_groups, st, &err) || !to_host(lens, context_lens, num_seqs, st, &err) ||
+        !to_host(bt, block_tables, (int64_t)num_seqs * max_blocks, st, &err))
+        return err;
+    if (starts[0] < 0 || starts[num_groups] > num_seqs)
+        return fail(PA_ERR_INDEX, "group_starts must lie in [0, num_seqs]");
+    for (int32_t g = 0; g < num_groups; ++g) {
+        const std::string who = "group " + std::to_string(g);
+        if (starts[g + 1] < starts[g]) return fail(PA_ERR_INDEX, who + ": group_starts must be non-decreasing");
+        if (prefix[g] < 0 || prefix[g] % block_size)
+            return fail(PA_ERR_INDEX, who + ": prefix_lens must be a non-negative multiple of block_size");
+        for (int32_t s = starts[g]; s < starts[g + 1]; ++s) {
+            if (prefix[g] > lens[s])
+                return fail(PA_ERR_INDEX, who + ": the prefix is longer than sequence " + std::to_string(s));
+            for (int32_t b = 0; b < prefix[g] / block_size; ++b)
+                if (bt[(size_t)s * max_blocks + b] != bt[(size_t)starts[g] * max_blocks + b])
+                    return fail(PA_ERR_INDEX, who + ": sequence " + std::to_string(s) + " does not share logical block " +
+                                                  std::to_string(b));
+        }
+    }
+    return PA_OK;
+}
+
+extern "C" {
+
+size_t pa_decode_shared_workspace_size(int32_t num_seqs, int32_t num_groups, int32_t num_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int32_t max_context, int dtype) {
+    (void)num_groups;
+    return decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, false);
+}
+
+pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, int32_t max_blocks, const int32_t* context_lens,
+                           const int32_t* group_starts, const int32_t* prefix_lens, int32_t num_groups,
+                           int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t num_blocks, int32_t block_size, int32_t max_context, float scale, int dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (num_groups < 0) return fail(PA_ERR_INVALID_ARG, "num_groups must be non-negative");
+    if (num_groups > 0 && (!group_starts || !prefix_lens)) return fail(PA_ERR_INVALID_ARG, "null pointer");
+    if (check_mode() && num_groups > 0 && num_seqs > 0 && block_size > 0 && block_tables && context_lens &&
+        max_blocks >= 0) {
+        pa_status err = (pa_status)pa::check_decode_indices(block_tables, max_blocks, context_lens, num_seqs,
+                                                            num_blocks, block_size, max_context, as_stream(stream));
+        if (err == PA_OK)
+            err = check_groups(group_starts, prefix_lens, num_groups, block_tables, max_blocks, context_lens, num_seqs,
+                               block_size, as_stream(stream));
+        if (err != PA_OK) return err;
+    }
+    return decode_impl(out, q, nullptr, nullptr, k_cache, v_cache, nullptr, nullptr, block_tables, max_blocks,
+                       context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_context,
+                       scale, dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

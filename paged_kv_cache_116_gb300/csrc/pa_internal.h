@@ -307,6 +307,56 @@ constexpr int32_t kEvictMaxContext = 1 << 19;
 size_t evict_workspace(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context, int32_t keep);
 cudaError_t launch_evict(const EvictArgs& a, void* workspace, cudaStream_t stream);
 
+// ---- latent cache: the write (pa_latent_write.cu) and attention over it
+struct LatentWriteArgs {
+    void* q_out;
+    const void* q;
+    const void* kv;
+    int64_t q_out_stride, q_out_head_stride, q_stride, q_head_stride, kv_stride;  // in elements
+    const void* norm_weight;  // [latent_dim], or nullptr: no norm
+    float eps;
+    const int64_t* positions;
+    const double* inv_freq;  // [rope_dim / 2]
+    int32_t rope_dim;
+    int interleaved;
+    const int64_t* slots;
+    int64_t n;
+    void* cache;
+    int32_t num_heads;  // 0: no queries
+    int32_t latent_dim;
+    int32_t tpb = 1;  // tokens per CTA (set by the launcher)
+};
+cudaError_t launch_latent_write(const LatentWriteArgs& a, int dtype, cudaStream_t stream);
+
+struct LatentArgs {
+    void* out;      // [total_q, num_heads, latent_dim]
+    const void* q;  // [total_q, num_heads, latent_dim + rope_dim]
+    const void* cache;
+    const int32_t* block_tables;
+    int32_t max_blocks;
+    const int32_t* seq_lens;
+    const int32_t* cu;  // nullptr: one query per sequence (row s = sequence s)
+    int32_t num_seqs;
+    int32_t total_q;
+    int32_t num_heads;
+    int32_t latent_dim;
+    int32_t rope_dim;
+    int32_t block_size;
+    int32_t max_context;
+    float scale;
+    int causal;
+    int dtype;
+};
+bool latent_simt_supported(int dtype, int32_t row_dim);  // pa_latent_simt.cu
+cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream);
+// The same on the tensor cores (pa_latent_umma.cu).  total_q * num_heads and
+// the key tiles of a launch must fit in int32.
+bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size);
+size_t latent_umma_workspace(int64_t rows);  // rows: total_q * num_heads
+cudaError_t launch_latent_umma(const LatentArgs& a, int32_t num_blocks, void* workspace, std::string* err,
+                               cudaStream_t stream);
+uint32_t latent_umma_status(bool clear);
+
 // SMs of the current device.
 int sm_count();
 

@@ -36,79 +36,13 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_launch.cuh"
+#include "pa_rotary.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 256;  // at most
 
-// inv_freq / (2 pi) as a fraction of a turn in 64 bits (two's complement).
-// freq = m 2^e with a 53-bit integer m: F = m * (2^64 / (2 pi)) * 2^e, whole
-// turns dropped; the truncations are below one unit of 2^-64 turns times
-// max(1, freq).
-__device__ __forceinline__ uint64_t turn_fraction(double freq) {
-    const uint64_t b = (uint64_t)__double_as_longlong(freq);
-    const int ex = (int)((b >> 52) & 0x7ff);
-    uint64_t m = b & 0xfffffffffffffull;
-    if (ex) m |= 1ull << 52;
-    const uint64_t c = 0x28be60db9391054aull;  // floor(2^64 / (2 pi))
-    const uint64_t lo = m * c, hi = __umul64hi(m, c);
-    const int sh = 1075 - (ex ? ex : 1);  // -e
-    uint64_t f = 0;
-    if (sh <= 0) f = -sh < 64 ? lo << -sh : 0;
-    else if (sh < 64) f = (hi << (64 - sh)) | (lo >> sh);
-    else if (sh < 128) f = hi >> (sh - 64);
-    return (b >> 63) ? 0 - f : f;
-}
-
-template <typename T, int VEC> struct alignas(VEC == 1 ? sizeof(T) : 16) RVec { T e[VEC]; };
-
-template <typename T, int VEC>
-__device__ __forceinline__ RVec<T, VEC> load_vec(const T* p) {
-    RVec<T, VEC> v;
-    if constexpr (VEC == 1) {
-        v.e[0] = *p;
-    } else {
-        uint4 r;
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-        memcpy(&v, &r, 16);
-    }
-    return v;
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const RVec<T, VEC>& v) {
-    *reinterpret_cast<RVec<T, VEC>*>(p) = v;
-}
-
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack(const RVec<T, VEC>& v, float (&x)[VEC]) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = Elt<T>::to_f(v.e[e]);
-}
-// Rotates the pairs held in a and b; cs: their cosines and sines.
-template <int VEC>
-__device__ __forceinline__ void rotate(float (&a)[VEC], float (&b)[VEC], const float2* cs, bool interleaved) {
-    if (VEC > 1 && interleaved) {
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-            const float2 c0 = cs[e], c1 = cs[VEC / 2 + e];
-            const float x0 = a[2 * e], y0 = a[2 * e + 1], x1 = b[2 * e], y1 = b[2 * e + 1];
-            a[2 * e] = x0 * c0.x - y0 * c0.y;
-            a[2 * e + 1] = y0 * c0.x + x0 * c0.y;
-            b[2 * e] = x1 * c1.x - y1 * c1.y;
-            b[2 * e + 1] = y1 * c1.x + x1 * c1.y;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float2 c = cs[e];
-            const float x = a[e], y = b[e];
-            a[e] = x * c.x - y * c.y;
-            b[e] = y * c.x + x * c.y;
-        }
-    }
-}
 // VEC codes of x / sc, as the quantizing write rounds them.
 template <int VEC>
 __device__ __forceinline__ void store_codes(uint8_t* d, const float (&x)[VEC], float sc) {
@@ -141,14 +75,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_write_kernel(const RopeA
     for (int i = threadIdx.x; i < nt * half; i += NT) {
         const int t = i / half, pr = i - t * half;
         const int ax = p.pair_axis ? min(max(p.pair_axis[pr], 0), p.num_axes - 1) : 0;
-        const double fr = p.inv_freq[pr];
-        const uint64_t turns = (uint64_t)p.positions[(int64_t)ax * p.n + t0 + t] * turn_fraction(fr);
-        // the nearest 32-bit fraction, as half turns in [-1, 1)
-        const float x = (float)(int32_t)((turns + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
-        float s, c;
-        sincospif(x, &s, &c);
-        if (!isfinite(fr)) s = c = __int_as_float(0x7fc00000);
-        tab[i] = make_float2(c, s);
+        tab[i] = turn_of(p.positions[(int64_t)ax * p.n + t0 + t], p.inv_freq[pr]);
     }
     __syncthreads();
 
