@@ -1387,12 +1387,13 @@ static bool use_latent_umma(int64_t want, int dtype, int32_t latent_dim, int32_t
     return ok && want != 1;
 }
 
-static size_t latent_workspace(int64_t want, int64_t total_q, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
+// tokens: of a request, at most.
+static size_t latent_workspace(int64_t want, int64_t tokens, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
                                int32_t block_size, int dtype) {
-    if (total_q <= 0 || num_heads <= 0 || want == 1 ||
+    if (tokens <= 0 || num_heads <= 0 || want == 1 ||
         !pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size))
         return 0;
-    return pa::latent_umma_workspace(total_q * num_heads);
+    return pa::latent_umma_workspace(tokens * num_heads);
 }
 
 // cu == nullptr: one query per sequence.
@@ -1458,7 +1459,7 @@ static pa_status latent_impl(void* out, const void* q, const void* cache, const 
     std::string err;
     cudaError_t e;
     if (tc) {
-        const size_t need = pa::latent_umma_workspace(rows);
+        const size_t need = pa::latent_umma_workspace(varlen ? rows : num_heads);
         if (workspace_bytes < need || !workspace)
             return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace ? workspace_bytes : 0) +
                                               " bytes, " + std::to_string(need) + " needed");
@@ -1477,8 +1478,8 @@ extern "C" {
 size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
                                        int32_t block_size, int32_t max_context, int dtype) {
     (void)max_context;
-    return latent_workspace(g_options[PA_OPT_DECODE_KERNEL], num_seqs, num_heads, latent_dim, rope_dim, block_size,
-                            dtype);
+    return latent_workspace(g_options[PA_OPT_DECODE_KERNEL], num_seqs > 0 ? 1 : 0, num_heads, latent_dim, rope_dim,
+                            block_size, dtype);
 }
 
 pa_status pa_latent_decode(void* out, const void* q, const void* cache, const int32_t* block_tables,

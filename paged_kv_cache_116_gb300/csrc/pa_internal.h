@@ -352,7 +352,7 @@ cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream);
 // The same on the tensor cores (pa_latent_umma.cu).  total_q * num_heads and
 // the key tiles of a launch must fit in int32.
 bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size);
-size_t latent_umma_workspace(int64_t rows);  // rows: total_q * num_heads
+size_t latent_umma_workspace(int64_t rows);  // rows of a request at most (num_heads per token)
 cudaError_t launch_latent_umma(const LatentArgs& a, int32_t num_blocks, void* workspace, std::string* err,
                                cudaStream_t stream);
 uint32_t latent_umma_status(bool clear);

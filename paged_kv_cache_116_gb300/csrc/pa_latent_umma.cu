@@ -1,14 +1,789 @@
-// pa_latent_umma.cu -- place of the tensor-core form of the latent attention:
-// no shape has one so far.
+// pa_latent_umma.cu -- attention over a latent cache on the 5th-generation
+// tensor cores, two SMs per tile (cta_group::2); bf16/f16, rows of 512 latent
+// and 64 rotated elements, block_size 8 or a multiple of 16.
+//
+// Row t of the cache is [c_t | r_t].  For query row (token i, head h):
+//   x_t = scale * q[i, h] . [c_t | r_t],  out[i, h] = softmax(x) C.
+// All heads of a request share its rows, so a tile is 128 consecutive (token,
+// head) rows of one request, whatever the number of heads: one row of 1,152
+// bytes then feeds 128 x 1,088 products.  A single token of 128 heads is one
+// tile, and at 16 heads a tile is an eighth full, which costs nothing while
+// the cache's bytes are the bound (below).
+//
+// Why two SMs.  O is 128 rows x 512 columns of fp32: all of an SM's tensor
+// memory, with no place for the scores.  A pair of SMs works the 128 rows as
+// 64 + 64: each holds its rows' O in 256 columns (lanes 0-63 dims 0-255, lanes
+// 64-127 dims 256-511) and two score buffers of 64 columns (lanes 0-63 keys
+// 0-63 of the tile, lanes 64-127 keys 64-127).  For S = Q K^T each CTA brings
+// 64 of the 128 keys (all 576 elements), for O += P C its half of the latent
+// dims of all 128 keys.  One SM with half of the dims would compute every
+// score twice (1.5 times the products).
+//
+// Roles of a CTA (192 threads):
+//   warps 0-3   softmax: a thread has one row and half of a tile's keys;
+//               partners (64 threads apart) swap their maxima through shared
+//               memory; P goes to shared memory as the A operand.  O is
+//               rescaled only when a row's maximum grows by more than 2^8.
+//   warp 4      loads: 16 KB stages -- two 64-element chunks of the CTA's 64
+//               keys, or two chunks of its dims of 64 keys -- into a ring of
+//               seven, boxes issued by a lane each; both CTAs' bytes are
+//               counted on the even CTA's barrier.
+//   warp 5      (even CTA) issues the MMAs: S of the next tile before P C of
+//               this one, so the softmax overlaps them.
+//
+// Work: all (request, row tile) units' key tiles form one list, cut into equal
+// runs, one per pair; a unit cut between pairs leaves (m, l, o) records that
+// latent_merge_kernel joins.  The cut depends on the lengths only.
+//
+// Bound: the cache's bytes for single tokens (1,152 per token; with 128 heads
+// the products need 0.7 of that time), the tensor pipe for prompts.
+//
+// Every wait is bounded in time; on expiry the kernel sets a status bit, the
+// roles leave their loops, and the pair still frees its tensor memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <string>
+#include <type_traits>
+
+#include "pa_cluster.cuh"
+#include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_launch.cuh"
+#include "pa_tmap.cuh"
 
 namespace pa {
+namespace {
 
-bool latent_umma_supported(int, int32_t, int32_t, int32_t) { return false; }
-size_t latent_umma_workspace(int64_t) { return 0; }
-cudaError_t launch_latent_umma(const LatentArgs&, int32_t, void*, std::string*, cudaStream_t) {
-    return cudaErrorNotSupported;
+__device__ unsigned int g_latent_status;
+
+constexpr int LAT = 512, ROT = 64, D = LAT + ROT;
+constexpr int CH = D / 64;     // 128-byte chunks of a row
+constexpr int TM = 128;        // query rows per tile, 64 per CTA
+constexpr int BK = 128;        // keys per tile, 64 per CTA
+constexpr int CHB = 64 * 128;  // bytes of a chunk of 64 rows
+constexpr int STAGE = 2 * CHB;
+constexpr int NST = 7;
+constexpr int NTHREADS = 192;
+constexpr int W_LOAD = 4, W_MMA = 5;
+constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;  // S: two buffers of 64
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr int kMaxSeqs = 2000;    // requests per launch (their tile counts' prefix is in shared memory)
+constexpr int REC = LAT + 4;      // floats of a record's row: o, m, l
+constexpr int kPairs = kSms / 2;
+
+constexpr int Q_OFF = 0;
+constexpr int P_OFF = CH * CHB;
+constexpr int ST_OFF = P_OFF + 2 * 2 * CHB;
+constexpr int BAR_OFF = ST_OFF + NST * STAGE;
+// full[NST], empty[NST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_empty, tail
+constexpr int NBAR = 2 * NST + 8 + 4;
+constexpr int X_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;  // float [2][128] swapped maxima (and sums)
+constexpr int MISC_OFF = X_OFF + 2 * 128 * 4;               // tensor-memory address, abort flag
+constexpr int PREFIX_OFF = MISC_OFF + 16;
+constexpr size_t smem_bytes(int seqs) { return 1024 + PREFIX_OFF + (size_t)(seqs + 1) * 4; }
+static_assert(smem_bytes(kMaxSeqs) <= 232448, "fits in shared memory");
+
+struct Params {
+    void* out;
+    const int32_t* block_tables;
+    int32_t max_blocks;
+    const int32_t* seq_lens;
+    const int32_t* cu;  // nullptr: one query per sequence
+    int32_t num_seqs;
+    int32_t num_heads;
+    int32_t block_size;
+    int32_t box_rows;  // rows of a box of the cache: 8, 16, 32 or 64
+    int32_t causal;
+    float scale_log2;
+    float* records;  // [2 pairs][rec_rows][REC]
+    int32_t rec_rows;
+};
+
+// A request: its first (token, head) row, rows, tokens cached before the new
+// ones, context.
+struct Request {
+    int64_t row0;
+    int rows, before, L;
+};
+__device__ __forceinline__ Request request(const Params& p, int s) {
+    Request r;
+    r.L = max(p.seq_lens[s], 0);
+    int q0 = s, n = 1;
+    if (p.cu) {
+        q0 = p.cu[s];
+        n = max(p.cu[s + 1] - q0, 0);
+    }
+    if (r.L == 0) n = 0;
+    r.row0 = (int64_t)q0 * p.num_heads;
+    r.rows = n * p.num_heads;
+    r.before = max(r.L - n, 0);
+    return r;
 }
-uint32_t latent_umma_status(bool) { return 0; }
+// Key tiles of the row tiles before t of a request.  With causal masking tile t
+// ends at row x = 128 t + 127, of token x / H, which sees before + x / H + 1
+// keys: ceil of that by 128 is floor((t + b) / H) with
+// b = floor((127 + H (before + 128)) / 128), so sums over t are closed forms.
+// The last tile sees the whole context.
+__device__ __forceinline__ int64_t floor_sum(int64_t x, int64_t h) {  // sum of floor(i / h), i < x
+    const int64_t q = x / h;
+    return h * (q * (q - 1) / 2) + (x - q * h) * q;
+}
+__device__ __forceinline__ int row_tiles(const Request& r) { return (r.rows + TM - 1) / TM; }
+__device__ __forceinline__ int64_t tile_sum(const Params& p, const Request& r, int t) {
+    const int nt = row_tiles(r), whole = (r.L + BK - 1) / BK;
+    if (!p.causal) return (int64_t)t * whole;
+    const int64_t h = p.num_heads, b = (127 + h * (r.before + 128)) / 128;
+    const int64_t u = min(t, nt - 1);
+    return t <= 0 ? 0 : floor_sum(b + u, h) - floor_sum(b, h) + (t == nt ? whole : 0);
+}
+__device__ __forceinline__ int key_tiles(const Params& p, const Request& r, int t) {
+    const int whole = (r.L + BK - 1) / BK;
+    if (!p.causal || t == row_tiles(r) - 1) return whole;
+    const int64_t h = p.num_heads, b = (127 + h * (r.before + 128)) / 128;
+    return (int)((t + b) / h);
+}
+
+// Exclusive prefix of the requests' key tiles, in shared memory (every thread;
+// ends with a block barrier).
+__device__ __forceinline__ void tile_prefix(const Params& p, int32_t* prefix) {
+    for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
+        const Request r = request(p, s);
+        prefix[s + 1] = (int)tile_sum(p, r, row_tiles(r));
+    }
+    if (threadIdx.x == 0) prefix[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, per = (p.num_seqs + 31) / 32;
+        const int lo = 1 + lane * per, hi = min(p.num_seqs + 1, lo + per);
+        int sum = 0;
+        for (int i = lo; i < hi; ++i) sum += prefix[i];
+        int incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        int run = incl - sum;
+        for (int i = lo; i < hi; ++i) {
+            run += prefix[i];
+            prefix[i] = run;
+        }
+    }
+    __syncthreads();
+}
+
+// A run of key tiles of one unit.
+struct Segment {
+    int req, t;        // request, row tile
+    int k0, k1, nk;    // key tiles [k0, k1) of nk
+    int64_t u0;        // the unit's first flat position
+    Request r;
+};
+// The segment that starts at flat position f and ends at f1 or with its unit.
+__device__ __forceinline__ Segment locate(const Params& p, const int32_t* prefix, int64_t f, int64_t f1) {
+    Segment s;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= f) lo = mid;
+        else hi = mid - 1;
+    }
+    s.req = lo;
+    s.r = request(p, lo);
+    const int64_t rem = f - prefix[lo];
+    int a = 0, b = row_tiles(s.r) - 1;
+    while (a < b) {
+        const int mid = (a + b + 1) >> 1;
+        if (tile_sum(p, s.r, mid) <= rem) a = mid;
+        else b = mid - 1;
+    }
+    s.t = a;
+    s.nk = key_tiles(p, s.r, a);
+    s.k0 = (int)(rem - tile_sum(p, s.r, a));
+    s.u0 = f - s.k0;
+    s.k1 = (int)min((int64_t)s.nk, s.k0 + f1 - f);
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    latent_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
+                       const Params p) {
+    constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + BAR_OFF);
+    uint64_t* full = bars;  // even CTA: both CTAs' loads of a stage
+    uint64_t* empty = full + NST;
+    uint64_t* s_full = empty + NST;
+    uint64_t* s_empty = s_full + 2;  // even CTA: both CTAs' softmax warps
+    uint64_t* p_full = s_empty + 2;  // even CTA, the same
+    uint64_t* p_empty = p_full + 2;
+    uint64_t* q_full = p_empty + 2;  // even CTA
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* o_empty = q_empty + 1;  // even CTA
+    uint64_t* tail = o_empty + 1;
+    float* xch = reinterpret_cast<float*>(base + X_OFF);
+    volatile uint32_t* taddr_slot = reinterpret_cast<volatile uint32_t*>(base + MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base + MISC_OFF + 4);
+    int32_t* prefix = reinterpret_cast<int32_t*>(base + PREFIX_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int H = p.num_heads;
+
+    if (threadIdx.x == 32 * W_LOAD) {
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmC);
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    tile_prefix(p, prefix);
+    if (!p.cu) {  // no context: a zero row
+        for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+            if (prefix[s + 1] != prefix[s]) continue;
+            uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)s * H * LAT);
+            for (int e = threadIdx.x; e < H * (LAT / 8); e += NTHREADS) o[e] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    const int64_t W = prefix[p.num_seqs], pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const int64_t f0 = pair * W / pairs, f1 = (pair + 1) * W / pairs;
+    if (f0 == f1) return;  // (both CTAs of the pair)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 2u);
+            mbar_init(&empty[i], 1u);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1u);
+            mbar_init(&s_empty[i], 8u);
+            mbar_init(&p_full[i], 8u);
+            mbar_init(&p_empty[i], 1u);
+        }
+        mbar_init(q_full, 2u);
+        mbar_init(q_empty, 1u);
+        mbar_init(o_empty, 8u);
+        mbar_init(tail, 1u);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == W_MMA) tmem_pair_alloc(const_cast<uint32_t*>(taddr_slot), TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *taddr_slot;
+    const uint32_t sb = smem_u32(base);
+
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(&g_latent_status, kStatusTimeout);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = mbar_wait_cluster_warp(bar, parity, WAIT_NS) && !*abort_flag;
+        if (!ok && lane == 0) fail();
+        return __all_sync(0xffffffffu, ok);
+    };
+
+    if (warp == W_LOAD) {
+        // ---------------- loads
+        const int br = p.box_rows, gpt = BK / br, gph = 64 / br;  // boxes per tile and chunk, per half tile
+        int slot = 0, seg = 0, tail_turn = 0;
+        uint32_t phase = 0;  // of the ring's current turn
+        bool run = true;
+        auto next_slot = [&]() {
+            if (++slot == NST) slot = 0, phase ^= 1;
+        };
+        for (int64_t f = f0; f < f1 && run; ++seg) {
+            const Segment s = locate(p, prefix, f, f1);
+            const int32_t* table = p.block_tables + (int64_t)s.req * p.max_blocks;
+            const int L = s.r.L;
+            // pool row of this lane's box of tile k
+            auto box_row = [&](int k) -> int32_t {
+                const int tok = k * BK + lane * br;
+                return lane < gpt && k < s.k1 && tok < L ? table[tok / p.block_size] * p.block_size + tok % p.block_size : 0;
+            };
+            int32_t cur = box_row(s.k0), prev = 0;
+            // the query rows of this CTA
+            if (!(run = wait(q_empty, (seg & 1) ^ 1))) break;
+            {
+                const int first = s.t * TM + 64 * (int)rank, rows = min(max(s.r.rows - first, 0), 64);
+                const int boxes = (rows + 15) / 16;
+                const uint32_t qb = smem_of(q_full, 0);
+                if (lane == 0) {
+                    if (boxes) mbar_arrive_expect_tx_at(qb, (uint32_t)(boxes * CH * 16 * 128));
+                    else mbar_arrive_at(qb);
+                }
+                __syncwarp();
+                for (int i = lane; i < boxes * CH; i += 32) {
+                    const int c = i / boxes, b = i - c * boxes;
+                    tma_load_3d_pair(base + Q_OFF + c * CHB + b * 16 * 128, &tmQ, qb, 0, c,
+                                     (int)(s.r.row0 + first + 16 * b));
+                }
+            }
+            for (int k = s.k0; k <= s.k1 && run; ++k) {
+                const int32_t nxt = box_row(k + 1);
+                if (k < s.k1) {
+                    // this CTA's 64 keys, two chunks a stage
+                    const int own = min(max(L - k * BK - 64 * (int)rank, 0), 64), boxes = (own + br - 1) / br;
+                    for (int c0 = 0; c0 < CH; c0 += 2) {
+                        if (!(run = wait(&empty[slot], phase ^ 1))) break;
+                        const int nc = min(2, CH - c0), b = lane % gph, c = lane / gph;
+                        const uint32_t fb = smem_of(&full[slot], 0);
+                        if (lane == 0) {
+                            if (boxes) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * nc * br * 128));
+                            else mbar_arrive_at(fb);
+                        }
+                        const int32_t row = __shfl_sync(0xffffffffu, cur, (int)rank * gph + b);
+                        if (c < nc && b < boxes)
+                            tma_load_3d_pair(base + ST_OFF + slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
+                                             c0 + c, row);
+                        next_slot();
+                    }
+                }
+                if (run && k > s.k0) {
+                    // this CTA's dims of the keys of tile k - 1: (half tile, two chunks) a stage
+                    const int valid = min(L - (k - 1) * BK, BK), halves = valid > 64 ? 2 : 1;
+                    const int rest = valid & 15;  // keys of the last, partial group of 16
+                    for (int h = 0; h < halves && run; ++h) {
+                        const int keys = min(valid - 64 * h, 64), boxes = (keys + br - 1) / br;
+                        const bool ragged = rest != 0 && h == halves - 1;
+                        int slots[2];
+                        for (int pc = 0; pc < 2; ++pc) {
+                            if (!(run = wait(&empty[slot], phase ^ 1))) break;
+                            const int b = lane % gph, c = lane / gph;
+                            const uint32_t fb = smem_of(ragged ? tail : &full[slot], ragged ? rank : 0);
+                            if (lane == 0 && !(ragged && pc))
+                                mbar_arrive_expect_tx_at(fb, (uint32_t)((ragged ? 2 : 1) * boxes * 2 * br * 128));
+                            const int32_t row = __shfl_sync(0xffffffffu, prev, h * gph + b);
+                            if (c < 2 && b < boxes)
+                                tma_load_3d_pair(base + ST_OFF + slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
+                                                 4 * (int)rank + 2 * pc + c, row);
+                            slots[pc] = slot;
+                            next_slot();
+                        }
+                        if (!run || !ragged) continue;
+                        // rows past the context hold anything, and P is zero
+                        // there: they are zeroed before the product reads them
+                        // (a segment has one such tile, its unit's last)
+                        if (!(run = wait(tail, tail_turn & 1))) break;
+                        ++tail_turn;
+                        const int lo = keys, hi = (keys + 15) / 16 * 16;
+                        for (int i = lane; i < (hi - lo) * 32; i += 32) {
+                            const int r = lo + i / 32, x = i % 32;  // stage, chunk, 16 bytes
+                            *reinterpret_cast<uint4*>(base + ST_OFF + slots[x >> 4] * STAGE + ((x >> 3) & 1) * CHB +
+                                                      r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane < 2) mbar_arrive_at(smem_of(&full[slots[lane]], 0));
+                    }
+                }
+                prev = cur;
+                cur = nxt;
+            }
+            f += s.k1 - s.k0;
+        }
+        // every stage handed back, and the last queries read: no arrival is
+        // still on its way to this CTA
+        for (int i = 0; i < NST && run; ++i) {
+            run = wait(&empty[slot], phase ^ 1);
+            next_slot();
+        }
+        if (run) run = wait(q_empty, (seg & 1) ^ 1);
+    } else if (warp == W_MMA) {
+        // ---------------- products (even CTA)
+        if (rank == 0) {
+            constexpr uint32_t idS = umma_idesc_f16(128, BK, kBF16, false);
+            constexpr uint32_t idO = umma_idesc_f16(128, 256, kBF16, true);
+            int slot = 0, seg = 0, it = 0;
+            uint32_t phase = 0;
+            bool run = true;
+            auto next_slot = [&]() {
+                if (++slot == NST) slot = 0, phase ^= 1;
+            };
+            for (int64_t f = f0; f < f1 && run; ++seg) {
+                const Segment s = locate(p, prefix, f, f1);
+                if (!(run = wait(q_full, seg & 1))) break;
+                tc_fence_after();
+                for (int k = s.k0; k <= s.k1 && run; ++k) {
+                    if (k < s.k1) {
+                        const int buf = it & 1;
+                        const uint32_t d = tmem + S_COL + 64 * buf;
+                        if (!(run = wait(&s_empty[buf], ((it >> 1) & 1) ^ 1))) break;
+                        tc_fence_after();
+                        for (int c0 = 0; c0 < CH; c0 += 2) {
+                            if (!(run = wait(&full[slot], phase))) break;
+                            tc_fence_after();
+                            if (elect_lane()) {
+                                const uint32_t a = sb + Q_OFF + c0 * CHB, b = sb + ST_OFF + slot * STAGE;
+                                const int steps = min(2, CH - c0) * 4;
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk) {
+                                    if (kk >= steps) break;
+                                    const uint32_t off = (kk >> 2) * CHB + (kk & 3) * 32;
+                                    umma_pair_f16(d, umma_sdesc_sw128(a + off, 16, 1024),
+                                                  umma_sdesc_sw128(b + off, 16, 1024), idS, c0 || kk ? 1u : 0u);
+                                }
+                                umma_pair_commit(&empty[slot]);
+                                if (c0 + 2 >= CH) {
+                                    umma_pair_commit(&s_full[buf]);
+                                    if (k == s.k1 - 1) umma_pair_commit(q_empty);
+                                }
+                            }
+                            __syncwarp();
+                            next_slot();
+                        }
+                    }
+                    if (run && k > s.k0) {
+                        const int pt = it - 1, buf = pt & 1;  // the tile before (`it` counts up below)
+                        if (k == s.k0 + 1 && !(run = wait(o_empty, (seg & 1) ^ 1))) break;
+                        if (!(run = wait(&p_full[buf], (pt >> 1) & 1))) break;
+                        tc_fence_after();
+                        const int valid = min(s.r.L - (k - 1) * BK, BK), nks = (valid + 15) / 16;
+                        const int halves = valid > 64 ? 2 : 1;
+                        for (int h = 0; h < halves && run; ++h)
+                            for (int pc = 0; pc < 2; ++pc) {
+                                if (!(run = wait(&full[slot], phase))) break;
+                                tc_fence_after();
+                                if (elect_lane()) {
+                                    const uint32_t a = sb + P_OFF + (2 * buf + h) * CHB;
+                                    const uint32_t b = sb + ST_OFF + slot * STAGE;
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        if (4 * h + j >= nks) break;
+                                        umma_pair_f16(tmem + O_COL + 128 * pc, umma_sdesc_sw128(a + 32 * j, 16, 1024),
+                                                      umma_sdesc_sw128(b + j * 16 * 128, CHB, 1024), idO,
+                                                      k > s.k0 + 1 || h || j ? 1u : 0u);
+                                    }
+                                    umma_pair_commit(&empty[slot]);
+                                    if (h == halves - 1 && pc == 1) umma_pair_commit(&p_empty[buf]);
+                                }
+                                __syncwarp();
+                                next_slot();
+                            }
+                    }
+                    if (k < s.k1) ++it;
+                }
+                f += s.k1 - s.k0;
+            }
+        }
+    } else {
+        // ---------------- softmax: row r of this CTA's 64, keys 64 hf .. of each tile
+        const int tid = threadIdx.x, hf = warp >> 1, r = (warp & 1) * 32 + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+        const float scale = p.scale_log2;
+        int it = 0, seg = 0;
+        bool ok = true, first_seg = true;
+        for (int64_t f = f0; f < f1; ++seg) {
+            const Segment s = locate(p, prefix, f, f1);
+            const int row = s.t * TM + 64 * (int)rank + r;
+            const bool mine = row < s.r.rows;
+            const bool some = __any_sync(0xffffffffu, mine);  // (of these 32 rows: the partner warp's too)
+            const int vis = p.causal ? min(s.r.L, s.r.before + min(row, s.r.rows - 1) / H + 1) : s.r.L;
+            int vmin = vis;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) vmin = min(vmin, __shfl_xor_sync(0xffffffffu, vmin, o));
+            float m = -INFINITY, l = 0.f;
+            for (int k = s.k0; k < s.k1; ++k, ++it) {
+                const int buf = it & 1;
+                const uint32_t turn = (it >> 1) & 1;
+                float x[64];
+                if (ok) ok = wait(&s_full[buf], turn);
+                float mx = -INFINITY;
+                if (!some) {  // rows past the request's: whatever P holds, their O is not stored
+                    if (ok && lane == 0) mbar_arrive_at(smem_of(&s_empty[buf], 0));
+                    ok = bar_all(1, 128, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_at(smem_of(&p_full[buf], 0));
+                    continue;
+                }
+                if (ok) {
+                    tc_fence_after();
+                    float (&xa)[32] = *reinterpret_cast<float (*)[32]>(&x[0]);
+                    float (&xb)[32] = *reinterpret_cast<float (*)[32]>(&x[32]);
+                    tmem_ld32(t_lane + S_COL + 64 * buf, xa);
+                    tmem_ld32(t_lane + S_COL + 64 * buf + 32, xb);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(smem_of(&s_empty[buf], 0));
+                    const int key0 = k * BK + 64 * hf;
+                    if (key0 + 64 <= vmin) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] *= scale;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] = key0 + i < vis ? x[i] * scale : -INFINITY;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    xch[buf * 128 + tid] = mx;
+                }
+                // all four warps go on, or none
+                ok = bar_all(1, 128, ok);
+                if (!ok) break;
+                mx = fmaxf(mx, xch[buf * 128 + (tid ^ 64)]);
+                const bool up = mine && (mx > m + 8.f || (m == -INFINITY && mx > m));
+                const float m_new = up ? mx : m, ms = m_new == -INFINITY ? 0.f : m_new;
+                float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float a = fast_exp2(x[i] - ms), b = fast_exp2(x[i + 1] - ms);
+                    s4[(i >> 1) & 3] += a + b;
+                    pk[i >> 1] = pack2<T>(a, b);
+                }
+                const float alpha = up ? fast_exp2(m - ms) : 1.f;  // (0 where nothing was seen yet)
+                l = fmaf(l, alpha, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+                m = m_new;
+                // P of two tiles ago has been read
+                ok = wait(&p_empty[buf], turn ^ 1);
+                if (ok) {
+                    const uint32_t dst = sb + P_OFF + (2 * buf + hf) * CHB + r * 128;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (r & 7)) << 4)),
+                                     "r"(pk[4 * j]), "r"(pk[4 * j + 1]), "r"(pk[4 * j + 2]), "r"(pk[4 * j + 3])
+                                     : "memory");
+                    fence_proxy_async_smem();
+                    if (k > s.k0 && __any_sync(0xffffffffu, up)) {
+                        // O holds the tiles before this one
+                        ok = wait(&p_empty[buf ^ 1], ((it - 1) >> 1) & 1);
+                        if (ok) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < 256; c += 32) {
+                                float o[32];
+                                tmem_ld32(t_lane + O_COL + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                                tmem_st32(t_lane + O_COL + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive_at(smem_of(&p_full[buf], 0));
+                }
+            }
+            // the segment's last product
+            if (ok) ok = wait(&p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            xch[(it & 1) * 128 + tid] = l;
+            ok = bar_all(1, 128, ok);
+            if (!ok) break;
+            tc_fence_after();
+            l += xch[(it & 1) * 128 + (tid ^ 64)];
+            const bool whole = s.k0 == 0 && s.k1 == s.nk;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            T* orow = static_cast<T*>(p.out) + (s.r.row0 + row) * LAT + 256 * hf;
+            float* rec = p.records + ((2 * pair + (first_seg ? 0 : 1)) * p.rec_rows + 64 * (int)rank + r) * (int64_t)REC;
+            if (mine && !whole && hf == 0) {
+                rec[LAT] = m;
+                rec[LAT + 1] = l;
+            }
+            rec += 256 * hf;
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+                float o[32];
+                tmem_ld32(t_lane + O_COL + c, o);
+                tmem_wait_ld();
+                if (!mine) continue;
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4*>(orow + c + 8 * j) =
+                            make_uint4(pack2<T>(o[8 * j] * inv, o[8 * j + 1] * inv),
+                                       pack2<T>(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                       pack2<T>(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                                       pack2<T>(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4*>(rec + c + 4 * j) =
+                            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(smem_of(o_empty, 0));
+            first_seg = false;
+            f += s.k1 - s.k0;
+        }
+    }
+
+    // After a wait that ran out: the copies in flight are given time to land
+    // before the shared memory is let go.
+    __syncwarp();
+    if (*abort_flag && warp == W_LOAD) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {}
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == W_MMA) tmem_pair_dealloc(tmem, TMEM_COLS);
+}
+
+// Joins the records of the units cut between pairs.  CTA (c, g): the unit whose
+// first piece ends pair c's run, rows 8 g .. 8 g + 7, a warp each.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int pairs) {
+    extern __shared__ int32_t mprefix[];
+    tile_prefix(p, mprefix);
+    const int64_t W = mprefix[p.num_seqs], c = blockIdx.x;
+    const int64_t f0 = c * W / pairs, f1 = (c + 1) * W / pairs;
+    pdl_wait_primary();  // (the lengths are older than the grid before this one)
+    pdl_launch_dependents();
+    if (f0 == f1 || f1 == W) return;
+    const Segment s = locate(p, mprefix, f1 - 1, f1);
+    const int64_t u1 = s.u0 + s.nk;
+    if (u1 <= f1 || s.u0 < f0) return;  // ends here, or began before
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= p.rec_rows || s.t * TM + row >= s.r.rows) return;
+    const int64_t last = (u1 * pairs + W - 1) / W - 1;  // the pair owning position u1 - 1
+    float M = -INFINITY, l = 0.f;
+    float4 o[4] = {};
+    for (int64_t q = c; q <= last; ++q) {
+        if (q * W / pairs == (q + 1) * W / pairs) continue;  // an empty run
+        const float* rec = p.records + ((2 * q + (q == c && s.u0 != f0 ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
+        const float m = __ldcg(rec + LAT), lq = __ldcg(rec + LAT + 1);
+        float4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane);
+        const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
+        const float e0 = exp2f(M - ms), e1 = exp2f(m - ms);
+        l = l * e0 + lq * e1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i].x = o[i].x * e0 + a[i].x * e1;
+            o[i].y = o[i].y * e0 + a[i].y * e1;
+            o[i].z = o[i].z * e0 + a[i].z * e1;
+            o[i].w = o[i].w * e0 + a[i].w * e1;
+        }
+        M = mn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* out = static_cast<T*>(p.out) + (s.r.row0 + s.t * TM + row) * LAT;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(out + 128 * i + 4 * lane) =
+            make_uint2(pack2<T>(o[i].x * inv, o[i].y * inv), pack2<T>(o[i].z * inv, o[i].w * inv));
+}
+
+// ---------------------------------------------------------------- host side
+
+int box_rows(int block_size) {
+    return block_size == 8 ? 8 : block_size % 64 == 0 ? 64 : block_size % 32 == 0 ? 32 : 16;
+}
+
+template <typename T>
+cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspace, int rec_rows, std::string* err,
+                         cudaStream_t stream) {
+    const CUtensorMapDataType ty = a.dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const int64_t rows = (int64_t)a.total_q * a.num_heads;
+    CUtensorMap tmQ, tmC;
+    const cuuint64_t strides[2] = {128, D * 2};
+    const cuuint64_t qdims[3] = {64, CH, (cuuint64_t)rows};
+    const cuuint32_t qbox[3] = {64, 1, 16};
+    const cuuint64_t cdims[3] = {64, CH, (cuuint64_t)num_blocks * a.block_size};
+    const cuuint32_t cbox[3] = {64, 1, (cuuint32_t)box_rows(a.block_size)};
+    if (!encode_tiled_3d(&tmQ, ty, a.q, qdims, strides, qbox, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, err) ||
+        !encode_tiled_3d(&tmC, ty, a.cache, cdims, strides, cbox, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, err))
+        return cudaErrorInvalidValue;
+    Params p;
+    p.out = a.out;
+    p.block_tables = a.block_tables;
+    p.max_blocks = a.max_blocks;
+    p.seq_lens = a.seq_lens;
+    p.cu = a.cu;
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.block_size = a.block_size;
+    p.box_rows = box_rows(a.block_size);
+    p.causal = a.causal;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.records = static_cast<float*>(workspace);
+    p.rec_rows = rec_rows;
+    // a pair per two SMs, fewer where even the longest contexts give them less
+    // than one tile each
+    const int64_t units = a.cu ? rows / TM + a.num_seqs : (int64_t)a.num_seqs * ((a.num_heads + TM - 1) / TM);
+    const int64_t tiles = units * ((a.max_context + BK - 1) / BK);
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>({kPairs, sm_count() / 2, tiles}));
+    const void* kfn = reinterpret_cast<const void*>(&latent_umma_kernel<T>);
+    cudaError_t e = allow_smem(kfn, smem_bytes(kMaxSeqs));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = smem_bytes(a.num_seqs);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, latent_umma_kernel<T>, tmQ, tmC, p);
+    if (e != cudaSuccess || pairs == 1) return e;
+    return launch_pdl_smem(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 7) / 8)),
+                           dim3(256), (size_t)(a.num_seqs + 1) * 4, stream, p, pairs);
+}
+
+}  // namespace
+
+bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size) {
+    return (dtype == 1 || dtype == 2) && latent_dim == LAT && rope_dim == ROT &&
+           (block_size == 8 || (block_size > 0 && block_size % 16 == 0));
+}
+
+size_t latent_umma_workspace(int64_t rows) {
+    return (size_t)2 * kPairs * (size_t)std::min<int64_t>(rows, TM) * REC * sizeof(float);
+}
+
+cudaError_t launch_latent_umma(const LatentArgs& a, int32_t num_blocks, void* workspace, std::string* err,
+                               cudaStream_t stream) {
+    if (a.total_q == 0 || a.num_seqs == 0) return cudaSuccess;
+    // rows of a tile (of one token in a decode)
+    const int rec_rows = (int)std::min<int64_t>((int64_t)(a.cu ? a.total_q : 1) * a.num_heads, TM);
+    for (int32_t s0 = 0; s0 < a.num_seqs; s0 += kMaxSeqs) {
+        LatentArgs c = a;
+        c.num_seqs = std::min(a.num_seqs - s0, kMaxSeqs);
+        c.seq_lens = a.seq_lens + s0;
+        c.block_tables = a.block_tables + (int64_t)s0 * a.max_blocks;
+        if (a.cu) {  // query rows keep their numbers
+            c.cu = a.cu + s0;
+        } else {
+            c.total_q = c.num_seqs;
+            c.q = static_cast<const uint8_t*>(a.q) + (int64_t)s0 * a.num_heads * D * 2;
+            c.out = static_cast<uint8_t*>(a.out) + (int64_t)s0 * a.num_heads * LAT * 2;
+        }
+        cudaError_t e = a.dtype == 1 ? launch_typed<__nv_bfloat16>(c, num_blocks, workspace, rec_rows, err, stream)
+                                     : launch_typed<__half>(c, num_blocks, workspace, rec_rows, err, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+uint32_t latent_umma_status(bool clear) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_latent_status, sizeof(v));
+    if (clear) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_latent_status, &z, sizeof(z));
+    }
+    return v;
+}
 
 }  // namespace pa
