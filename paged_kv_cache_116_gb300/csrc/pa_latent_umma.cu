@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         atomicOr(&g_latent_status, kStatusTimeout);
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_cluster_warp(bar, parity, WAIT_NS) && !*abort_flag;
+        const bool ok = mbar_wait_ns_warp(bar, parity, WAIT_NS) && !*abort_flag;
         if (!ok && lane == 0) fail();
         return __all_sync(0xffffffffu, ok);
     };
@@ -292,6 +292,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (warp == W_LOAD) {
         // ---------------- loads
         const int br = p.box_rows, gpt = BK / br, gph = 64 / br;  // boxes per tile and chunk, per half tile
+        const int b = lane % gph, c = lane / gph;                 // this lane's box of a stage and its chunk
+        const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(tail, rank);
         int slot = 0, seg = 0, tail_turn = 0;
         uint32_t phase = 0;  // of the ring's current turn
         bool run = true;
@@ -320,9 +322,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 __syncwarp();
                 for (int i = lane; i < boxes * CH; i += 32) {
-                    const int c = i / boxes, b = i - c * boxes;
-                    tma_load_3d_pair(base + Q_OFF + c * CHB + b * 16 * 128, &tmQ, qb, 0, c,
-                                     (int)(s.r.row0 + first + 16 * b));
+                    const int qc = i / boxes, g = i - qc * boxes;
+                    tma_load_3d_pair(base + Q_OFF + qc * CHB + g * 16 * 128, &tmQ, qb, 0, qc,
+                                     (int)(s.r.row0 + first + 16 * g));
                 }
             }
             for (int k = s.k0; k <= s.k1 && run; ++k) {
@@ -332,8 +334,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const int own = min(max(L - k * BK - 64 * (int)rank, 0), 64), boxes = (own + br - 1) / br;
                     for (int c0 = 0; c0 < CH; c0 += 2) {
                         if (!(run = wait(&empty[slot], phase ^ 1))) break;
-                        const int nc = min(2, CH - c0), b = lane % gph, c = lane / gph;
-                        const uint32_t fb = smem_of(&full[slot], 0);
+                        const int nc = min(2, CH - c0);
+                        const uint32_t fb = full0 + 8 * slot;
                         if (lane == 0) {
                             if (boxes) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * nc * br * 128));
                             else mbar_arrive_at(fb);
@@ -355,8 +357,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         int slots[2];
                         for (int pc = 0; pc < 2; ++pc) {
                             if (!(run = wait(&empty[slot], phase ^ 1))) break;
-                            const int b = lane % gph, c = lane / gph;
-                            const uint32_t fb = smem_of(ragged ? tail : &full[slot], ragged ? rank : 0);
+                            const uint32_t fb = ragged ? tail_bar : full0 + 8 * slot;
                             if (lane == 0 && !(ragged && pc))
                                 mbar_arrive_expect_tx_at(fb, (uint32_t)((ragged ? 2 : 1) * boxes * 2 * br * 128));
                             const int32_t row = __shfl_sync(0xffffffffu, prev, h * gph + b);
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane < 2) mbar_arrive_at(smem_of(&full[slots[lane]], 0));
+                        if (lane < 2) mbar_arrive_at(full0 + 8 * slots[lane]);
                     }
                 }
                 prev = cur;
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int tid = threadIdx.x, hf = warp >> 1, r = (warp & 1) * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
         const float scale = p.scale_log2;
+        const uint32_t s_empty0 = smem_of(s_empty, 0), p_full0 = smem_of(p_full, 0), o_empty0 = smem_of(o_empty, 0);
         int it = 0, seg = 0;
         bool ok = true, first_seg = true;
         for (int64_t f = f0; f < f1; ++seg) {
@@ -496,10 +498,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 if (ok) ok = wait(&s_full[buf], turn);
                 float mx = -INFINITY;
                 if (!some) {  // rows past the request's: whatever P holds, their O is not stored
-                    if (ok && lane == 0) mbar_arrive_at(smem_of(&s_empty[buf], 0));
+                    if (ok && lane == 0) mbar_arrive_at(s_empty0 + 8 * buf);
                     ok = bar_all(1, 128, ok);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_at(smem_of(&p_full[buf], 0));
+                    if (lane == 0) mbar_arrive_at(p_full0 + 8 * buf);
                     continue;
                 }
                 if (ok) {
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_at(smem_of(&s_empty[buf], 0));
+                    if (lane == 0) mbar_arrive_at(s_empty0 + 8 * buf);
                     const int key0 = k * BK + 64 * hf;
                     if (key0 + 64 <= vmin) {
 #pragma unroll
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive_at(smem_of(&p_full[buf], 0));
+                    if (ok && lane == 0) mbar_arrive_at(p_full0 + 8 * buf);
                 }
             }
             // the segment's last product
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(smem_of(o_empty, 0));
+            if (lane == 0) mbar_arrive_at(o_empty0);
             first_seg = false;
             f += s.k1 - s.k0;
         }
