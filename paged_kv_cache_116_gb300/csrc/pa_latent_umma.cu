@@ -19,16 +19,16 @@
 // dims of all 128 keys.  One SM with half of the dims would compute every
 // score twice (1.5 times the products).
 //
-// Roles of a CTA (192 threads):
+// Roles of a CTA (288 threads):
 //   warps 0-3   softmax: a thread has one row and half of a tile's keys;
 //               partners (64 threads apart) swap their maxima through shared
 //               memory; P goes to shared memory as the A operand.  O is
 //               rescaled only when a row's maximum grows by more than 2^8.
-//   warp 4      loads: 16 KB stages -- two 64-element chunks of the CTA's 64
+//   warps 4-7   loads: 16 KB stages -- two 64-element chunks of the CTA's 64
 //               keys, or two chunks of its dims of 64 keys -- into a ring of
-//               seven, boxes issued by a lane each; both CTAs' bytes are
-//               counted on the even CTA's barrier.
-//   warp 5      (even CTA) issues the MMAs: S of the next tile before P C of
+//               seven, a stage to each warp in turn, boxes issued by a lane
+//               each; both CTAs' bytes are counted on the even CTA's barrier.
+//   warp 8      (even CTA) issues the MMAs: S of the next tile before P C of
 //               this one, so the softmax overlaps them.
 //
 // Work: all (request, row tile) units' key tiles form one list, cut into equal
@@ -67,8 +67,9 @@ constexpr int BK = 128;        // keys per tile, 64 per CTA
 constexpr int CHB = 64 * 128;  // bytes of a chunk of 64 rows
 constexpr int STAGE = 2 * CHB;
 constexpr int NST = 7;
-constexpr int NTHREADS = 192;
-constexpr int W_LOAD = 4, W_MMA = 5;
+constexpr int NP = 4;  // loading warps
+constexpr int W_LOAD = 4, W_MMA = W_LOAD + NP;
+constexpr int NTHREADS = 32 * (W_MMA + 1);
 constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;  // S: two buffers of 64
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int kMaxSeqs = 2000;    // requests per launch (their tile counts' prefix is in shared memory)
@@ -79,8 +80,8 @@ constexpr int Q_OFF = 0;
 constexpr int P_OFF = CH * CHB;
 constexpr int ST_OFF = P_OFF + 2 * 2 * CHB;
 constexpr int BAR_OFF = ST_OFF + NST * STAGE;
-// full[NST], empty[NST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_empty, tail
-constexpr int NBAR = 2 * NST + 8 + 4;
+// full[NST], empty[NST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_empty, tail[NP]
+constexpr int NBAR = 2 * NST + 8 + 3 + NP;
 constexpr int X_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;  // float [2][128] swapped maxima (and sums)
 constexpr int MISC_OFF = X_OFF + 2 * 128 * 4;               // tensor-memory address, abort flag
 constexpr int PREFIX_OFF = MISC_OFF + 16;
@@ -209,6 +210,13 @@ __device__ __forceinline__ Segment locate(const Params& p, const int32_t* prefix
     return s;
 }
 
+__device__ __forceinline__ uint32_t lane0(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand from its low
+// word (address >> 4 | leading byte offset >> 4 << 16): stride 1024 bytes.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t lo) {
+    return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS, 1)
     latent_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
@@ -264,10 +272,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             mbar_init(&p_full[i], 8u);
             mbar_init(&p_empty[i], 1u);
         }
-        mbar_init(q_full, 2u);
+        mbar_init(q_full, 2u * NP);
         mbar_init(q_empty, 1u);
         mbar_init(o_empty, 8u);
-        mbar_init(tail, 1u);
+        for (int i = 0; i < NP; ++i) mbar_init(&tail[i], 1u);
         *abort_flag = 0;
         mbar_fence_init();
     }
@@ -289,16 +297,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         return __all_sync(0xffffffffu, ok);
     };
 
-    if (warp == W_LOAD) {
-        // ---------------- loads
+    if (warp >= W_LOAD && warp < W_LOAD + NP) {
+        // ---------------- loads: a stage to each warp in turn
+        const int w = warp - W_LOAD;
         const int br = p.box_rows, gpt = BK / br, gph = 64 / br;  // boxes per tile and chunk, per half tile
         const int b = lane % gph, c = lane / gph;                 // this lane's box of a stage and its chunk
-        const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(tail, rank);
-        int slot = 0, seg = 0, tail_turn = 0;
+        const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(&tail[w], rank);
+        int slot = 0, seg = 0, turn = 0, tail_turn = 0;
         uint32_t phase = 0;  // of the ring's current turn
         bool run = true;
         auto next_slot = [&]() {
             if (++slot == NST) slot = 0, phase ^= 1;
+            if (++turn == NP) turn = 0;
         };
         for (int64_t f = f0; f < f1 && run; ++seg) {
             const Segment s = locate(p, prefix, f, f1);
@@ -316,16 +326,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int first = s.t * TM + 64 * (int)rank, rows = min(max(s.r.rows - first, 0), 64);
                 const int boxes = (rows + 15) / 16;
                 const uint32_t qb = smem_of(q_full, 0);
+                const int chunks = (CH - w + NP - 1) / NP;  // w, w + NP, ..
                 if (lane == 0) {
-                    if (boxes) mbar_arrive_expect_tx_at(qb, (uint32_t)(boxes * CH * 16 * 128));
+                    if (boxes) mbar_arrive_expect_tx_at(qb, (uint32_t)(boxes * chunks * 16 * 128));
                     else mbar_arrive_at(qb);
                 }
                 __syncwarp();
-                for (int i = lane; i < boxes * CH; i += 32) {
-                    const int qc = i / boxes, g = i - qc * boxes;
+                const int qc = w + NP * (lane / 4), g = lane % 4;
+                if (qc < CH && g < boxes)
                     tma_load_3d_pair(base + Q_OFF + qc * CHB + g * 16 * 128, &tmQ, qb, 0, qc,
                                      (int)(s.r.row0 + first + 16 * g));
-                }
             }
             for (int k = s.k0; k <= s.k1 && run; ++k) {
                 const int32_t nxt = box_row(k + 1);
@@ -333,6 +343,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     // this CTA's 64 keys, two chunks a stage
                     const int own = min(max(L - k * BK - 64 * (int)rank, 0), 64), boxes = (own + br - 1) / br;
                     for (int c0 = 0; c0 < CH; c0 += 2) {
+                        if (turn != w) {
+                            next_slot();
+                            continue;
+                        }
                         if (!(run = wait(&empty[slot], phase ^ 1))) break;
                         const int nc = min(2, CH - c0);
                         const uint32_t fb = full0 + 8 * slot;
@@ -354,34 +368,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     for (int h = 0; h < halves && run; ++h) {
                         const int keys = min(valid - 64 * h, 64), boxes = (keys + br - 1) / br;
                         const bool ragged = rest != 0 && h == halves - 1;
-                        int slots[2];
-                        for (int pc = 0; pc < 2; ++pc) {
+                        for (int pc = 0; pc < 2; ++pc, next_slot()) {
+                            if (turn != w) continue;
                             if (!(run = wait(&empty[slot], phase ^ 1))) break;
                             const uint32_t fb = ragged ? tail_bar : full0 + 8 * slot;
-                            if (lane == 0 && !(ragged && pc))
-                                mbar_arrive_expect_tx_at(fb, (uint32_t)((ragged ? 2 : 1) * boxes * 2 * br * 128));
+                            if (lane == 0) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * 2 * br * 128));
                             const int32_t row = __shfl_sync(0xffffffffu, prev, h * gph + b);
+                            uint8_t* st = base + ST_OFF + slot * STAGE;
                             if (c < 2 && b < boxes)
-                                tma_load_3d_pair(base + ST_OFF + slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
+                                tma_load_3d_pair(st + c * CHB + b * br * 128, &tmC, fb, 0,
                                                  4 * (int)rank + 2 * pc + c, row);
-                            slots[pc] = slot;
-                            next_slot();
+                            if (!ragged) continue;
+                            // rows past the context hold anything, and P is
+                            // zero there: they are zeroed before the product
+                            // reads them (only a unit's last tile has such)
+                            if (!(run = wait(&tail[w], tail_turn & 1))) break;
+                            ++tail_turn;
+                            const int end = (keys + 15) / 16 * 16;
+                            for (int i = lane; i < (end - keys) * 16; i += 32)
+                                *reinterpret_cast<uint4*>(st + ((i >> 3) & 1) * CHB + (keys + i / 16) * 128 +
+                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_at(full0 + 8 * slot);
                         }
-                        if (!run || !ragged) continue;
-                        // rows past the context hold anything, and P is zero
-                        // there: they are zeroed before the product reads them
-                        // (a segment has one such tile, its unit's last)
-                        if (!(run = wait(tail, tail_turn & 1))) break;
-                        ++tail_turn;
-                        const int lo = keys, hi = (keys + 15) / 16 * 16;
-                        for (int i = lane; i < (hi - lo) * 32; i += 32) {
-                            const int r = lo + i / 32, x = i % 32;  // stage, chunk, 16 bytes
-                            *reinterpret_cast<uint4*>(base + ST_OFF + slots[x >> 4] * STAGE + ((x >> 3) & 1) * CHB +
-                                                      r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane < 2) mbar_arrive_at(full0 + 8 * slots[lane]);
                     }
                 }
                 prev = cur;
@@ -407,6 +417,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             auto next_slot = [&]() {
                 if (++slot == NST) slot = 0, phase ^= 1;
             };
+            // operands as lane 0 has them: in uniform registers
+            const uint32_t tm0 = lane0(tmem), q_lo = lane0(((sb + Q_OFF) & 0x3ffffu) >> 4 | 1u << 16);
+            const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4), p_lo = lane0(((sb + P_OFF) & 0x3ffffu) >> 4 | 1u << 16);
             for (int64_t f = f0; f < f1 && run; ++seg) {
                 const Segment s = locate(p, prefix, f, f1);
                 if (!(run = wait(q_full, seg & 1))) break;
@@ -414,21 +427,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 for (int k = s.k0; k <= s.k1 && run; ++k) {
                     if (k < s.k1) {
                         const int buf = it & 1;
-                        const uint32_t d = tmem + S_COL + 64 * buf;
+                        const uint32_t d = lane0(tm0 + S_COL + 64 * buf);
                         if (!(run = wait(&s_empty[buf], ((it >> 1) & 1) ^ 1))) break;
                         tc_fence_after();
+#pragma unroll
                         for (int c0 = 0; c0 < CH; c0 += 2) {
                             if (!(run = wait(&full[slot], phase))) break;
                             tc_fence_after();
+                            const uint32_t a = q_lo + c0 * (CHB / 16);
+                            const uint32_t b = lane0(st_lo + slot * (STAGE / 16)) | 1u << 16;
                             if (elect_lane()) {
-                                const uint32_t a = sb + Q_OFF + c0 * CHB, b = sb + ST_OFF + slot * STAGE;
-                                const int steps = min(2, CH - c0) * 4;
 #pragma unroll
                                 for (int kk = 0; kk < 8; ++kk) {
-                                    if (kk >= steps) break;
-                                    const uint32_t off = (kk >> 2) * CHB + (kk & 3) * 32;
-                                    umma_pair_f16(d, umma_sdesc_sw128(a + off, 16, 1024),
-                                                  umma_sdesc_sw128(b + off, 16, 1024), idS, c0 || kk ? 1u : 0u);
+                                    if (c0 + (kk >> 2) >= CH) break;
+                                    const uint32_t off = ((kk >> 2) * CHB + (kk & 3) * 32) / 16;
+                                    umma_pair_f16(d, sw128_desc(a + off), sw128_desc(b + off), idS, c0 || kk ? 1u : 0u);
                                 }
                                 umma_pair_commit(&empty[slot]);
                                 if (c0 + 2 >= CH) {
@@ -451,15 +464,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             for (int pc = 0; pc < 2; ++pc) {
                                 if (!(run = wait(&full[slot], phase))) break;
                                 tc_fence_after();
+                                const uint32_t a = lane0(p_lo + (2 * buf + h) * (CHB / 16));
+                                const uint32_t b = lane0(st_lo + slot * (STAGE / 16)) | (CHB / 16) << 16;
+                                const uint32_t d = lane0(tm0 + O_COL + 128 * pc);
+                                const uint32_t old = lane0(k > s.k0 + 1 || h ? 1u : 0u);
                                 if (elect_lane()) {
-                                    const uint32_t a = sb + P_OFF + (2 * buf + h) * CHB;
-                                    const uint32_t b = sb + ST_OFF + slot * STAGE;
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) {
                                         if (4 * h + j >= nks) break;
-                                        umma_pair_f16(tmem + O_COL + 128 * pc, umma_sdesc_sw128(a + 32 * j, 16, 1024),
-                                                      umma_sdesc_sw128(b + j * 16 * 128, CHB, 1024), idO,
-                                                      k > s.k0 + 1 || h || j ? 1u : 0u);
+                                        umma_pair_f16(d, sw128_desc(a + 2 * j), sw128_desc(b + j * 128), idO,
+                                                      j ? 1u : old);
                                     }
                                     umma_pair_commit(&empty[slot]);
                                     if (h == halves - 1 && pc == 1) umma_pair_commit(&p_empty[buf]);
@@ -625,7 +639,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // After a wait that ran out: the copies in flight are given time to land
     // before the shared memory is let go.
     __syncwarp();
-    if (*abort_flag && warp == W_LOAD) {
+    if (*abort_flag && warp == W_MMA) {
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 1000000ull) {}
     }
