@@ -19,17 +19,19 @@
 // dims of all 128 keys.  One SM with half of the dims would compute every
 // score twice (1.5 times the products).
 //
-// Roles of a CTA (288 threads):
+// Roles of a CTA (320 threads):
 //   warps 0-3   softmax: a thread has one row and half of a tile's keys;
 //               partners (64 threads apart) swap their maxima through shared
 //               memory; P goes to shared memory as the A operand.  O is
 //               rescaled only when a row's maximum grows by more than 2^8.
 //   warps 4-7   loads: 16 KB stages -- two 64-element chunks of the CTA's 64
-//               keys, or two chunks of its dims of 64 keys -- into a ring of
-//               seven, a stage to each warp in turn, boxes issued by a lane
-//               each; both CTAs' bytes are counted on the even CTA's barrier.
-//   warp 8      (even CTA) issues the MMAs: S of the next tile before P C of
-//               this one, so the softmax overlaps them.
+//               keys in a ring of four (warps 4, 5), two chunks of its dims of
+//               64 keys in a ring of three (warps 6, 7), boxes issued by a
+//               lane each; both CTAs' bytes are counted on the even CTA's
+//               barrier.
+//   warp 8, 9   (even CTA) issue the MMAs of S and of P C: two warps, because
+//               a stage's wait, descriptors and commit take one warp longer
+//               than its products take the tensor pipe.
 //
 // Work: all (request, row tile) units' key tiles form one list, cut into equal
 // runs, one per pair; a unit cut between pairs leaves (m, l, o) records that
@@ -46,6 +48,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 #include <type_traits>
 
@@ -66,10 +69,10 @@ constexpr int TM = 128;        // query rows per tile, 64 per CTA
 constexpr int BK = 128;        // keys per tile, 64 per CTA
 constexpr int CHB = 64 * 128;  // bytes of a chunk of 64 rows
 constexpr int STAGE = 2 * CHB;
-constexpr int NST = 7;
-constexpr int NP = 4;  // loading warps
-constexpr int W_LOAD = 4, W_MMA = W_LOAD + NP;
-constexpr int NTHREADS = 32 * (W_MMA + 1);
+constexpr int NK = 4, NV = 3, NST = NK + NV;  // stages of keys and of values
+constexpr int W_LOAD = 4, NP = 2;  // NP loading warps for keys, NP for values
+constexpr int W_S = W_LOAD + 2 * NP, W_O = W_S + 1;
+constexpr int NTHREADS = 32 * (W_O + 1);
 constexpr uint32_t TMEM_COLS = 512, O_COL = 0, S_COL = 256;  // S: two buffers of 64
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr int kMaxSeqs = 2000;    // requests per launch (their tile counts' prefix is in shared memory)
@@ -81,6 +84,7 @@ constexpr int P_OFF = CH * CHB;
 constexpr int ST_OFF = P_OFF + 2 * 2 * CHB;
 constexpr int BAR_OFF = ST_OFF + NST * STAGE;
 // full[NST], empty[NST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_empty, tail[NP]
+// (full and empty: NK of the keys' ring, then NV of the values')
 constexpr int NBAR = 2 * NST + 8 + 3 + NP;
 constexpr int X_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;  // float [2][128] swapped maxima (and sums)
 constexpr int MISC_OFF = X_OFF + 2 * 128 * 4;               // tensor-memory address, abort flag
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         *abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == W_MMA) tmem_pair_alloc(const_cast<uint32_t*>(taddr_slot), TMEM_COLS);
+    if (warp == W_S) tmem_pair_alloc(const_cast<uint32_t*>(taddr_slot), TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -291,24 +295,49 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         *abort_flag = 1;
         atomicOr(&g_latent_status, kStatusTimeout);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait_ns_warp(bar, parity, WAIT_NS) && !*abort_flag;
+    // A whole warp's bounded wait, with one answer for all lanes (every lane
+    // polls: one lane's polls and a shuffle were slower).  `ready`: what an
+    // earlier look told this lane.
+    auto look = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_try_wait(bar, parity); };
+    auto wait_after = [&](uint64_t* bar, uint32_t parity, bool ready) -> bool {
+        if (__all_sync(0xffffffffu, ready)) return true;
+        const uint64_t t0 = global_ns();
+        bool ok = true;
+        for (int i = 0; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); ++i)
+            if ((i & 15) == 15 && __any_sync(0xffffffffu, *abort_flag != 0 || global_ns() - t0 > WAIT_NS)) {
+                ok = false;
+                break;
+            }
         if (!ok && lane == 0) fail();
-        return __all_sync(0xffffffffu, ok);
+        return ok;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_after(bar, parity, look(bar, parity)); };
+
+    // A role's place in its ring: slots [first, first + n) of the stages.
+    struct Ring {
+        int first, n, slot;
+        uint32_t phase;  // of the current turn
+        __device__ __forceinline__ void next() {
+            if (++slot == first + n) slot = first, phase ^= 1;
+        }
     };
 
-    if (warp >= W_LOAD && warp < W_LOAD + NP) {
-        // ---------------- loads: a stage to each warp in turn
-        const int w = warp - W_LOAD;
+    if (warp >= W_LOAD && warp < W_S) {
+        // ---------------- loads: the stages of a ring go to its NP warps in turn
+        const int w = (warp - W_LOAD) % NP;
+        const bool values = warp >= W_LOAD + NP;
         const int br = p.box_rows, gpt = BK / br, gph = 64 / br;  // boxes per tile and chunk, per half tile
         const int b = lane % gph, c = lane / gph;                 // this lane's box of a stage and its chunk
-        const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(&tail[w], rank);
-        int slot = 0, seg = 0, turn = 0, tail_turn = 0;
-        uint32_t phase = 0;  // of the ring's current turn
+        const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(&tail[w], rank), q_bar = smem_of(q_full, 0);
+        Ring ring = values ? Ring{NK, NV, NK, 0} : Ring{0, NK, 0, 0};
+        int seg = 0, turn = 0, tail_turn = 0;
         bool run = true;
-        auto next_slot = [&]() {
-            if (++slot == NST) slot = 0, phase ^= 1;
+        // the next stage, and whether it is this warp's
+        auto skip = [&]() -> bool {
+            const bool other = turn != w;
             if (++turn == NP) turn = 0;
+            if (other) ring.next();
+            return other;
         };
         for (int64_t f = f0; f < f1 && run; ++seg) {
             const Segment s = locate(p, prefix, f, f1);
@@ -319,170 +348,177 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int tok = k * BK + lane * br;
                 return lane < gpt && k < s.k1 && tok < L ? table[tok / p.block_size] * p.block_size + tok % p.block_size : 0;
             };
-            int32_t cur = box_row(s.k0), prev = 0;
-            // the query rows of this CTA
-            if (!(run = wait(q_empty, (seg & 1) ^ 1))) break;
-            {
+            int32_t cur = box_row(s.k0);
+            if (!values) {
+                // the query rows of this CTA: chunks w, w + NP, ..
+                if (!(run = wait(q_empty, (seg & 1) ^ 1))) break;
                 const int first = s.t * TM + 64 * (int)rank, rows = min(max(s.r.rows - first, 0), 64);
-                const int boxes = (rows + 15) / 16;
-                const uint32_t qb = smem_of(q_full, 0);
-                const int chunks = (CH - w + NP - 1) / NP;  // w, w + NP, ..
+                const int boxes = (rows + 15) / 16, chunks = (CH - w + NP - 1) / NP;
                 if (lane == 0) {
-                    if (boxes) mbar_arrive_expect_tx_at(qb, (uint32_t)(boxes * chunks * 16 * 128));
-                    else mbar_arrive_at(qb);
+                    if (boxes) mbar_arrive_expect_tx_at(q_bar, (uint32_t)(boxes * chunks * 16 * 128));
+                    else mbar_arrive_at(q_bar);
                 }
                 __syncwarp();
                 const int qc = w + NP * (lane / 4), g = lane % 4;
                 if (qc < CH && g < boxes)
-                    tma_load_3d_pair(base + Q_OFF + qc * CHB + g * 16 * 128, &tmQ, qb, 0, qc,
+                    tma_load_3d_pair(base + Q_OFF + qc * CHB + g * 16 * 128, &tmQ, q_bar, 0, qc,
                                      (int)(s.r.row0 + first + 16 * g));
             }
-            for (int k = s.k0; k <= s.k1 && run; ++k) {
+            for (int k = s.k0; k < s.k1 && run; ++k) {
                 const int32_t nxt = box_row(k + 1);
-                if (k < s.k1) {
+                if (!values) {
                     // this CTA's 64 keys, two chunks a stage
                     const int own = min(max(L - k * BK - 64 * (int)rank, 0), 64), boxes = (own + br - 1) / br;
+                    const int32_t row = __shfl_sync(0xffffffffu, cur, (int)rank * gph + b);
                     for (int c0 = 0; c0 < CH; c0 += 2) {
-                        if (turn != w) {
-                            next_slot();
-                            continue;
-                        }
-                        if (!(run = wait(&empty[slot], phase ^ 1))) break;
+                        if (skip()) continue;
+                        if (!(run = wait(&empty[ring.slot], ring.phase ^ 1))) break;
                         const int nc = min(2, CH - c0);
-                        const uint32_t fb = full0 + 8 * slot;
+                        const uint32_t fb = full0 + 8 * ring.slot;
                         if (lane == 0) {
                             if (boxes) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * nc * br * 128));
                             else mbar_arrive_at(fb);
                         }
-                        const int32_t row = __shfl_sync(0xffffffffu, cur, (int)rank * gph + b);
+                        __syncwarp();
                         if (c < nc && b < boxes)
-                            tma_load_3d_pair(base + ST_OFF + slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
+                            tma_load_3d_pair(base + ST_OFF + ring.slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
                                              c0 + c, row);
-                        next_slot();
+                        ring.next();
                     }
-                }
-                if (run && k > s.k0) {
-                    // this CTA's dims of the keys of tile k - 1: (half tile, two chunks) a stage
-                    const int valid = min(L - (k - 1) * BK, BK), halves = valid > 64 ? 2 : 1;
+                } else {
+                    // this CTA's dims of all keys: (half tile, two chunks) a stage
+                    const int valid = min(L - k * BK, BK), halves = valid > 64 ? 2 : 1;
                     const int rest = valid & 15;  // keys of the last, partial group of 16
                     for (int h = 0; h < halves && run; ++h) {
                         const int keys = min(valid - 64 * h, 64), boxes = (keys + br - 1) / br;
                         const bool ragged = rest != 0 && h == halves - 1;
-                        for (int pc = 0; pc < 2; ++pc, next_slot()) {
-                            if (turn != w) continue;
-                            if (!(run = wait(&empty[slot], phase ^ 1))) break;
-                            const uint32_t fb = ragged ? tail_bar : full0 + 8 * slot;
+                        const int32_t row = __shfl_sync(0xffffffffu, cur, h * gph + b);
+                        for (int pc = 0; pc < 2; ++pc) {
+                            if (skip()) continue;
+                            if (!(run = wait(&empty[ring.slot], ring.phase ^ 1))) break;
+                            const uint32_t fb = ragged ? tail_bar : full0 + 8 * ring.slot;
                             if (lane == 0) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * 2 * br * 128));
-                            const int32_t row = __shfl_sync(0xffffffffu, prev, h * gph + b);
-                            uint8_t* st = base + ST_OFF + slot * STAGE;
+                            __syncwarp();
+                            uint8_t* st = base + ST_OFF + ring.slot * STAGE;
                             if (c < 2 && b < boxes)
                                 tma_load_3d_pair(st + c * CHB + b * br * 128, &tmC, fb, 0,
                                                  4 * (int)rank + 2 * pc + c, row);
-                            if (!ragged) continue;
-                            // rows past the context hold anything, and P is
-                            // zero there: they are zeroed before the product
-                            // reads them (only a unit's last tile has such)
-                            if (!(run = wait(&tail[w], tail_turn & 1))) break;
-                            ++tail_turn;
-                            const int end = (keys + 15) / 16 * 16;
-                            for (int i = lane; i < (end - keys) * 16; i += 32)
-                                *reinterpret_cast<uint4*>(st + ((i >> 3) & 1) * CHB + (keys + i / 16) * 128 +
-                                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_at(full0 + 8 * slot);
+                            if (ragged) {
+                                // rows past the context hold anything, and P
+                                // is zero there: they are zeroed before the
+                                // product reads them (only a unit's last tile
+                                // has such)
+                                if (!(run = wait(&tail[w], tail_turn & 1))) break;
+                                ++tail_turn;
+                                const int end = (keys + 15) / 16 * 16;
+                                for (int i = lane; i < (end - keys) * 16; i += 32)
+                                    *reinterpret_cast<uint4*>(st + ((i >> 3) & 1) * CHB + (keys + i / 16) * 128 +
+                                                              (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_at(full0 + 8 * ring.slot);
+                            }
+                            ring.next();
                         }
                     }
                 }
-                prev = cur;
                 cur = nxt;
             }
             f += s.k1 - s.k0;
         }
         // every stage handed back, and the last queries read: no arrival is
         // still on its way to this CTA
-        for (int i = 0; i < NST && run; ++i) {
-            run = wait(&empty[slot], phase ^ 1);
-            next_slot();
+        for (int i = 0; i < ring.n && run; ++i) {
+            run = wait(&empty[ring.slot], ring.phase ^ 1);
+            ring.next();
         }
-        if (run) run = wait(q_empty, (seg & 1) ^ 1);
-    } else if (warp == W_MMA) {
-        // ---------------- products (even CTA)
+        if (run && !values) run = wait(q_empty, (seg & 1) ^ 1);
+    } else if (warp == W_S) {
+        // ---------------- S = Q K^T (even CTA)
         if (rank == 0) {
             constexpr uint32_t idS = umma_idesc_f16(128, BK, kBF16, false);
-            constexpr uint32_t idO = umma_idesc_f16(128, 256, kBF16, true);
-            int slot = 0, seg = 0, it = 0;
-            uint32_t phase = 0;
+            Ring ring{0, NK, 0, 0};
+            int seg = 0, it = 0;
             bool run = true;
-            auto next_slot = [&]() {
-                if (++slot == NST) slot = 0, phase ^= 1;
-            };
             // operands as lane 0 has them: in uniform registers
             const uint32_t tm0 = lane0(tmem), q_lo = lane0(((sb + Q_OFF) & 0x3ffffu) >> 4 | 1u << 16);
-            const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4), p_lo = lane0(((sb + P_OFF) & 0x3ffffu) >> 4 | 1u << 16);
+            const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4 | 1u << 16);
             for (int64_t f = f0; f < f1 && run; ++seg) {
                 const Segment s = locate(p, prefix, f, f1);
                 if (!(run = wait(q_full, seg & 1))) break;
-                tc_fence_after();
-                for (int k = s.k0; k <= s.k1 && run; ++k) {
-                    if (k < s.k1) {
-                        const int buf = it & 1;
-                        const uint32_t d = lane0(tm0 + S_COL + 64 * buf);
-                        if (!(run = wait(&s_empty[buf], ((it >> 1) & 1) ^ 1))) break;
-                        tc_fence_after();
+                bool ready = look(&full[ring.slot], ring.phase);
+                for (int k = s.k0; k < s.k1 && run; ++k, ++it) {
+                    const int buf = it & 1;
+                    const uint32_t d = lane0(tm0 + S_COL + 64 * buf);
+                    if (!(run = wait(&s_empty[buf], ((it >> 1) & 1) ^ 1))) break;
+                    tc_fence_after();
 #pragma unroll
-                        for (int c0 = 0; c0 < CH; c0 += 2) {
-                            if (!(run = wait(&full[slot], phase))) break;
-                            tc_fence_after();
-                            const uint32_t a = q_lo + c0 * (CHB / 16);
-                            const uint32_t b = lane0(st_lo + slot * (STAGE / 16)) | 1u << 16;
+                    for (int c0 = 0; c0 < CH; c0 += 2) {
+                        if (!(run = wait_after(&full[ring.slot], ring.phase, ready))) break;
+                        const uint32_t a = q_lo + c0 * (CHB / 16), b = lane0(st_lo + ring.slot * (STAGE / 16));
+                        uint64_t* done = &empty[ring.slot];
+                        ring.next();
+                        ready = look(&full[ring.slot], ring.phase);  // (looked at while the MMAs go out)
+                        if (elect_lane()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                if (c0 + (kk >> 2) >= CH) break;
+                                const uint32_t off = ((kk >> 2) * CHB + (kk & 3) * 32) / 16;
+                                umma_pair_f16(d, sw128_desc(a + off), sw128_desc(b + off), idS, c0 || kk ? 1u : 0u);
+                            }
+                            umma_pair_commit(done);
+                            if (c0 + 2 >= CH) {
+                                umma_pair_commit(&s_full[buf]);
+                                if (k == s.k1 - 1) umma_pair_commit(q_empty);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                f += s.k1 - s.k0;
+            }
+        }
+    } else if (warp == W_O) {
+        // ---------------- O += P C (even CTA)
+        if (rank == 0) {
+            constexpr uint32_t idO = umma_idesc_f16(128, 256, kBF16, true);
+            Ring ring{NK, NV, NK, 0};
+            int seg = 0, it = 0;
+            bool run = true;
+            const uint32_t tm0 = lane0(tmem), p_lo = lane0(((sb + P_OFF) & 0x3ffffu) >> 4 | 1u << 16);
+            const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4 | (CHB / 16) << 16);
+            for (int64_t f = f0; f < f1 && run; ++seg) {
+                const Segment s = locate(p, prefix, f, f1);
+                if (!(run = wait(o_empty, (seg & 1) ^ 1))) break;
+                for (int k = s.k0; k < s.k1 && run; ++k, ++it) {
+                    const int buf = it & 1;
+                    bool ready = look(&full[ring.slot], ring.phase);
+                    if (!(run = wait(&p_full[buf], (it >> 1) & 1))) break;
+                    tc_fence_after();
+                    const int valid = min(s.r.L - k * BK, BK), nks = (valid + 15) / 16;
+                    const int halves = valid > 64 ? 2 : 1;
+                    for (int h = 0; h < halves && run; ++h)
+#pragma unroll
+                        for (int pc = 0; pc < 2; ++pc) {
+                            if (!(run = wait_after(&full[ring.slot], ring.phase, ready))) break;
+                            const uint32_t a = lane0(p_lo + (2 * buf + h) * (CHB / 16));
+                            const uint32_t b = lane0(st_lo + ring.slot * (STAGE / 16));
+                            const uint32_t old = lane0(k > s.k0 || h ? 1u : 0u);
+                            uint64_t* done = &empty[ring.slot];
+                            ring.next();
+                            ready = look(&full[ring.slot], ring.phase);
                             if (elect_lane()) {
 #pragma unroll
-                                for (int kk = 0; kk < 8; ++kk) {
-                                    if (c0 + (kk >> 2) >= CH) break;
-                                    const uint32_t off = ((kk >> 2) * CHB + (kk & 3) * 32) / 16;
-                                    umma_pair_f16(d, sw128_desc(a + off), sw128_desc(b + off), idS, c0 || kk ? 1u : 0u);
+                                for (int j = 0; j < 4; ++j) {
+                                    if (4 * h + j >= nks) break;
+                                    umma_pair_f16(tm0 + O_COL + 128 * pc, sw128_desc(a + 2 * j),
+                                                  sw128_desc(b + j * 128), idO, j ? 1u : old);
                                 }
-                                umma_pair_commit(&empty[slot]);
-                                if (c0 + 2 >= CH) {
-                                    umma_pair_commit(&s_full[buf]);
-                                    if (k == s.k1 - 1) umma_pair_commit(q_empty);
-                                }
+                                umma_pair_commit(done);
+                                if (h == halves - 1 && pc == 1) umma_pair_commit(&p_empty[buf]);
                             }
                             __syncwarp();
-                            next_slot();
                         }
-                    }
-                    if (run && k > s.k0) {
-                        const int pt = it - 1, buf = pt & 1;  // the tile before (`it` counts up below)
-                        if (k == s.k0 + 1 && !(run = wait(o_empty, (seg & 1) ^ 1))) break;
-                        if (!(run = wait(&p_full[buf], (pt >> 1) & 1))) break;
-                        tc_fence_after();
-                        const int valid = min(s.r.L - (k - 1) * BK, BK), nks = (valid + 15) / 16;
-                        const int halves = valid > 64 ? 2 : 1;
-                        for (int h = 0; h < halves && run; ++h)
-                            for (int pc = 0; pc < 2; ++pc) {
-                                if (!(run = wait(&full[slot], phase))) break;
-                                tc_fence_after();
-                                const uint32_t a = lane0(p_lo + (2 * buf + h) * (CHB / 16));
-                                const uint32_t b = lane0(st_lo + slot * (STAGE / 16)) | (CHB / 16) << 16;
-                                const uint32_t d = lane0(tm0 + O_COL + 128 * pc);
-                                const uint32_t old = lane0(k > s.k0 + 1 || h ? 1u : 0u);
-                                if (elect_lane()) {
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        if (4 * h + j >= nks) break;
-                                        umma_pair_f16(d, sw128_desc(a + 2 * j), sw128_desc(b + j * 128), idO,
-                                                      j ? 1u : old);
-                                    }
-                                    umma_pair_commit(&empty[slot]);
-                                    if (h == halves - 1 && pc == 1) umma_pair_commit(&p_empty[buf]);
-                                }
-                                __syncwarp();
-                                next_slot();
-                            }
-                    }
-                    if (k < s.k1) ++it;
                 }
                 f += s.k1 - s.k0;
             }
@@ -639,7 +675,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // After a wait that ran out: the copies in flight are given time to land
     // before the shared memory is let go.
     __syncwarp();
-    if (*abort_flag && warp == W_MMA) {
+    if (*abort_flag && warp == W_S) {
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 1000000ull) {}
     }
@@ -647,7 +683,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    if (warp == W_MMA) tmem_pair_dealloc(tmem, TMEM_COLS);
+    if (warp == W_S) tmem_pair_dealloc(tmem, TMEM_COLS);
 }
 
 // Joins the records of the units cut between pairs.  CTA (c, g): the unit whose
@@ -702,6 +738,35 @@ int box_rows(int block_size) {
     return block_size == 8 ? 8 : block_size % 64 == 0 ? 64 : block_size % 32 == 0 ? 32 : 16;
 }
 
+// Pairs of SMs that run at once.  Not every two SMs are a pair (a cluster lies
+// within one part of the GPU): with a pair for every two of the 152 SMs a few
+// ran after the others and the kernel took twice as long.  Asked once a device.
+int resident_pairs(const void* kernel) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < kDevices && known[dev].load(std::memory_order_relaxed)) return known[dev].load(std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * kPairs);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = smem_bytes(kMaxSeqs);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return kPairs / 2;  // (asked again by the next call)
+    }
+    n = std::min(n, kPairs);
+    if (dev < kDevices) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 template <typename T>
 cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspace, int rec_rows, std::string* err,
                          cudaStream_t stream) {
@@ -730,14 +795,14 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.records = static_cast<float*>(workspace);
     p.rec_rows = rec_rows;
-    // a pair per two SMs, fewer where even the longest contexts give them less
+    // every pair there is, fewer where even the longest contexts give them less
     // than one tile each
     const int64_t units = a.cu ? rows / TM + a.num_seqs : (int64_t)a.num_seqs * ((a.num_heads + TM - 1) / TM);
     const int64_t tiles = units * ((a.max_context + BK - 1) / BK);
-    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>({kPairs, sm_count() / 2, tiles}));
     const void* kfn = reinterpret_cast<const void*>(&latent_umma_kernel<T>);
     cudaError_t e = allow_smem(kfn, smem_bytes(kMaxSeqs));
     if (e != cudaSuccess) return e;
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(resident_pairs(kfn), tiles));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(NTHREADS);
