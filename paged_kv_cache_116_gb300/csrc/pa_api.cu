@@ -1423,7 +1423,7 @@ static pa_status latent_impl(void* out, const void* q, const void* cache, const 
     const int64_t rows = (int64_t)total_q * num_heads;
     if (!tc && num_heads > 4 * 65535) return fail(PA_ERR_UNSUPPORTED, "too many heads");
     if (tc && (rows > INT32_MAX - 128 ||
-               (rows / 128 + num_seqs) * (((int64_t)max_context + 127) / 128) > INT32_MAX))
+               (rows / 128 + num_seqs) * (((int64_t)max_context + 127) / 128 + 8) > INT32_MAX))
         return fail(PA_ERR_UNSUPPORTED, "too many query rows for one call");
     cudaStream_t st = as_stream(stream);
     if (check_mode()) {

@@ -109,10 +109,10 @@ struct Params {
 };
 
 // A request: its first (token, head) row, rows, tokens cached before the new
-// ones, context.
+// ones, context; its row tiles, the key tiles of its context, and b (below).
 struct Request {
-    int64_t row0;
-    int rows, before, L;
+    int64_t row0, b;
+    int rows, before, L, tiles, whole;
 };
 __device__ __forceinline__ Request request(const Params& p, int s) {
     Request r;
@@ -126,38 +126,42 @@ __device__ __forceinline__ Request request(const Params& p, int s) {
     r.row0 = (int64_t)q0 * p.num_heads;
     r.rows = n * p.num_heads;
     r.before = max(r.L - n, 0);
+    r.tiles = (r.rows + TM - 1) / TM;
+    r.whole = (r.L + BK - 1) / BK;
+    r.b = (127 + (int64_t)p.num_heads * (r.before + 128)) >> 7;
     return r;
 }
-// Key tiles of the row tiles before t of a request.  With causal masking tile t
-// ends at row x = 128 t + 127, of token x / H, which sees before + x / H + 1
-// keys: ceil of that by 128 is floor((t + b) / H) with
-// b = floor((127 + H (before + 128)) / 128), so sums over t are closed forms.
-// The last tile sees the whole context.
+// Key tiles of row tile t.  With causal masking tile t ends at row x = 128 t +
+// 127, of token x / H, which sees before + x / H + 1 keys: ceil of that by 128
+// is floor((t + b) / H) with b = floor((127 + H (before + 128)) / 128), so sums
+// over t are closed forms.  The last tile sees the whole context.
+__device__ __forceinline__ int key_tiles(const Params& p, const Request& r, int t) {
+    if (!p.causal || t == r.tiles - 1) return r.whole;
+    const uint64_t x = (uint64_t)(t + r.b);
+    return x >> 32 ? (int)(x / (uint64_t)p.num_heads) : (int)((uint32_t)x / (uint32_t)p.num_heads);
+}
+// A unit (row tile of a request) costs its key tiles and kUnit more: what
+// loading its queries, its first maxima and its output cost in tiles.
+constexpr int kUnit = 2;
 __device__ __forceinline__ int64_t floor_sum(int64_t x, int64_t h) {  // sum of floor(i / h), i < x
     const int64_t q = x / h;
     return h * (q * (q - 1) / 2) + (x - q * h) * q;
 }
-__device__ __forceinline__ int row_tiles(const Request& r) { return (r.rows + TM - 1) / TM; }
-__device__ __forceinline__ int64_t tile_sum(const Params& p, const Request& r, int t) {
-    const int nt = row_tiles(r), whole = (r.L + BK - 1) / BK;
-    if (!p.causal) return (int64_t)t * whole;
-    const int64_t h = p.num_heads, b = (127 + h * (r.before + 128)) / 128;
-    const int64_t u = min(t, nt - 1);
-    return t <= 0 ? 0 : floor_sum(b + u, h) - floor_sum(b, h) + (t == nt ? whole : 0);
-}
-__device__ __forceinline__ int key_tiles(const Params& p, const Request& r, int t) {
-    const int whole = (r.L + BK - 1) / BK;
-    if (!p.causal || t == row_tiles(r) - 1) return whole;
-    const int64_t h = p.num_heads, b = (127 + h * (r.before + 128)) / 128;
-    return (int)((t + b) / h);
+// Cost of a request's units before t.
+__device__ __forceinline__ int64_t cost_before(const Params& p, const Request& r, int t) {
+    if (t <= 0) return 0;
+    if (!p.causal || r.tiles == 1) return (int64_t)t * (r.whole + kUnit);
+    const int64_t u = min(t, r.tiles - 1);
+    return floor_sum(r.b + u, p.num_heads) - floor_sum(r.b, p.num_heads) + (t == r.tiles ? r.whole : 0) +
+           (int64_t)t * kUnit;
 }
 
-// Exclusive prefix of the requests' key tiles, in shared memory (every thread;
+// Exclusive prefix of the requests' costs, in shared memory (every thread;
 // ends with a block barrier).
-__device__ __forceinline__ void tile_prefix(const Params& p, int32_t* prefix) {
+__device__ __forceinline__ void cost_prefix(const Params& p, int32_t* prefix) {
     for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
         const Request r = request(p, s);
-        prefix[s + 1] = (int)tile_sum(p, r, row_tiles(r));
+        prefix[s + 1] = (int)cost_before(p, r, r.tiles);
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
@@ -181,15 +185,35 @@ __device__ __forceinline__ void tile_prefix(const Params& p, int32_t* prefix) {
     __syncthreads();
 }
 
-// A run of key tiles of one unit.
+// The unit at a place of the flat list of costs, and its key tiles [k0, k1) of
+// nk that lie in the run [f0, f1) of a pair: none where the run ends within the
+// unit's own cost.  Walks the units of a run one after the other.
 struct Segment {
-    int req, t;        // request, row tile
-    int k0, k1, nk;    // key tiles [k0, k1) of nk
-    int64_t u0;        // the unit's first flat position
+    int req, t;      // request, row tile
+    int k0, k1, nk;
+    int64_t u0;      // the unit's place
     Request r;
+    __device__ __forceinline__ int64_t end() const { return u0 + kUnit + nk; }
+    // A continuation is its pair's first piece, any other piece that does not
+    // end its unit the pair's last: a record each.
+    __device__ __forceinline__ int slot() const { return k0 ? 0 : 1; }
+    __device__ __forceinline__ void cut(const Params& p, int64_t f0, int64_t f1) {
+        nk = key_tiles(p, r, t);
+        k0 = (int)max(f0 - u0 - kUnit, (int64_t)0);
+        k1 = (int)max(min((int64_t)nk, f1 - u0 - kUnit), (int64_t)0);
+    }
+    // to the unit after this one (before the list's end)
+    __device__ __forceinline__ void next(const Params& p, int64_t f0, int64_t f1) {
+        u0 = end();
+        if (++t >= r.tiles) {
+            t = 0;
+            do r = request(p, ++req);
+            while (r.tiles == 0);
+        }
+        cut(p, f0, f1);
+    }
 };
-// The segment that starts at flat position f and ends at f1 or with its unit.
-__device__ __forceinline__ Segment locate(const Params& p, const int32_t* prefix, int64_t f, int64_t f1) {
+__device__ __forceinline__ Segment locate(const Params& p, const int32_t* prefix, int64_t f, int64_t f0, int64_t f1) {
     Segment s;
     int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {
@@ -200,17 +224,15 @@ __device__ __forceinline__ Segment locate(const Params& p, const int32_t* prefix
     s.req = lo;
     s.r = request(p, lo);
     const int64_t rem = f - prefix[lo];
-    int a = 0, b = row_tiles(s.r) - 1;
+    int a = 0, b = s.r.tiles - 1;
     while (a < b) {
         const int mid = (a + b + 1) >> 1;
-        if (tile_sum(p, s.r, mid) <= rem) a = mid;
+        if (cost_before(p, s.r, mid) <= rem) a = mid;
         else b = mid - 1;
     }
     s.t = a;
-    s.nk = key_tiles(p, s.r, a);
-    s.k0 = (int)(rem - tile_sum(p, s.r, a));
-    s.u0 = f - s.k0;
-    s.k1 = (int)min((int64_t)s.nk, s.k0 + f1 - f);
+    s.u0 = prefix[lo] + cost_before(p, s.r, a);
+    s.cut(p, f0, f1);
     return s;
 }
 
@@ -253,7 +275,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     pdl_wait_primary();
     pdl_launch_dependents();
-    tile_prefix(p, prefix);
+    cost_prefix(p, prefix);
     if (!p.cu) {  // no context: a zero row
         for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
             if (prefix[s + 1] != prefix[s]) continue;
@@ -264,6 +286,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int64_t W = prefix[p.num_seqs], pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int64_t f0 = pair * W / pairs, f1 = (pair + 1) * W / pairs;
     if (f0 == f1) return;  // (both CTAs of the pair)
+    const Segment first = locate(p, prefix, f0, f0, f1);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -339,8 +362,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (other) ring.next();
             return other;
         };
-        for (int64_t f = f0; f < f1 && run; ++seg) {
-            const Segment s = locate(p, prefix, f, f1);
+        for (Segment s = first; run; s.next(p, f0, f1)) {
+            if (s.k1 <= s.k0) break;
             const int32_t* table = p.block_tables + (int64_t)s.req * p.max_blocks;
             const int L = s.r.L;
             // pool row of this lane's box of tile k
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (!values) {
                 // the query rows of this CTA: chunks w, w + NP, ..
                 if (!(run = wait(q_empty, (seg & 1) ^ 1))) break;
-                const int first = s.t * TM + 64 * (int)rank, rows = min(max(s.r.rows - first, 0), 64);
+                const int row = s.t * TM + 64 * (int)rank, rows = min(max(s.r.rows - row, 0), 64);
                 const int boxes = (rows + 15) / 16, chunks = (CH - w + NP - 1) / NP;
                 if (lane == 0) {
                     if (boxes) mbar_arrive_expect_tx_at(q_bar, (uint32_t)(boxes * chunks * 16 * 128));
@@ -362,7 +385,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const int qc = w + NP * (lane / 4), g = lane % 4;
                 if (qc < CH && g < boxes)
                     tma_load_3d_pair(base + Q_OFF + qc * CHB + g * 16 * 128, &tmQ, q_bar, 0, qc,
-                                     (int)(s.r.row0 + first + 16 * g));
+                                     (int)(s.r.row0 + row + 16 * g));
             }
             for (int k = s.k0; k < s.k1 && run; ++k) {
                 const int32_t nxt = box_row(k + 1);
@@ -424,7 +447,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
                 cur = nxt;
             }
-            f += s.k1 - s.k0;
+            ++seg;
+            if (s.end() >= f1) break;
         }
         // every stage handed back, and the last queries read: no arrival is
         // still on its way to this CTA
@@ -443,8 +467,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // operands as lane 0 has them: in uniform registers
             const uint32_t tm0 = lane0(tmem), q_lo = lane0(((sb + Q_OFF) & 0x3ffffu) >> 4 | 1u << 16);
             const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4 | 1u << 16);
-            for (int64_t f = f0; f < f1 && run; ++seg) {
-                const Segment s = locate(p, prefix, f, f1);
+            for (Segment s = first; run; s.next(p, f0, f1)) {
+                if (s.k1 <= s.k0) break;
                 if (!(run = wait(q_full, seg & 1))) break;
                 bool ready = look(&full[ring.slot], ring.phase);
                 for (int k = s.k0; k < s.k1 && run; ++k, ++it) {
@@ -452,19 +476,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const uint32_t d = lane0(tm0 + S_COL + 64 * buf);
                     if (!(run = wait(&s_empty[buf], ((it >> 1) & 1) ^ 1))) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int c0 = 0; c0 < CH; c0 += 2) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < CH; c0 += 2) {  // (short loops: instructions are fetched once)
                         if (!(run = wait_after(&full[ring.slot], ring.phase, ready))) break;
-                        const uint32_t a = q_lo + c0 * (CHB / 16), b = lane0(st_lo + ring.slot * (STAGE / 16));
+                        const uint32_t a = lane0(q_lo + c0 * (CHB / 16)), b = lane0(st_lo + ring.slot * (STAGE / 16));
+                        const uint32_t old = lane0(c0 ? 1u : 0u);
+                        const bool two = c0 + 2 <= CH;
                         uint64_t* done = &empty[ring.slot];
                         ring.next();
                         ready = look(&full[ring.slot], ring.phase);  // (looked at while the MMAs go out)
                         if (elect_lane()) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {
-                                if (c0 + (kk >> 2) >= CH) break;
+                                if (kk == 4 && !two) break;
                                 const uint32_t off = ((kk >> 2) * CHB + (kk & 3) * 32) / 16;
-                                umma_pair_f16(d, sw128_desc(a + off), sw128_desc(b + off), idS, c0 || kk ? 1u : 0u);
+                                umma_pair_f16(d, sw128_desc(a + off), sw128_desc(b + off), idS, kk ? 1u : old);
                             }
                             umma_pair_commit(done);
                             if (c0 + 2 >= CH) {
@@ -475,7 +501,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         __syncwarp();
                     }
                 }
-                f += s.k1 - s.k0;
+                ++seg;
+                if (s.end() >= f1) break;
             }
         }
     } else if (warp == W_O) {
@@ -487,8 +514,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             bool run = true;
             const uint32_t tm0 = lane0(tmem), p_lo = lane0(((sb + P_OFF) & 0x3ffffu) >> 4 | 1u << 16);
             const uint32_t st_lo = lane0(((sb + ST_OFF) & 0x3ffffu) >> 4 | (CHB / 16) << 16);
-            for (int64_t f = f0; f < f1 && run; ++seg) {
-                const Segment s = locate(p, prefix, f, f1);
+            for (Segment s = first; run; s.next(p, f0, f1)) {
+                if (s.k1 <= s.k0) break;
                 if (!(run = wait(o_empty, (seg & 1) ^ 1))) break;
                 for (int k = s.k0; k < s.k1 && run; ++k, ++it) {
                     const int buf = it & 1;
@@ -498,10 +525,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     const int valid = min(s.r.L - k * BK, BK), nks = (valid + 15) / 16;
                     const int halves = valid > 64 ? 2 : 1;
                     for (int h = 0; h < halves && run; ++h)
-#pragma unroll
+#pragma unroll 1
                         for (int pc = 0; pc < 2; ++pc) {
                             if (!(run = wait_after(&full[ring.slot], ring.phase, ready))) break;
-                            const uint32_t a = lane0(p_lo + (2 * buf + h) * (CHB / 16));
+                            const uint32_t a = lane0(p_lo + (2 * buf + h) * (CHB / 16)), d = lane0(tm0 + O_COL + 128 * pc);
                             const uint32_t b = lane0(st_lo + ring.slot * (STAGE / 16));
                             const uint32_t old = lane0(k > s.k0 || h ? 1u : 0u);
                             uint64_t* done = &empty[ring.slot];
@@ -511,8 +538,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     if (4 * h + j >= nks) break;
-                                    umma_pair_f16(tm0 + O_COL + 128 * pc, sw128_desc(a + 2 * j),
-                                                  sw128_desc(b + j * 128), idO, j ? 1u : old);
+                                    umma_pair_f16(d, sw128_desc(a + 2 * j), sw128_desc(b + j * 128), idO, j ? 1u : old);
                                 }
                                 umma_pair_commit(done);
                                 if (h == halves - 1 && pc == 1) umma_pair_commit(&p_empty[buf]);
@@ -520,19 +546,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             __syncwarp();
                         }
                 }
-                f += s.k1 - s.k0;
+                ++seg;
+                if (s.end() >= f1) break;
             }
         }
     } else {
         // ---------------- softmax: row r of this CTA's 64, keys 64 hf .. of each tile
         const int tid = threadIdx.x, hf = warp >> 1, r = (warp & 1) * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
-        const float scale = p.scale_log2;
+        const float scale = p.scale_log2 == 0.f ? 1e-38f : p.scale_log2;  // (0: every score counts alike)
+        const float hidden = scale > 0.f ? -INFINITY : INFINITY;
         const uint32_t s_empty0 = smem_of(s_empty, 0), p_full0 = smem_of(p_full, 0), o_empty0 = smem_of(o_empty, 0);
         int it = 0, seg = 0;
-        bool ok = true, first_seg = true;
-        for (int64_t f = f0; f < f1; ++seg) {
-            const Segment s = locate(p, prefix, f, f1);
+        bool ok = true;
+        for (Segment s = first;; s.next(p, f0, f1)) {
+            if (s.k1 <= s.k0) break;
             const int row = s.t * TM + 64 * (int)rank + r;
             const bool mine = row < s.r.rows;
             const bool some = __any_sync(0xffffffffu, mine);  // (of these 32 rows: the partner warp's too)
@@ -544,88 +572,108 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int k = s.k0; k < s.k1; ++k, ++it) {
                 const int buf = it & 1;
                 const uint32_t turn = (it >> 1) & 1;
-                float x[64];
+                // the scores, and P of two tiles ago read
                 if (ok) ok = wait(&s_full[buf], turn);
-                float mx = -INFINITY;
-                if (!some) {  // rows past the request's: whatever P holds, their O is not stored
-                    if (ok && lane == 0) mbar_arrive_at(s_empty0 + 8 * buf);
-                    ok = bar_all(1, 128, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_at(p_full0 + 8 * buf);
-                    continue;
-                }
-                if (ok) {
-                    tc_fence_after();
-                    float (&xa)[32] = *reinterpret_cast<float (*)[32]>(&x[0]);
-                    float (&xb)[32] = *reinterpret_cast<float (*)[32]>(&x[32]);
-                    tmem_ld32(t_lane + S_COL + 64 * buf, xa);
-                    tmem_ld32(t_lane + S_COL + 64 * buf + 32, xb);
+                if (ok) ok = wait(&p_empty[buf], turn ^ 1);
+                if (ok) tc_fence_after();
+                const int key0 = k * BK + 64 * hf;
+                const bool masked = key0 + 64 > vmin;
+                // this thread's scores 32 c ..; those it may not see end at -inf once scaled
+                auto scores = [&](int c, float (&x)[32]) {
+                    tmem_ld32(t_lane + S_COL + 64 * buf + 32 * c, x);
                     tmem_wait_ld();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(s_empty0 + 8 * buf);
-                    const int key0 = k * BK + 64 * hf;
-                    if (key0 + 64 <= vmin) {
+                    if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] *= scale;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = key0 + i < vis ? x[i] * scale : -INFINITY;
+                        for (int i = 0; i < 32; ++i) x[i] = key0 + 32 * c + i < vis ? x[i] : hidden;
                     }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    xch[buf * 128 + tid] = mx;
-                }
-                // all four warps go on, or none
-                ok = bar_all(1, 128, ok);
-                if (!ok) break;
-                mx = fmaxf(mx, xch[buf * 128 + (tid ^ 64)]);
-                const bool up = mine && (mx > m + 8.f || (m == -INFINITY && mx > m));
-                const float m_new = up ? mx : m, ms = m_new == -INFINITY ? 0.f : m_new;
-                float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t pk[32];
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float a = fast_exp2(x[i] - ms), b = fast_exp2(x[i + 1] - ms);
-                    s4[(i >> 1) & 3] += a + b;
-                    pk[i >> 1] = pack2<T>(a, b);
-                }
-                const float alpha = up ? fast_exp2(m - ms) : 1.f;  // (0 where nothing was seen yet)
-                l = fmaf(l, alpha, (s4[0] + s4[1]) + (s4[2] + s4[3]));
-                m = m_new;
-                // P of two tiles ago has been read
-                ok = wait(&p_empty[buf], turn ^ 1);
-                if (ok) {
-                    const uint32_t dst = sb + P_OFF + (2 * buf + hf) * CHB + r * 128;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((j ^ (r & 7)) << 4)),
-                                     "r"(pk[4 * j]), "r"(pk[4 * j + 1]), "r"(pk[4 * j + 2]), "r"(pk[4 * j + 3])
-                                     : "memory");
-                    fence_proxy_async_smem();
-                    if (k > s.k0 && __any_sync(0xffffffffu, up)) {
-                        // O holds the tiles before this one
-                        ok = wait(&p_empty[buf ^ 1], ((it - 1) >> 1) & 1);
-                        if (ok) {
-                            tc_fence_after();
+                };
+                // P is taken against the row's reference as it stands: a sum of
+                // at most 2^8 proves that no score is more than 8 above it.
+                // Otherwise (and on a segment's first tile) the partners swap
+                // their maxima, the reference moves, and P is taken again.
+                bool move = k == s.k0;
+                float alpha = 1.f, sum = 0.f;
+                while (true) {
+                    if (move) {
+                        float mx = -INFINITY;
+                        if (ok && some) {
 #pragma unroll 1
-                            for (int c = 0; c < 256; c += 32) {
-                                float o[32];
-                                tmem_ld32(t_lane + O_COL + c, o);
-                                tmem_wait_ld();
+                            for (int c = 0; c < 2; ++c) {
+                                float x[32];
+                                scores(c, x);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= alpha;
-                                tmem_st32(t_lane + O_COL + c, o);
+                                for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i] * scale);
                             }
-                            tmem_wait_st();
+                        }
+                        xch[buf * 128 + tid] = mx;
+                        ok = bar_all(1, 128, ok);  // all four warps go on, or none
+                        if (!ok) break;
+                        mx = fmaxf(mx, xch[buf * 128 + (tid ^ 64)]);
+                        if (mine && (mx > m + 8.f || (m == -INFINITY && mx > m))) {
+                            alpha = fast_exp2(m - mx);  // (0 where nothing was seen yet)
+                            m = mx;
                         }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (ok && lane == 0) mbar_arrive_at(p_full0 + 8 * buf);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    if (ok && some) {
+                        const unsigned long long sc2 = f32x2_pack(scale, scale), off2 = f32x2_pack(-ms, -ms);
+                        unsigned long long sum2 = 0ull;
+                        uint32_t dst = sb + P_OFF + (2 * buf + hf) * CHB + r * 128, piece = r & 7;
+#pragma unroll 1
+                        for (int c = 0; c < 2; ++c, piece ^= 4) {
+                            float x[32];
+                            scores(c, x);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t pk[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    float a, b;
+                                    const int i = 8 * j + 2 * e;
+                                    f32x2_unpack(fma_f32x2(f32x2_pack(x[i], x[i + 1]), sc2, off2), a, b);
+                                    a = fast_exp2(a);
+                                    b = fast_exp2(b);
+                                    sum2 = add_f32x2(sum2, f32x2_pack(a, b));
+                                    pk[e] = pack2<T>(a, b);
+                                }
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((piece ^ j) << 4)),
+                                             "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                                             : "memory");
+                            }
+                        }
+                        float sa, sb2;
+                        f32x2_unpack(sum2, sa, sb2);
+                        sum = sa + sb2;
+                    }
+                    if (move || bar_all(1, 128, ok && (!mine || (sum <= 256.f && m != -INFINITY)))) break;
+                    move = true;
                 }
+                if (!ok) break;
+                l = fmaf(l, alpha, sum);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(s_empty0 + 8 * buf);
+                fence_proxy_async_smem();
+                if (k > s.k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // O holds the tiles before this one
+                    ok = wait(&p_empty[buf ^ 1], ((it - 1) >> 1) & 1);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            float o[32];
+                            tmem_ld32(t_lane + O_COL + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+                            tmem_st32(t_lane + O_COL + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive_at(p_full0 + 8 * buf);
             }
             // the segment's last product
             if (ok) ok = wait(&p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
@@ -637,7 +685,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const bool whole = s.k0 == 0 && s.k1 == s.nk;
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
             T* orow = static_cast<T*>(p.out) + (s.r.row0 + row) * LAT + 256 * hf;
-            float* rec = p.records + ((2 * pair + (first_seg ? 0 : 1)) * p.rec_rows + 64 * (int)rank + r) * (int64_t)REC;
+            float* rec = p.records + ((2 * pair + s.slot()) * p.rec_rows + 64 * (int)rank + r) * (int64_t)REC;
             if (mine && !whole && hf == 0) {
                 rec[LAT] = m;
                 rec[LAT + 1] = l;
@@ -667,8 +715,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_at(o_empty0);
-            first_seg = false;
-            f += s.k1 - s.k0;
+            ++seg;
+            if (s.end() >= f1) break;
         }
     }
 
@@ -691,15 +739,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 template <typename T>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int pairs) {
     extern __shared__ int32_t mprefix[];
-    tile_prefix(p, mprefix);
+    cost_prefix(p, mprefix);
     const int64_t W = mprefix[p.num_seqs], c = blockIdx.x;
     const int64_t f0 = c * W / pairs, f1 = (c + 1) * W / pairs;
     pdl_wait_primary();  // (the lengths are older than the grid before this one)
     pdl_launch_dependents();
     if (f0 == f1 || f1 == W) return;
-    const Segment s = locate(p, mprefix, f1 - 1, f1);
-    const int64_t u1 = s.u0 + s.nk;
-    if (u1 <= f1 || s.u0 < f0) return;  // ends here, or began before
+    const Segment s = locate(p, mprefix, f1 - 1, f0, f1);
+    const int64_t u1 = s.end();
+    if (u1 <= f1 || s.k0 > 0 || s.k1 == 0) return;  // ends here, began before, or begins after
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= p.rec_rows || s.t * TM + row >= s.r.rows) return;
     const int64_t last = (u1 * pairs + W - 1) / W - 1;  // the pair owning position u1 - 1
@@ -707,7 +755,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int p
     float4 o[4] = {};
     for (int64_t q = c; q <= last; ++q) {
         if (q * W / pairs == (q + 1) * W / pairs) continue;  // an empty run
-        const float* rec = p.records + ((2 * q + (q == c && s.u0 != f0 ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
+        const float* rec = p.records + ((2 * q + (q == c ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
         const float m = __ldcg(rec + LAT), lq = __ldcg(rec + LAT + 1);
         float4 a[4];
 #pragma unroll
