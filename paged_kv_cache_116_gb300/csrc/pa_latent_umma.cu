@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // A whole warp's bounded wait, with one answer for all lanes (every lane
     // polls: one lane's polls and a shuffle were slower).  `ready`: what an
     // earlier look told this lane.
-    auto look = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_try_wait(bar, parity); };
+    auto look = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_test(bar, parity); };
     auto wait_after = [&](uint64_t* bar, uint32_t parity, bool ready) -> bool {
         if (__all_sync(0xffffffffu, ready)) return true;
         const uint64_t t0 = global_ns();
