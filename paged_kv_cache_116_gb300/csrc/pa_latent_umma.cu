@@ -142,7 +142,7 @@ __device__ __forceinline__ int key_tiles(const Params& p, const Request& r, int 
 }
 // A unit (row tile of a request) costs its key tiles and kUnit more: what
 // loading its queries, its first maxima and its output cost in tiles.
-constexpr int kUnit = 2;
+constexpr int kUnit = 3;
 __device__ __forceinline__ int64_t floor_sum(int64_t x, int64_t h) {  // sum of floor(i / h), i < x
     const int64_t q = x / h;
     return h * (q * (q - 1) / 2) + (x - q * h) * q;
@@ -684,32 +684,63 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             l += xch[(it & 1) * 128 + (tid ^ 64)];
             const bool whole = s.k0 == 0 && s.k1 == s.nk;
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            T* orow = static_cast<T*>(p.out) + (s.r.row0 + row) * LAT + 256 * hf;
-            float* rec = p.records + ((2 * pair + s.slot()) * p.rec_rows + 64 * (int)rank + r) * (int64_t)REC;
-            if (mine && !whole && hf == 0) {
-                rec[LAT] = m;
-                rec[LAT + 1] = l;
-            }
-            rec += 256 * hf;
+            // The rows go out through P's place, 8 KB a warp (P of this segment
+            // is read, and the next segment's first tile has a barrier of the
+            // four warps before P): written a row per lane, 16 of 16 bytes at a
+            // time, they are stored 256 bytes of a row together.  Stored
+            // straight from the lanes a tile took 9,500 cycles.
+            const int row0 = row - lane, rows = min(max(s.r.rows - row0, 0), 32);  // of this warp
+            uint8_t* stage = base + P_OFF + warp * CHB;
+            const int half = lane >> 4, u = lane & 15;
+            if (whole) {
+                T* o0 = static_cast<T*>(p.out) + (s.r.row0 + row0) * LAT + 256 * hf;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-                float o[32];
-                tmem_ld32(t_lane + O_COL + c, o);
-                tmem_wait_ld();
-                if (!mine) continue;
-                if (whole) {
+                for (int c = 0; c < 256; c += 128) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        tmem_ld32(t_lane + O_COL + c + 32 * q, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4*>(orow + c + 8 * j) =
-                            make_uint4(pack2<T>(o[8 * j] * inv, o[8 * j + 1] * inv),
-                                       pack2<T>(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                                       pack2<T>(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                                       pack2<T>(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
-                } else {
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * q + j) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack2<T>(o[8 * j] * inv, o[8 * j + 1] * inv),
+                                           pack2<T>(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                           pack2<T>(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                                           pack2<T>(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = half; i < rows; i += 2)
+                        *reinterpret_cast<uint4*>(o0 + (int64_t)i * LAT + c + 8 * u) =
+                            *reinterpret_cast<const uint4*>(stage + i * 256 + ((u ^ (i & 7)) << 4));
+                    __syncwarp();
+                }
+            } else {
+                float* rec = p.records + ((2 * pair + s.slot()) * p.rec_rows + (row0 - s.t * TM)) * (int64_t)REC;
+                if (mine && hf == 0) {
+                    rec[(int64_t)lane * REC + LAT] = m;
+                    rec[(int64_t)lane * REC + LAT + 1] = l;
+                }
+                rec += 256 * hf;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 64) {
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        float o[32];
+                        tmem_ld32(t_lane + O_COL + c + 32 * q, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4*>(rec + c + 4 * j) =
-                            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(stage + lane * 256 + (((8 * q + j) ^ (lane & 7)) << 4)) =
+                                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = half; i < rows; i += 2)
+                        *reinterpret_cast<float4*>(rec + (int64_t)i * REC + c + 4 * u) =
+                            *reinterpret_cast<const float4*>(stage + i * 256 + ((u ^ (i & 7)) << 4));
+                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -753,22 +784,39 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int p
     const int64_t last = (u1 * pairs + W - 1) / W - 1;  // the pair owning position u1 - 1
     float M = -INFINITY, l = 0.f;
     float4 o[4] = {};
-    for (int64_t q = c; q <= last; ++q) {
-        if (q * W / pairs == (q + 1) * W / pairs) continue;  // an empty run
-        const float* rec = p.records + ((2 * q + (q == c ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
-        const float m = __ldcg(rec + LAT), lq = __ldcg(rec + LAT + 1);
-        float4 a[4];
+    constexpr int B = 4;  // records in flight
+    for (int64_t q0 = c; q0 <= last; q0 += B) {
+        float m[B], lq[B];
+        float4 a[B][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane);
-        const float mn = fmaxf(M, m), ms = mn == -INFINITY ? 0.f : mn;
-        const float e0 = exp2f(M - ms), e1 = exp2f(m - ms);
-        l = l * e0 + lq * e1;
+        for (int k = 0; k < B; ++k) {
+            const int64_t q = q0 + k;
+            const bool there = q <= last && q * W / pairs != (q + 1) * W / pairs;  // (an empty run has none)
+            const float* rec = p.records + ((2 * q + (q == c ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
+            m[k] = there ? __ldcg(rec + LAT) : -INFINITY;
+            lq[k] = there ? __ldcg(rec + LAT + 1) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[i].x = o[i].x * e0 + a[i].x * e1;
-            o[i].y = o[i].y * e0 + a[i].y * e1;
-            o[i].z = o[i].z * e0 + a[i].z * e1;
-            o[i].w = o[i].w * e0 + a[i].w * e1;
+            for (int i = 0; i < 4; ++i)
+                a[k][i] = there ? __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < B; ++k) mn = fmaxf(mn, m[k]);
+        const float ms = mn == -INFINITY ? 0.f : mn, e0 = exp2f(M - ms);
+        l *= e0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = make_float4(o[i].x * e0, o[i].y * e0, o[i].z * e0, o[i].w * e0);
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const float e = exp2f(m[k] - ms);
+            l = fmaf(lq[k], e, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i].x = fmaf(a[k][i].x, e, o[i].x);
+                o[i].y = fmaf(a[k][i].y, e, o[i].y);
+                o[i].z = fmaf(a[k][i].z, e, o[i].z);
+                o[i].w = fmaf(a[k][i].w, e, o[i].w);
+            }
         }
         M = mn;
     }
