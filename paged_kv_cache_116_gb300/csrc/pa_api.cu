@@ -265,7 +265,8 @@ pa_status pa_device_status(int clear) {
     const uint32_t bits =
         pa::decode_tc_status(clear != 0) | pa::decode_weights_status(clear != 0) |
                           pa::varlen_umma_status(clear != 0) | pa::weights_umma_status(clear != 0) |
-                          pa::latent_umma_status(clear != 0) |
+                          pa::latent_umma_status(clear != 0) | pa::prefix_umma_status(clear != 0) |
+                          pa::decode_shared_status(clear != 0) |
                           pa::selftest_status(clear != 0);
     if (bits & 1u) return fail(PA_ERR_TIMEOUT, "a kernel's bounded barrier wait ran out");
     return PA_OK;
@@ -1514,6 +1515,24 @@ pa_status pa_latent_varlen(void* out, const void* q, const void* cache, const in
 
 // ------------------------------------------------------------------ shared prefixes
 
+// Whether a call works its prefixes apart, and what it then needs.
+static bool shares_prefixes(int32_t num_seqs, int32_t num_groups, int32_t num_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t block_size, int32_t max_context, int dtype) {
+    const int G = num_heads / num_kv_heads;
+    if (g_options[PA_OPT_DECODE_KERNEL] == 1 ||
+        !pa::decode_shared_supported(dtype, head_dim, block_size, G, num_seqs, num_groups, max_context))
+        return false;
+    // the units' costs are counted in int32
+    const double units = ((double)num_seqs * G / 128 + num_groups) * 2 * num_kv_heads;
+    return units * (max_context / 128 + 4.0) < 2e9;
+}
+static size_t shared_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t max_context, int dtype) {
+    const int grid = pa::decode_shared_grid(num_seqs, num_kv_heads, head_dim, max_context, dtype,
+                                            num_heads / num_kv_heads, g_options[PA_OPT_DECODE_CTAS]);
+    return pa::decode_shared_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, grid);
+}
+
 // Check-mode validation of the groups: their ranges, whole blocks, within the
 // members' contexts, one run of blocks for all members.
 static pa_status check_groups(const int32_t* group_starts, const int32_t* prefix_lens, int32_t num_groups,
@@ -1548,8 +1567,12 @@ extern "C" {
 
 size_t pa_decode_shared_workspace_size(int32_t num_seqs, int32_t num_groups, int32_t num_heads, int32_t num_kv_heads,
                                        int32_t head_dim, int32_t block_size, int32_t max_context, int dtype) {
-    (void)num_groups;
-    return decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, false);
+    const size_t plain =
+        decode_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype, false);
+    if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || block_size <= 0 ||
+        !shares_prefixes(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype))
+        return plain;
+    return std::max(plain, shared_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype));
 }
 
 pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1568,6 +1591,28 @@ pa_status pa_decode_shared(void* out, const void* q, const void* k_cache, const 
             err = check_groups(group_starts, prefix_lens, num_groups, block_tables, max_blocks, context_lens, num_seqs,
                                block_size, as_stream(stream));
         if (err != PA_OK) return err;
+    }
+    if (num_heads > 0 && num_kv_heads > 0 && block_size > 0 && num_seqs > 0 &&
+        shares_prefixes(num_seqs, num_groups, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype)) {
+        pa::AttnArgs a{};
+        cudaStream_t st = as_stream(stream);
+        pa_status g = decode_args(a, out, q, nullptr, nullptr, k_cache, v_cache, nullptr, nullptr, block_tables,
+                                  max_blocks, context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks,
+                                  block_size, max_context, scale, dtype, st);
+        if (g != PA_OK) return g;
+        const size_t need = shared_workspace(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context, dtype);
+        if (workspace_bytes < need || !workspace)
+            return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace ? workspace_bytes : 0) +
+                                              " bytes, " + std::to_string(need) + " needed");
+        if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+        const int grid = pa::decode_shared_grid(num_seqs, num_kv_heads, head_dim, max_context, dtype,
+                                                num_heads / num_kv_heads, g_options[PA_OPT_DECODE_CTAS]);
+        std::string err;
+        cudaError_t e =
+            pa::launch_decode_shared(a, group_starts, prefix_lens, num_groups, num_blocks, grid, workspace, &err, st);
+        if (e != cudaSuccess)
+            return err.empty() ? cuda_fail(e, "pa_decode_shared launch") : fail(PA_ERR_CUDA, "pa_decode_shared: " + err);
+        return PA_OK;
     }
     return decode_impl(out, q, nullptr, nullptr, k_cache, v_cache, nullptr, nullptr, block_tables, max_blocks,
                        context_lens, num_seqs, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_context,

@@ -116,6 +116,8 @@ struct TcParams {
     // (maximum, 1 / sum) of units worked whole at row_stats[s * num_heads + head]
     float* scores;
     float2* row_stats;
+    // PART instances: records of units worked whole, [num_seqs * num_heads][HD + 4]
+    float* rows;
 };
 
 // Warps per CTA, stages per warp, 16-token tiles per stage, and CTAs per SM
@@ -220,7 +222,9 @@ __host__ __device__ constexpr bool tma_block_size(int bs) { return bs == 8 || (b
 // brought there by the power of two that puts its largest element into
 // [2^14, 2^15) (exact for elements down to 2^-28 of the largest, nothing
 // leaves f16's range), which the fp32 scores are divided by.
-template <typename T, int HD, int NT, bool FP8, bool PAIR, bool GATHER = false, bool SCORES = false>
+// PART (pa_decode_shared.cu): nothing goes to out; a unit worked whole leaves its
+// state, as a record's, in its query rows' records.
+template <typename T, int HD, int NT, bool FP8, bool PAIR, bool GATHER = false, bool SCORES = false, bool PART = false>
 __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const TcParams p) {
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
     const int64_t W = (int64_t)prefix[S] * Hkv;
     // sequences with no context get a zero row (and nothing to merge)
     for (int s = blockIdx.x; s < S; s += gridDim.x) {
-        if (prefix[s + 1] == prefix[s]) {
+        if (!PART && prefix[s + 1] == prefix[s]) {
             T* o = static_cast<T*>(p.out) + (int64_t)s * p.num_heads * HD;
             for (int e = threadIdx.x; e < p.num_heads * HD; e += blockDim.x) o[e] = Elt<T>::from_f(0.f);
         }
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
                 lt[nt][e] = l;
             }
         const bool complete = (seg_b0 == 0 && bend == nb);
-        if (complete) {
+        if (!PART && complete) {
             T* out = static_cast<T*>(p.out) + ((int64_t)cs * p.num_heads + (int64_t)ch * G) * HD;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -576,6 +580,7 @@ __global__ void __launch_bounds__(Pipe<HD, FP8>::NW * 32, Pipe<HD, FP8>::MINB)
             // last); decode_merge_kernel combines the pieces after this grid
             const int slot = first_seg ? 0 : 1;
             float* rec = p.ws_part + (gw * 2 + slot) * (int64_t)G * (HD + 4);
+            if (PART && complete) rec = p.rows + ((int64_t)cs * p.num_heads + (int64_t)ch * G) * (HD + 4);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1413,6 +1418,7 @@ cudaError_t launch_typed(const AttnArgs& a, int32_t num_blocks, int grid, void* 
     p.v_scales = a.v_scales;
     p.scores = SCORES ? weights->scores : nullptr;
     p.row_stats = SCORES ? weights->row_stats : nullptr;
+    p.rows = nullptr;
 
     const void* kfn = kernel_ptr<T, HD, NT, FP8, PAIR, GATHER, SCORES>();
     const size_t smem = smem_bytes<HD, FP8>(a.num_seqs);

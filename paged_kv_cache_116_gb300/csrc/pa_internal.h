@@ -357,6 +357,24 @@ cudaError_t launch_latent_umma(const LatentArgs& a, int32_t num_blocks, void* wo
                                cudaStream_t stream);
 uint32_t latent_umma_status(bool clear);
 
+// ---- decode of shared prefixes (pa_prefix_umma.cu, pa_decode_shared.cu)
+struct SharedGroups;  // pa_shared.cuh
+cudaError_t launch_prefix_umma(const AttnArgs& a, const SharedGroups& g, int32_t num_blocks, int ctas,
+                               std::string* err, cudaStream_t stream);
+uint32_t prefix_umma_status(bool clear);
+// Whether the prefixes are worked apart (otherwise the call is the plain decode).
+bool decode_shared_supported(int dtype, int head_dim, int block_size, int group, int32_t num_seqs, int32_t num_groups,
+                             int32_t max_context);
+// Bytes beside the plain decode's workspace for `grid_ctas`.
+size_t decode_shared_workspace(int32_t num_seqs, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                               int32_t block_size, int32_t max_context, int grid_ctas);
+int decode_shared_grid(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t max_context, int dtype,
+                       int32_t group, int64_t ctas_override);
+cudaError_t launch_decode_shared(const AttnArgs& a, const int32_t* group_starts, const int32_t* prefix_lens,
+                                 int32_t num_groups, int32_t num_blocks, int grid_ctas, void* workspace,
+                                 std::string* err, cudaStream_t stream);
+uint32_t decode_shared_status(bool clear);
+
 // SMs of the current device.
 int sm_count();
 
