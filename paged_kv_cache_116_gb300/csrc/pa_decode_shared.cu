@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const TcParams p, con
     int32_t* gcost = sm + p.num_seqs + 1;      // [groups + 1]
     constexpr int E = HD / 16, REC = HD + 4;
     const int S = p.num_seqs, Hkv = p.num_kv_heads, G = p.group;
-    // (the plan is older than the grid before this one)
+    // (the plan is older than the two grids before this one)
     tile_prefix(p.context_lens, S, rest, nullptr);
     shared_prefix(g, gcost);
     const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -184,9 +184,6 @@ cudaError_t launch_part(const AttnArgs& a, const SharedGroups& g, int32_t num_bl
     cudaError_t e = launch_pdl(shared_plan_kernel, dim3((unsigned)a.num_seqs), dim3(128), stream, g, a.seq_lens,
                                a.block_tables, a.max_blocks, lens, tables, sp.rest_blocks, group_of);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(kSms, sm_count());
-    e = launch_prefix_umma(a, g, num_blocks, ctas, err, stream);
-    if (e != cudaSuccess) return e;
     TcParams p{};
     p.out = a.out;
     p.q = a.q;
@@ -209,6 +206,9 @@ cudaError_t launch_part(const AttnArgs& a, const SharedGroups& g, int32_t num_bl
     using Pp = Pipe<HD, false>;
     e = launch_pdl_smem(kernel, dim3((unsigned)grid), dim3(Pp::NW * 32), smem_bytes<HD, false>(a.num_seqs), stream,
                         tmK, tmV, p);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(kSms, sm_count());
+    e = launch_prefix_umma(a, g, num_blocks, ctas, err, stream);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.num_seqs * a.num_heads;
     return launch_pdl_smem(shared_merge_kernel<T, HD>, dim3((unsigned)((rows + 15) / 16)), dim3(256),

@@ -773,8 +773,10 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int p
     cost_prefix(p, mprefix);
     const int64_t W = mprefix[p.num_seqs], c = blockIdx.x;
     const int64_t f0 = c * W / pairs, f1 = (c + 1) * W / pairs;
-    pdl_wait_primary();  // (the lengths are older than the grid before this one)
+    // (the lengths are older than the grid before this one; the kernel behind
+    // this one waits for it only, so one CTA always waits)
     pdl_launch_dependents();
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_primary();
     if (f0 == f1 || f1 == W) return;
     const Segment s = locate(p, mprefix, f1 - 1, f0, f1);
     const int64_t u1 = s.end();
@@ -782,6 +784,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int p
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= p.rec_rows || s.t * TM + row >= s.r.rows) return;
     const int64_t last = (u1 * pairs + W - 1) / W - 1;  // the pair owning position u1 - 1
+    pdl_wait_primary();
     float M = -INFINITY, l = 0.f;
     float4 o[4] = {};
     constexpr int B = 4;  // records in flight

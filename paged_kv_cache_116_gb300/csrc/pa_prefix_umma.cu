@@ -180,12 +180,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
-    pdl_wait_primary();
+    // Launched behind the decode of the rests, whose output this kernel does not
+    // read: it starts on each SM as the decode leaves it.  Its inputs are older
+    // than that grid, which waited for the grids before it.  The join behind
+    // waits for this grid only, so one CTA waits for the decode at its end.
     pdl_launch_dependents();
     shared_prefix(p.g, prefix);
     const int64_t W = prefix[p.g.groups], C = gridDim.x;
     const int64_t f0 = blockIdx.x * W / C, f1 = (blockIdx.x + 1) * W / C;
-    if (f0 == f1) return;
+    if (f0 == f1) {
+        if (blockIdx.x == 0) pdl_wait_primary();
+        return;
+    }
     const Segment first = locate(p, prefix, f0, f1);
 
     if (threadIdx.x == 0) {
@@ -515,6 +521,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 rec[HD + 1] = l;
             }
             if (n > 0) {
+                float* out[8];  // of rows lane / 8, + 4, ..
+#pragma unroll
+                for (int i = 0; i < 8; ++i) out[i] = record(min((lane >> 3) + 4 * i, n - 1)) + 4 * (lane & 7);
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     float o[32];
@@ -525,9 +534,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                             make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     __syncwarp();
-                    for (int i = lane >> 3; i < n; i += 4)
-                        *reinterpret_cast<float4*>(record(i) + c + 4 * (lane & 7)) =
-                            *reinterpret_cast<const float4*>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = (lane >> 3) + 4 * i;
+                        if (row < n)
+                            *reinterpret_cast<float4*>(out[i] + c) =
+                                *reinterpret_cast<const float4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+                    }
                     __syncwarp();
                 }
             }
@@ -543,6 +556,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == W_S) tmem_dealloc(tmem, TMEM_COLS);
+    if (blockIdx.x == 0) pdl_wait_primary();
 }
 
 // ---------------------------------------------------------------- host side
