@@ -757,10 +757,14 @@ PA_API pa_status pa_latent_varlen(void* out, const void* q, const void* cache, c
  *                 blocks
  *   workspace:    pa_decode_shared_workspace_size(...) bytes, 16-byte aligned;
  *                 its content on entry does not matter
- * num_groups == 0 is pa_decode.  The other arguments, the error behaviour and
- * PA_OPT_DECODE_KERNEL are pa_decode's.  Where pa_decode runs on the CUDA
- * cores (and for block sizes that no TMA box fits) nothing is shared and the
- * call is pa_decode.
+ * num_groups == 0 is pa_decode, and so is a call with little to save: the bytes
+ * that (num_seqs - num_groups) sequences of max_context tokens would read
+ * again are compared with what the additional launches cost.
+ * PA_OPT_DECODE_KERNEL = 2 always works the prefixes apart where the kernels
+ * apply; the other arguments, the error behaviour and that option's other
+ * values are pa_decode's.  Where pa_decode runs on the CUDA cores, for block
+ * sizes that no TMA box fits and for more than 4,096 sequences nothing is
+ * shared either.
  */
 PA_API size_t pa_decode_shared_workspace_size(int32_t num_seqs, int32_t num_groups, int32_t num_heads,
                                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,

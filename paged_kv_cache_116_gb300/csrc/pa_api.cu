@@ -1515,13 +1515,24 @@ pa_status pa_latent_varlen(void* out, const void* q, const void* cache, const in
 
 // ------------------------------------------------------------------ shared prefixes
 
-// Whether a call works its prefixes apart, and what it then needs.
+// Whether a call works its prefixes apart.  That takes three launches more, 12
+// to 20 us, so there has to be something to save: the members beyond one a
+// group would read their prefixes again, which the host can bound by
+// max_context.  Measured on 55 batches (1-60 groups of 2-64 members, prefixes
+// of 144-8,192 tokens, five head layouts): with 13-70 MB to save 25-47 us
+// against 17-46 us by the plain decode, 200-290 MB 34-84 against 35-90, from
+// 345 MB on 34-153 against 45-567 (one exception: 60 x 4 members behind 288
+// tokens with tails of 256, 78 against 71).  PA_OPT_DECODE_KERNEL = 2 always
+// works them apart.
+static constexpr double kSharedMinBytes = 192e6;
 static bool shares_prefixes(int32_t num_seqs, int32_t num_groups, int32_t num_heads, int32_t num_kv_heads,
                             int32_t head_dim, int32_t block_size, int32_t max_context, int dtype) {
     const int G = num_heads / num_kv_heads;
-    if (g_options[PA_OPT_DECODE_KERNEL] == 1 ||
-        !pa::decode_shared_supported(dtype, head_dim, block_size, G, num_seqs, num_groups, max_context))
+    const int64_t want = g_options[PA_OPT_DECODE_KERNEL];
+    if (want == 1 || !pa::decode_shared_supported(dtype, head_dim, block_size, G, num_seqs, num_groups, max_context))
         return false;
+    const double saved = ((double)num_seqs - num_groups) * max_context * num_kv_heads * head_dim * 4;
+    if (want != 2 && saved < kSharedMinBytes) return false;
     // the units' costs are counted in int32
     const double units = ((double)num_seqs * G / 128 + num_groups) * 2 * num_kv_heads;
     return units * (max_context / 128 + 4.0) < 2e9;

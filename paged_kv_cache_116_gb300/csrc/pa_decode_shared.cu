@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(128) shared_plan_kernel(const SharedGroups g, 
 // Half a warp per (sequence, query head): its records in order, B at a time.
 template <typename T, int HD, int B = HD <= 128 ? 8 : 4>
 __global__ void __launch_bounds__(256) shared_merge_kernel(const TcParams p, const int64_t TW, const SharedGroups g,
-                                                           const int32_t* group_of, const int64_t C) {
+                                                           const int32_t* group_of, const int ctas) {
     extern __shared__ int32_t sm[];
     int32_t* rest = sm;                        // [num_seqs + 1] 16-token tiles of the rests
     int32_t* gcost = sm + p.num_seqs + 1;      // [groups + 1]
@@ -56,52 +56,51 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const TcParams p, con
     // (the plan is older than the two grids before this one)
     tile_prefix(p.context_lens, S, rest, nullptr);
     shared_prefix(g, gcost);
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int hl = threadIdx.x & 15;
-    const bool mine = row < (int64_t)S * p.num_heads;
-    const int s = mine ? (int)(row / p.num_heads) : 0, hq = mine ? (int)(row - (int64_t)s * p.num_heads) : 0;
+    const int row = blockIdx.x * 16 + (threadIdx.x >> 4), hl = threadIdx.x & 15;
+    const bool mine = row < S * p.num_heads;
+    const int s = mine ? row / p.num_heads : 0, hq = mine ? row - s * p.num_heads : 0;
     const int kv = hq / G, j = hq - kv * G;
     // the prefix's pieces: the row's own record, then those of the CTAs behind
-    int64_t np = 0, c0 = 0;
-    int tile_row = 0;
-    const int64_t WP = gcost[g.groups];
+    int np = 0, c0 = 0, tile_row = 0;
     const int grp = group_of[s];
     if (grp >= 0) {
+        const int64_t WP = gcost[g.groups], C = shared_ctas(WP, ctas);
         const int nk = (shared_tokens(g, grp) + kPrefixKeys - 1) / kPrefixKeys, at = s - g.starts[grp];
         const int t = at / g.tokens, unit = kv * shared_row_tiles(g, grp) + t;
         const int64_t u0 = gcost[grp] + (int64_t)unit * (nk + kPrefixUnit) + kPrefixUnit;  // its first key tile
-        c0 = ((u0 + 1) * C + WP - 1) / WP - 1;
-        np = ((u0 + nk) * C + WP - 1) / WP - c0;
+        c0 = (int)(((u0 + 1) * C + WP - 1) / WP) - 1;
+        np = (int)(((u0 + nk) * C + WP - 1) / WP) - c0;
         tile_row = (at - t * g.tokens) * G + j;
     }
-    // the rest's pieces: warps wf .. of the decode
+    // the rest's pieces: warps wf .. of the decode, or (fewer tiles than warps:
+    // a warp has one or none) the owners of its tiles one by one
     const int nb = rest[s + 1] - rest[s];
     const int64_t W = (int64_t)rest[S] * Hkv, u0 = (int64_t)rest[s] * Hkv + (int64_t)kv * nb;
-    int64_t wf = 0, nw = 0;
-    int slot0 = 0;
+    const bool sparse = W < TW;
+    auto owner = [&](int64_t f) -> int {
+        const int64_t x = (f + 1) * TW + W - 1;
+        return (x >> 32 ? (int)(x / W) : (int)((uint32_t)x / (uint32_t)W)) - 1;
+    };
+    int wf = 0, nw = 0, slot0 = 0;
     if (nb > 0) {
-        wf = ((u0 + 1) * TW + W - 1) / W - 1;
-        nw = ((u0 + nb) * TW + W - 1) / W - wf;
+        wf = owner(u0);
+        nw = sparse ? nb : owner(u0 + nb - 1) - wf + 1;
         slot0 = u0 == wf * W / TW ? 0 : 1;
     }
-    auto record = [&](int64_t i) -> const float* {
-        if (i < np) {
-            if (i == 0) return g.rows + row * REC;
-            const int64_t c = c0 + i;
-            return WP < C && c * WP / C == (c + 1) * WP / C ? nullptr : g.cont + (c * 128 + tile_row) * REC;
-        }
-        const int64_t w = wf + i - np;
-        if (nw == 1) return p.rows + row * REC;
-        if (W < TW && w * W / TW == (w + 1) * W / TW) return nullptr;  // an empty range
-        return p.ws_part + ((w * 2 + (w == wf ? slot0 : 0)) * (int64_t)G + j) * REC;
+    auto record = [&](int i) -> const float* {
+        if (i < np) return i == 0 ? g.rows + (int64_t)row * REC : g.cont + ((int64_t)(c0 + i) * 128 + tile_row) * REC;
+        i -= np;
+        if (nw == 1) return p.rows + (int64_t)row * REC;
+        const int w = sparse ? owner(u0 + i) : wf + i;
+        return p.ws_part + (((int64_t)w * 2 + (i == 0 ? slot0 : 0)) * G + j) * REC;
     };
     pdl_wait_primary();
     if (!mine) return;
-    const int64_t n = np + nw;
+    const int n = np + nw;
     float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
     for (int t = 0; t < E; ++t) o[t] = 0.f;
-    for (int64_t i0 = 0; i0 < n; i0 += B) {
+    for (int i0 = 0; i0 < n; i0 += B) {
         float m[B], l[B];
         float4 a[B][E / 4];
 #pragma unroll
@@ -135,7 +134,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const TcParams p, con
         M = mn;
     }
     const float inv = n > 0 ? 1.f / L : 0.f;  // (no context: a zero row)
-    T* out = static_cast<T*>(p.out) + row * HD + hl * E;
+    T* out = static_cast<T*>(p.out) + (int64_t)row * HD + hl * E;
 #pragma unroll
     for (int t = 0; t < E; t += 4)
         *reinterpret_cast<uint2*>(out + t) =
@@ -213,7 +212,7 @@ cudaError_t launch_part(const AttnArgs& a, const SharedGroups& g, int32_t num_bl
     const int64_t rows = (int64_t)a.num_seqs * a.num_heads;
     return launch_pdl_smem(shared_merge_kernel<T, HD>, dim3((unsigned)((rows + 15) / 16)), dim3(256),
                            (size_t)(a.num_seqs + g.groups + 2) * sizeof(int32_t), stream, p,
-                           (int64_t)grid * Pp::NW, g, (const int32_t*)group_of, (int64_t)ctas);
+                           (int64_t)grid * Pp::NW, g, (const int32_t*)group_of, ctas);
 }
 
 template <typename T, int HD>

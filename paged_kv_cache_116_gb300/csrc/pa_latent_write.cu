@@ -44,9 +44,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) latent_write_kernel(cons
         tab[i] = turn_of(p.positions[t0 + t], p.inv_freq[pr]);
     }
     __syncthreads();
-    // the pair at o0, o1 (VEC pairs from `pr` on)
-    auto first = [&](int pr) { return p.interleaved ? 2 * pr : pr; };
-    auto second = [&](int pr) { return p.interleaved ? 2 * pr + VEC : pr + half; };  // (VEC 1: 2 pr + 1)
+    // Item r of R: two vectors that hold VEC whole pairs, each next to the same
+    // vector of item r + 1: both halves of pairs r VEC .. (pairs i, i + half), or
+    // pairs of the first and of the second half (pairs 2 i, 2 i + 1).
+    const int R = half / VEC;
+    auto first = [&](int r) { return VEC == 1 && p.interleaved ? 2 * r : r * VEC; };
+    auto second = [&](int r) { return VEC == 1 && p.interleaved ? 2 * r + 1 : half + r * VEC; };
+    auto turn = [&](RVec<T, VEC>& a, RVec<T, VEC>& b, int t, int r) {
+        float f[2][VEC];
+        unpack<T, VEC>(a, f[0]);
+        unpack<T, VEC>(b, f[1]);
+        const float2* cs = tab + t * half;
+        if (VEC > 1 && p.interleaved) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const float2* c = cs + (v * half + r * VEC) / 2;
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    const float x = f[v][2 * e], y = f[v][2 * e + 1];
+                    f[v][2 * e] = x * c[e].x - y * c[e].y;
+                    f[v][2 * e + 1] = y * c[e].x + x * c[e].y;
+                }
+            }
+        } else {
+            rotate<VEC>(f[0], f[1], cs + r * VEC, false);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            a.e[e] = Elt<T>::from_f(f[0][e]);
+            b.e[e] = Elt<T>::from_f(f[1][e]);
+        }
+    };
 
     if (blockIdx.y == 0) {
         constexpr int NV = 4, SPAN = 32 * VEC * NV;  // a lane's vectors at a time
@@ -100,55 +128,45 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) latent_write_kernel(cons
                     store_vec<T, VEC>(row + i, v[k]);
                 }
             }
-            for (int pr = lane * VEC; pr < half; pr += 32 * VEC) {
-                const int o0 = lat + first(pr), o1 = lat + second(pr);
-                RVec<T, VEC> a = load_vec<T, VEC>(x + o0), b = load_vec<T, VEC>(x + o1);
-                float f[2][VEC];
-                unpack<T, VEC>(a, f[0]);
-                unpack<T, VEC>(b, f[1]);
-                rotate<VEC>(f[0], f[1], tab + t * half + pr, p.interleaved);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    a.e[e] = Elt<T>::from_f(f[0][e]);
-                    b.e[e] = Elt<T>::from_f(f[1][e]);
-                }
-                store_vec<T, VEC>(row + o0, a);
-                store_vec<T, VEC>(row + o1, b);
+            for (int r = lane; r < R; r += 32) {
+                RVec<T, VEC> a = load_vec<T, VEC>(x + lat + first(r)), b = load_vec<T, VEC>(x + lat + second(r));
+                turn(a, b, t, r);
+                store_vec<T, VEC>(row + lat + first(r), a);
+                store_vec<T, VEC>(row + lat + second(r), b);
             }
         }
     }
 
-    // the queries: an item is VEC pairs of one head of one token
-    constexpr int U = 4;  // items in flight
-    const int R = half / VEC, items = p.num_heads * R, all = nt * items, step = gridDim.y * kThreads;
-    for (int i0 = blockIdx.y * kThreads + threadIdx.x; i0 < all; i0 += U * step) {
-        RVec<T, VEC> a[U], b[U];
+    // The queries.  A thread finds its item (of a head) once and works it for
+    // all tokens of the CTA; where a token's items do not fill the CTA, for every
+    // `step`th token.
+    constexpr int U = 4;  // tokens in flight
+    const int items = p.num_heads * R, step = items && items < kThreads ? kThreads / items : 1;
+    const int begin = step > 1 ? threadIdx.x / items : 0;
+    if (begin >= step) return;
+    for (int it = step > 1 ? threadIdx.x - begin * items : blockIdx.y * kThreads + threadIdx.x; it < items;
+         it += step > 1 ? items : gridDim.y * kThreads) {
+        const int h = it / R, r = it - h * R;
+        const T* s = static_cast<const T*>(p.q) + t0 * p.q_stride + h * p.q_head_stride;
+        T* d = static_cast<T*>(p.q_out) + t0 * p.q_out_stride + h * p.q_out_head_stride;
+        const int o0 = first(r), o1 = second(r);
+        for (int t = begin; t < nt; t += U * step) {
+            RVec<T, VEC> a[U], b[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * step;
-            if (i >= all) break;
-            const int t = i / items, r = i - t * items, h = r / R, pr = (r - h * R) * VEC;
-            const T* s = static_cast<const T*>(p.q) + (t0 + t) * p.q_stride + h * p.q_head_stride;
-            a[u] = load_vec<T, VEC>(s + first(pr));
-            b[u] = load_vec<T, VEC>(s + second(pr));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * step;
-            if (i >= all) break;
-            const int t = i / items, r = i - t * items, h = r / R, pr = (r - h * R) * VEC;
-            float f[2][VEC];
-            unpack<T, VEC>(a[u], f[0]);
-            unpack<T, VEC>(b[u], f[1]);
-            rotate<VEC>(f[0], f[1], tab + t * half + pr, p.interleaved);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                a[u].e[e] = Elt<T>::from_f(f[0][e]);
-                b[u].e[e] = Elt<T>::from_f(f[1][e]);
+            for (int u = 0; u < U; ++u) {
+                if (t + u * step >= nt) break;
+                const T* x = s + (t + u * step) * p.q_stride;
+                a[u] = load_vec<T, VEC>(x + o0);
+                b[u] = load_vec<T, VEC>(x + o1);
             }
-            T* d = static_cast<T*>(p.q_out) + (t0 + t) * p.q_out_stride + h * p.q_out_head_stride;
-            store_vec<T, VEC>(d + first(pr), a[u]);
-            store_vec<T, VEC>(d + second(pr), b[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (t + u * step >= nt) break;
+                turn(a[u], b[u], t + u * step, r);
+                T* y = d + (t + u * step) * p.q_out_stride;
+                store_vec<T, VEC>(y + o0, a[u]);
+                store_vec<T, VEC>(y + o1, b[u]);
+            }
         }
     }
 }
@@ -167,7 +185,7 @@ cudaError_t launch_typed(const LatentWriteArgs& a, cudaStream_t stream) {
     const int64_t slots = (int64_t)kSms * kCtasPerSm;
     p.tpb = (int)std::min<int64_t>(16, (a.n + slots - 1) / slots);
     const int64_t ctas = (a.n + p.tpb - 1) / p.tpb;
-    const int64_t items = (int64_t)p.tpb * a.num_heads * (a.rope_dim / (vec ? 2 * V : 2));
+    const int64_t items = (int64_t)a.num_heads * (a.rope_dim / (vec ? 2 * V : 2));
     const int64_t parts =
         std::max<int64_t>(1, std::min<int64_t>({slots / 2 / ctas, (items + kThreads - 1) / kThreads, 65535}));
     const dim3 grid((unsigned)ctas, (unsigned)parts);

@@ -186,9 +186,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // waits for this grid only, so one CTA waits for the decode at its end.
     pdl_launch_dependents();
     shared_prefix(p.g, prefix);
-    const int64_t W = prefix[p.g.groups], C = gridDim.x;
+    const int64_t W = prefix[p.g.groups], C = shared_ctas(W, gridDim.x);
     const int64_t f0 = blockIdx.x * W / C, f1 = (blockIdx.x + 1) * W / C;
-    if (f0 == f1) {
+    if (blockIdx.x >= C || f0 == f1) {
         if (blockIdx.x == 0) pdl_wait_primary();
         return;
     }

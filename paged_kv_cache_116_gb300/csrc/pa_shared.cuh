@@ -42,6 +42,9 @@ __device__ __forceinline__ int shared_cost(const SharedGroups& p, int g) {
     const int nk = (shared_tokens(p, g) + kPrefixKeys - 1) / kPrefixKeys;
     return nk ? p.num_kv_heads * shared_row_tiles(p, g) * (nk + kPrefixUnit) : 0;
 }
+// CTAs that the list of cost W is cut for: runs of four at least, so that a
+// row's pieces are few (and no run is empty).
+__device__ __forceinline__ int shared_ctas(int64_t W, int ctas) { return (int)max(min((int64_t)ctas, W / 4), (int64_t)1); }
 // Exclusive prefix of the groups' costs, in shared memory (every thread of the
 // block; ends with a block barrier).
 __device__ __forceinline__ void shared_prefix(const SharedGroups& p, int32_t* prefix) {

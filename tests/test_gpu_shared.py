@@ -21,8 +21,17 @@ def pa():
     pa.pa_set_option(1, 0)
 
 
-def shared(pa, b, q, scale, out=None, fill=0xFF, starts=None, prefix=None):
+@pytest.fixture(autouse=True)
+def _apart(pa):
+    """Small batches are worked as pa_decode unless the tensor cores are pinned; the pin is off where they do not
+    apply (shared, below)."""
+    yield
+    pa.pa_set_option(1, 0)
+
+
+def shared(pa, b, q, scale, out=None, fill=0xFF, starts=None, prefix=None, kernel=2):
     S, hq, hd = q.shape
+    pa.pa_set_option(1, kernel if _tensor_cores(b, hq) else 0)
     starts = b.dstarts if starts is None else starts
     prefix = b.dprefix if prefix is None else prefix
     if out is None:
@@ -63,11 +72,13 @@ def test_against_64_bits(pa, groups, loners, hq, hkv, hd, bs, dtype):
     b = SharedBatch(groups, hkv, hd, bs, dtype, 3, loners).to(DEV)
     q = rand((len(b.lens), hq, hd), dtype, 4)
     scale = hd ** -0.5
-    out = shared(pa, b, q.to(DEV), scale)
-    close(out, *shared_exact(b, q, scale, _tensor_cores(b, hq)))
-    for s, L in enumerate(b.lens):
-        if L == 0:
-            assert (out[s] == 0).all()
+    exact, bound = shared_exact(b, q, scale, _tensor_cores(b, hq))
+    for kernel in (2, 0):  # apart, and as the sizes say
+        out = shared(pa, b, q.to(DEV), scale, kernel=kernel)
+        close(out, exact, bound)
+        for s, L in enumerate(b.lens):
+            if L == 0:
+                assert (out[s] == 0).all()
     assert pa.lib().pa_device_status(1) == 0
 
 
@@ -81,6 +92,16 @@ def test_without_groups_it_is_the_plain_decode(pa):
     plain = torch.zeros_like(q)
     pa.pa_decode(plain, q, b.dk, b.dv, b.dtables, b.dlens, b.max_context, 0.1, workspace=ws)
     assert torch.equal(out, plain)
+
+
+def test_large_batches_are_worked_apart(pa):
+    """Without a pinned kernel: 64 requests behind 2,048 tokens, and the workspace that takes."""
+    b = SharedBatch([(2048, [5 + 3 * i for i in range(64)])], 8, 128, 16, "bf16", 6).to(DEV)
+    q = rand((64, 32, 128), "bf16", 7)
+    size, plain = (f(64, *g, 32, 8, 128, 16, b.max_context, q.dtype) for f, g in
+                   ((pa.pa_decode_shared_workspace_size, (1,)), (pa.pa_decode_workspace_size, ())))
+    assert size > plain
+    close(shared(pa, b, q.to(DEV), 0.09, kernel=0), *shared_exact(b, q, 0.09, True))
 
 
 def test_groups_may_lie_anywhere(pa):
@@ -120,6 +141,7 @@ def test_graph_replays_follow_lengths_and_groups(pa):
     b = SharedBatch([(256, [64, 100, 1]), (128, [5, 300])], 2, 128, 16, "bf16", 6).to(DEV)
     q = rand((5, 12, 128), "bf16", 7).to(DEV)
     out = torch.zeros_like(q)
+    pa.pa_set_option(1, 2)
     ws = torch.zeros(pa.pa_decode_shared_workspace_size(5, 2, 12, 2, 128, 16, b.max_context, q.dtype),
                      dtype=torch.uint8, device=DEV)
     run = lambda: pa.pa_decode_shared(out, q, b.dk, b.dv, b.dtables, b.dlens, b.dstarts, b.dprefix,  # noqa: E731
