@@ -106,6 +106,14 @@ struct Params {
     float scale_log2;
     float* records;  // [2 pairs][rec_rows][REC]
     int32_t rec_rows;
+    struct Cut* cuts;  // [pairs]
+};
+// The unit that a pair begins and others end, for the kernel that joins its
+// records: its rows from row0 on (0 rows: there is none), the last pair of it,
+// and the list's cost (pairs beyond it have no piece).
+struct alignas(16) Cut {
+    int32_t rows, last, cost, pad;
+    int64_t row0, pad2;
 };
 
 // A request: its first (token, head) row, rows, tokens cached before the new
@@ -285,6 +293,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     const int64_t W = prefix[p.num_seqs], pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     const int64_t f0 = pair * W / pairs, f1 = (pair + 1) * W / pairs;
+    if (threadIdx.x == 0 && rank == 0) p.cuts[pair].rows = 0;  // (the same thread may write it again below)
     if (f0 == f1) return;  // (both CTAs of the pair)
     const Segment first = locate(p, prefix, f0, f0, f1);
 
@@ -718,6 +727,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 }
             } else {
                 float* rec = p.records + ((2 * pair + s.slot()) * p.rec_rows + (row0 - s.t * TM)) * (int64_t)REC;
+                if (threadIdx.x == 0 && rank == 0 && s.k0 == 0) {
+                    Cut cut;
+                    cut.rows = min(s.r.rows - s.t * TM, TM);
+                    cut.last = (int)((s.end() * pairs + W - 1) / W) - 1;  // of the pair owning its last place
+                    cut.cost = (int)W;
+                    cut.row0 = s.r.row0 + s.t * TM;
+                    p.cuts[pair] = cut;
+                }
                 if (mine && hf == 0) {
                     rec[(int64_t)lane * REC + LAT] = m;
                     rec[(int64_t)lane * REC + LAT + 1] = l;
@@ -765,37 +782,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (warp == W_S) tmem_pair_dealloc(tmem, TMEM_COLS);
 }
 
-// Joins the records of the units cut between pairs.  CTA (c, g): the unit whose
-// first piece ends pair c's run, rows 8 g .. 8 g + 7, a warp each.
+// Joins the records of the units cut between pairs.  CTA (c, g): the unit that
+// pair c begins, rows 4 g .. 4 g + 3, a warp each (small CTAs: they are resident
+// beside the kernel whose end they wait for).
 template <typename T>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int pairs) {
-    extern __shared__ int32_t mprefix[];
-    cost_prefix(p, mprefix);
-    const int64_t W = mprefix[p.num_seqs], c = blockIdx.x;
-    const int64_t f0 = c * W / pairs, f1 = (c + 1) * W / pairs;
-    // (the lengths are older than the grid before this one; the kernel behind
-    // this one waits for it only, so one CTA always waits)
-    pdl_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait_primary();
-    if (f0 == f1 || f1 == W) return;
-    const Segment s = locate(p, mprefix, f1 - 1, f0, f1);
-    const int64_t u1 = s.end();
-    if (u1 <= f1 || s.k0 > 0 || s.k1 == 0) return;  // ends here, began before, or begins after
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= p.rec_rows || s.t * TM + row >= s.r.rows) return;
-    const int64_t last = (u1 * pairs + W - 1) / W - 1;  // the pair owning position u1 - 1
+__global__ void __launch_bounds__(128) latent_merge_kernel(const Params p, int pairs) {
     pdl_wait_primary();
+    pdl_launch_dependents();
+    const int c = blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + c));
+    if (row >= cut.x) return;
+    const int last = cut.y;
+    const int64_t row0 = __ldcg(&p.cuts[c].row0), W = cut.z;
     float M = -INFINITY, l = 0.f;
     float4 o[4] = {};
     constexpr int B = 4;  // records in flight
-    for (int64_t q0 = c; q0 <= last; q0 += B) {
+    for (int q0 = c; q0 <= last; q0 += B) {
         float m[B], lq[B];
         float4 a[B][4];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const int64_t q = q0 + k;
-            const bool there = q <= last && q * W / pairs != (q + 1) * W / pairs;  // (an empty run has none)
-            const float* rec = p.records + ((2 * q + (q == c ? 1 : 0)) * p.rec_rows + row) * (int64_t)REC;
+            const int q = q0 + k;
+            const bool there = q <= last && (W >= pairs || q * W / pairs != (q + 1) * W / pairs);  // (no empty run)
+            const float* rec = p.records + ((2ll * q + (q == c ? 1 : 0)) * p.rec_rows + row) * REC;
             m[k] = there ? __ldcg(rec + LAT) : -INFINITY;
             lq[k] = there ? __ldcg(rec + LAT + 1) : 0.f;
 #pragma unroll
@@ -824,7 +833,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const Params p, int p
         M = mn;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* out = static_cast<T*>(p.out) + (s.r.row0 + s.t * TM + row) * LAT;
+    T* out = static_cast<T*>(p.out) + (row0 + row) * LAT;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint2*>(out + 128 * i + 4 * lane) =
@@ -893,6 +902,7 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     p.causal = a.causal;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.records = static_cast<float*>(workspace);
+    p.cuts = reinterpret_cast<Cut*>(p.records + (int64_t)2 * kPairs * rec_rows * REC);
     p.rec_rows = rec_rows;
     // every pair there is, fewer where even the longest contexts give them less
     // than one tile each
@@ -917,8 +927,8 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, latent_umma_kernel<T>, tmQ, tmC, p);
     if (e != cudaSuccess || pairs == 1) return e;
-    return launch_pdl_smem(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 7) / 8)),
-                           dim3(256), (size_t)(a.num_seqs + 1) * 4, stream, p, pairs);
+    return launch_pdl_smem(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 3) / 4)),
+                           dim3(128), 0, stream, p, pairs);
 }
 
 }  // namespace
@@ -929,7 +939,7 @@ bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int3
 }
 
 size_t latent_umma_workspace(int64_t rows) {
-    return (size_t)2 * kPairs * (size_t)std::min<int64_t>(rows, TM) * REC * sizeof(float);
+    return (size_t)2 * kPairs * (size_t)std::min<int64_t>(rows, TM) * REC * sizeof(float) + kPairs * sizeof(Cut);
 }
 
 cudaError_t launch_latent_umma(const LatentArgs& a, int32_t num_blocks, void* workspace, std::string* err,
