@@ -685,13 +685,12 @@ def pa_evict(new_lens, weights_out, positions_out, weights, k_cache, v_cache, bl
     return new_lens
 
 
-def _heads_of(name, t, n, rope_dim, dtype):
+def _heads_of(name, t, shape, dtype):
     """Token and head stride (elements) of q or q_out [n, heads, rope_dim], heads and tokens at any stride."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[0] != n or t.shape[2] != rope_dim or t.dtype != dtype or \
-            (t.stride(2) != 1 and rope_dim > 1):
-        raise ValueError("%s must be a CUDA tensor [%d, heads, %d] of kv's dtype, its last axis contiguous"
-                         % (name, n, rope_dim))
-    return t.stride(0), t.stride(1)
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or st[2] != 1:
+        raise ValueError("%s must be a CUDA tensor [n, heads, rope_dim] of kv's dtype, its last axis contiguous" % name)
+    return st[0], st[1]
 
 
 def pa_latent_write(kv, positions, inv_freq, slot_mapping, latent_cache, norm_weight=None, eps=1e-6, q=None,
@@ -703,13 +702,13 @@ def pa_latent_write(kv, positions, inv_freq, slot_mapping, latent_cache, norm_we
     positions, slot_mapping [n] int64, inv_freq float64, all on the device.  Tokens of kv, and tokens and heads of q
     and q_out, may lie at any stride (slices of wider heads)."""
     _dev(positions, inv_freq, slot_mapping, latent_cache, norm_weight)
-    if latent_cache.dim() != 3 or kv.dim() != 2 or positions.dim() != 1:
-        raise ValueError("latent_cache must be [num_blocks, block_size, row], kv [n, row] and positions [n]")
-    nb, bs, row = latent_cache.shape
-    n, dt, rope_dim = positions.shape[0], kv.dtype, 2 * inv_freq.numel()
+    shape, pool, dt = positions.shape, latent_cache.shape, kv.dtype
+    if len(pool) != 3 or len(shape) != 1:
+        raise ValueError("latent_cache must be [num_blocks, block_size, row] and positions [n]")
+    (nb, bs, row), n, rope_dim = pool, shape[0], 2 * inv_freq.numel()
     if positions.dtype != torch.int64 or inv_freq.dtype != torch.float64 or slot_mapping.dtype != torch.int64:
         raise TypeError("positions and slot_mapping must be int64 and inv_freq float64")
-    if not kv.is_cuda or kv.shape != (n, row) or kv.stride(1) != 1 or slot_mapping.shape != (n,):
+    if kv.shape != (n, row) or slot_mapping.shape != shape or not kv.is_cuda or kv.stride(1) != 1:
         raise ValueError("kv must be a CUDA tensor [n, latent_dim + rope_dim] with contiguous rows, and positions and "
                          "slot_mapping hold one entry per token")
     if latent_cache.dtype != dt or rope_dim >= row or (q is None) != (q_out is None):
@@ -718,14 +717,15 @@ def pa_latent_write(kv, positions, inv_freq, slot_mapping, latent_cache, norm_we
         raise ValueError("norm_weight must be [latent_dim] of kv's dtype")
     heads, qs, qo = 0, (0, 0), (0, 0)
     if q is not None:
-        heads = q.shape[1]
-        qs, qo = _heads_of("q", q, n, rope_dim, dt), _heads_of("q_out", q_out, n, rope_dim, dt)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    st = lib().pa_latent_write(_raw(q_out), *qo, _raw(q), *qs, _raw(kv), kv.stride(0) if n > 1 else row,
-                               _raw(norm_weight), float(eps), _raw(positions), _raw(inv_freq), rope_dim,
-                               1 if interleaved else 0, _raw(slot_mapping), n, _raw(latent_cache), nb, bs, heads,
-                               row - rope_dim, _dtype(kv),
+        want = q.shape
+        if len(want) != 3 or want[0] != n or want[2] != rope_dim:
+            raise ValueError("q must be [n, heads, rope_dim]")
+        heads = want[1]
+        qs, qo = _heads_of("q", q, want, dt), _heads_of("q_out", q_out, want, dt)
+    st = lib().pa_latent_write(_raw(q_out), *qo, _raw(q), *qs, kv.data_ptr(), kv.stride(0) if n > 1 else row,
+                               _raw(norm_weight), eps, positions.data_ptr(), inv_freq.data_ptr(), rope_dim,
+                               1 if interleaved else 0, slot_mapping.data_ptr(), n, latent_cache.data_ptr(), nb, bs,
+                               heads, row - rope_dim, _dtype(kv),
                                _raw_stream(stream, kv, positions, inv_freq, slot_mapping, latent_cache, norm_weight, q,
                                            q_out))
     _check(st, "pa_latent_write")

@@ -1326,7 +1326,8 @@ extern "C" pa_status pa_latent_write(void* q_out, int64_t q_out_stride, int64_t 
                                      void* stream) {
     if (num_heads < 0 || latent_dim <= 0 || rope_dim < 2 || rope_dim % 2 || rope_dim > 256)
         return fail(PA_ERR_INVALID_ARG, "latent_dim must be positive, rope_dim even and in [2, 256], num_heads >= 0");
-    if (latent_dim > 4096) return fail(PA_ERR_UNSUPPORTED, "latent_dim must be at most 4096");
+    if (latent_dim > 4096 || num_heads > (1 << 20))
+        return fail(PA_ERR_UNSUPPORTED, "latent_dim must be at most 4096, num_heads at most 2^20");
     pa_status g = check_geometry(std::max(num_heads, 1), 1, latent_dim + rope_dim, num_blocks, block_size, dtype);
     if (g != PA_OK) return g;
     if (n < 0) return fail(PA_ERR_INVALID_ARG, "n must be non-negative");

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) latent_write_kernel(cons
     // The queries.  A thread finds its item (of a head) once and works it for
     // all tokens of the CTA; where a token's items do not fill the CTA, for every
     // `step`th token.
-    constexpr int U = 4;  // tokens in flight
+    constexpr int U = 2;  // tokens in flight (more spill: three and four took 87 and 98 us where two take 63)
     const int items = p.num_heads * R, step = items && items < kThreads ? kThreads / items : 1;
     const int begin = step > 1 ? threadIdx.x / items : 0;
     if (begin >= step) return;
