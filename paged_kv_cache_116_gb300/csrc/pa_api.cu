@@ -1558,9 +1558,10 @@ static pa_status check_groups(const int32_t* group_starts, const int32_t* prefix
         return err;
     if (starts[0] < 0 || starts[num_groups] > num_seqs)
         return fail(PA_ERR_INDEX, "group_starts must lie in [0, num_seqs]");
+    for (int32_t g = 0; g < num_groups; ++g)  // (all of them first: what follows indexes by them)
+        if (starts[g + 1] < starts[g]) return fail(PA_ERR_INDEX, "group_starts must be non-decreasing");
     for (int32_t g = 0; g < num_groups; ++g) {
         const std::string who = "group " + std::to_string(g);
-        if (starts[g + 1] < starts[g]) return fail(PA_ERR_INDEX, who + ": group_starts must be non-decreasing");
         if (prefix[g] < 0 || prefix[g] % block_size)
             return fail(PA_ERR_INDEX, who + ": prefix_lens must be a non-negative multiple of block_size");
         for (int32_t s = starts[g]; s < starts[g + 1]; ++s) {
