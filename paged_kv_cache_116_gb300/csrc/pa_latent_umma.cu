@@ -907,7 +907,7 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     // every pair there is, fewer where even the longest contexts give them less
     // than one tile each
     const int64_t units = a.cu ? rows / TM + a.num_seqs : (int64_t)a.num_seqs * ((a.num_heads + TM - 1) / TM);
-    const int64_t tiles = units * ((a.max_context + BK - 1) / BK);
+    const int64_t tiles = units * (((int64_t)a.max_context + BK - 1) / BK);
     const void* kfn = reinterpret_cast<const void*>(&latent_umma_kernel<T>);
     cudaError_t e = allow_smem(kfn, smem_bytes(kMaxSeqs));
     if (e != cudaSuccess) return e;
