@@ -25,8 +25,9 @@
 //               memory; P goes to shared memory as the A operand.  O is
 //               rescaled only when a row's maximum grows by more than 2^8.
 //   warps 4-7   loads: 16 KB stages -- two 64-element chunks of the CTA's 64
-//               keys in a ring of four (warps 4, 5), two chunks of its dims of
-//               64 keys in a ring of three (warps 6, 7), boxes issued by a
+//               keys in a ring of four or five (warps 4, 5), two chunks of its
+//               dims of 64 keys in a ring of the other three or two (warps 6,
+//               7), boxes issued by a
 //               lane each; both CTAs' bytes are counted on the even CTA's
 //               barrier.
 //   warp 8, 9   (even CTA) issue the MMAs of S and of P C: two warps, because
@@ -69,7 +70,7 @@ constexpr int TM = 128;        // query rows per tile, 64 per CTA
 constexpr int BK = 128;        // keys per tile, 64 per CTA
 constexpr int CHB = 64 * 128;  // bytes of a chunk of 64 rows
 constexpr int STAGE = 2 * CHB;
-constexpr int NK = 4, NV = 3, NST = NK + NV;  // stages of keys and of values
+constexpr int NST = 7;  // stages, of keys and of values
 constexpr int W_LOAD = 4, NP = 2;  // NP loading warps for keys, NP for values
 constexpr int W_S = W_LOAD + 2 * NP, W_O = W_S + 1;
 constexpr int NTHREADS = 32 * (W_O + 1);
@@ -84,7 +85,7 @@ constexpr int P_OFF = CH * CHB;
 constexpr int ST_OFF = P_OFF + 2 * 2 * CHB;
 constexpr int BAR_OFF = ST_OFF + NST * STAGE;
 // full[NST], empty[NST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, q_empty, o_empty, tail[NP]
-// (full and empty: NK of the keys' ring, then NV of the values')
+// (full and empty: the keys' ring, then the values')
 constexpr int NBAR = 2 * NST + 8 + 3 + NP;
 constexpr int X_OFF = (BAR_OFF + NBAR * 8 + 15) / 16 * 16;  // float [2][128] swapped maxima (and sums)
 constexpr int MISC_OFF = X_OFF + 2 * 128 * 4;               // tensor-memory address, abort flag
@@ -251,11 +252,16 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t lo) {
     return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
 }
 
-template <typename T>
+// SINGLE: one token per request.  The keys come from memory, the values mostly
+// from L2 behind them: five stages for the keys (8 x 32,768 tokens 88 -> 85 us,
+// 64 x 16 heads 60 -> 56; four and three for prompts, whose rows stay in L2:
+// 8,192 tokens 800 us against 884, 16 chunks 261 against 296).
+template <typename T, bool SINGLE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     latent_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                        const Params p) {
     constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NK = SINGLE ? 5 : 4, NV = NST - NK;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + BAR_OFF);
@@ -908,7 +914,8 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     // than one tile each
     const int64_t units = a.cu ? rows / TM + a.num_seqs : (int64_t)a.num_seqs * ((a.num_heads + TM - 1) / TM);
     const int64_t tiles = units * (((int64_t)a.max_context + BK - 1) / BK);
-    const void* kfn = reinterpret_cast<const void*>(&latent_umma_kernel<T>);
+    const auto kernel = a.cu ? latent_umma_kernel<T, false> : latent_umma_kernel<T, true>;
+    const void* kfn = reinterpret_cast<const void*>(kernel);
     cudaError_t e = allow_smem(kfn, smem_bytes(kMaxSeqs));
     if (e != cudaSuccess) return e;
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(resident_pairs(kfn), tiles));
@@ -925,7 +932,7 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, latent_umma_kernel<T>, tmQ, tmC, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmC, p);
     if (e != cudaSuccess || pairs == 1) return e;
     return launch_pdl_smem(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 3) / 4)),
                            dim3(128), 0, stream, p, pairs);
