@@ -1389,13 +1389,13 @@ static bool use_latent_umma(int64_t want, int dtype, int32_t latent_dim, int32_t
     return ok && want != 1;
 }
 
-// tokens: of a request, at most.
-static size_t latent_workspace(int64_t want, int64_t tokens, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
-                               int32_t block_size, int dtype) {
-    if (tokens <= 0 || num_heads <= 0 || want == 1 ||
-        !pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size))
-        return 0;
-    return pa::latent_umma_workspace(tokens * num_heads);
+static size_t latent_workspace(int64_t want, bool varlen, int32_t num_seqs, int64_t total_q, int32_t num_heads,
+                               int32_t latent_dim, int32_t rope_dim, int32_t block_size, int32_t max_context,
+                               int dtype) {
+    if (num_seqs <= 0 || total_q <= 0 || num_heads <= 0 || latent_dim <= 0) return 0;
+    if (want != 1 && pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size))
+        return pa::latent_umma_workspace(varlen ? total_q * num_heads : num_heads);  // rows of a request at most
+    return pa::latent_simt_workspace(total_q, num_heads, latent_dim, max_context);
 }
 
 // cu == nullptr: one query per sequence.
@@ -1423,7 +1423,7 @@ static pa_status latent_impl(void* out, const void* q, const void* cache, const 
                                     rope_dim, block_size, &sel);
     if (sel != PA_OK) return sel;
     const int64_t rows = (int64_t)total_q * num_heads;
-    if (!tc && num_heads > 4 * 65535) return fail(PA_ERR_UNSUPPORTED, "too many heads");
+    if (!tc && num_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "too many heads");
     if (tc && (rows > INT32_MAX - 128 ||
                (rows / 128 + num_seqs) * (((int64_t)max_context + 127) / 128 + 8) > INT32_MAX))
         return fail(PA_ERR_UNSUPPORTED, "too many query rows for one call");
@@ -1460,16 +1460,14 @@ static pa_status latent_impl(void* out, const void* q, const void* cache, const 
     a.dtype = dtype;
     std::string err;
     cudaError_t e;
-    if (tc) {
-        const size_t need = pa::latent_umma_workspace(varlen ? rows : num_heads);
-        if (workspace_bytes < need || !workspace)
-            return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace ? workspace_bytes : 0) +
-                                              " bytes, " + std::to_string(need) + " needed");
-        if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-        e = pa::launch_latent_umma(a, num_blocks, workspace, &err, st);
-    } else {
-        e = pa::launch_latent_simt(a, st);
-    }
+    const size_t need = latent_workspace(g_options[varlen ? PA_OPT_VARLEN_KERNEL : PA_OPT_DECODE_KERNEL], varlen,
+                                         num_seqs, total_q, num_heads, latent_dim, rope_dim, block_size, max_context,
+                                         dtype);
+    if (need && (workspace_bytes < need || !workspace))
+        return fail(PA_ERR_WORKSPACE, "workspace holds " + std::to_string(workspace ? workspace_bytes : 0) +
+                                          " bytes, " + std::to_string(need) + " needed");
+    if (!aligned16(workspace)) return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    e = tc ? pa::launch_latent_umma(a, num_blocks, workspace, &err, st) : pa::launch_latent_simt(a, workspace, st);
     if (e != cudaSuccess)
         return err.empty() ? cuda_fail(e, name) : fail(PA_ERR_CUDA, std::string(name) + ": " + err);
     return PA_OK;
@@ -1479,9 +1477,8 @@ extern "C" {
 
 size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t rope_dim,
                                        int32_t block_size, int32_t max_context, int dtype) {
-    (void)max_context;
-    return latent_workspace(g_options[PA_OPT_DECODE_KERNEL], num_seqs > 0 ? 1 : 0, num_heads, latent_dim, rope_dim,
-                            block_size, dtype);
+    return latent_workspace(g_options[PA_OPT_DECODE_KERNEL], false, num_seqs, num_seqs, num_heads, latent_dim, rope_dim,
+                            block_size, max_context, dtype);
 }
 
 pa_status pa_latent_decode(void* out, const void* q, const void* cache, const int32_t* block_tables,
@@ -1497,9 +1494,9 @@ pa_status pa_latent_decode(void* out, const void* q, const void* cache, const in
 size_t pa_latent_varlen_workspace_size(int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_heads,
                                        int32_t latent_dim, int32_t rope_dim, int32_t block_size, int32_t max_context,
                                        int dtype) {
-    (void)max_q, (void)max_context;
-    return num_seqs <= 0 ? 0 : latent_workspace(g_options[PA_OPT_VARLEN_KERNEL], total_q, num_heads, latent_dim,
-                                                rope_dim, block_size, dtype);
+    (void)max_q;
+    return latent_workspace(g_options[PA_OPT_VARLEN_KERNEL], true, num_seqs, total_q, num_heads, latent_dim, rope_dim,
+                            block_size, max_context, dtype);
 }
 
 pa_status pa_latent_varlen(void* out, const void* q, const void* cache, const int32_t* block_tables,

@@ -348,7 +348,9 @@ struct LatentArgs {
     int dtype;
 };
 bool latent_simt_supported(int dtype, int32_t row_dim);  // pa_latent_simt.cu
-cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream);
+// Bytes for pieces of the rows' keys (few rows), and the launch with them.
+size_t latent_simt_workspace(int64_t total_q, int32_t num_heads, int32_t latent_dim, int32_t max_context);
+cudaError_t launch_latent_simt(const LatentArgs& a, void* workspace, cudaStream_t stream);
 // The same on the tensor cores (pa_latent_umma.cu).  total_q * num_heads and
 // the key tiles of a launch must fit in int32.
 bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size);

@@ -10,14 +10,17 @@
 // the row's latent part, so a row is read once for all the CTA's heads and for
 // both products.
 //
-// One CTA of four warps per (query row, four heads): lanes split the row's
-// elements, each warp keeps one online softmax per head over an interleaved
-// share of the keys, and the warps' states are joined at the end.  Bound: the
-// shuffles of the scores' sums (five per head and key).  Two keys per warp in
-// flight hide the table's and the row's round trips.
+// One CTA of four warps per (query row, four heads), and per piece of the keys
+// where there are too few rows to fill the GPU: lanes split the row's elements,
+// each warp keeps one online softmax per head over an interleaved share of the
+// keys, and the warps' states are joined at the end; pieces leave (o, m, l)
+// records that latent_simt_join_kernel joins in order.  Bound: the shuffles of
+// the scores' sums (five per head and key).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
@@ -30,13 +33,15 @@ constexpr int kWarps = 4;
 constexpr int GH = 4;  // heads per CTA
 
 // DPL: elements of a row per lane.
+// splits pieces of each row's keys; records (splits > 1): [rows][heads][splits]
+// of latent_dim + 2 floats.
 template <typename T, int DPL>
-__global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentArgs a, int splits, float* records) {
     __shared__ float sm_m[kWarps][GH], sm_l[kWarps][GH];
     __shared__ float sm_acc[GH][DPL * 32];
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int row = blockIdx.x, h0 = blockIdx.y * GH, nh = min(GH, a.num_heads - h0);
+    const int row = blockIdx.x, h0 = blockIdx.y * GH, nh = min(GH, a.num_heads - h0), piece = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int req = row, num_new = 1, j = 0;
     if (a.cu != nullptr) {
@@ -52,7 +57,9 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
         j = row - a.cu[req];
     }
     const int L = a.seq_lens[req];
-    const int visible = a.causal ? min(L, L - num_new + j + 1) : L;
+    const int seen = a.causal ? min(L, L - num_new + j + 1) : L;  // keys this row sees, and this piece of them
+    const int from = (int)((int64_t)max(seen, 0) * piece / splits);
+    const int visible = (int)((int64_t)max(seen, 0) * (piece + 1) / splits);
     const int lat = a.latent_dim, D = lat + a.rope_dim;
     const T* q = static_cast<const T*>(a.q) + ((int64_t)row * a.num_heads + h0) * D;
     const T* cache = static_cast<const T*>(a.cache);
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
         }
     }
     constexpr int U = DPL <= 9 ? 2 : 1;
-    for (int t0 = warp; t0 < visible; t0 += U * kWarps) {
+    for (int t0 = from + warp; t0 < visible; t0 += U * kWarps) {
         float x[U][DPL];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -140,31 +147,79 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
         for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm_m[v][h]);
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) sum += sm_m[v][h] == -INFINITY ? 0.f : exp2f(sm_m[v][h] - M) * sm_l[v][h];
+        if (splits > 1) {
+            float* rec = records + (((int64_t)row * a.num_heads + h0 + h) * splits + piece) * (lat + 2);
+            rec[d] = visible > from ? sm_acc[h][d] : 0.f;
+            if (d == 0) {
+                rec[lat] = M;
+                rec[lat + 1] = sum;
+            }
+            continue;
+        }
         // (a row that sees nothing is zero; a NaN sum stays NaN)
         static_cast<T*>(a.out)[((int64_t)row * a.num_heads + h0 + h) * lat + d] =
             Elt<T>::from_f(visible > 0 ? sm_acc[h][d] / sum : 0.f);
     }
 }
 
+// Joins the pieces of a (row, head), in order.
 template <typename T>
-cudaError_t launch_typed(const LatentArgs& a, cudaStream_t stream) {
-    const int D = a.latent_dim + a.rope_dim;
-    const dim3 grid((unsigned)a.total_q, (unsigned)((a.num_heads + GH - 1) / GH)), block(kWarps * 32);
-    if (D <= 128) return launch_pdl(latent_simt_kernel<T, 4>, grid, block, stream, a);
-    if (D <= 288) return launch_pdl(latent_simt_kernel<T, 9>, grid, block, stream, a);
-    return launch_pdl(latent_simt_kernel<T, 18>, grid, block, stream, a);
+__global__ void __launch_bounds__(128) latent_simt_join_kernel(const LatentArgs a, int splits, const float* records) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int lat = a.latent_dim;
+    const int64_t rh = (int64_t)blockIdx.x * a.num_heads + blockIdx.y;
+    if (a.cu && (int)blockIdx.x >= a.cu[a.num_seqs]) return;  // behind the last request
+    const float* rec = records + rh * splits * (lat + 2);
+    float M = -INFINITY, sum = 0.f;
+    for (int i = 0; i < splits; ++i) M = fmaxf(M, rec[(int64_t)i * (lat + 2) + lat]);
+    const float ms = M == -INFINITY ? 0.f : M;
+    for (int i = 0; i < splits; ++i)
+        sum += exp2f(rec[(int64_t)i * (lat + 2) + lat] - ms) * rec[(int64_t)i * (lat + 2) + lat + 1];
+    for (int d = threadIdx.x; d < lat; d += blockDim.x) {
+        float o = 0.f;
+        for (int i = 0; i < splits; ++i)
+            o = fmaf(exp2f(rec[(int64_t)i * (lat + 2) + lat] - ms), rec[(int64_t)i * (lat + 2) + d], o);
+        static_cast<T*>(a.out)[rh * lat + d] = Elt<T>::from_f(sum == 0.f ? 0.f : o / sum);
+    }
+}
+
+// Pieces of each row's keys: enough CTAs for four on every SM, of 64 keys at
+// least (1 x 32,768 fp32 tokens of 16 heads are 4 CTAs otherwise).
+int simt_splits(int64_t total_q, int32_t num_heads, int32_t max_context) {
+    const int64_t ctas = total_q * ((num_heads + GH - 1) / GH);
+    const int64_t want = (4 * kSms + ctas - 1) / ctas, most = ((int64_t)max_context + 63) / 64;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min<int64_t>(most, 1024)));
+}
+
+template <typename T>
+cudaError_t launch_typed(const LatentArgs& a, float* records, cudaStream_t stream) {
+    const int D = a.latent_dim + a.rope_dim, splits = simt_splits(a.total_q, a.num_heads, a.max_context);
+    const dim3 grid((unsigned)a.total_q, (unsigned)((a.num_heads + GH - 1) / GH), (unsigned)splits), block(kWarps * 32);
+    cudaError_t e = D <= 128   ? launch_pdl(latent_simt_kernel<T, 4>, grid, block, stream, a, splits, records)
+                    : D <= 288 ? launch_pdl(latent_simt_kernel<T, 9>, grid, block, stream, a, splits, records)
+                               : launch_pdl(latent_simt_kernel<T, 18>, grid, block, stream, a, splits, records);
+    if (e != cudaSuccess || splits == 1) return e;
+    return launch_pdl(latent_simt_join_kernel<T>, dim3((unsigned)a.total_q, (unsigned)a.num_heads), dim3(128), stream, a,
+                      splits, (const float*)records);
 }
 
 }  // namespace
 
 bool latent_simt_supported(int dtype, int32_t row_dim) { return dtype >= 0 && dtype <= 2 && row_dim <= 576; }
 
-cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream) {
+size_t latent_simt_workspace(int64_t total_q, int32_t num_heads, int32_t latent_dim, int32_t max_context) {
+    const int splits = simt_splits(total_q, num_heads, max_context);
+    return splits == 1 ? 0 : (size_t)total_q * num_heads * splits * (latent_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_latent_simt(const LatentArgs& a, void* workspace, cudaStream_t stream) {
+    float* records = static_cast<float*>(workspace);
     if (a.total_q == 0 || a.num_seqs == 0) return cudaSuccess;
     switch (a.dtype) {
-        case 0: return launch_typed<float>(a, stream);
-        case 1: return launch_typed<__nv_bfloat16>(a, stream);
-        default: return launch_typed<__half>(a, stream);
+        case 0: return launch_typed<float>(a, records, stream);
+        case 1: return launch_typed<__nv_bfloat16>(a, records, stream);
+        default: return launch_typed<__half>(a, records, stream);
     }
 }
 

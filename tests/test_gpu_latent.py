@@ -69,6 +69,8 @@ DECODE = [
     ([70, 33], 9, 96, 32, 16, "bf16"),
     ([70, 33], 3, 50, 0, 4, "f32"),
     ([20], 5, 256, 32, 16, "f16"),
+    ([3000], 4, 512, 64, 16, "f32"),                 # CUDA cores, a row's keys in pieces
+    ([900, 0, 1, 70], 6, 96, 32, 4, "f16"),
 ]
 
 
@@ -115,7 +117,7 @@ def test_varlen(pa, reqs, heads, bs, dtype, causal):
 
 def test_rows_behind_the_last_request_stay(pa):
     for dtype in ("bf16", "f32"):
-        b = LatentBatch([20, 50], 512, 64, 16, dtype, 3).to(DEV)
+        b = LatentBatch([20, 500], 512, 64, 16, dtype, 3).to(DEV)
         q = rand((40, 16, 576), dtype, 4)
         out = torch.full((40, 16, 512), 3.0, dtype=q.dtype, device=DEV)
         varlen(pa, b, q.to(DEV), [0, 7, 30], 0.07, True, out=out)
