@@ -14,8 +14,8 @@
 // where there are too few rows to fill the GPU: lanes split the row's elements,
 // each warp keeps one online softmax per head over an interleaved share of the
 // keys, and the warps' states are joined at the end; pieces leave (o, m, l)
-// records that latent_simt_join_kernel joins in order.  Bound: the shuffles of
-// the scores' sums (five per head and key).
+// records that latent_simt_join_kernel joins in order.  Bound: instructions (per
+// key and four heads 144 products of a lane's elements and ten shuffles).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -78,43 +78,64 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
             acc[h][k] = 0.f;
         }
     }
-    constexpr int U = DPL <= 9 ? 2 : 1;
-    for (int t0 = from + warp; t0 < visible; t0 += U * kWarps) {
-        float x[U][DPL];
+    // the next key's row is on its way while one is worked, and the table entry
+    // of the one after it
+    auto row_of = [&](int t) -> const T* {
+        t = min(t, visible - 1);
+        return cache + ((int64_t)table[t / a.block_size] * a.block_size + t % a.block_size) * D;
+    };
+    auto fetch = [&](const T* r, float (&x)[DPL]) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = min(t0 + u * kWarps, visible - 1);
-            const T* r = cache + ((int64_t)table[t / a.block_size] * a.block_size + t % a.block_size) * D;
+        for (int k = 0; k < DPL; ++k) {
+            const int d = lane + 32 * k;
+            x[k] = d < D ? Elt<T>::to_f(r[d]) : 0.f;
+        }
+    };
+    int t = from + warp;
+    float x[DPL], ahead[DPL];
+    const T* next = nullptr;
+    if (t < visible) {
+        fetch(row_of(t), x);
+        next = row_of(t + kWarps);
+    }
+    for (; t < visible; t += kWarps) {
+        fetch(next, ahead);
+        next = row_of(t + 2 * kWarps);
+        float dot[GH];
 #pragma unroll
-            for (int k = 0; k < DPL; ++k) {
-                const int d = lane + 32 * k;
-                x[u][k] = d < D ? Elt<T>::to_f(r[d]) : 0.f;
+        for (int h = 0; h < GH; ++h) {
+            dot[h] = 0.f;
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) dot[h] = fmaf(qv[h][k], x[k], dot[h]);
+        }
+        // the four sums over the lanes: each exchange halves what a lane
+        // keeps, so ten shuffles instead of twenty
+        static_assert(GH == 4, "two exchanges leave one head a lane");
+        const bool upper = lane & 16, odd = lane & 8;
+        float a0 = upper ? dot[2] : dot[0], a1 = upper ? dot[3] : dot[1];
+        a0 += __shfl_xor_sync(0xffffffffu, upper ? dot[0] : dot[2], 16);
+        a1 += __shfl_xor_sync(0xffffffffu, upper ? dot[1] : dot[3], 16);
+        float z = odd ? a1 : a0;
+        z += __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+#pragma unroll
+        for (int h = 0; h < GH; ++h) {
+            const float s = __shfl_sync(0xffffffffu, z, 8 * h) * scale_log2;
+            if (s > m[h]) {  // (the whole warp, and ever more seldom)
+                const float c = exp2f(m[h] - s);
+                l[h] *= c;
+#pragma unroll
+                for (int k = 0; k < DPL; ++k) acc[h][k] *= c;
+                m[h] = s;
             }
+            const float p = exp2f(s - (m[h] == -INFINITY ? 0.f : m[h]));
+            l[h] += p;
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) acc[h][k] = fmaf(p, x[k], acc[h][k]);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t0 + u * kWarps >= visible) break;  // (the whole warp)
-            float dot[GH];
-#pragma unroll
-            for (int h = 0; h < GH; ++h) {
-                dot[h] = 0.f;
-#pragma unroll
-                for (int k = 0; k < DPL; ++k) dot[h] = fmaf(qv[h][k], x[u][k], dot[h]);
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-                for (int h = 0; h < GH; ++h) dot[h] += __shfl_xor_sync(0xffffffffu, dot[h], off);
-#pragma unroll
-            for (int h = 0; h < GH; ++h) {
-                const float s = dot[h] * scale_log2, m_new = fmaxf(m[h], s);
-                const float c = exp2f(m[h] - m_new), p = exp2f(s - m_new);
-                l[h] = l[h] * c + p;
-#pragma unroll
-                for (int k = 0; k < DPL; ++k) acc[h][k] = fmaf(p, x[u][k], acc[h][k] * c);
-                m[h] = m_new;
-            }
-        }
+        for (int k = 0; k < DPL; ++k) x[k] = ahead[k];
     }
     if (lane == 0) {
 #pragma unroll

@@ -1,6 +1,6 @@
 // pa_latent_umma.cu -- attention over a latent cache on the 5th-generation
 // tensor cores, two SMs per tile (cta_group::2); bf16/f16, rows of 512 latent
-// and 64 rotated elements, block_size 8 or a multiple of 16.
+// and 64 rotated elements, block_size a multiple of 4.
 //
 // Row t of the cache is [c_t | r_t].  For query row (token i, head h):
 //   x_t = scale * q[i, h] . [c_t | r_t],  out[i, h] = softmax(x) C.
@@ -102,7 +102,7 @@ struct Params {
     int32_t num_seqs;
     int32_t num_heads;
     int32_t block_size;
-    int32_t box_rows;  // rows of a box of the cache: 8, 16, 32 or 64
+    int32_t box_rows;  // rows of a box of the cache: 4, 8, 16, 32 or 64
     int32_t causal;
     float scale_log2;
     float* records;  // [2 pairs][rec_rows][REC]
@@ -848,8 +848,13 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const Params p, int p
 
 // ---------------------------------------------------------------- host side
 
+// Rows of a box: as many as lie together in every block, up to half a tile.
+// (A box need not fill the eight rows of a swizzle pattern, which goes by the
+// address; fewer than four rows would take more boxes than there are lanes.)
 int box_rows(int block_size) {
-    return block_size == 8 ? 8 : block_size % 64 == 0 ? 64 : block_size % 32 == 0 ? 32 : 16;
+    int n = 64;
+    while (block_size % n) n /= 2;
+    return n;
 }
 
 // Pairs of SMs that run at once.  Not every two SMs are a pair (a cluster lies
@@ -942,7 +947,7 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
 
 bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size) {
     return (dtype == 1 || dtype == 2) && latent_dim == LAT && rope_dim == ROT &&
-           (block_size == 8 || (block_size > 0 && block_size % 16 == 0));
+           block_size > 0 && block_size % 4 == 0;
 }
 
 size_t latent_umma_workspace(int64_t rows) {

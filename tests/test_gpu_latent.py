@@ -25,7 +25,7 @@ def pa():
 
 
 def _tensor_cores(b):
-    return b.dtype != "f32" and (b.lat, b.rot) == (512, 64) and (b.bs == 8 or b.bs % 16 == 0)
+    return b.dtype != "f32" and (b.lat, b.rot) == (512, 64) and b.bs % 4 == 0
 
 
 def decode(pa, b, q, scale, out=None, ws_fill=0xFF, stream=None):
@@ -63,7 +63,10 @@ DECODE = [
     ([400, 31], 8, 512, 64, 256, "bf16"),
     ([100] * 97 + [777], 16, 512, 64, 16, "bf16"),   # more units than SM pairs
     ([4000, 4100], 32, 512, 64, 16, "f16"),          # a unit in many pieces
-    ([130, 7], 16, 512, 64, 12, "bf16"),             # CUDA cores: no box
+    ([130, 7, 300], 16, 512, 64, 12, "bf16"),        # boxes of four rows
+    ([257, 66], 40, 512, 64, 4, "f16"),
+    ([140, 501], 24, 512, 64, 24, "bf16"),
+    ([130, 7], 16, 512, 64, 6, "bf16"),              # CUDA cores: no box
     ([90, 0, 5], 7, 512, 64, 1, "f16"),
     ([150, 64], 16, 512, 64, 16, "f32"),
     ([70, 33], 9, 96, 32, 16, "bf16"),
@@ -96,7 +99,8 @@ VARLEN = [
     ([(300, 700)], 8, 32, "f16", True),
     ([(2, 1000), (700, 700)], 1, 16, "bf16", True),
     ([(5, 77)], 200, 48, "bf16", True),
-    ([(4, 20), (6, 6)], 6, 4, "bf16", True),          # CUDA cores
+    ([(4, 20), (6, 6), (70, 200)], 6, 4, "bf16", True),
+    ([(4, 20), (6, 6)], 6, 3, "bf16", True),          # CUDA cores
     ([(30, 100), (1, 3)], 5, 16, "f32", True),
     ([(30, 100), (1, 3)], 5, 16, "f32", False),
 ]
