@@ -81,7 +81,9 @@ typedef enum {
      * the stream).  0 (default): no validation. */
     PA_OPT_CHECK_MODE = 0,
     /* Decode kernel: 0 automatic (default), 1 the CUDA-core kernel, 2 the
-     * tensor-core kernel (PA_ERR_UNSUPPORTED where it does not apply). */
+     * tensor-core kernel (PA_ERR_UNSUPPORTED where it does not apply).  Also
+     * of pa_latent_decode; pa_decode_shared works its prefixes apart with 2
+     * whatever the sizes, and never with 1. */
     PA_OPT_DECODE_KERNEL = 1,
     /* Number of CTAs of the tensor-core decode kernel's balanced split;
      * 0 (default) picks one per resident slot of the device. */
@@ -89,7 +91,7 @@ typedef enum {
     /* Varlen kernel: 0 automatic (default: the tcgen05 kernel where it
      * applies, else the CUDA-core kernel), 1 the CUDA-core kernel, 2 the
      * tcgen05 (tensor-memory) kernel (PA_ERR_UNSUPPORTED where it does not
-     * apply). */
+     * apply).  Also of pa_latent_varlen. */
     PA_OPT_VARLEN_KERNEL = 3,
     /* Code-cache decode, head_dim 128: work the two tiles of a pipeline stage
      * that belong to one (sequence, KV head) as one 32-token step (one

@@ -9,7 +9,8 @@
 //
 // Bound: the bytes of the prefixes, once a group, and of the rest of each
 // context; 64 requests of 20-1,500 tokens behind 8,192 shared ones read 233 MB
-// instead of 2,336.
+// instead of 2,336 (67 us instead of 228).  The decode runs first and the
+// prefixes start as it leaves each SM: both need most of an SM's shared memory.
 #include "pa_decode_tc.cuh"
 #include "pa_shared.cuh"
 

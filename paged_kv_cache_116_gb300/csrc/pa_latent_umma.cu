@@ -38,8 +38,14 @@
 // runs, one per pair; a unit cut between pairs leaves (m, l, o) records that
 // latent_merge_kernel joins.  The cut depends on the lengths only.
 //
-// Bound: the cache's bytes for single tokens (1,152 per token; with 128 heads
-// the products need 0.7 of that time), the tensor pipe for prompts.
+// Bound: shared memory.  Per tile and SM the products read 147 KB (S: 4 KB per
+// M 128 x N 128 instruction of a pair) and 98 KB (P C), the loads write 136 KB
+// (each CTA's keys, and its dims of all keys once more) and P 16 KB: 3,100
+// cycles at 128 bytes each, where the tensor pipe needs 2,180 and memory, for
+// single tokens, 3,140.  A tile takes 2,700-3,000 cycles of 8,192 new tokens
+// (1.35-1.4 PFLOP/s) and 3,700 from memory (8 x 32,768 tokens: 4.2 TB/s over the
+// call).  A unit costs kUnit tiles more, and the first products of a launch
+// come 10 us after its start: 152 SMs fill their rings at once.
 //
 // Every wait is bounded in time; on expiry the kernel sets a status bit, the
 // roles leave their loops, and the pair still frees its tensor memory.

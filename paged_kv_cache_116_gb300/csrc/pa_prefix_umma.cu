@@ -20,9 +20,12 @@
 // O += P V.  Tensor memory: O, then two buffers of S (one at head_dim 256) and
 // two of P.
 //
-// Bound: with 64 members of 4 heads per KV head the tensor pipe (S and P V:
-// 1,040 cycles per 128 keys at head_dim 128) and the loads of 64 KB beside it;
-// with few members the prefix's bytes.
+// Bound: with 64 members of 4 heads per KV head a tile of 128 keys takes 1,750
+// cycles where its products need 1,040 and shared memory 1,250 (64 KB loaded,
+// 96 KB read by the products), but a CTA has seven of them behind 16,000 cycles
+// of start (its first loads) and before 5,000 of records: 21 us for 8,192 keys,
+// most of the start hidden behind the end of the decode before it.  With few
+// members the prefix's bytes (5 x 13 members, 40 KV heads: 210 MB in 47 us).
 //
 // Every wait is bounded in time; on expiry the kernel sets a status bit, the
 // roles leave their loops and the CTA still frees its tensor memory.
