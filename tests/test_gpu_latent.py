@@ -224,3 +224,43 @@ def test_more_sequences_than_a_launch_lists(pa):
     close(decode(pa, b, q.to(DEV), 0.07), *latent_exact(b, q, None, 0.07, True, True))
     cu = list(range(S + 1))
     close(varlen(pa, b, q.to(DEV), cu, 0.07, True), *latent_exact(b, q, cu, 0.07, True, True))
+
+
+def test_back_to_back_calls_share_a_workspace(pa):
+    """Prompts and single tokens of different sizes on one stream with one scratch: none sees what another leaves."""
+    parts, size = [], 0
+    for i, (new, lens) in enumerate((([1] * 4, [900, 5, 64, 333]), ([70, 3], [70, 500]), ([1], [1]), ([300], [300]))):
+        b = LatentBatch(lens, 512, 64, 16, "bf16", i).to(DEV)
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        parts.append((b, cu, rand((cu[-1], 24, 576), "bf16", 70 + i).to(DEV)))
+        size = max(size, pa.pa_latent_varlen_workspace_size(len(lens), cu[-1], max(new), 24, 512, 64, 16, b.max_context,
+                                                            torch.bfloat16))
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    outs = []
+    for _ in range(6):
+        for b, cu, q in parts:
+            out = torch.empty((q.shape[0], 24, 512), dtype=q.dtype, device=DEV)
+            if cu == list(range(len(cu))):
+                pa.pa_latent_decode(out, q, b.dcache, b.dtables, b.dlens, b.max_context, 0.07, workspace=ws)
+            else:
+                pa.pa_latent_varlen(out, q, b.dcache, b.dtables, b.dlens, torch.tensor(cu, dtype=torch.int32, device=DEV),
+                                    max(b_ - a for a, b_ in zip(cu, cu[1:])), b.max_context, 0.07, workspace=ws)
+            outs.append(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, outs[i % len(parts)])
+    for (b, cu, q), out in zip(parts, outs):
+        close(out, *latent_exact(b, q.cpu(), cu, 0.07, True, True))
+
+
+def test_infinite_and_nan_tokens_reach_only_who_sees_them(pa):
+    """A NaN row of one sequence, and one of a token that comes after the query: the other sequences, and earlier rows
+    whose tiles do not hold it, are what they are without it."""
+    b = LatentBatch([300, 300], 512, 64, 16, "bf16", 2)
+    q = rand((2, 16, 576), "bf16", 3)
+    clean = decode(pa, b.to(DEV), q.to(DEV), 0.07)
+    b.dcache[b.tables[0, 3].long(), 5] = float("nan")
+    out = decode(pa, b, q.to(DEV), 0.07)
+    assert torch.isnan(out[0].float()).all() and torch.equal(out[1], clean[1])

@@ -162,3 +162,64 @@ def test_graph_replays_follow_lengths_and_groups(pa):
         assert torch.equal(got, out)
         b.lens = lens
         close(out, *shared_exact(b, q.cpu(), 0.09, True))
+
+
+@pytest.mark.parametrize("ctas", [1, 7, 152, 3000])
+def test_any_split_of_the_rests(pa, ctas):
+    """PA_OPT_DECODE_CTAS from one CTA (units worked whole) to more warps than tiles (one tile or none each)."""
+    b = SharedBatch([(96, [0, 1, 40, 300]), (16, [5, 5])], 2, 128, 16, "bf16", 8, [33]).to(DEV)
+    q = rand((7, 12, 128), "bf16", 9)
+    exact = shared_exact(b, q, 0.09, True)
+    pa.pa_set_option(2, ctas)
+    try:
+        close(shared(pa, b, q.to(DEV), 0.09), *exact)
+    finally:
+        pa.pa_set_option(2, 0)
+
+
+def test_no_group_shares_anything(pa):
+    """Groups without a prefix, of one member, or of none: the work of the prefixes is empty."""
+    b = SharedBatch([(0, [40, 50]), (64, [8]), (32, [])], 2, 128, 16, "f16", 6, [200]).to(DEV)
+    q = rand((4, 12, 128), "f16", 7)
+    close(shared(pa, b, q.to(DEV), 0.09), *shared_exact(b, q, 0.09, True))
+
+
+def test_streams_side_by_side(pa):
+    parts = []
+    for i in range(3):
+        b = SharedBatch([(256 + 64 * i, [64, 100, 1, 7])], 2, 128, 16, "bf16", i, [90]).to(DEV)
+        parts.append((b, rand((5, 12, 128), "bf16", 50 + i).to(DEV)))
+    alone = [shared(pa, b, q, 0.09) for b, q in parts]
+    torch.cuda.synchronize()
+    outs = []
+    for b, q in parts:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            outs.append([shared(pa, b, q, 0.09) for _ in range(5)])
+    torch.cuda.synchronize()
+    for a, os_ in zip(alone, outs):
+        for o in os_:
+            assert torch.equal(a, o)
+
+
+def test_back_to_back_calls_share_a_workspace(pa):
+    """Calls of different sizes on one stream, one scratch for all: none sees what another leaves."""
+    parts = []
+    for i, (pre, tails) in enumerate(((512, [5] * 20), (16, [300, 2]), (0, [40, 50]), (2048, [0, 9]))):
+        b = SharedBatch([(pre, tails)], 4, 128, 16, "bf16", i, [17]).to(DEV)
+        parts.append((b, rand((len(b.lens), 16, 128), "bf16", 70 + i).to(DEV)))
+    pa.pa_set_option(1, 2)
+    size = max(pa.pa_decode_shared_workspace_size(len(b.lens), 1, 16, 4, 128, 16, b.max_context, q.dtype) for b, q in parts)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    outs = []
+    for _ in range(6):
+        for b, q in parts:
+            out = torch.empty_like(q)
+            pa.pa_decode_shared(out, q, b.dk, b.dv, b.dtables, b.dlens, b.dstarts, b.dprefix, b.max_context, 0.09,
+                                workspace=ws)
+            outs.append(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        b, q = parts[i % len(parts)]
+        assert torch.equal(out, outs[i % len(parts)])
+    for (b, q), out in zip(parts, outs):
+        close(out, *shared_exact(b, q.cpu(), 0.09, True))
