@@ -794,27 +794,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (warp == W_S) tmem_pair_dealloc(tmem, TMEM_COLS);
 }
 
-// Joins the records of the units cut between pairs.  CTA (c, g): the unit that
-// pair c begins, rows 4 g .. 4 g + 3, a warp each (small CTAs: they are resident
-// beside the kernel whose end they wait for).
-template <typename T>
-__global__ void __launch_bounds__(128) latent_merge_kernel(const Params p, int pairs) {
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    const int c = blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + c));
-    if (row >= cut.x) return;
-    const int last = cut.y;
-    const int64_t row0 = __ldcg(&p.cuts[c].row0), W = cut.z;
+// Joins the records of the units cut between pairs: a warp folds every step-th
+// record of a row (o: 16 of its dims, the warp's lanes beside each other), B of
+// them in flight.
+struct Joined {
     float M = -INFINITY, l = 0.f;
     float4 o[4] = {};
-    constexpr int B = 4;  // records in flight
-    for (int q0 = c; q0 <= last; q0 += B) {
+};
+__device__ __forceinline__ Joined join_records(const Params& p, int pairs, int c, int row, const int4 cut, int from,
+                                               int step) {
+    constexpr int B = 4;
+    const int lane = threadIdx.x & 31, last = cut.y;
+    const int64_t W = cut.z;
+    Joined j;
+    for (int q0 = c + from; q0 <= last; q0 += B * step) {
         float m[B], lq[B];
         float4 a[B][4];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const int q = q0 + k;
+            const int q = q0 + k * step;
             const bool there = q <= last && (W >= pairs || q * W / pairs != (q + 1) * W / pairs);  // (no empty run)
             const float* rec = p.records + ((2ll * q + (q == c ? 1 : 0)) * p.rec_rows + row) * REC;
             m[k] = there ? __ldcg(rec + LAT) : -INFINITY;
@@ -823,33 +821,82 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const Params p, int p
             for (int i = 0; i < 4; ++i)
                 a[k][i] = there ? __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        float mn = M;
+        float mn = j.M;
 #pragma unroll
         for (int k = 0; k < B; ++k) mn = fmaxf(mn, m[k]);
-        const float ms = mn == -INFINITY ? 0.f : mn, e0 = exp2f(M - ms);
-        l *= e0;
+        const float ms = mn == -INFINITY ? 0.f : mn, e0 = exp2f(j.M - ms);
+        j.l *= e0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = make_float4(o[i].x * e0, o[i].y * e0, o[i].z * e0, o[i].w * e0);
+        for (int i = 0; i < 4; ++i) j.o[i] = make_float4(j.o[i].x * e0, j.o[i].y * e0, j.o[i].z * e0, j.o[i].w * e0);
 #pragma unroll
         for (int k = 0; k < B; ++k) {
             const float e = exp2f(m[k] - ms);
-            l = fmaf(lq[k], e, l);
+            j.l = fmaf(lq[k], e, j.l);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                o[i].x = fmaf(a[k][i].x, e, o[i].x);
-                o[i].y = fmaf(a[k][i].y, e, o[i].y);
-                o[i].z = fmaf(a[k][i].z, e, o[i].z);
-                o[i].w = fmaf(a[k][i].w, e, o[i].w);
+                j.o[i].x = fmaf(a[k][i].x, e, j.o[i].x);
+                j.o[i].y = fmaf(a[k][i].y, e, j.o[i].y);
+                j.o[i].z = fmaf(a[k][i].z, e, j.o[i].z);
+                j.o[i].w = fmaf(a[k][i].w, e, j.o[i].w);
             }
         }
-        M = mn;
+        j.M = mn;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    return j;
+}
+
+// CTA (c, g): the unit that pair c begins, rows 4 g .. 4 g + 3, a warp each
+// (small CTAs: they are resident beside the kernel whose end they wait for).
+template <typename T>
+__global__ void __launch_bounds__(128) latent_merge_kernel(const Params p, int pairs) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int c = blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + c));
+    if (row >= cut.x) return;
+    const int64_t row0 = __ldcg(&p.cuts[c].row0);
+    const Joined j = join_records(p, pairs, c, row, cut, 0, 1);
+    const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
     T* out = static_cast<T*>(p.out) + (row0 + row) * LAT;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint2*>(out + 128 * i + 4 * lane) =
-            make_uint2(pack2<T>(o[i].x * inv, o[i].y * inv), pack2<T>(o[i].z * inv, o[i].w * inv));
+            make_uint2(pack2<T>(j.o[i].x * inv, j.o[i].y * inv), pack2<T>(j.o[i].z * inv, j.o[i].w * inv));
+}
+
+// The same for units in many pieces: a CTA per row, whose eight warps fold every
+// eighth record each and then their results in order (a row's warp reading 75
+// records of 2 KB by itself took 18 us: 1 x 32,768 tokens of 16 heads 45.7 ->
+// 33.4 us, 1 x 1,999 17.4 -> 15.9; 8 x 32,768, nine pieces each, 72 either way).
+template <typename T>
+__global__ void __launch_bounds__(256) latent_merge_many_kernel(const Params p, int pairs) {
+    __shared__ float4 part[8][LAT / 4];
+    __shared__ float2 ml[8];
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int c = blockIdx.x, row = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 cut = __ldcg(reinterpret_cast<const int4*>(p.cuts + c));
+    if (row >= cut.x) return;
+    const int64_t row0 = __ldcg(&p.cuts[c].row0);
+    const Joined j = join_records(p, pairs, c, row, cut, warp, 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[warp][32 * i + lane] = j.o[i];
+    if (lane == 0) ml[warp] = make_float2(j.M, j.l);
+    __syncthreads();
+    float M = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, ml[w].x);
+    const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const float e = exp2f(ml[w].x - ms);
+        const float2 v = reinterpret_cast<const float2*>(part[w])[threadIdx.x];
+        l = fmaf(ml[w].y, e, l);
+        x = fmaf(v.x, e, x);
+        y = fmaf(v.y, e, y);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + (row0 + row) * LAT)[threadIdx.x] = pack2<T>(x * inv, y * inv);
 }
 
 // ---------------------------------------------------------------- host side
@@ -945,8 +992,12 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmC, p);
     if (e != cudaSuccess || pairs == 1) return e;
-    return launch_pdl_smem(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 3) / 4)),
-                           dim3(128), 0, stream, p, pairs);
+    // units in more than eight pieces on average: a CTA a row (see there)
+    if (pairs > 8 * units)
+        return launch_pdl(latent_merge_many_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)rec_rows), dim3(256), stream,
+                          p, pairs);
+    return launch_pdl(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 3) / 4)), dim3(128),
+                      stream, p, pairs);
 }
 
 }  // namespace
