@@ -706,7 +706,7 @@ PA_API pa_status pa_latent_write(void* q_out, int64_t q_out_stride, int64_t q_ou
  *   rope_dim:  >= 0; latent_dim + rope_dim <= 576
  *   workspace: pa_latent_decode_workspace_size(...) bytes, 16-byte aligned;
  *              its content on entry does not matter
- * bf16/f16 with latent_dim 512, rope_dim 64 and block_size a multiple of 4 run
+ * bf16/f16 with latent_dim 512 and rope_dim 64 run
  * on the tensor cores (tcgen05, two SMs per tile; probabilities enter the
  * second product in the query's type, sums are fp32), the rest in fp32 on the
  * CUDA cores.  PA_OPT_DECODE_KERNEL pins a kernel as it does for pa_decode.

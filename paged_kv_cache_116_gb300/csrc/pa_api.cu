@@ -1384,8 +1384,7 @@ static bool use_latent_umma(int64_t want, int dtype, int32_t latent_dim, int32_t
     const bool ok = pa::latent_umma_supported(dtype, latent_dim, rope_dim, block_size);
     *st = PA_OK;
     if (want == 2 && !ok)
-        *st = fail(PA_ERR_UNSUPPORTED, "the tensor-core latent kernel takes bf16/f16, latent_dim 512, rope_dim 64 and "
-                                       "block_size a multiple of 4");
+        *st = fail(PA_ERR_UNSUPPORTED, "the tensor-core latent kernel takes bf16/f16, latent_dim 512 and rope_dim 64");
     return ok && want != 1;
 }
 

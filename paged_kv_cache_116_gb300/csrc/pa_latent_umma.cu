@@ -1,6 +1,6 @@
 // pa_latent_umma.cu -- attention over a latent cache on the 5th-generation
 // tensor cores, two SMs per tile (cta_group::2); bf16/f16, rows of 512 latent
-// and 64 rotated elements, block_size a multiple of 4.
+// and 64 rotated elements.
 //
 // Row t of the cache is [c_t | r_t].  For query row (token i, head h):
 //   x_t = scale * q[i, h] . [c_t | r_t],  out[i, h] = softmax(x) C.
@@ -108,7 +108,7 @@ struct Params {
     int32_t num_seqs;
     int32_t num_heads;
     int32_t block_size;
-    int32_t box_rows;  // rows of a box of the cache: 4, 8, 16, 32 or 64
+    int32_t box_rows;  // rows of a box of the cache: a power of two, up to 64
     int32_t causal;
     float scale_log2;
     float* records;  // [2 pairs][rec_rows][REC]
@@ -258,11 +258,15 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t lo) {
     return (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32 | lo;
 }
 
+// FINE: boxes of one or two rows (block sizes that are no multiple of 4), more
+// than a box a lane and stage: 64 x 2,048 tokens of 16 heads in blocks of 6 take
+// 109 us and in blocks of one 189 (on the CUDA cores 912, in blocks of 16 58).
+// An instance of its own: as a branch it cost the other sizes 1 to 5 %.
 // SINGLE: one token per request.  The keys come from memory, the values mostly
 // from L2 behind them: five stages for the keys (8 x 32,768 tokens 88 -> 85 us,
 // 64 x 16 heads 60 -> 56; four and three for prompts, whose rows stay in L2:
 // 8,192 tokens 800 us against 884, 16 chunks 261 against 296).
-template <typename T, bool SINGLE>
+template <typename T, bool SINGLE, bool FINE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     latent_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                        const Params p) {
@@ -371,7 +375,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int w = (warp - W_LOAD) % NP;
         const bool values = warp >= W_LOAD + NP;
         const int br = p.box_rows, gpt = BK / br, gph = 64 / br;  // boxes per tile and chunk, per half tile
-        const int b = lane % gph, c = lane / gph;                 // this lane's box of a stage and its chunk
+        // a lane has a box of a stage (b, of chunk c); FINE: boxes lane and
+        // lane + 32 of both chunks
+        const int b = lane % gph, c = lane / gph;
         const uint32_t full0 = smem_of(full, 0), tail_bar = smem_of(&tail[w], rank), q_bar = smem_of(q_full, 0);
         Ring ring = values ? Ring{NK, NV, NK, 0} : Ring{0, NK, 0, 0};
         int seg = 0, turn = 0, tail_turn = 0;
@@ -387,12 +393,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (s.k1 <= s.k0) break;
             const int32_t* table = p.block_tables + (int64_t)s.req * p.max_blocks;
             const int L = s.r.L;
-            // pool row of this lane's box of tile k
-            auto box_row = [&](int k) -> int32_t {
-                const int tok = k * BK + lane * br;
-                return lane < gpt && k < s.k1 && tok < L ? table[tok / p.block_size] * p.block_size + tok % p.block_size : 0;
+            // pool rows of this lane's boxes of tile k: box `lane` of the
+            // tile, or boxes lane and lane + 32 of each half
+            auto box_rows_of = [&](int k, int32_t (&to)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    to[i] = 0;
+                    if (i && !FINE) continue;
+                    const int in = lane + 32 * (i & 1), tok = k * BK + 64 * (i >> 1) + in * br;
+                    if (in < (FINE ? gph : gpt) && k < s.k1 && tok < L)
+                        to[i] = table[tok / p.block_size] * p.block_size + tok % p.block_size;
+                }
             };
-            int32_t cur = box_row(s.k0);
+            int32_t cur[4], nxt[4];
+            box_rows_of(s.k0, cur);
+            // boxes of half tile h, n chunks from `chunk` on, to a stage
+            // (row: half_row(h))
+            auto half_row = [&](int h) -> int32_t {
+                return FINE ? 0 : __shfl_sync(0xffffffffu, cur[0], h * gph + b);
+            };
+            auto load = [&](uint8_t* st, uint32_t bar, int h, int32_t row, int boxes, int n, int chunk) {
+                if (!FINE) {
+                    if (c < n && b < boxes)
+                        tma_load_3d_pair(st + c * CHB + b * br * 128, &tmC, bar, 0, chunk + c, row);
+                    return;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (lane + 32 * e < boxes)
+                        for (int i = 0; i < n; ++i)
+                            tma_load_3d_pair(st + i * CHB + (lane + 32 * e) * br * 128, &tmC, bar, 0, chunk + i,
+                                             h ? cur[2 + e] : cur[e]);
+            };
             if (!values) {
                 // the query rows of this CTA: chunks w, w + NP, ..
                 if (!(run = wait(q_empty, (seg & 1) ^ 1))) break;
@@ -409,11 +441,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                      (int)(s.r.row0 + row + 16 * g));
             }
             for (int k = s.k0; k < s.k1 && run; ++k) {
-                const int32_t nxt = box_row(k + 1);
+                box_rows_of(k + 1, nxt);
                 if (!values) {
                     // this CTA's 64 keys, two chunks a stage
                     const int own = min(max(L - k * BK - 64 * (int)rank, 0), 64), boxes = (own + br - 1) / br;
-                    const int32_t row = __shfl_sync(0xffffffffu, cur, (int)rank * gph + b);
+                    const int32_t row = half_row((int)rank);
                     for (int c0 = 0; c0 < CH; c0 += 2) {
                         if (skip()) continue;
                         if (!(run = wait(&empty[ring.slot], ring.phase ^ 1))) break;
@@ -424,9 +456,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             else mbar_arrive_at(fb);
                         }
                         __syncwarp();
-                        if (c < nc && b < boxes)
-                            tma_load_3d_pair(base + ST_OFF + ring.slot * STAGE + c * CHB + b * br * 128, &tmC, fb, 0,
-                                             c0 + c, row);
+                        load(base + ST_OFF + ring.slot * STAGE, fb, (int)rank, row, boxes, nc, c0);
                         ring.next();
                     }
                 } else {
@@ -436,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     for (int h = 0; h < halves && run; ++h) {
                         const int keys = min(valid - 64 * h, 64), boxes = (keys + br - 1) / br;
                         const bool ragged = rest != 0 && h == halves - 1;
-                        const int32_t row = __shfl_sync(0xffffffffu, cur, h * gph + b);
+                        const int32_t row = half_row(h);
                         for (int pc = 0; pc < 2; ++pc) {
                             if (skip()) continue;
                             if (!(run = wait(&empty[ring.slot], ring.phase ^ 1))) break;
@@ -444,9 +474,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                             if (lane == 0) mbar_arrive_expect_tx_at(fb, (uint32_t)(boxes * 2 * br * 128));
                             __syncwarp();
                             uint8_t* st = base + ST_OFF + ring.slot * STAGE;
-                            if (c < 2 && b < boxes)
-                                tma_load_3d_pair(st + c * CHB + b * br * 128, &tmC, fb, 0,
-                                                 4 * (int)rank + 2 * pc + c, row);
+                            load(st, fb, h, row, boxes, 2, 4 * (int)rank + 2 * pc);
                             if (ragged) {
                                 // rows past the context hold anything, and P
                                 // is zero there: they are zeroed before the
@@ -466,7 +494,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         }
                     }
                 }
-                cur = nxt;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
             }
             ++seg;
             if (s.end() >= f1) break;
@@ -819,7 +848,8 @@ __device__ __forceinline__ Joined join_records(const Params& p, int pairs, int c
             lq[k] = there ? __ldcg(rec + LAT + 1) : 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                a[k][i] = there ? __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                a[k][i] = there ? __ldcg(reinterpret_cast<const float4*>(rec) + 32 * i + lane)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mn = j.M;
 #pragma unroll
@@ -903,7 +933,7 @@ __global__ void __launch_bounds__(256) latent_merge_many_kernel(const Params p, 
 
 // Rows of a box: as many as lie together in every block, up to half a tile.
 // (A box need not fill the eight rows of a swizzle pattern, which goes by the
-// address; fewer than four rows would take more boxes than there are lanes.)
+// address.)
 int box_rows(int block_size) {
     int n = 64;
     while (block_size % n) n /= 2;
@@ -972,7 +1002,8 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     // than one tile each
     const int64_t units = a.cu ? rows / TM + a.num_seqs : (int64_t)a.num_seqs * ((a.num_heads + TM - 1) / TM);
     const int64_t tiles = units * (((int64_t)a.max_context + BK - 1) / BK);
-    const auto kernel = a.cu ? latent_umma_kernel<T, false> : latent_umma_kernel<T, true>;
+    const auto kernel = p.box_rows < 4 ? (a.cu ? latent_umma_kernel<T, false, true> : latent_umma_kernel<T, true, true>)
+                                       : (a.cu ? latent_umma_kernel<T, false, false> : latent_umma_kernel<T, true, false>);
     const void* kfn = reinterpret_cast<const void*>(kernel);
     cudaError_t e = allow_smem(kfn, smem_bytes(kMaxSeqs));
     if (e != cudaSuccess) return e;
@@ -994,8 +1025,8 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
     if (e != cudaSuccess || pairs == 1) return e;
     // units in more than eight pieces on average: a CTA a row (see there)
     if (pairs > 8 * units)
-        return launch_pdl(latent_merge_many_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)rec_rows), dim3(256), stream,
-                          p, pairs);
+        return launch_pdl(latent_merge_many_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)rec_rows), dim3(256),
+                          stream, p, pairs);
     return launch_pdl(latent_merge_kernel<T>, dim3((unsigned)(pairs - 1), (unsigned)((rec_rows + 3) / 4)), dim3(128),
                       stream, p, pairs);
 }
@@ -1004,7 +1035,7 @@ cudaError_t launch_typed(const LatentArgs& a, int32_t num_blocks, void* workspac
 
 bool latent_umma_supported(int dtype, int32_t latent_dim, int32_t rope_dim, int32_t block_size) {
     return (dtype == 1 || dtype == 2) && latent_dim == LAT && rope_dim == ROT &&
-           block_size > 0 && block_size % 4 == 0;
+           block_size > 0;
 }
 
 size_t latent_umma_workspace(int64_t rows) {

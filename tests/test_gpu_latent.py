@@ -25,7 +25,7 @@ def pa():
 
 
 def _tensor_cores(b):
-    return b.dtype != "f32" and (b.lat, b.rot) == (512, 64) and b.bs % 4 == 0
+    return b.dtype != "f32" and (b.lat, b.rot) == (512, 64)
 
 
 def decode(pa, b, q, scale, out=None, ws_fill=0xFF, stream=None):
@@ -66,8 +66,12 @@ DECODE = [
     ([130, 7, 300], 16, 512, 64, 12, "bf16"),        # boxes of four rows
     ([257, 66], 40, 512, 64, 4, "f16"),
     ([140, 501], 24, 512, 64, 24, "bf16"),
-    ([130, 7], 16, 512, 64, 6, "bf16"),              # CUDA cores: no box
-    ([90, 0, 5], 7, 512, 64, 1, "f16"),
+    ([130, 7], 16, 512, 64, 6, "bf16"),              # boxes of two rows
+    ([129, 500, 0, 64], 128, 512, 64, 10, "f16"),
+    ([90, 0, 5], 7, 512, 64, 1, "f16"),              # boxes of one row
+    ([128, 1, 1100, 33, 95], 130, 512, 64, 1, "bf16"),
+    ([63, 400], 16, 512, 64, 7, "bf16"),
+    ([100] * 90 + [515], 16, 512, 64, 2, "bf16"),
     ([150, 64], 16, 512, 64, 16, "f32"),
     ([70, 33], 9, 96, 32, 16, "bf16"),
     ([70, 33], 3, 50, 0, 4, "f32"),
@@ -100,7 +104,9 @@ VARLEN = [
     ([(2, 1000), (700, 700)], 1, 16, "bf16", True),
     ([(5, 77)], 200, 48, "bf16", True),
     ([(4, 20), (6, 6), (70, 200)], 6, 4, "bf16", True),
-    ([(4, 20), (6, 6)], 6, 3, "bf16", True),          # CUDA cores
+    ([(4, 20), (6, 6)], 6, 3, "bf16", True),          # boxes of one row
+    ([(300, 333), (1, 258)], 16, 1, "bf16", True),
+    ([(70, 201), (129, 129)], 24, 14, "f16", True),   # boxes of two rows
     ([(30, 100), (1, 3)], 5, 16, "f32", True),
     ([(30, 100), (1, 3)], 5, 16, "f32", False),
 ]

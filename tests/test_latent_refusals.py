@@ -83,7 +83,7 @@ def test_pinned_tensor_cores_refuse_what_they_do_not_take(lib):
     for opt, call in ((1, _decode), (3, _varlen)):
         assert lib.pa_set_option(opt, 2) == 0
         try:
-            for kw in (dict(dtype=0), dict(lat=256), dict(rot=32), dict(bs=6)):
+            for kw in (dict(dtype=0), dict(lat=256), dict(rot=32)):
                 assert call(lib, **kw) == UNSUPPORTED
         finally:
             lib.pa_set_option(opt, 0)
@@ -93,8 +93,8 @@ def test_workspace_sizes(lib):
     size = lib.pa_latent_decode_workspace_size
     assert size(0, 16, 512, 64, 16, 100, 1) == 0
     assert size(4, 16, 512, 64, 16, 64, 0) == 0          # CUDA cores: pieces of 64 keys at least
-    assert 0 < size(4, 16, 512, 64, 6, 1000, 1) < size(4, 16, 512, 64, 6, 4000, 1)
-    assert size(4000, 16, 512, 64, 6, 4000, 1) == 0     # rows enough
+    assert 0 < size(4, 16, 512, 64, 6, 1000, 0) < size(4, 16, 512, 64, 6, 4000, 0)
+    assert size(4000, 16, 512, 64, 6, 4000, 0) == 0     # rows enough
     small, full = size(64, 16, 512, 64, 16, 4000, 1), size(1, 128, 512, 64, 16, 100, 1)  # a tile has 128 rows
     assert 0 < small < full
     assert lib.pa_latent_varlen_workspace_size(4, 1000, 500, 128, 512, 64, 16, 4000, 1) == full
