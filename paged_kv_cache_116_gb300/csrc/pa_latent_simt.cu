@@ -10,12 +10,17 @@
 // the row's latent part, so a row is read once for all the CTA's heads and for
 // both products.
 //
-// One CTA of four warps per (query row, four heads), and per piece of the keys
-// where there are too few rows to fill the GPU: lanes split the row's elements,
-// each warp keeps one online softmax per head over an interleaved share of the
-// keys, and the warps' states are joined at the end; pieces leave (o, m, l)
-// records that latent_simt_join_kernel joins in order.  Bound: instructions (per
-// key and four heads 144 products of a lane's elements and ten shuffles).
+// One CTA of four warps per (query row, 16 heads), and per piece of the keys
+// where there are too few rows to fill the GPU: the rows of eight keys at a time
+// go through shared memory, three stages ahead (cp.async; element by element
+// where rows are no multiple of 16 bytes), and are read there by every warp, each
+// with four heads of its own: lanes split the row's elements, two keys are worked
+// at once.  With eight heads or fewer the warps share out the keys instead and
+// their states are joined at the end, in order; pieces leave (o, m, l) records
+// that latent_simt_join_kernel joins in order.  Bound: instructions (per key and
+// four heads 72 packed products of a lane's elements).  64 x 2,048
+// fp32 tokens of 16 heads 289 us (412 with a row at a time straight from memory,
+// for four heads a CTA), 1 x 32,768 173 (257).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -29,19 +34,38 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int GH = 4;  // heads per CTA
+// Two neighbouring elements of shared memory.
+__device__ __forceinline__ unsigned long long pair_of(const float* x) {
+    const float2 v = *reinterpret_cast<const float2*>(x);
+    return f32x2_pack(v.x, v.y);
+}
+__device__ __forceinline__ unsigned long long pair_of(const __nv_bfloat16* x) {
+    const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(x));
+    return f32x2_pack(v.x, v.y);
+}
+__device__ __forceinline__ unsigned long long pair_of(const __half* x) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(x));
+    return f32x2_pack(v.x, v.y);
+}
 
-// DPL: elements of a row per lane.
+constexpr int kWarps = 4;
+constexpr int GH = 4;                // heads per warp
+constexpr int HEADS = GH * kWarps;   // heads per CTA
+constexpr int KEYS = 8, STAGES = 4;  // keys per stage
+constexpr int kMaxSplits = 2 * kSms; // pieces of a row
+
+// DPL: elements of a row per lane, in pairs (2 lane + 64 j).
 // splits pieces of each row's keys; records (splits > 1): [rows][heads][splits]
 // of latent_dim + 2 floats.
 template <typename T, int DPL>
-__global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentArgs a, int splits, float* records) {
+__global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const LatentArgs a, int splits, float* records) {
+    constexpr int PITCH = DPL * 32;  // elements of a row in shared memory
+    extern __shared__ __align__(16) uint8_t smem[];  // [STAGES][KEYS][PITCH] of T; at the end [HEADS][PITCH] floats
     __shared__ float sm_m[kWarps][GH], sm_l[kWarps][GH];
-    __shared__ float sm_acc[GH][DPL * 32];
+    static_assert(STAGES * KEYS * sizeof(T) >= HEADS * sizeof(float), "the sums fit in the stages");
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int row = blockIdx.x, h0 = blockIdx.y * GH, nh = min(GH, a.num_heads - h0), piece = blockIdx.z;
+    const int row = blockIdx.x, h0 = blockIdx.y * HEADS, nh = min(HEADS, a.num_heads - h0), piece = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int req = row, num_new = 1, j = 0;
     if (a.cu != nullptr) {
@@ -61,82 +85,131 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
     const int from = (int)((int64_t)max(seen, 0) * piece / splits);
     const int visible = (int)((int64_t)max(seen, 0) * (piece + 1) / splits);
     const int lat = a.latent_dim, D = lat + a.rope_dim;
-    const T* q = static_cast<const T*>(a.q) + ((int64_t)row * a.num_heads + h0) * D;
     const T* cache = static_cast<const T*>(a.cache);
     const int32_t* table = a.block_tables + (int64_t)req * a.max_blocks;
     const float scale_log2 = a.scale * 1.4426950408889634f;
+    // this warp's heads, and its share of the keys
+    const int groups = nh <= GH ? 1 : nh <= 2 * GH ? 2 : 4, shares = kWarps / groups;
+    const int group = warp % groups, share = warp / groups, mine = min(GH, nh - GH * group);
 
-    float qv[GH][DPL], acc[GH][DPL], m[GH], l[GH];
+    unsigned long long qv[GH][DPL / 2], acc[GH][DPL / 2];
+    float m[GH], l[GH];
+    const T* q = static_cast<const T*>(a.q) + ((int64_t)row * a.num_heads + h0 + GH * group) * D;
 #pragma unroll
     for (int h = 0; h < GH; ++h) {
         m[h] = -INFINITY;
         l[h] = 0.f;
 #pragma unroll
-        for (int k = 0; k < DPL; ++k) {
-            const int d = lane + 32 * k;
-            qv[h][k] = h < nh && d < D ? Elt<T>::to_f(q[(int64_t)h * D + d]) : 0.f;
-            acc[h][k] = 0.f;
+        for (int k = 0; k < DPL / 2; ++k) {
+            const int d = 2 * lane + 64 * k;
+            qv[h][k] = f32x2_pack(h < mine && d < D ? Elt<T>::to_f(q[(int64_t)h * D + d]) : 0.f,
+                                  h < mine && d + 1 < D ? Elt<T>::to_f(q[(int64_t)h * D + d + 1]) : 0.f);
+            acc[h][k] = 0ull;
         }
     }
-    // the next key's row is on its way while one is worked, and the table entry
-    // of the one after it
-    auto row_of = [&](int t) -> const T* {
-        t = min(t, visible - 1);
-        return cache + ((int64_t)table[t / a.block_size] * a.block_size + t % a.block_size) * D;
-    };
-    auto fetch = [&](const T* r, float (&x)[DPL]) {
-#pragma unroll
-        for (int k = 0; k < DPL; ++k) {
-            const int d = lane + 32 * k;
-            x[k] = d < D ? Elt<T>::to_f(r[d]) : 0.f;
-        }
-    };
-    int t = from + warp;
-    float x[DPL], ahead[DPL];
-    const T* next = nullptr;
-    if (t < visible) {
-        fetch(row_of(t), x);
-        next = row_of(t + kWarps);
+    T* const stages = reinterpret_cast<T*>(smem);
+    if (D < PITCH) {  // what no row fills is zero
+        for (int i = threadIdx.x; i < STAGES * KEYS * PITCH * (int)sizeof(T) / 16; i += kWarps * 32)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
     }
-    for (; t < visible; t += kWarps) {
-        fetch(next, ahead);
-        next = row_of(t + 2 * kWarps);
-        float dot[GH];
+    // loads: keys warp and warp + 4 of a tile
+    const int bytes = D * (int)sizeof(T), tiles = (visible - from + KEYS - 1) / KEYS;
+    const bool vec = bytes % 16 == 0;
+    const T* ahead[2];  // the rows of the tile to load next
+    auto rows_of = [&](int tile) {
 #pragma unroll
-        for (int h = 0; h < GH; ++h) {
-            dot[h] = 0.f;
-#pragma unroll
-            for (int k = 0; k < DPL; ++k) dot[h] = fmaf(qv[h][k], x[k], dot[h]);
+        for (int i = 0; i < 2; ++i) {
+            const int t = from + tile * KEYS + warp + kWarps * i;
+            ahead[i] = t < visible ? cache + ((int64_t)table[t / a.block_size] * a.block_size + t % a.block_size) * D
+                                   : nullptr;
         }
-        // the four sums over the lanes: each exchange halves what a lane
-        // keeps, so ten shuffles instead of twenty
-        static_assert(GH == 4, "two exchanges leave one head a lane");
-        const bool upper = lane & 16, odd = lane & 8;
-        float a0 = upper ? dot[2] : dot[0], a1 = upper ? dot[3] : dot[1];
-        a0 += __shfl_xor_sync(0xffffffffu, upper ? dot[0] : dot[2], 16);
-        a1 += __shfl_xor_sync(0xffffffffu, upper ? dot[1] : dot[3], 16);
-        float z = odd ? a1 : a0;
-        z += __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+    };
+    auto load = [&](int tile) {
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-#pragma unroll
-        for (int h = 0; h < GH; ++h) {
-            const float s = __shfl_sync(0xffffffffu, z, 8 * h) * scale_log2;
-            if (s > m[h]) {  // (the whole warp, and ever more seldom)
-                const float c = exp2f(m[h] - s);
-                l[h] *= c;
-#pragma unroll
-                for (int k = 0; k < DPL; ++k) acc[h][k] *= c;
-                m[h] = s;
+        for (int i = 0; i < 2; ++i) {
+            T* to = stages + (tile % STAGES * KEYS + warp + kWarps * i) * PITCH;
+            if (ahead[i] == nullptr) continue;
+            if (vec) {
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(ahead[i]);
+                const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+                for (int c = 16 * lane; c < bytes; c += 512)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + c), "l"(src + c) : "memory");
+            } else {
+                for (int d = lane; d < D; d += 32) to[d] = ahead[i][d];
             }
-            const float p = exp2f(s - (m[h] == -INFINITY ? 0.f : m[h]));
-            l[h] += p;
-#pragma unroll
-            for (int k = 0; k < DPL; ++k) acc[h][k] = fmaf(p, x[k], acc[h][k]);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        rows_of(tile + 1);
+    };
+    rows_of(0);
+    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    for (int tile = 0; tile < tiles; ++tile) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncthreads();  // this tile is there, and the one before it read
+        load(tile + STAGES - 1);
+        const int keys = min(KEYS, visible - from - tile * KEYS);
+        if (mine <= 0) continue;
+        for (int t = 2 * share; t < keys; t += 2 * shares) {
+            const T* x0 = stages + (tile % STAGES * KEYS + t) * PITCH + 2 * lane;
+            const bool two = t + 1 < keys;
+            unsigned long long x[2][DPL / 2];
 #pragma unroll
-        for (int k = 0; k < DPL; ++k) x[k] = ahead[k];
+            for (int k = 0; k < DPL / 2; ++k) {
+                x[0][k] = pair_of(x0 + 64 * k);
+                x[1][k] = two ? pair_of(x0 + PITCH + 64 * k) : 0ull;
+            }
+            float dot[2 * GH];  // of key 0, then of key 1
+#pragma unroll
+            for (int h = 0; h < GH; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    unsigned long long d2 = 0ull;
+#pragma unroll
+                    for (int k = 0; k < DPL / 2; ++k) d2 = fma_f32x2(qv[h][k], x[e][k], d2);
+                    float u, v;
+                    f32x2_unpack(d2, u, v);
+                    dot[GH * e + h] = u + v;
+                }
+            // the eight sums over the lanes: each exchange halves what a lane
+            // keeps, so nine shuffles instead of forty; lane 4 i has sum i
+            static_assert(GH == 4, "three exchanges leave one sum a lane");
+            float z[4], y[2], s1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool up = lane & 16;
+                z[i] = (up ? dot[4 + i] : dot[i]) + __shfl_xor_sync(0xffffffffu, up ? dot[i] : dot[4 + i], 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool up = lane & 8;
+                y[i] = (up ? z[2 + i] : z[i]) + __shfl_xor_sync(0xffffffffu, up ? z[i] : z[2 + i], 8);
+            }
+            s1 = (lane & 4 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0] : y[1], 4);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+#pragma unroll
+            for (int h = 0; h < GH; ++h) {
+                const float sa = __shfl_sync(0xffffffffu, s1, 4 * h) * scale_log2;
+                const float sb = two ? __shfl_sync(0xffffffffu, s1, 16 + 4 * h) * scale_log2 : -INFINITY;
+                const float mx = fmaxf(sa, sb);
+                if (mx > m[h]) {  // (the whole warp, and ever more seldom)
+                    const float c = exp2f(m[h] - mx);
+                    l[h] *= c;
+#pragma unroll
+                    for (int k = 0; k < DPL / 2; ++k) acc[h][k] = fma_f32x2(acc[h][k], f32x2_pack(c, c), 0ull);
+                    m[h] = mx;
+                }
+                const float ms = m[h] == -INFINITY ? 0.f : m[h], wa = exp2f(sa - ms), wb = exp2f(sb - ms);
+                l[h] += wa + wb;
+                const unsigned long long wa2 = f32x2_pack(wa, wa), wb2 = f32x2_pack(wb, wb);
+#pragma unroll
+                for (int k = 0; k < DPL / 2; ++k)
+                    acc[h][k] = fma_f32x2(wb2, x[1][k], fma_f32x2(wa2, x[0][k], acc[h][k]));
+            }
+        }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (lane == 0) {
 #pragma unroll
         for (int h = 0; h < GH; ++h) {
@@ -144,33 +217,37 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
             sm_l[warp][h] = l[h];
         }
     }
-    // the warps' sums, one warp after the other (a fixed order)
-    for (int w = 0; w < kWarps; ++w) {
+    // a head's sums, one share after the other (a fixed order)
+    float* const sums = reinterpret_cast<float*>(smem);
+    for (int w = 0; w < shares; ++w) {
         __syncthreads();
-        if (warp != w) continue;
+        if (share != w) continue;
 #pragma unroll
         for (int h = 0; h < GH; ++h) {
             float M = -INFINITY;
-            for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm_m[v][h]);
-            const float f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - M);
+            for (int v = group; v < kWarps; v += groups) M = fmaxf(M, sm_m[v][h]);
+            const float f = exp2f(m[h] - (M == -INFINITY ? 0.f : M));
 #pragma unroll
-            for (int k = 0; k < DPL; ++k) {
-                float* s = &sm_acc[h][lane + 32 * k];
-                *s = (w ? *s : 0.f) + f * acc[h][k];
+            for (int k = 0; k < DPL / 2; ++k) {
+                float2* s = reinterpret_cast<float2*>(sums + (GH * group + h) * PITCH + 2 * lane + 64 * k);
+                float u, v;
+                f32x2_unpack(acc[h][k], u, v);
+                const float2 old = w ? *s : make_float2(0.f, 0.f);
+                *s = make_float2(old.x + f * u, old.y + f * v);
             }
         }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < nh * lat; e += blockDim.x) {
-        const int h = e / lat, d = e - h * lat;
+        const int h = e / lat, d = e - h * lat, g = h / GH;
         float M = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int v = 0; v < kWarps; ++v) M = fmaxf(M, sm_m[v][h]);
-#pragma unroll
-        for (int v = 0; v < kWarps; ++v) sum += sm_m[v][h] == -INFINITY ? 0.f : exp2f(sm_m[v][h] - M) * sm_l[v][h];
+        for (int v = g; v < kWarps; v += groups) M = fmaxf(M, sm_m[v][h % GH]);
+        for (int v = g; v < kWarps; v += groups)
+            sum += exp2f(sm_m[v][h % GH] - (M == -INFINITY ? 0.f : M)) * sm_l[v][h % GH];
+        const float o = sums[h * PITCH + d];
         if (splits > 1) {
             float* rec = records + (((int64_t)row * a.num_heads + h0 + h) * splits + piece) * (lat + 2);
-            rec[d] = visible > from ? sm_acc[h][d] : 0.f;
+            rec[d] = o;
             if (d == 0) {
                 rec[lat] = M;
                 rec[lat + 1] = sum;
@@ -179,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32) latent_simt_kernel(const LatentAr
         }
         // (a row that sees nothing is zero; a NaN sum stays NaN)
         static_cast<T*>(a.out)[((int64_t)row * a.num_heads + h0 + h) * lat + d] =
-            Elt<T>::from_f(visible > 0 ? sm_acc[h][d] / sum : 0.f);
+            Elt<T>::from_f(visible > 0 ? o / sum : 0.f);
     }
 }
 
@@ -192,37 +269,60 @@ __global__ void __launch_bounds__(128) latent_simt_join_kernel(const LatentArgs 
     const int64_t rh = (int64_t)blockIdx.x * a.num_heads + blockIdx.y;
     if (a.cu && (int)blockIdx.x >= a.cu[a.num_seqs]) return;  // behind the last request
     const float* rec = records + rh * splits * (lat + 2);
+    __shared__ float weight[kMaxSplits], top[4], total[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float M = -INFINITY, sum = 0.f;
-    for (int i = 0; i < splits; ++i) M = fmaxf(M, rec[(int64_t)i * (lat + 2) + lat]);
+    for (int i = threadIdx.x; i < splits; i += 128) M = fmaxf(M, weight[i] = rec[(int64_t)i * (lat + 2) + lat]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) top[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     const float ms = M == -INFINITY ? 0.f : M;
-    for (int i = 0; i < splits; ++i)
-        sum += exp2f(rec[(int64_t)i * (lat + 2) + lat] - ms) * rec[(int64_t)i * (lat + 2) + lat + 1];
-    for (int d = threadIdx.x; d < lat; d += blockDim.x) {
+    for (int i = threadIdx.x; i < splits; i += 128)
+        sum = fmaf(weight[i] = exp2f(weight[i] - ms), rec[(int64_t)i * (lat + 2) + lat + 1], sum);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) total[warp] = sum;
+    __syncthreads();
+    sum = (total[0] + total[1]) + (total[2] + total[3]);
+    for (int d = threadIdx.x; d < lat; d += 128) {
         float o = 0.f;
-        for (int i = 0; i < splits; ++i)
-            o = fmaf(exp2f(rec[(int64_t)i * (lat + 2) + lat] - ms), rec[(int64_t)i * (lat + 2) + d], o);
+#pragma unroll 8
+        for (int i = 0; i < splits; ++i) o = fmaf(weight[i], rec[(int64_t)i * (lat + 2) + d], o);
         static_cast<T*>(a.out)[rh * lat + d] = Elt<T>::from_f(sum == 0.f ? 0.f : o / sum);
     }
 }
 
-// Pieces of each row's keys: enough CTAs for four on every SM, of 64 keys at
-// least (1 x 32,768 fp32 tokens of 16 heads are 4 CTAs otherwise).
+// Pieces of each row's keys: four CTAs for every SM (two run at once) or a few
+// less, of 64 keys at least (1 x 32,768 fp32 tokens of 16 heads are one CTA
+// otherwise).
 int simt_splits(int64_t total_q, int32_t num_heads, int32_t max_context) {
-    const int64_t ctas = total_q * ((num_heads + GH - 1) / GH);
-    const int64_t want = (4 * kSms + ctas - 1) / ctas, most = ((int64_t)max_context + 63) / 64;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min<int64_t>(most, 1024)));
+    const int64_t ctas = total_q * ((num_heads + HEADS - 1) / HEADS);
+    const int64_t want = ctas <= kSms ? 4 * kSms / ctas : (4 * kSms + ctas - 1) / ctas;
+    const int64_t most = ((int64_t)max_context + 63) / 64;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), most));
+}
+
+template <typename T, int DPL>
+cudaError_t launch_rows(const LatentArgs& a, int splits, float* records, cudaStream_t stream) {
+    const dim3 grid((unsigned)a.total_q, (unsigned)((a.num_heads + HEADS - 1) / HEADS), (unsigned)splits);
+    const size_t smem = (size_t)STAGES * KEYS * DPL * 32 * sizeof(T);
+    const auto kernel = latent_simt_kernel<T, DPL>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl_smem(kernel, grid, dim3(kWarps * 32), smem, stream, a, splits, records);
 }
 
 template <typename T>
 cudaError_t launch_typed(const LatentArgs& a, float* records, cudaStream_t stream) {
     const int D = a.latent_dim + a.rope_dim, splits = simt_splits(a.total_q, a.num_heads, a.max_context);
-    const dim3 grid((unsigned)a.total_q, (unsigned)((a.num_heads + GH - 1) / GH), (unsigned)splits), block(kWarps * 32);
-    cudaError_t e = D <= 128   ? launch_pdl(latent_simt_kernel<T, 4>, grid, block, stream, a, splits, records)
-                    : D <= 288 ? launch_pdl(latent_simt_kernel<T, 9>, grid, block, stream, a, splits, records)
-                               : launch_pdl(latent_simt_kernel<T, 18>, grid, block, stream, a, splits, records);
+    cudaError_t e = D <= 128   ? launch_rows<T, 4>(a, splits, records, stream)
+                    : D <= 320 ? launch_rows<T, 10>(a, splits, records, stream)
+                               : launch_rows<T, 18>(a, splits, records, stream);
     if (e != cudaSuccess || splits == 1) return e;
-    return launch_pdl(latent_simt_join_kernel<T>, dim3((unsigned)a.total_q, (unsigned)a.num_heads), dim3(128), stream, a,
-                      splits, (const float*)records);
+    return launch_pdl(latent_simt_join_kernel<T>, dim3((unsigned)a.total_q, (unsigned)a.num_heads), dim3(128), stream,
+                      a, splits, (const float*)records);
 }
 
 }  // namespace

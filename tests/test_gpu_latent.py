@@ -78,6 +78,10 @@ DECODE = [
     ([20], 5, 256, 32, 16, "f16"),
     ([3000], 4, 512, 64, 16, "f32"),                 # CUDA cores, a row's keys in pieces
     ([900, 0, 1, 70], 6, 96, 32, 4, "f16"),
+    ([600, 0, 33], 37, 512, 64, 16, "f32"),          # several CTAs of heads, the last one short
+    ([77, 8, 1], 12, 300, 13, 16, "bf16"),           # rows that are no vectors
+    ([40, 515], 8, 129, 0, 3, "f32"),
+    ([200, 9], 1, 512, 64, 16, "f32"),
 ]
 
 
