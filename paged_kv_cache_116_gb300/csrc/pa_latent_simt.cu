@@ -17,10 +17,11 @@
 // with four heads of its own: lanes split the row's elements, two keys are worked
 // at once.  With eight heads or fewer the warps share out the keys instead and
 // their states are joined at the end, in order; pieces leave (o, m, l) records
-// that latent_simt_join_kernel joins in order.  Bound: instructions (per key and
-// four heads 72 packed products of a lane's elements).  64 x 2,048
-// fp32 tokens of 16 heads 289 us (412 with a row at a time straight from memory,
-// for four heads a CTA), 1 x 32,768 173 (257).
+// that latent_simt_join_kernel joins in order.  Bound: the issue of instructions
+// with two warps a scheduler (180 registers hold four heads' queries and sums).
+// 64 x 2,048 fp32 tokens of 16 heads 245 us (409 with a row at a time straight
+// from memory for four heads a CTA, 289 with every lane taking all weights), 1 x
+// 32,768 107 (255); bf16, 256 + 32 elements, 64 x 2,048: 183 (348).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -52,7 +53,7 @@ constexpr int kWarps = 4;
 constexpr int GH = 4;                // heads per warp
 constexpr int HEADS = GH * kWarps;   // heads per CTA
 constexpr int KEYS = 8, STAGES = 4;  // keys per stage
-constexpr int kMaxSplits = 2 * kSms; // pieces of a row
+constexpr int kMaxSplits = kSms; // pieces of a row
 
 // DPL: elements of a row per lane, in pairs (2 lane + 64 j).
 // splits pieces of each row's keys; records (splits > 1): [rows][heads][splits]
@@ -93,12 +94,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
     const int group = warp % groups, share = warp / groups, mine = min(GH, nh - GH * group);
 
     unsigned long long qv[GH][DPL / 2], acc[GH][DPL / 2];
-    float m[GH], l[GH];
+    // of head lane / 4 % 4; l: of the first (lanes 0 ..) and second keys of the pairs
+    float m = -INFINITY, l = 0.f;
     const T* q = static_cast<const T*>(a.q) + ((int64_t)row * a.num_heads + h0 + GH * group) * D;
 #pragma unroll
     for (int h = 0; h < GH; ++h) {
-        m[h] = -INFINITY;
-        l[h] = 0.f;
 #pragma unroll
         for (int k = 0; k < DPL / 2; ++k) {
             const int d = 2 * lane + 64 * k;
@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             T* to = stages + (tile % STAGES * KEYS + warp + kWarps * i) * PITCH;
-            if (ahead[i] == nullptr) continue;
-            if (vec) {
+            if (ahead[i] == nullptr) {  // zero beside the last key
+                for (int d = lane; d < D; d += 32) to[d] = Elt<T>::from_f(0.f);
+            } else if (vec) {
                 const uint8_t* src = reinterpret_cast<const uint8_t*>(ahead[i]);
                 const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
                 for (int c = 16 * lane; c < bytes; c += 512)
@@ -152,12 +153,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
         if (mine <= 0) continue;
         for (int t = 2 * share; t < keys; t += 2 * shares) {
             const T* x0 = stages + (tile % STAGES * KEYS + t) * PITCH + 2 * lane;
-            const bool two = t + 1 < keys;
             unsigned long long x[2][DPL / 2];
 #pragma unroll
             for (int k = 0; k < DPL / 2; ++k) {
                 x[0][k] = pair_of(x0 + 64 * k);
-                x[1][k] = two ? pair_of(x0 + PITCH + 64 * k) : 0ull;
+                x[1][k] = pair_of(x0 + PITCH + 64 * k);  // (zero where there is none)
             }
             float dot[2 * GH];  // of key 0, then of key 1
 #pragma unroll
@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
                     dot[GH * e + h] = u + v;
                 }
             // the eight sums over the lanes: each exchange halves what a lane
-            // keeps, so nine shuffles instead of forty; lane 4 i has sum i
+            // keeps, so nine shuffles instead of forty; lanes 4 i .. 4 i + 3
+            // end with sum i and take its weight for all
             static_assert(GH == 4, "three exchanges leave one sum a lane");
             float z[4], y[2], s1;
 #pragma unroll
@@ -188,20 +189,26 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
             s1 = (lane & 4 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0] : y[1], 4);
             s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
             s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+            const float x2 = lane < 16 || t + 1 < keys ? s1 * scale_log2 : -INFINITY;
+            const float mx = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 16));
+            if (__any_sync(0xffffffffu, mx > m)) {  // (ever more seldom)
+                const float mn = fmaxf(m, mx), c = mn == -INFINITY ? 1.f : exp2f(m - mn);
+                m = mn;
+                l *= c;
+#pragma unroll
+                for (int h = 0; h < GH; ++h) {
+                    const float ch = __shfl_sync(0xffffffffu, c, 4 * h);
+                    if (ch == 1.f) continue;
+                    const unsigned long long c2 = f32x2_pack(ch, ch);
+#pragma unroll
+                    for (int k = 0; k < DPL / 2; ++k) acc[h][k] = fma_f32x2(acc[h][k], c2, 0ull);
+                }
+            }
+            const float w = exp2f(x2 - (m == -INFINITY ? 0.f : m));
+            l += w;
 #pragma unroll
             for (int h = 0; h < GH; ++h) {
-                const float sa = __shfl_sync(0xffffffffu, s1, 4 * h) * scale_log2;
-                const float sb = two ? __shfl_sync(0xffffffffu, s1, 16 + 4 * h) * scale_log2 : -INFINITY;
-                const float mx = fmaxf(sa, sb);
-                if (mx > m[h]) {  // (the whole warp, and ever more seldom)
-                    const float c = exp2f(m[h] - mx);
-                    l[h] *= c;
-#pragma unroll
-                    for (int k = 0; k < DPL / 2; ++k) acc[h][k] = fma_f32x2(acc[h][k], f32x2_pack(c, c), 0ull);
-                    m[h] = mx;
-                }
-                const float ms = m[h] == -INFINITY ? 0.f : m[h], wa = exp2f(sa - ms), wb = exp2f(sb - ms);
-                l[h] += wa + wb;
+                const float wa = __shfl_sync(0xffffffffu, w, 4 * h), wb = __shfl_sync(0xffffffffu, w, 16 + 4 * h);
                 const unsigned long long wa2 = f32x2_pack(wa, wa), wb2 = f32x2_pack(wb, wb);
 #pragma unroll
                 for (int k = 0; k < DPL / 2; ++k)
@@ -210,13 +217,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (lane == 0) {
-#pragma unroll
-        for (int h = 0; h < GH; ++h) {
-            sm_m[warp][h] = m[h];
-            sm_l[warp][h] = l[h];
-        }
-    }
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (lane < 16 && lane % 4 == 0) sm_m[warp][lane / 4] = m, sm_l[warp][lane / 4] = l;
     // a head's sums, one share after the other (a fixed order)
     float* const sums = reinterpret_cast<float*>(smem);
     for (int w = 0; w < shares; ++w) {
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
         for (int h = 0; h < GH; ++h) {
             float M = -INFINITY;
             for (int v = group; v < kWarps; v += groups) M = fmaxf(M, sm_m[v][h]);
-            const float f = exp2f(m[h] - (M == -INFINITY ? 0.f : M));
+            const float f = exp2f(sm_m[warp][h] - (M == -INFINITY ? 0.f : M));
 #pragma unroll
             for (int k = 0; k < DPL / 2; ++k) {
                 float2* s = reinterpret_cast<float2*>(sums + (GH * group + h) * PITCH + 2 * lane + 64 * k);
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) latent_simt_kernel(const Laten
     }
 }
 
-// Joins the pieces of a (row, head), in order.
+// Joins the pieces of a (row, head), in order: 128 dims a CTA.
 template <typename T>
 __global__ void __launch_bounds__(128) latent_simt_join_kernel(const LatentArgs a, int splits, const float* records) {
     pdl_wait_primary();
@@ -286,9 +288,9 @@ __global__ void __launch_bounds__(128) latent_simt_join_kernel(const LatentArgs 
     if (lane == 0) total[warp] = sum;
     __syncthreads();
     sum = (total[0] + total[1]) + (total[2] + total[3]);
-    for (int d = threadIdx.x; d < lat; d += 128) {
+    if (const int d = blockIdx.z * 128 + threadIdx.x; d < lat) {
         float o = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < splits; ++i) o = fmaf(weight[i], rec[(int64_t)i * (lat + 2) + d], o);
         static_cast<T*>(a.out)[rh * lat + d] = Elt<T>::from_f(sum == 0.f ? 0.f : o / sum);
     }
@@ -321,8 +323,8 @@ cudaError_t launch_typed(const LatentArgs& a, float* records, cudaStream_t strea
                     : D <= 320 ? launch_rows<T, 10>(a, splits, records, stream)
                                : launch_rows<T, 18>(a, splits, records, stream);
     if (e != cudaSuccess || splits == 1) return e;
-    return launch_pdl(latent_simt_join_kernel<T>, dim3((unsigned)a.total_q, (unsigned)a.num_heads), dim3(128), stream,
-                      a, splits, (const float*)records);
+    return launch_pdl(latent_simt_join_kernel<T>, dim3((unsigned)a.total_q, (unsigned)a.num_heads, (unsigned)((a.latent_dim + 127) / 128)),
+                      dim3(128), stream, a, splits, (const float*)records);
 }
 
 }  // namespace
